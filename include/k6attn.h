@@ -442,10 +442,142 @@ k6attn_status k6attn_forward_static_scratch(k6attn_t h, const void *q, const voi
                                             const void *joint_k, const void *joint_v, const void *rope_tables,
                                             int n_chunks, void *out, float *lse, void *stream);
 
+/*
+ * Packed sequences: clips (images, prompts, new tokens of running streams) of
+ * different lengths lie one behind another in [tokens][heads][d] tensors, in
+ * place of a padded batch.  The pages describe one geometry per call; these
+ * entry points carry the same layer ([CP] "Self-Attention with Context
+ * Parallelism": QK-norm, rotary embedding, attention) to mixed batches, grouped
+ * key heads, causal masks, new tokens over kept keys, and training.
+ *
+ * Shared by the packed calls:
+ *  - The handle supplies H (query heads), d, axis_dim, theta, the element type
+ *    and the error word; its B, grid and joint settings are not used.
+ *  - A tensor is its first element's pointer (16-byte aligned) and the stride
+ *    in elements from one token to the next (at least heads * d, a multiple of
+ *    16 bytes); heads and d are dense.  So q, k and v may be the parts of one
+ *    fused projection [tokens][(H + 2 kv_heads) * d], and so may their
+ *    gradients: rows of equal stride that interleave do not count as overlap.
+ *  - kv_heads key/value heads, a divisor of H for attention: query head h uses
+ *    key head h / (H / kv_heads).
+ *  - Zero tokens are allowed; the tensors may then be NULL.
+ *
+ * k6attn_packed_norm_rope: per-head QK-norm and multi-axis rotary embedding in
+ * one pass.  For a token at positions[token] = (t, h, w) (int32, any value) and
+ * each head row x of q and k:
+ *   y = x / sqrt(mean over d (x^2) + eps) * weight     (weights fp32 [d], one
+ *       for q and one for k; both NULL: y = x, eps unused),
+ *   pair (2i, 2i+1) of axis a's segment turns by p_a * theta^(-2i / axis_dim[a]).
+ * A token with positions (0, 0, 0) is not rotated.  Statistics and angles are
+ * fp32 or finer, each output element is rounded once.  q, k, q_out, k_out:
+ * [tokens][H][d] and [tokens][kv_heads][d]; q and k of the handle's type,
+ * outputs of out_dtype (the handle's type, or F16 for BF16 handles; a value
+ * that is not finite in fp16 sets K6ATTN_ERR_RANGE, at k6attn_sync).  An output
+ * may be its input (same pointer and stride, same type); otherwise outputs
+ * overlap nothing.
+ *
+ * k6attn_packed_norm_rope_backward: from dq_out, dk_out (gradients of the
+ * outputs, of the handle's type) the gradients dq, dk of q and k (the handle's
+ * type) and dq_weight, dk_weight (fp32 [d], overwritten; summed over tokens and
+ * heads in fp32 in an order that does not change from run to run).  Without
+ * weights, q, k and the weights' gradients may be NULL.  dq may be dq_out (same
+ * pointer and stride), dk dk_out.  workspace: at least
+ * k6attn_packed_norm_rope_backward_workspace_bytes (0 without weights).
+ */
+k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, const int *positions, const void *q,
+                                      long q_stride, const void *k, long k_stride, const float *q_weight,
+                                      const float *k_weight, float eps, void *q_out, long q_out_stride, void *k_out,
+                                      long k_out_stride, k6attn_dtype out_dtype, void *stream);
+size_t k6attn_packed_norm_rope_backward_workspace_bytes(k6attn_t h, long tokens, int kv_heads);
+k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *positions,
+                                               const void *dq_out, long dq_out_stride, const void *dk_out,
+                                               long dk_out_stride, const void *q, long q_stride, const void *k,
+                                               long k_stride, const float *q_weight, const float *k_weight, float eps,
+                                               void *dq, long dq_stride, void *dk, long dk_stride, float *dq_weight,
+                                               float *dk_weight, void *workspace, size_t workspace_bytes,
+                                               void *stream);
+
+/*
+ * A batch of packed sequences for attention (BF16 handles).
+ *  n_seq       sequences; sequence s has the query tokens [cu_q[s], cu_q[s+1])
+ *              and the key tokens [cu_k[s], cu_k[s+1]).  Either may be empty.
+ *  kv_heads    key/value heads (H / kv_heads <= 128).
+ *  mask_block  0: every query sees every key of its sequence.  F >= 1: query i
+ *              of Lq sits at key position i + Lk - Lq (the queries are the
+ *              newest tokens) and sees the keys below
+ *              (floor((i + Lk - Lq) / F) + 1) * F: F = 1 is causal, F > 1
+ *              causal by frames of F tokens.  A query that sees no key (Lk = 0,
+ *              or Lq > Lk) gets a zero output and lse = -inf.
+ *  q_tokens, k_tokens  token rows of q and of k and v (at least the last
+ *              offset; rows outside the sequences are neither written nor do
+ *              they influence a result, whatever they hold).
+ */
+typedef struct {
+    int n_seq;
+    int kv_heads;
+    int mask_block;
+    long q_tokens, k_tokens;
+} k6attn_packed;
+
+/*
+ * The work list of a batch, made on the device from its offsets (int32 device
+ * arrays of n_seq + 1 ascending values; cu_k NULL = cu_q) into `plan`, a
+ * caller-owned, 16-byte aligned device buffer of k6attn_packed_plan_bytes.  A
+ * plan serves any number of forward and backward calls of the same batch
+ * (every layer of a model) and is not changed by them.  Offsets that are
+ * not ascending or leave [0, tokens] make K6ATTN_ERR_INVALID_ARG at k6attn_sync,
+ * and so does a call with a batch other than the plan's; the call then writes
+ * nothing.  A plan that was never made is recognised with near certainty only.
+ */
+size_t k6attn_packed_plan_bytes(k6attn_t h, const k6attn_packed *batch);
+k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const int *cu_q, const int *cu_k, void *plan,
+                                 size_t plan_bytes, void *stream);
+
+/*
+ * Attention of a packed batch: out = softmax(q k^T / sqrt(d)) v over the keys
+ * that each query sees.
+ *  q  [q_tokens][H][d], k [k_tokens][kv_heads][d] of qk_dtype (BF16 or F16, both
+ *     alike); v [k_tokens][kv_heads][d] bf16.  k and v of a sequence must be
+ *     finite, also where the mask hides them (a hidden key has weight 0, and
+ *     0 * NaN is NaN within its tile of 128 keys).
+ *  out  bf16 [q_tokens][H][d];  lse fp32 [H][q_tokens], dense, natural log (may
+ *     be NULL).  Neither overlaps an input.
+ *  workspace  at least k6attn_packed_workspace_bytes (0 for short batches; it
+ *     holds the partials of long key ranges that are split among SMs).  Calls
+ *     that can overlap on the GPU need a workspace each.
+ * Results do not depend on the other sequences of the batch beyond the last bits
+ * that the splitting of long key ranges moves, and are the same in every run.
+ */
+size_t k6attn_packed_workspace_bytes(k6attn_t h, const k6attn_packed *batch);
+k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,
+                                    long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                    k6attn_dtype qk_dtype, void *out, long out_stride, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients, from out and lse as k6attn_packed_forward wrote them and dout
+ * (bf16): dq [q_tokens][H][d], dk, dv [k_tokens][kv_heads][d], bf16, overwritten
+ * for every row of a sequence; dk and dv are summed over the query heads of
+ * their key head.  dout must be finite.  Gradients overlap no input and one
+ * another nowhere.  The same bits in every run.  workspace: at least
+ * k6attn_packed_backward_workspace_bytes.
+ * P is rounded to bf16 and dS to qk_dtype before their products (for F16, dS is
+ * carried times a power of two that follows max |dout| and max |v|, so that
+ * small gradients do not vanish); products accumulate in fp32.
+ */
+size_t k6attn_packed_backward_workspace_bytes(k6attn_t h, const k6attn_packed *batch);
+k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,
+                                     long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                     k6attn_dtype qk_dtype, const void *out, long out_stride, const void *dout,
+                                     long dout_stride, const float *lse, void *dq, long dq_stride, void *dk,
+                                     long dk_stride, void *dv, long dv_stride, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* Synchronise `stream`, then read and clear the handle's device error word:
  * K6ATTN_ERR_TIMEOUT if any kernel of this handle gave up on a wait,
  * K6ATTN_ERR_RANGE if a rotation into fp16 overflowed or a constant-max row
  * underflowed,
+ * K6ATTN_ERR_INVALID_ARG if a packed plan's offsets or its use were wrong,
  * K6ATTN_ERR_CUDA on an asynchronous CUDA error, or if the device placed
  * the attention kernel's dynamic shared memory off a 1024-byte boundary (the
  * kernel then computes nothing; its tiles need that alignment and its 227 KB

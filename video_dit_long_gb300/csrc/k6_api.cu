@@ -2,6 +2,7 @@
 // layout and the launch sequence of one forward pass.  Every check runs on
 // the host before any launch; nothing here aborts.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -10,18 +11,6 @@
 
 #include "k6attn.h"
 #include "k6_internal.h"
-
-struct k6attn_handle {
-    k6attn_desc desc;
-    k6::Geom g;
-    float2 *tables = nullptr;
-    size_t table_bytes = 0;
-    int *err = nullptr;                 // device error word
-    unsigned long long wait_limit_ns = 2000000000ull;
-    int strict_order = 0;
-    int rotate_bf16 = 0;                // forward: rotated copies in bf16 instead of fp16
-    int device = 0;
-};
 
 namespace k6 {
 
@@ -35,19 +24,11 @@ k6attn_status set_error(k6attn_status s, const char *fmt, ...) {
     return s;
 }
 
+void clear_error() { g_msg[0] = 0; }
+
 k6attn_status cuda_check(cudaError_t e, const char *what) {
     if (e == cudaSuccess) return K6ATTN_OK;
     return set_error(K6ATTN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-static bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || !na || !nb) return false;
-    uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
 }
 
 struct WsLayout {
@@ -175,6 +156,28 @@ k6attn_status check_handle(const char *fn, k6attn_t h) {
     return K6ATTN_OK;
 }
 
+// Rotary frequencies in turns per position, as 64-bit fixed-point fractions of
+// a turn: pair i of an axis of a dims turns by theta^(-2i/a) / (2 pi) per
+// position, and position * turns modulo 2^64 is the angle reduced to one turn
+// without rounding, however far the position is.
+static k6attn_status make_turns(k6attn_handle *h) {
+    const Geom &g = h->g;
+    unsigned long long t[64];  // d / 2 <= 64 pairs
+    int n = 0;
+    for (int a = 0; a < 3; a++)
+        for (int i = 0; i < g.axis_dim[a] / 2; i++) {
+            const double turns = pow(h->desc.theta, -2.0 * i / g.axis_dim[a]) / 6.283185307179586476925;
+            // 2^64 * fraction, rounded; a fraction that rounds up to one turn is no turn
+            const double x = rint(ldexp(turns - floor(turns), 64));
+            t[n++] = x < 18446744073709551616.0 ? (unsigned long long)x : 0ull;
+        }
+    k6attn_status st = cuda_check(cudaMalloc(&h->turns, n * sizeof(t[0])), "create: rotary frequencies");
+    if (st == K6ATTN_OK)
+        st = cuda_check(cudaMemcpy(h->turns, t, n * sizeof(t[0]), cudaMemcpyHostToDevice),
+                        "create: rotary frequencies");
+    return st;
+}
+
 }  // namespace k6
 
 using namespace k6;
@@ -243,9 +246,11 @@ k6attn_status k6attn_create(const k6attn_desc *desc, k6attn_t *out) {
     if (st == K6ATTN_OK && h->table_bytes)
         st = cuda_check(cudaMalloc(&h->tables, h->table_bytes), "create: rotary tables");
     if (st == K6ATTN_OK) st = cuda_check(launch_rope_tables(g, d.theta, h->tables, 0), "create: rotary tables");
+    if (st == K6ATTN_OK) st = make_turns(h);
     if (st == K6ATTN_OK) st = cuda_check(cudaDeviceSynchronize(), "create: rotary tables");
     if (st != K6ATTN_OK) {
         cudaFree(h->tables);
+        cudaFree(h->turns);
         cudaFree(h->err);
         delete h;
         return st;
@@ -262,6 +267,7 @@ void k6attn_destroy(k6attn_t h) {
     if (other) cudaSetDevice(h->device);
     cudaDeviceSynchronize();
     cudaFree(h->tables);
+    cudaFree(h->turns);
     cudaFree(h->err);
     if (other) cudaSetDevice(cur);
     delete h;
@@ -798,6 +804,10 @@ k6attn_status k6attn_sync(k6attn_t h, void *stream) {
     if (s != K6ATTN_OK) return s;
     if (word) {
         cudaMemset(h->err, 0, sizeof(int));
+        if (word == DEV_PLAN)
+            return set_error(K6ATTN_ERR_INVALID_ARG,
+                             "a packed plan's offsets are not ascending within the tokens, or a packed call was given a "
+                             "plan made for another batch");
         if (word == DEV_RANGE) return set_error(K6ATTN_ERR_RANGE, "a rotated q/k value does not fit fp16");
         if (word == DEV_LAYOUT)
             return set_error(K6ATTN_ERR_CUDA, "the device placed the attention kernel's shared memory off a 1024-byte boundary");

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "k6_internal.h"
+#include "k6_packed_tma.h"
 
 namespace k6 {
 
@@ -78,6 +79,27 @@ bool make_bshd_map(CUtensorMap *m, const void *base, long rows, int H, int B, bo
     if (f.encode(m, type, 4,
                  const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+        if (why) *why = "cuTensorMapEncodeTiled rejected a tensor";
+        return false;
+    }
+    return true;
+}
+
+bool make_rows_map(CUtensorMap *m, const void *base, long tokens, int heads, long stride, int box_heads,
+                   int box_tokens, const char **why) {
+    const DriverFns &f = driver();
+    if (!f.encode) {
+        if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
+        return false;
+    }
+    cuuint64_t dims[4] = {128, (cuuint64_t)heads, (cuuint64_t)tokens, 1};
+    cuuint64_t strides[3] = {256, (cuuint64_t)stride * 2, (cuuint64_t)tokens * (cuuint64_t)stride * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    // bf16 and fp16 elements travel alike
+    if (f.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
         if (why) *why = "cuTensorMapEncodeTiled rejected a tensor";
         return false;

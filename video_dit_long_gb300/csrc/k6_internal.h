@@ -12,7 +12,7 @@
 namespace k6 {
 
 // Device error word codes (written with atomicCAS, first error wins).
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_RANGE = 2, DEV_LAYOUT = 3 };
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_RANGE = 2, DEV_LAYOUT = 3, DEV_PLAN = 4 };
 
 // Geometry of one joint attention problem, as the kernels see it.
 struct Geom {
@@ -26,6 +26,35 @@ struct Geom {
     k6attn_dtype dtype;      // storage type of q, k, v, out (BF16 or F32)
 };
 
+}  // namespace k6
+
+struct k6attn_handle {
+    k6attn_desc desc;
+    k6::Geom g;
+    float2 *tables = nullptr;
+    size_t table_bytes = 0;
+    unsigned long long *turns = nullptr;  // rotary turns per position [d/2], 64-bit fixed point (packed calls)
+    int *err = nullptr;                 // device error word
+    unsigned long long wait_limit_ns = 2000000000ull;
+    int strict_order = 0;
+    int rotate_bf16 = 0;                // forward: rotated copies in bf16 instead of fp16
+    int device = 0;
+};
+
+namespace k6 {
+
+// ---- host helpers of the entry points ----
+
+static inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+static inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+static inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    if (!a || !b || !na || !nb) return false;
+    uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // Offsets (in float2 entries) of the rotary tables inside one buffer.
 struct RopeLayout {
     long off[4];             // axis t, h, w, joint
@@ -37,6 +66,7 @@ RopeLayout rope_layout(const Geom &g);
 // Error reporting of the host side (thread-local message).
 k6attn_status set_error(k6attn_status s, const char *fmt, ...);
 k6attn_status cuda_check(cudaError_t e, const char *what);
+void clear_error();  // the thread's last message
 
 // A handle is usable only while its own device is current (its tables and
 // error word live there): INVALID_ARG otherwise, and for a null handle.
@@ -129,5 +159,64 @@ cudaError_t launch_attn_bwd(const Geom &g, bool qk_f16, const void *q, const voi
                             const void *jv, const void *out, const void *dout, const float *lse, float2 *LD, float *dq,
                             float *dk, float *dv, float *djk, float *djv, unsigned long long wait_limit_ns, int *err,
                             cudaStream_t st, const char **why);
+
+// ---- packed sequences (k6_packed_*.cu) ----
+
+// Per-head norm and rotation of packed token rows; strides in elements between tokens.
+struct PackedNormRope {
+    long tokens;
+    int Hkv;
+    const int *positions;             // [tokens][3]
+    const unsigned long long *turns;  // the handle's rotary frequencies
+    const void *x[2];                 // [0] queries, [1] keys (the norm's inputs; unused by the backward pass without norm)
+    long x_stride[2];
+    void *z[2];                       // the outputs, or (backward, read only) their gradients
+    long z_stride[2];
+    void *dx[2];                      // backward: gradients of x
+    long dx_stride[2];
+    const float *w[2];                // [d] each, or null: rotation only
+    float eps;
+    int *err;
+};
+cudaError_t launch_packed_norm_rope(const Geom &g, const PackedNormRope &p, k6attn_dtype out, cudaStream_t st);
+size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens);
+cudaError_t launch_packed_norm_rope_bwd(const Geom &g, const PackedNormRope &p, float *dq_w, float *dk_w, void *ws,
+                                        cudaStream_t st);
+
+// A batch of packed sequences as the attention kernels see it: G query heads
+// per key head; a tile of query rows holds `tpt` tokens x G heads = `rows` <= 128
+// rows of one key head, row = token * G + head.
+struct PackedGeom {
+    int n_seq, H, Hkv, G, block;
+    int Tq, Tk;                       // token rows of q and of k, v
+    int tpt, rows;
+    int cap_q, cap_k;                 // upper bounds: query tiles, 128-key tiles
+    int extra;                        // work items that splitting long key ranges may add, per key head
+    int cap_slots;                    // partial outputs per key head
+};
+PackedGeom packed_geom(const Geom &g, const k6attn_packed &b);
+
+struct PackedPtrs {
+    const void *q, *k, *v;
+    long q_stride, k_stride, v_stride;  // elements between tokens
+    bool qk_f16;
+    const void *plan;
+    unsigned long long wait_limit_ns;
+    int *err;
+};
+
+size_t packed_plan_bytes(const PackedGeom &p);
+cudaError_t launch_packed_plan(const PackedGeom &p, const int *cu_q, const int *cu_k, void *plan, int *err,
+                               cudaStream_t st);
+
+size_t packed_fwd_workspace(const PackedGeom &p);
+cudaError_t launch_packed_fwd(const PackedGeom &p, const PackedPtrs &t, void *out, long out_stride, float *lse,
+                              void *ws, cudaStream_t st, const char **why);
+
+size_t packed_bwd_workspace(const PackedGeom &p);
+cudaError_t launch_packed_bwd(const PackedGeom &p, const PackedPtrs &t, const void *out, long out_stride,
+                              const void *dout, long dout_stride, const float *lse, void *dq, long dq_stride,
+                              void *dk, long dk_stride, void *dv, long dv_stride, void *ws, cudaStream_t st,
+                              const char **why);
 
 }  // namespace k6

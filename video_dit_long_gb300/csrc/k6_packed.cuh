@@ -1,0 +1,97 @@
+// k6_packed.cuh -- the plan of a batch of packed sequences: what the plan kernel
+// writes and the attention kernels read, and the mask they share.
+//
+// Mask.  Query token i (of Lq) of a sequence sits at key position
+// i + Lk - Lq (the queries are the newest tokens) and sees the keys j < limit:
+//   block == 0: limit = Lk;
+//   block == F: limit = clip((floor((i + Lk - Lq) / F) + 1) F, 0, Lk),
+// F = 1 causal, F > 1 causal by frames of F tokens.  The limit never falls with
+// i, so a tile of query tokens needs the key tiles below its last token's
+// limit, and key j is seen by the query tokens i >= floor(j / F) F - (Lk - Lq).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "k6_internal.h"
+
+namespace k6 {
+
+constexpr unsigned PACKED_MAGIC = 0x6b36504cu;
+
+struct PackedHeader {
+    unsigned magic;
+    int n_seq, H, Hkv, block, Tq, Tk;  // what the plan was made for
+    int n_fwd, n_merge, n_q, n_k;      // items in each list
+    int n_slots;
+    int chunk;                         // key tiles that one forward item takes at most
+    int q_lo, q_hi, k_lo, k_hi;        // token rows that belong to a sequence
+    int bad;                           // the offsets are not ascending within the tokens: no list is valid
+};
+constexpr size_t PACKED_HEADER_BYTES = 256;
+static_assert(sizeof(PackedHeader) <= PACKED_HEADER_BYTES, "plan header");
+
+// One tile of query tokens over key tiles [kt0, kt1) of its sequence.
+struct __align__(16) PackedItem {
+    int tok0, n_tok;   // first token row of q, tokens (1 .. tpt)
+    int krow0, Lk;     // the sequence's first row of k, and its keys
+    int pos0;          // key position of token tok0
+    int kt0, kt1;
+    int slot;          // partial output, or -1: the item covers all of its tile's keys
+};
+// One tile of 128 keys over query tiles [qt0, qt1) of its sequence.
+struct __align__(16) PackedKItem {
+    int krow0, n_key;  // first row of k, keys (1 .. 128)
+    int key0;          // position of the first key in its sequence
+    int qrow0, Lq;     // the sequence's first row of q, and its queries
+    int off;           // Lk - Lq
+    int qt0, qt1;
+};
+// The partials [slot0, slot0 + n) of a split tile.
+struct __align__(16) PackedMerge {
+    int tok0, n_tok, slot0, n;
+};
+
+struct PackedPlan {
+    PackedHeader *head;
+    PackedItem *fwd;    // [cap_q + extra], heaviest first
+    PackedItem *q;      // [cap_q], unsplit (backward), heaviest first
+    PackedKItem *k;     // [cap_k], heaviest first
+    PackedMerge *merge; // [extra]
+};
+
+static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const PackedGeom &p) {
+    PackedPlan r;
+    char *b = static_cast<char *>(base);
+    r.head = reinterpret_cast<PackedHeader *>(b);
+    b += PACKED_HEADER_BYTES;
+    r.fwd = reinterpret_cast<PackedItem *>(b);
+    b += ((size_t)p.cap_q + p.extra) * sizeof(PackedItem);
+    r.q = reinterpret_cast<PackedItem *>(b);
+    b += (size_t)p.cap_q * sizeof(PackedItem);
+    r.k = reinterpret_cast<PackedKItem *>(b);
+    b += (size_t)p.cap_k * sizeof(PackedKItem);
+    r.merge = reinterpret_cast<PackedMerge *>(b);
+    return r;
+}
+
+// True if the plan was made for this batch and holds valid lists.
+static inline __device__ bool packed_plan_ok(const PackedHeader &h, const PackedGeom &p) {
+    return h.magic == PACKED_MAGIC && !h.bad && h.n_seq == p.n_seq && h.H == p.H && h.Hkv == p.Hkv &&
+           h.block == p.block && h.Tq == p.Tq && h.Tk == p.Tk;
+}
+
+// Keys that the token at key position `pos` sees (pos may be negative: none).
+// The host keeps block and Lk below 2^30, so the product stays below 2^31.
+static inline __device__ int packed_limit(int pos, int Lk, int block) {
+    if (block == 0) return Lk;
+    if (pos < 0) return 0;
+    return min(Lk, (pos / block + 1) * block);
+}
+
+// The first query token that sees key `key`.
+static inline __device__ int packed_first_query(int key, int off, int block) {
+    if (block == 0) return 0;
+    return max(0, key / block * block - off);
+}
+
+}  // namespace k6

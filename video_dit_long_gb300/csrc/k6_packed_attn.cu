@@ -1,0 +1,587 @@
+// k6_packed_attn.cu -- attention over packed sequences with grouped key heads,
+// on tcgen05 tensor cores: full, causal, or causal by frames, from one query
+// token over a long cache to whole clips.
+//
+// For query token i of a sequence, query head h and its key head h / G,
+//   o = sum_{j < L_i} softmax_j(q . k_j / sqrt(d)) v_j,   lse = log sum_{j < L_i} exp(q . k_j / sqrt(d)),
+// L_i the mask's limit (k6_packed.cuh).  A row that sees no key gets o = 0 and
+// lse = -inf.
+//
+// A tile of 128 query rows holds 128 / G tokens of ALL G query heads of one key
+// head (one TMA box of tokens x heads), so K and V are read once per key head,
+// and a single new token fills G rows of a tile instead of one.  A work item is
+// one such tile over a range of 128-key tiles.  The CTAs are persistent (one a
+// SM); each takes items of the plan's list in turn, key head slowest, so that
+// the CTAs running together share a head's K and V in L2.  Items of few query
+// tiles over many keys are split by the plan; their partials (fp32 O
+// normalised, lse in base 2) go to the workspace and packed_merge_kernel joins
+// them in key order.
+//
+// Roles in a CTA (384 threads), shared memory (Q tile, six 32 KB K/V slots)
+// and tensor memory (three S/P buffers, O) are those of attn_tc_single_kernel:
+//   warp 8   TMA: K and V tiles in the order K_0 K_1 V_0 K_2 V_1 ..., and the
+//            item's Q tile, which waits for the last S of the item before;
+//   warp 9   S(n) = Q K_n^T;   warp 10   O += P(n) V_n, and the zeroing of the
+//            rows of V behind the sequence's last key, where another
+//            sequence's rows or unwritten memory lie: P is zero there, but
+//            0 * NaN is not;
+//   warps 0-7  two softmax groups on alternate tiles, one thread a row.
+// Warps 8-10 run ahead into the next item while the softmax groups finish one:
+// its first K/V tiles, Q and S are in place when they get there.
+// All waits are bounded (DEV_TIMEOUT), as in the other kernels.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "k6_device.cuh"
+#include "k6_packed.cuh"
+#include "k6_packed_tma.h"
+
+namespace k6 {
+
+namespace pf {
+constexpr int D = 128, BM = 128, BN = 128;
+constexpr int PANEL = BM * 64 * 2;
+constexpr int TILE = 2 * PANEL;
+constexpr int NSTAGE = 6;                     // K/V slots: even, so that inside an item a slot keeps one kind
+constexpr int KAHEAD = 2;                     // K runs two tiles ahead of V
+constexpr int NSBUF = 3;                      // S/P buffers in tensor memory
+constexpr int P_PARTS = 2;
+constexpr int KP = BN / P_PARTS;
+constexpr int SMEM_Q = 0;
+constexpr int SMEM_KV = TILE;
+constexpr int SMEM_BAR = SMEM_KV + NSTAGE * TILE;
+// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, drain, pv_buf [S buffer],
+// m_ready [tile parity][warp], epi [warp], epi_done [warp]
+constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 2 + NSBUF + 8 + 4 + 4;
+constexpr int SMEM_XCH = (SMEM_BAR + NBAR * 8 + 8 + 15) & ~15;  // + TMEM address, abort flag
+constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) of each group
+static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
+constexpr int THREADS = 384;
+// Register split (launch: 384 x 168 = 64512): 2*128*184 + 128*136 = 64512.
+constexpr int REGS_SOFTMAX = 184;
+constexpr int REGS_CONTROL = 136;
+constexpr int TMEM_COLS = 512;
+constexpr int O_COL = NSBUF * BN;
+constexpr float RESCALE_THRESHOLD = 8.0f;     // log2 units: O is rescaled when the max grows past 2^8
+constexpr unsigned long long DRAIN_NS = 1000000000ull;
+}  // namespace pf
+
+struct PackedFwdParams {
+    PackedGeom g;
+    const void *plan;
+    float scale_log2;                         // log2(e) / sqrt(d)
+    __nv_bfloat16 *out;
+    long out_stride;
+    float *lse;                               // [H][Tq], or null
+    float *part_o, *part_lse;                 // [slot][Hkv][128][128], [slot][Hkv][128]
+    uint32_t idesc_qk;
+    unsigned long long wait_limit_ns;
+    int *err;
+};
+
+namespace {
+
+// Index of K_t's and V_j's load within an item of T tiles: K_0 K_1, then V_j
+// followed by K_{j+2} while there is one.
+__device__ __forceinline__ uint32_t k_load_at(int t) { return t < pf::KAHEAD ? t : 2 * t - pf::KAHEAD + 1; }
+__device__ __forceinline__ uint32_t v_load_at(int j, int T) {
+    const int lead = T < pf::KAHEAD ? T : pf::KAHEAD;
+    const int more = T > pf::KAHEAD ? T - pf::KAHEAD : 0;
+    return lead + j + (j < more ? j : more);
+}
+
+// exp2 of a difference from a maximum that may be -inf (nothing seen yet): 0 then.
+__device__ __forceinline__ float ex2_from(float m, float m_new) { return m == -INFINITY ? 0.f : ex2(m - m_new); }
+
+__global__ void __launch_bounds__(pf::THREADS, 1)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const PackedFwdParams p) {
+    using namespace pf;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_LAYOUT);
+        return;
+    }
+    if (!packed_plan_ok(*plan.head, p.g)) {
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+        return;
+    }
+    const uint32_t n_items = (uint32_t)plan.head->n_fwd;
+    const uint32_t units = n_items * (uint32_t)p.g.Hkv;
+    if (blockIdx.x >= units) return;
+
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
+    uint64_t *q_empty = q_full + 1;
+    uint64_t *kv_full = q_empty + 1;
+    uint64_t *kv_empty = kv_full + NSTAGE;
+    uint64_t *s_full = kv_empty + NSTAGE;
+    uint64_t *p_part = s_full + NSBUF;     // [S buffer][part], 128 arrivals each
+    uint64_t *o_final = p_part + NSBUF * P_PARTS;
+    uint64_t *drain = o_final + 1;
+    uint64_t *pv_buf = drain + 1;          // [S buffer]: P.V of the tile in that buffer done
+    uint64_t *m_ready = pv_buf + NSBUF;    // [tile parity][warp % 4]: row max after the tile published
+    uint64_t *epi = m_ready + 8;           // [warp % 4]: both warps of a row pair posted (l, m)
+    uint64_t *epi_done = epi + 4;          // [warp % 4]: both warps of a row pair have read O
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(epi_done + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < NSTAGE; s++) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        for (int b = 0; b < NSBUF; b++) {
+            mbar_init(&s_full[b], 1);
+            mbar_init(&pv_buf[b], 1);
+        }
+        for (int q = 0; q < NSBUF * P_PARTS; q++) mbar_init(&p_part[q], BM);
+        mbar_init(o_final, 1);
+        mbar_init(drain, 2);  // one commit per MMA issuer
+        for (int q = 0; q < 8; q++) mbar_init(&m_ready[q], 32);
+        for (int q = 0; q < 4; q++) {
+            mbar_init(&epi[q], 64);
+            mbar_init(&epi_done[q], 64);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
+
+    if (warp >= 8) {
+        regs_decrease<REGS_CONTROL>();
+        if (warp == 8) {
+            // -------------------------------------------------- TMA producer
+            const bool leader = elect_one();
+            if (leader) {
+                prefetch_tmap(&tm_q);
+                prefetch_tmap(&tm_k);
+                prefetch_tmap(&tm_v);
+            }
+            uint32_t kv_idx = 0;  // K/V tile loads issued
+            uint32_t uc = 0;      // items with keys so far
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const int hk = (int)(u / n_items);
+                const PackedItem it = plan.fwd[u % n_items];
+                const int T = it.kt1 - it.kt0;
+                if (T <= 0) continue;
+                auto load = [&](const CUtensorMap *tm, int j) -> bool {
+                    const uint32_t slot = kv_idx % NSTAGE;
+                    if (!mbar_wait_w(&kv_empty[slot], ((kv_idx / NSTAGE) & 1) ^ 1, w)) return false;
+                    if (leader) {
+                        uint8_t *dst = smem + SMEM_KV + slot * TILE;
+                        const int row = it.krow0 + (it.kt0 + j) * BN;
+                        mbar_arrive_expect_tx(&kv_full[slot], TILE);
+                        tma_load_4d(dst, tm, &kv_full[slot], 0, hk, row, 0);
+                        tma_load_4d(dst + PANEL, tm, &kv_full[slot], 64, hk, row, 0);
+                    }
+                    kv_idx++;
+                    return true;
+                };
+                // Q once the last S of the item before has read its tile; ahead of the first K tiles, since
+                // the slot of K_1 may hold a V that is only freed at this item's first S
+                if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)p.g.rows * 256u);
+                    tma_load_4d(smem + SMEM_Q, &tm_q, q_full, 0, hk * p.g.G, it.tok0, 0);
+                    tma_load_4d(smem + SMEM_Q + PANEL, &tm_q, q_full, 64, hk * p.g.G, it.tok0, 0);
+                }
+                uc++;
+                for (int t = 0; t < KAHEAD && t < T && ok; t++) ok = load(&tm_k, t);
+                for (int j = 0; j < T && ok; j++) ok = load(&tm_v, j) && (j + KAHEAD >= T || load(&tm_k, j + KAHEAD));
+            }
+            // every copy issued lands before the CTA can exit
+            if (uc > 0) mbar_drain(q_full, (uc - 1) & 1, DRAIN_NS);
+            for (uint32_t idx = kv_idx > NSTAGE ? kv_idx - NSTAGE : 0; idx < kv_idx; idx++)
+                mbar_drain(&kv_full[idx % NSTAGE], (idx / NSTAGE) & 1, DRAIN_NS);
+        } else if (warp == 9 || warp == 10) {
+            // ------------------------------------------------- MMA issuers
+            const uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
+            const uint32_t sKV = smem_u32(smem + SMEM_KV);
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(smem + SMEM_Q), 16, 1024);  // Q / K: K-major
+            const uint64_t dv0 = smem_desc_sw128(sKV, PANEL, 1024);                   // V: MN-major
+            uint32_t kv_idx = 0;  // K/V loads of earlier items
+            uint32_t tile = 0;    // K/V tiles of earlier items
+            uint32_t uc = 0;
+            bool ok = true;
+            uint32_t vslot[4] = {0, 0, 0, 0};  // warp 9: ring slot of V(m) at m % 4
+            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const PackedItem it = plan.fwd[u % n_items];
+                const int T = it.kt1 - it.kt0;
+                if (T <= 0) continue;
+                if (warp == 9) {
+                    ok = mbar_wait_w(q_full, uc & 1, w);
+                    for (int t = 0; t < T && ok; t++) {
+                        const uint32_t n = tile + t;
+                        const uint32_t kidx = kv_idx + k_load_at(t);
+                        vslot[n % 4] = (kv_idx + v_load_at(t, T)) % NSTAGE;
+                        if (n >= NSBUF) {  // S(n)'s buffer held P(n-3): its P.V is done, and V(n-3)'s slot free
+                            if (!(ok = mbar_wait_w(&pv_buf[n % NSBUF], (n / NSBUF - 1) & 1, w))) break;
+                            if (lane == 0) mbar_arrive(&kv_empty[vslot[(n - NSBUF) % 4]]);
+                        }
+                        if (!(ok = mbar_wait_w(&kv_full[kidx % NSTAGE], (kidx / NSTAGE) & 1, w))) break;
+                        tc_fence_after();
+                        const uint64_t kb = dq0 + ((uint64_t)(SMEM_KV - SMEM_Q + (kidx % NSTAGE) * TILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; kk++) {
+                            const uint64_t off = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
+                            mma_ss_w(tmem + (n % NSBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
+                        }
+                        tc_commit_w(&s_full[n % NSBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
+                    }
+                    if (ok) tc_commit_w(q_empty);
+                } else {
+                    for (int j = 0; j < T && ok; j++) {
+                        const uint32_t n = tile + j;
+                        const uint32_t vidx = kv_idx + v_load_at(j, T);
+                        if (!(ok = mbar_wait_w(&kv_full[vidx % NSTAGE], (vidx / NSTAGE) & 1, w))) break;
+                        const int valid = it.Lk - (it.kt0 + j) * BN;
+                        if (valid < BN) {  // rows behind the sequence's last key: zero (P is)
+                            uint8_t *v = smem + SMEM_KV + (vidx % NSTAGE) * TILE;
+                            for (int c = valid * 8 + lane; c < BN * 8; c += 32) {
+                                *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(v + PANEL + c * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
+                        const uint64_t vb = dv0 + ((uint64_t)((vidx % NSTAGE) * TILE) >> 4);
+                        const uint32_t pb = tmem + (n % NSBUF) * BN;
+                        for (int q = 0; q < P_PARTS && ok; q++) {
+                            if (!(ok = mbar_wait_w(&p_part[(n % NSBUF) * P_PARTS + q], (n / NSBUF) & 1, w))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = q * (KP / 16); kk < (q + 1) * (KP / 16); kk++)
+                                mma_ts_w(tmem + O_COL, pb + kk * 8, vb + ((uint64_t)(kk * 16 * 128) >> 4), idesc_pv,
+                                         (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (!ok) break;
+                        tc_commit_w(&pv_buf[n % NSBUF]);
+                        if (j + 1 == T) tc_commit_w(o_final);
+                    }
+                }
+                kv_idx += 2 * T;
+                tile += T;
+                uc++;
+            }
+            // every MMA issued completes before tensor memory is freed (one commit per issuer)
+            tc_commit_w(drain);
+            mbar_drain(drain, 0, DRAIN_NS);
+        }
+        __syncwarp();
+    } else {
+        regs_increase<REGS_SOFTMAX>();
+        // ------------------------------------ softmax / epilogue (group hf)
+        // Group hf takes the tiles n with n % 2 == hf, whole rows (thread = row =
+        // TMEM lane).  The groups share the row's running max through shared
+        // memory (m_ready); O is rescaled in tensor memory only when a tile's max
+        // exceeds it by 2^8.  Each group keeps the row sum of its own tiles, in
+        // the max it last saw; the epilogue combines the two.
+        const int hf = warp / 4, wq = warp % 4;
+        const int r = threadIdx.x % BM;
+        const int rtok = r / p.g.G, rhead = r % p.g.G;  // this row's token of a tile and head of a group
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
+        const uint32_t tO = lane_base + O_COL;
+        float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
+        float *xe = xm + BM;                                      // [group][row][l, m]
+        const float sl2 = p.scale_log2;
+        uint32_t tile = 0, n_epi = 0, kv_idx = 0;
+        bool ok = true;
+        for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const int hk = (int)(u / n_items);
+            const PackedItem it = plan.fwd[u % n_items];
+            const int T = it.kt1 - it.kt0;
+            const bool live = rtok < it.n_tok && r < p.g.rows;
+            const long tok = (long)it.tok0 + (live ? rtok : 0);
+            const int head = hk * p.g.G + rhead;
+            __nv_bfloat16 *orow = p.out + tok * p.out_stride + (long)head * D + hf * (D / 2);
+            if (T <= 0) {  // no key is seen by any row of the tile
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < D / 2; k += 8) *reinterpret_cast<uint4 *>(orow + k) = make_uint4(0, 0, 0, 0);
+                    if (p.lse && hf == 0) p.lse[(long)head * p.g.Tq + tok] = -INFINITY;
+                }
+                continue;
+            }
+            // keys this row sees; rows past the tile's tokens see what the sequence has (their results are dropped)
+            const int lim = live ? packed_limit(it.pos0 + rtok, it.Lk, p.g.block) : it.Lk;
+            float m_run = -INFINITY;  // the row max in force after the latest tile
+            float m_own = -INFINITY;  // the max l_own is expressed in
+            float l_own = 0.f;
+            for (int j = 0; j < T; j++) {
+                const uint32_t n = tile + j;
+                if ((int)(n & 1) != hf) continue;
+                const uint32_t tS = lane_base + (n % NSBUF) * BN;
+                if (!mbar_wait(&s_full[n % NSBUF], (n / NSBUF) & 1, w)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (r == 0) mbar_arrive(&kv_empty[(kv_idx + k_load_at(j)) % NSTAGE]);  // K(n) read
+                if (n > 0) {  // the max after tile n-1, every phase waited for in turn
+                    if (!mbar_wait(&m_ready[((n - 1) & 1) * 4 + wq], ((n - 1) >> 1) & 1, w)) {
+                        ok = false;
+                        break;
+                    }
+                    if (j > 0) m_run = xm[r];
+                }
+                uint32_t s[BN];
+#pragma unroll
+                for (int cc = 0; cc < BN / 32; cc++)
+                    tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[cc * 32]));
+                tmem_ld_wait();
+                const int rel = lim - (it.kt0 + j) * BN;  // columns below rel are seen
+                if (__any_sync(0xffffffffu, rel < BN)) {
+#pragma unroll
+                    for (int k = 0; k < BN; k++)
+                        if (k >= rel) s[k] = 0xff800000u;
+                }
+                float mc[4];
+#pragma unroll
+                for (int c4 = 0; c4 < 4; c4++) {
+                    const uint32_t *x = &s[c4 * 32];
+                    float m = fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+                    for (int k = 3; k < 31; k += 2) m = fmax3(m, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    mc[c4] = fmaxf(m, __uint_as_float(x[31]));
+                }
+                const float mt = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * sl2;
+                bool need = false, rescale = false;  // rescale: warp-uniform
+                float alpha = 1.f;
+                if (j == 0) m_run = mt;
+                else need = mt > m_run + RESCALE_THRESHOLD;  // also from -inf: nothing seen before
+                if (__any_sync(0xffffffffu, need)) {
+                    rescale = true;
+                    if (need) {
+                        alpha = ex2_from(m_run, mt);
+                        m_run = mt;
+                    }
+                }
+                xm[r] = m_run;
+                mbar_arrive(&m_ready[(n & 1) * 4 + wq]);
+                if (m_own != m_run) {
+                    l_own *= ex2_from(m_own, m_run);
+                    m_own = m_run;
+                }
+                // p = 2^(s * scale*log2e - m); with nothing seen so far every s is -inf and p = 0
+                const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                const uint64_t scale2 = f2(sl2, sl2), negm2 = f2(-m_use, -m_use);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                for (int q = 0; q < P_PARTS; q++) {
+                    uint32_t pk[KP / 2];
+#pragma unroll
+                    for (int k = 0; k < KP; k += 2) {
+                        const int kk = q * KP + k;
+                        float a, b2;
+                        f2_split(ffma2(f2(__uint_as_float(s[kk]), __uint_as_float(s[kk + 1])), scale2, negm2), a, b2);
+                        const float p0 = ex2(a), p1 = ex2(b2);
+                        // P in bf16, the type of V (one MMA takes one type): 2^-9 of each term, the
+                        // row sum keeps fp32
+                        pk[k / 2] = pack_bf16x2(p0, p1);
+                        acc[(k / 2) & 3] = fadd2(acc[(k / 2) & 3], f2(p0, p1));
+                    }
+                    tmem_st_cols<KP / 2>(tS + q * (KP / 2), pk);
+                    if (q == 0 && rescale) {
+                        // O holds P.V of tiles < n once P(n-1).V is done; rescale it before P(n).V
+                        if (!mbar_wait(&pv_buf[(n - 1) % NSBUF], ((n - 1) / NSBUF) & 1, w)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int cc = 0; cc < D / 32; cc++) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + cc * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st32(tO + cc * 32, o);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&p_part[(n % NSBUF) * P_PARTS + q]);
+                }
+                if (!ok) break;
+                float a0, a1, b0, b1;
+                f2_split(fadd2(acc[0], acc[1]), a0, a1);
+                f2_split(fadd2(acc[2], acc[3]), b0, b1);
+                l_own += (a0 + a1) + (b0 + b1);
+            }
+            if (!ok) break;
+            // epilogue: the two groups combine their row sums, each writes half of O's
+            // columns; both have read O before either publishes the next item's P
+            if (!mbar_wait(o_final, n_epi & 1, w)) {
+                ok = false;
+                break;
+            }
+            xe[(hf * BM + r) * 2] = l_own;
+            xe[(hf * BM + r) * 2 + 1] = m_own;
+            mbar_arrive(&epi[wq]);
+            if (!mbar_wait(&epi[wq], n_epi & 1, w)) {
+                ok = false;
+                break;
+            }
+            const float l_oth = xe[((hf ^ 1) * BM + r) * 2], m_oth = xe[((hf ^ 1) * BM + r) * 2 + 1];
+            const float m_fin = fmaxf(m_own, m_oth);  // the max O is expressed in
+            const float l_tot = l_own * ex2_from(m_own, m_fin) + l_oth * ex2_from(m_oth, m_fin);
+            const bool none = l_tot == 0.f;
+            const float inv = none ? 0.f : 1.f / l_tot;
+            const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
+            tc_fence_after();
+            const long prow = ((long)it.slot * p.g.Hkv + hk) * BM + r;
+#pragma unroll
+            for (int cc = 0; cc < D / 64; cc++) {
+                uint32_t o[32];
+                tmem_ld32(tO + hf * (D / 2) + cc * 32, o);
+                tmem_ld_wait();
+                if (!live) continue;
+                float f[32];
+#pragma unroll
+                for (int k = 0; k < 32; k++) f[k] = none ? 0.f : __uint_as_float(o[k]) * inv;
+                if (it.slot >= 0) {
+                    float *dst = p.part_o + prow * D + hf * (D / 2) + cc * 32;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<float4 *>(dst + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4 *>(orow + cc * 32 + k) =
+                            make_uint4(pack_bf16x2(f[k], f[k + 1]), pack_bf16x2(f[k + 2], f[k + 3]),
+                                       pack_bf16x2(f[k + 4], f[k + 5]), pack_bf16x2(f[k + 6], f[k + 7]));
+                }
+            }
+            if (live && hf == 0) {
+                if (it.slot >= 0) p.part_lse[prow] = lse2;
+                else if (p.lse) p.lse[(long)head * p.g.Tq + tok] = lse2 * 0.69314718055994531f;
+            }
+            tc_fence_before();
+            mbar_arrive(&epi_done[wq]);
+            if (!mbar_wait(&epi_done[wq], n_epi & 1, w)) {
+                ok = false;
+                break;
+            }
+            n_epi++;
+            tile += T;
+            kv_idx += 2 * T;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Joins the partials of the split tiles: one warp per (tile, key head, row),
+//   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
+__global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams p) {
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    if (!packed_plan_ok(*plan.head, p.g)) return;  // the attention kernel reported it
+    const int lane = threadIdx.x & 31;
+    const long warp0 = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
+    const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
+    const long rows = (long)plan.head->n_merge * p.g.Hkv * p.g.rows;
+    for (long x = warp0; x < rows; x += nwarps) {
+        const int r = (int)(x % p.g.rows);
+        const long y = x / p.g.rows;
+        const int hk = (int)(y % p.g.Hkv);
+        const PackedMerge m = plan.merge[y / p.g.Hkv];
+        if (r / p.g.G >= m.n_tok) continue;
+        const long base = ((long)m.slot0 * p.g.Hkv + hk) * 128 + r, step = (long)p.g.Hkv * 128;
+        float top = -INFINITY;
+        for (int c = lane; c < m.n; c += 32) top = fmaxf(top, p.part_lse[base + c * step]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int c = 0; c < m.n; c += 4) {
+            float4 o[4];
+            float l[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                l[i] = -INFINITY, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + i < m.n) {
+                    l[i] = p.part_lse[base + (c + i) * step];
+                    o[i] = reinterpret_cast<const float4 *>(p.part_o + (base + (c + i) * step) * 128)[lane];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float f = ex2(l[i] - ref);
+                sum += f;
+                acc.x = fmaf(f, o[i].x, acc.x), acc.y = fmaf(f, o[i].y, acc.y);
+                acc.z = fmaf(f, o[i].z, acc.z), acc.w = fmaf(f, o[i].w, acc.w);
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const long tok = (long)m.tok0 + r / p.g.G;
+        const int head = hk * p.g.G + r % p.g.G;
+        *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head * 128 + lane * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (lane == 0 && p.lse)
+            p.lse[(long)head * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+    }
+}
+
+}  // namespace
+
+size_t packed_fwd_workspace(const PackedGeom &p) {
+    const size_t rows = (size_t)p.cap_slots * p.Hkv * 128;
+    return round256(rows * 128 * 4) + round256(rows * 4);
+}
+
+cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *out, long out_stride, float *lse,
+                              void *ws, cudaStream_t st, const char **why) {
+    if (g.Tq == 0) return cudaSuccess;
+    CUtensorMap mq, mk, mv;
+    // without key rows no tile has keys and the maps of k and v are never used
+    if (!packed_q_map(&mq, t.q, g, t.q_stride, why) ||
+        !packed_kv_map(&mk, g.Tk ? t.k : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.k_stride : t.q_stride, why) ||
+        !packed_kv_map(&mv, g.Tk ? t.v : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.v_stride : t.q_stride, why))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel, pf::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    PackedFwdParams p;
+    p.g = g;
+    p.plan = t.plan;
+    p.scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.out_stride = out_stride;
+    p.lse = lse;
+    const size_t rows = (size_t)g.cap_slots * g.Hkv * 128;
+    p.part_o = static_cast<float *>(ws);
+    p.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + round256(rows * 128 * 4));
+    // Q.K^T operands: bf16 (A/B format 1) or fp16 (format 0)
+    p.idesc_qk = idesc_bf16_f32(128, 128, false);
+    if (t.qk_f16) p.idesc_qk &= ~((7u << 7) | (7u << 10));
+    p.wait_limit_ns = t.wait_limit_ns;
+    p.err = t.err;
+    int dev = 0, sms = 152;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long most = ((long)g.cap_q + g.extra) * g.Hkv;
+    packed_fwd_kernel<<<(unsigned)(most < sms ? most : sms), pf::THREADS, pf::SMEM_TOTAL, st>>>(mq, mk, mv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || g.extra == 0) return e;
+    packed_merge_kernel<<<(unsigned)sms, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace k6

@@ -1,0 +1,807 @@
+// k6_packed_bwd.cu -- gradients of packed attention on tcgen05.
+//
+// Of out = softmax(S) V over the keys each row sees (k6_packed.cuh), S = Q K^T / sqrt(d):
+//   D_i = sum_e dO_ie O_ie,   P = exp(S - lse),   dS = P o (dO V^T - D),
+//   dV = P^T dO,   dQ = dS K / sqrt(d),   dK = dS^T Q / sqrt(d),
+// dK and dV summed over the G query heads of a key head inside the accumulator:
+// a tile of query rows holds 128 / G tokens of all G heads (one TMA box), so
+// the sum over heads is part of the product over rows.  Both kernels are those
+// of the joint-sequence backward (one stationary 128-row tile per CTA, the
+// other side streamed by TMA; warps 0-7 form P and dS, warp 8 copies, warp 9
+// issues the MMAs), walking the plan's lists: query tiles over the key tiles
+// below their limit (dq), key tiles over the query tiles that see them
+// (dk, dv), heaviest first.  Each output row is written by one CTA: no atomics,
+// the same bits every run.
+//
+// Streamed tiles that reach past their sequence hold another sequence's rows
+// (or unwritten memory, or NaN): the MMA warp zeroes those rows in shared
+// memory before they enter a product over rows, since 0 * NaN is not 0.
+//
+// fp16 q/k: dS must have K's and Q's type, and gradients are often far below
+// fp16's 2^-24.  The pre-pass takes max |dO_i| and max |v_j|, which bound
+// |dS| <= 2 max|dO| max|v|, and the kernels carry dS times the power of two that
+// brings this bound to 2^15; the epilogue takes it out again (exact).  bf16 q/k
+// need none.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "k6_device.cuh"
+#include "k6_packed.cuh"
+#include "k6_packed_tma.h"
+
+namespace k6 {
+
+namespace pb {
+constexpr int D = 128, BM = 128;
+constexpr int PANEL = BM * 64 * 2;
+constexpr int TILE = 2 * PANEL;
+constexpr int THREADS = 320;                // warps 0-7 rows, 8 TMA, 9 MMA + TMEM
+constexpr int SMEM_DATA = 7 * TILE;
+constexpr int SMEM_ALLOC = SMEM_DATA + 256 + 1024;  // barriers, TMEM slot, abort flag, alignment
+constexpr unsigned long long DRAIN_NS = 1000000000ull;
+constexpr float LOG2E = 1.4426950408889634f;
+}  // namespace pb
+
+struct PackedBwdParams {
+    PackedGeom g;
+    const void *plan;
+    float scale_log2, scale;                // log2(e)/sqrt(d), 1/sqrt(d)
+    const float2 *LD;                       // [Hkv][Tq * G] {lse * log2(e), D}; lse = +inf for a row that sees nothing
+    const unsigned *norms;                  // max |dO_i|^2, max |v_j|^2 (float bits), or null: dS is not scaled
+    __nv_bfloat16 *dq, *dk, *dv;
+    long dq_stride, dk_stride, dv_stride;
+    uint32_t idesc_qk, idesc_bf16, idesc_bf16_mn, idesc_ds_mn;
+    int ds_f16;
+    unsigned long long wait_limit_ns;
+    int *err;
+};
+
+namespace {
+
+__device__ __forceinline__ uint32_t pack_ds(float lo, float hi, bool f16) {
+    if (f16) {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+    return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ void tmem_ld16_here(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8_here(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// 2^x in program order, so the exps of a row pass run before the wait that follows them.
+__device__ __forceinline__ float ex2_in_order(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// The power of two that dS is carried with: 2^e, 2 max|dO| max|v| 2^e in (2^14, 2^15].
+__device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
+    if (!p.norms) return 0;
+    const float a = __uint_as_float(p.norms[0]), b = __uint_as_float(p.norms[1]);
+    // the product of the squares may leave fp32: add exponents instead
+    if (!(a > 0.f) || !(b > 0.f)) return 60;  // all zero, or squares below fp32
+    const int e = 14 - (int)ceilf(0.5f * (log2f(a) + log2f(b)));
+    return max(-60, min(60, e));
+}
+
+// -------------------------------------------------------------- pre-pass
+
+// LD of every query row of the sequences, and for fp16 q/k the largest squared
+// row norms of dO and v (finite ones: a row that is not makes its own results
+// NaN, whatever the scale).  Half a warp (16 lanes x 8 elements) covers one row.
+template <bool NORMS>
+__global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g, const void *plan_base,
+                                                              const char *out, long out_stride, const char *dout,
+                                                              long dout_stride, const char *v, long v_stride,
+                                                              const float *__restrict__ lse, float2 *__restrict__ LD,
+                                                              unsigned *norms) {
+    const int lane = threadIdx.x & 31, sub = lane & 15;
+    const long warp = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
+    const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(plan_base), g);
+    if (!packed_plan_ok(*plan.head, g)) return;  // the next kernels report it
+    const int q_lo = plan.head->q_lo, k_lo = plan.head->k_lo;
+    const long rows = (long)(plan.head->q_hi - q_lo) * g.H;
+    const long vrows = NORMS ? (long)(plan.head->k_hi - k_lo) * g.Hkv : 0;
+    float top_do = 0.f, top_v = 0.f;
+    for (long r0 = warp * 2; r0 < rows; r0 += nwarps * 2) {
+        const long r = r0 + (lane >> 4);
+        const long rr = r < rows ? r : rows - 1;
+        const long t0 = rr / g.H;
+        const int h = (int)(rr - t0 * g.H);
+        const long tok = q_lo + t0;
+        const uint4 a = reinterpret_cast<const uint4 *>(out + tok * out_stride + (long)h * 256)[sub];
+        const uint4 b = reinterpret_cast<const uint4 *>(dout + tok * dout_stride + (long)h * 256)[sub];
+        const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a);
+        const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(&b);
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 fx = __bfloat1622float2(x[k]), fy = __bfloat1622float2(y[k]);
+            s = fmaf(fx.x, fy.x, s);
+            s = fmaf(fx.y, fy.y, s);
+            if (NORMS) q = fmaf(fy.x, fy.x, fmaf(fy.y, fy.y, q));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+            if (NORMS) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
+        }
+        if (r < rows) {
+            const float l = sub == 0 ? lse[(long)h * g.Tq + tok] : 0.f;
+            if (sub == 0)
+                LD[((long)(h / g.G) * g.Tq + tok) * g.G + h % g.G] =
+                    make_float2(l == -INFINITY ? INFINITY : l * pb::LOG2E, s);
+            // a row that sees nothing has no say in the scale
+            if (NORMS && sub == 0 && l > -INFINITY && q < INFINITY) top_do = fmaxf(top_do, q);
+        }
+    }
+    if constexpr (NORMS) {
+        for (long r0 = warp * 2; r0 < vrows; r0 += nwarps * 2) {
+            const long r = r0 + (lane >> 4) < vrows ? r0 + (lane >> 4) : vrows - 1;
+            const long t0 = r / g.Hkv;
+            const uint4 a = reinterpret_cast<const uint4 *>(v + (k_lo + t0) * v_stride + (r - t0 * g.Hkv) * 256)[sub];
+            const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a);
+            float q = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = __bfloat1622float2(x[k]);
+                q = fmaf(f.x, f.x, fmaf(f.y, f.y, q));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
+            if (q < INFINITY) top_v = fmaxf(top_v, q);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            top_do = fmaxf(top_do, __shfl_xor_sync(0xffffffffu, top_do, o));
+            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+        }
+        // bits of non-negative floats order as integers: a maximum does not depend on the order
+        if (lane == 0) {
+            if (top_do > 0.f) atomicMax(norms, __float_as_uint(top_do));
+            if (top_v > 0.f) atomicMax(norms + 1, __float_as_uint(top_v));
+        }
+    }
+}
+
+// ----------------------------------------------------------- shared set-up
+
+template <int NB>
+__device__ __forceinline__ uint32_t setup(uint8_t *smem, const int (&counts)[NB], uint64_t *&bars,
+                                          volatile int *&abort_flag) {
+    bars = reinterpret_cast<uint64_t *>(smem + pb::SMEM_DATA);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NB);
+    abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NB; i++) mbar_init(bars + i, counts[i]);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x / 32 == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return *tmem_slot;
+}
+
+__device__ __forceinline__ void teardown(uint32_t tmem) {
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x / 32 == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Two 64-element panels into dst (completing on bar).
+__device__ __forceinline__ void load_panels(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int head, int row) {
+    tma_load_4d(dst, m, bar, 0, head, row, 0);
+    tma_load_4d(dst + pb::PANEL, m, bar, 64, head, row, 0);
+}
+
+// Rows [from, 128) of a tile in shared memory to zero, by one whole warp, before its MMAs read them.
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int from, int lane) {
+    for (int c = from * 8 + lane; c < pb::BM * 8; c += 32) {
+        *reinterpret_cast<uint4 *>(tile + c * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(tile + pb::PANEL + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
+// Step kk of a K-major SS MMA chain over d = 128.
+__device__ __forceinline__ void mma_k(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int kk) {
+    const uint64_t off = (uint64_t)((kk >> 2) * pb::PANEL + (kk & 3) * 32) >> 4;
+    mma_ss_w(d, a + off, b + off, idesc, kk > 0);
+}
+
+// 64 columns of this thread's TMEM lane, times `scale`, as bf16 to dst (null: read only).
+__device__ __forceinline__ void store_half_row(uint32_t taddr, __nv_bfloat16 *dst, float scale) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        uint32_t o[32];
+        tmem_ld32(taddr + c * 32, o);
+        tmem_ld_wait();
+        if (dst) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                uint4 u;
+                u.x = pack_bf16x2(__uint_as_float(o[k]) * scale, __uint_as_float(o[k + 1]) * scale);
+                u.y = pack_bf16x2(__uint_as_float(o[k + 2]) * scale, __uint_as_float(o[k + 3]) * scale);
+                u.z = pack_bf16x2(__uint_as_float(o[k + 4]) * scale, __uint_as_float(o[k + 5]) * scale);
+                u.w = pack_bf16x2(__uint_as_float(o[k + 6]) * scale, __uint_as_float(o[k + 7]) * scale);
+                *reinterpret_cast<uint4 *>(dst + c * 32 + k) = u;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void zero_half_row(__nv_bfloat16 *dst) {
+#pragma unroll
+    for (int k = 0; k < 64; k += 8) *reinterpret_cast<uint4 *>(dst + k) = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ dq kernel
+//
+// smem tiles: Q 0, dO 1, K slots 2-4, V slots 5-6.  Tensor memory: S 0-127,
+// dP 128-255, dQ 256-383, dS buffers 384-447 and 448-511.
+
+namespace dqk {
+constexpr int STAT = 0, KFULL = 1, KEMPTY = 4, VFULL = 7, VEMPTY = 9, SFULL = 11, DSFULL = 12, ACC = 13,
+              DRAIN = 14, NB = 15;
+}
+
+__global__ void __launch_bounds__(pb::THREADS, 1)
+    packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const PackedBwdParams p) {
+    using namespace pb;
+    using namespace dqk;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    if (!packed_plan_ok(*plan.head, p.g)) {
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+        return;
+    }
+    const uint32_t n_items = (uint32_t)plan.head->n_q;
+    if (blockIdx.x >= n_items * (uint32_t)p.g.Hkv) return;
+    const int hk = (int)(blockIdx.x / n_items);
+    const PackedItem it = plan.q[blockIdx.x % n_items];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int T = it.kt1;
+    // rows: lane quarter q4, key half g
+    const int q4 = warp & 3, g = (warp >> 2) & 1;
+    const int r = 32 * q4 + lane;
+    const int rtok = r / p.g.G, rhead = r % p.g.G;
+    const bool live = warp < 8 && rtok < it.n_tok && r < p.g.rows;
+    const long tok = (long)it.tok0 + (live ? rtok : 0);
+    __nv_bfloat16 *drow = p.dq + tok * p.dq_stride + (long)(hk * p.g.G + rhead) * D + 64 * g;
+    if (T <= 0) {  // no key is seen by any row of the tile
+        if (live) zero_half_row(drow);
+        return;
+    }
+    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 1, 1};
+    uint64_t *bar;
+    volatile int *abort_flag;
+    const uint32_t tmem = setup<NB>(smem, counts, bar, abort_flag);
+    const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
+    uint8_t *sQ = smem, *sDO = smem + TILE, *sK = smem + 2 * TILE, *sV = smem + 5 * TILE;
+
+    if (warp == 8) {
+        const bool leader = elect_one();
+        if (leader) {
+            mbar_arrive_expect_tx(bar + STAT, 2u * (uint32_t)p.g.rows * 256u);
+            load_panels(sQ, &tm_q, bar + STAT, hk * p.g.G, it.tok0);
+            load_panels(sDO, &tm_do, bar + STAT, hk * p.g.G, it.tok0);
+        }
+        int nk = 0, nv = 0;  // K and V tiles issued
+        for (int t = 0; t < T; t++) {
+            const int ks = t % 3, vs = t & 1, row = it.krow0 + t * BM;
+            if (!mbar_wait_w(bar + KEMPTY + ks, ((t / 3) & 1) ^ 1, w)) break;
+            if (leader) {
+                mbar_arrive_expect_tx(bar + KFULL + ks, TILE);
+                load_panels(sK + ks * TILE, &tm_k, bar + KFULL + ks, hk, row);
+            }
+            nk++;
+            if (!mbar_wait_w(bar + VEMPTY + vs, ((t >> 1) & 1) ^ 1, w)) break;
+            if (leader) {
+                mbar_arrive_expect_tx(bar + VFULL + vs, TILE);
+                load_panels(sV + vs * TILE, &tm_v, bar + VFULL + vs, hk, row);
+            }
+            nv++;
+        }
+        // let copies in flight land before the CTA exits
+        mbar_drain(bar + STAT, 0, DRAIN_NS);
+        for (int t = nk > 3 ? nk - 3 : 0; t < nk; t++) mbar_drain(bar + KFULL + t % 3, (t / 3) & 1, DRAIN_NS);
+        for (int t = nv > 2 ? nv - 2 : 0; t < nv; t++) mbar_drain(bar + VFULL + (t & 1), (t >> 1) & 1, DRAIN_NS);
+        __syncwarp();
+    } else if (warp == 9) {
+        const uint32_t tS = tmem, tP = tmem + 128, tA = tmem + 256, tDS = tmem + 384;
+        const uint64_t dq_ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t ddo = smem_desc_sw128(smem_u32(sDO), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dkmn = smem_desc_sw128(smem_u32(sK), PANEL, 1024);
+        // S(t) = Q K^T and dP(t) = dO V^T, two interleaved chains; then free the
+        // V slot and publish S/dP (each commit also covers every earlier MMA).
+        auto issue_sdp = [&](int t) -> bool {
+            const int ks = t % 3, vs = t & 1;
+            if (!mbar_wait_w(bar + KFULL + ks, (t / 3) & 1, w)) return false;
+            // keys behind the sequence enter dQ += dS K times zero
+            if (it.Lk - t * BM < BM) zero_rows(sK + ks * TILE, it.Lk - t * BM, lane);
+            if (!mbar_wait_w(bar + VFULL + vs, (t >> 1) & 1, w)) return false;
+            tc_fence_after();
+            const uint64_t kd = dk0 + (uint64_t)((ks * TILE) >> 4), vd = dv0 + (uint64_t)((vs * TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) {
+                mma_k(tS, dq_, kd, p.idesc_qk, kk);
+                mma_k(tP, ddo, vd, p.idesc_bf16, kk);
+            }
+            tc_commit_w(bar + VEMPTY + vs);
+            tc_commit_w(bar + SFULL);
+            return true;
+        };
+        bool ok = mbar_wait_w(bar + STAT, 0, w) && issue_sdp(0);
+        for (int t = 0; t < T && ok; t++) {
+            // the row pass has read S(t)/dP(t) and written dS(t) to buffer t & 1
+            if (!(ok = mbar_wait_w(bar + DSFULL, t & 1, w))) break;
+            tc_fence_after();
+            if (t + 1 < T && !(ok = issue_sdp(t + 1))) break;
+            const uint64_t kmn = dkmn + (uint64_t)(((t % 3) * TILE) >> 4);
+            const uint32_t ads = tDS + (t & 1) * 64;
+#pragma unroll
+            for (int kk = 0; kk < BM / 16; kk++)
+                mma_ts_w(tA, ads + kk * 8, kmn + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
+                         (t > 0 || kk > 0) ? 1u : 0u);  // dQ += dS K
+            tc_commit_w(bar + KEMPTY + t % 3);
+        }
+        if (ok) tc_commit_w(bar + ACC);
+        tc_commit_w(bar + DRAIN);
+        mbar_drain(bar + DRAIN, 0, DRAIN_NS);
+        __syncwarp();
+    } else {
+        const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
+        const int e = ds_exponent(p);
+        const int lim = live ? packed_limit(it.pos0 + rtok, it.Lk, p.g.block) : it.Lk;
+        float2 ld = make_float2(INFINITY, 0.f);
+        if (live) ld = p.LD[((long)hk * p.g.Tq + tok) * p.g.G + rhead];
+        ld.x -= (float)e;  // P, and with it dS, is carried times 2^e
+        const float sl2 = p.scale_log2;
+        bool ok = true;
+        for (int t = 0; t < T; t++) {
+            if (!mbar_wait(bar + SFULL, t & 1, w)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int rel = lim - t * BM - 64 * g;  // columns below rel of this half are seen
+            const bool masked = __any_sync(0xffffffffu, rel < 64);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t sv[32], pv[32], ds[16];
+                tmem_ld32(lb + 64 * g + 32 * c, sv);
+                tmem_ld32(lb + 128 + 64 * g + 32 * c, pv);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float p0 = ex2(fmaf(__uint_as_float(sv[k]), sl2, -ld.x));
+                    const float p1 = ex2(fmaf(__uint_as_float(sv[k + 1]), sl2, -ld.x));
+                    float d0 = p0 * (__uint_as_float(pv[k]) - ld.y), d1 = p1 * (__uint_as_float(pv[k + 1]) - ld.y);
+                    if (masked) {
+                        if (32 * c + k >= rel) d0 = 0.f;
+                        if (32 * c + k + 1 >= rel) d1 = 0.f;
+                    }
+                    // dS in K's type (one MMA takes one type): 2^-9 (bf16) or 2^-12 (fp16) of each term
+                    ds[k / 2] = pack_ds(d0, d1, p.ds_f16);
+                }
+                tmem_st16(lb + 384 + 64 * (t & 1) + 32 * g + 16 * c, ds);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar + DSFULL);
+        }
+        if (ok && mbar_wait(bar + ACC, 0, w)) {
+            tc_fence_after();
+            store_half_row(lb + 256 + 64 * g, live ? drow : nullptr, p.scale * exp2f((float)-e));
+        }
+    }
+    teardown(tmem);
+}
+
+// Row pass of the dk/dv kernel: P of one key row and 64 queries from S^T in
+// registers.  Queries outside [lo, nq) get P = 0 (FULL: all are seen).
+template <bool FULL>
+__device__ __forceinline__ void p_row(float (&pr)[64], const uint32_t (&sv)[2][32], const float2 *ldq, int lo, int nq,
+                                      float sl2) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+#pragma unroll
+        for (int k = 0; k < 32; k++) {
+            const int j = 32 * c + k;
+            const float l2 = (FULL || j < nq) ? ldq[j].x : INFINITY;
+            pr[j] = ex2_in_order(fmaf(__uint_as_float(sv[c][k]), sl2, -l2));
+            if (!FULL && !(j >= lo && j < nq)) pr[j] = 0.f;
+        }
+        asm volatile("" ::: "memory");  // one half's loads at a time (register pressure)
+    }
+}
+
+// dS^T = P (dP^T - D) over 16-query chunks [C0, C1) of the 64 columns at taddr
+// (each chunk's dS^T lands on columns already read), times `sc`, and P rounded
+// to bf16 into this thread's row of the swizzled P^T panel at prow.
+template <bool FULL, int C0, int C1>
+__device__ __forceinline__ void ds_row(const float (&pr)[64], const float2 *ldq, int nq, uint32_t taddr,
+                                       uint32_t prow, int r, int ds_f16, float sc) {
+#pragma unroll
+    for (int c = C0; c < C1; c++) {
+        uint32_t pv[16], ds[8], pk[8];
+        tmem_ld16_here(taddr + 16 * c, pv);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            float de[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int j = 16 * c + k + e;
+                // plain load: the clobber of the tensor-memory load above keeps it in this chunk
+                const float dd = (FULL || j < nq) ? ldq[j].y : 0.f;
+                de[e] = pr[j] * (__uint_as_float(pv[k + e]) - dd);
+            }
+            ds[k / 2] = ds_f16 ? pack_ds(de[0] * sc, de[1] * sc, true) : pack_ds(de[0], de[1], false);
+            pk[k / 2] = pack_bf16x2(pr[16 * c + k], pr[16 * c + k + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int chunk = 2 * c + i;  // 16-byte chunk of the 128-byte row
+            st_shared_16(prow + ((chunk ^ (r & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        tmem_st8_here(taddr + 8 * c, ds);
+    }
+}
+
+// ----------------------------------------------------------------- dkv kernel
+//
+// smem tiles: K 0, V 1, ring slot s: Q 2+2s, dO 3+2s; P^T 6.  Tensor memory:
+// S^T 0-127, dP^T 128-255 (dS^T over it), dV 256-383, dK 384-511.  The schedule
+// of the MMA warp (S^T(i+1) under the row pass of tile i, P^T/dS^T published in
+// two parts, dP^T(i+1) after the last dK(i) step that reads dS^T(i)) is that of
+// bwd_dkv_kernel.
+
+namespace dkvk {
+constexpr int STAT = 0, QFULL = 1, DOFULL = 3, QEMPTY = 5, DOEMPTY = 7, SREADY = 9, CONSUMED = 10, PDS = 11,
+              WIN = 13, ACC = 14, DRAIN = 15, NB = 16;  // PDS, PDS + 1: the two parts of a tile's P^T / dS^T
+}
+
+__global__ void __launch_bounds__(pb::THREADS, 1)
+    packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PackedBwdParams p) {
+    using namespace pb;
+    using namespace dkvk;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    if (!packed_plan_ok(*plan.head, p.g)) {
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+        return;
+    }
+    const uint32_t n_items = (uint32_t)plan.head->n_k;
+    if (blockIdx.x >= n_items * (uint32_t)p.g.Hkv) return;
+    const int hk = (int)(blockIdx.x / n_items);
+    const PackedKItem it = plan.k[blockIdx.x % n_items];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int T = it.qt1 - it.qt0;
+    // rows: key row r, query half g
+    const int q4 = warp & 3, g = (warp >> 2) & 1;
+    const int r = 32 * q4 + lane;
+    const bool live = warp < 8 && r < it.n_key;
+    __nv_bfloat16 *krow = p.dk + ((long)it.krow0 + (live ? r : 0)) * p.dk_stride + (long)hk * D + 64 * g;
+    __nv_bfloat16 *vrow = p.dv + ((long)it.krow0 + (live ? r : 0)) * p.dv_stride + (long)hk * D + 64 * g;
+    if (T <= 0) {  // no query sees any key of the tile
+        if (live) {
+            zero_half_row(krow);
+            zero_half_row(vrow);
+        }
+        return;
+    }
+    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 256, 256, 1, 1, 1};
+    uint64_t *bar;
+    volatile int *abort_flag;
+    // rows that a copy of g.rows rows does not reach stay zero
+    for (int t = 2; t < 6 && p.g.rows < BM; t++) {
+        for (int c = p.g.rows * 8 + (int)threadIdx.x; c < BM * 8; c += THREADS) {
+            *reinterpret_cast<uint4 *>(smem + t * TILE + c * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(smem + t * TILE + PANEL + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+    }
+    const uint32_t tmem = setup<NB>(smem, counts, bar, abort_flag);
+    const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
+    uint8_t *sK = smem, *sV = smem + TILE, *sRing = smem + 2 * TILE, *sP = smem + 6 * TILE;
+    // query rows of tile t (of the item's T) that belong to the sequence
+    auto rows_of = [&](int t) { return min(p.g.rows, (it.Lq - (it.qt0 + t) * p.g.tpt) * p.g.G); };
+
+    if (warp == 8) {
+        const bool leader = elect_one();
+        if (leader) {
+            mbar_arrive_expect_tx(bar + STAT, 2 * TILE);
+            load_panels(sK, &tm_k, bar + STAT, hk, it.krow0);
+            load_panels(sV, &tm_v, bar + STAT, hk, it.krow0);
+        }
+        const uint32_t bytes = (uint32_t)p.g.rows * 256u;
+        int nq = 0, ndo = 0;  // Q and dO tiles issued
+        for (int t = 0; t < T; t++) {
+            const int s = t & 1, row = it.qrow0 + (it.qt0 + t) * p.g.tpt;
+            const uint32_t par = ((t >> 1) & 1) ^ 1;
+            if (!mbar_wait_w(bar + QEMPTY + s, par, w)) break;
+            if (leader) {
+                mbar_arrive_expect_tx(bar + QFULL + s, bytes);
+                load_panels(sRing + 2 * s * TILE, &tm_q, bar + QFULL + s, hk * p.g.G, row);
+            }
+            nq++;
+            if (!mbar_wait_w(bar + DOEMPTY + s, par, w)) break;
+            if (leader) {
+                mbar_arrive_expect_tx(bar + DOFULL + s, bytes);
+                load_panels(sRing + (2 * s + 1) * TILE, &tm_do, bar + DOFULL + s, hk * p.g.G, row);
+            }
+            ndo++;
+        }
+        mbar_drain(bar + STAT, 0, DRAIN_NS);
+        for (int t = nq > 2 ? nq - 2 : 0; t < nq; t++) mbar_drain(bar + QFULL + (t & 1), (t >> 1) & 1, DRAIN_NS);
+        for (int t = ndo > 2 ? ndo - 2 : 0; t < ndo; t++) mbar_drain(bar + DOFULL + (t & 1), (t >> 1) & 1, DRAIN_NS);
+        __syncwarp();
+    } else if (warp == 9) {
+        const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dring = smem_desc_sw128(smem_u32(sRing), 16, 1024);
+        const uint64_t dring_mn = smem_desc_sw128(smem_u32(sRing), PANEL, 1024);
+        const uint64_t dp = smem_desc_sw128(smem_u32(sP), 16, 1024);
+        // descriptor of tile `which` (0 Q, 1 dO) of the ring slot of tile t
+        auto slot = [&](uint64_t base, int t, int which) {
+            return base + (uint64_t)(((2 * (t & 1) + which) * TILE) >> 4);
+        };
+        // wait for tile t; queries behind the sequence enter dK and dV times zero
+        auto wait_tile = [&](int t, int full, int which) {
+            if (!mbar_wait_w(bar + full + (t & 1), (t >> 1) & 1, w)) return false;
+            if (rows_of(t) < p.g.rows) zero_rows(sRing + (2 * (t & 1) + which) * TILE, rows_of(t), lane);
+            return true;
+        };
+        auto wait_q = [&](int t) { return wait_tile(t, QFULL, 0); };
+        auto wait_do = [&](int t) { return wait_tile(t, DOFULL, 1); };
+        bool ok = mbar_wait_w(bar + STAT, 0, w) && wait_q(0);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) mma_k(tS, dk0, slot(dring, 0, 0), p.idesc_qk, kk);  // S^T = K Q^T
+            tc_commit_w(bar + SREADY);
+            ok = wait_do(0);
+        }
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) mma_k(tP, dv0, slot(dring, 0, 1), p.idesc_bf16, kk);  // dP^T = V dO^T
+            tc_commit_w(bar + WIN);
+        }
+        for (int t = 0; t < T && ok; t++) {
+            // the row pass has read S^T(t): S^T(t+1) may overwrite its columns
+            if (!(ok = mbar_wait_w(bar + CONSUMED, t & 1, w))) break;
+            tc_fence_after();
+            const bool next = t + 1 < T;
+            if (next) {
+                if (!(ok = wait_q(t + 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) mma_k(tS, dk0, slot(dring, t + 1, 0), p.idesc_qk, kk);
+                tc_commit_w(bar + SREADY);
+            }
+            // the first part of P^T(t) is in shared memory and of dS^T(t) over dP^T(t)
+            if (!(ok = mbar_wait_w(bar + PDS, t & 1, w))) break;
+            if (next && !(ok = wait_do(t + 1))) break;
+            tc_fence_after();
+            const uint32_t acc = t > 0 ? 1u : 0u;
+            // K-step kk covers queries 16 kk .. 16 kk + 15: the first part holds kk 0, 1, 4, 5
+            auto dv_step = [&](int kk) {  // dV += P^T dO
+                const uint64_t poff = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
+                mma_ss_w(tV, dp + poff, slot(dring_mn, t, 1) + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_bf16_mn,
+                         acc | (kk > 0 ? 1u : 0u));
+            };
+            auto dk_step = [&](int kk) {  // dK += dS^T Q
+                mma_ts_w(tK, tP + (kk >> 2) * 64 + (kk & 3) * 8,
+                         slot(dring_mn, t, 0) + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
+                         acc | (kk > 0 ? 1u : 0u));
+            };
+            constexpr int part0[4] = {0, 1, 4, 5}, part1[4] = {2, 3, 6, 7};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                dk_step(part0[i]);
+                dv_step(part0[i]);
+            }
+            if (!(ok = mbar_wait_w(bar + PDS + 1, t & 1, w))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                dk_step(part1[i]);
+                if (i < 2) dv_step(part1[i]);
+            }
+            tc_commit_w(bar + QEMPTY + (t & 1));  // Q(t): S^T(t) and dK(t) done
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) {
+                if (next) mma_k(tP, dv0, slot(dring, t + 1, 1), p.idesc_bf16, kk);  // dP^T(t+1)
+                if (kk < 2) dv_step(part1[2 + kk]);
+            }
+            tc_commit_w(bar + DOEMPTY + (t & 1));  // dO(t): dP^T(t) and dV(t) done
+            tc_commit_w(bar + WIN);
+        }
+        if (ok) tc_commit_w(bar + ACC);
+        tc_commit_w(bar + DRAIN);
+        mbar_drain(bar + DRAIN, 0, DRAIN_NS);
+        __syncwarp();
+    } else {
+        const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
+        const float sl2 = p.scale_log2;
+        const int e = ds_exponent(p);
+        const float sc = exp2f((float)e);
+        const float2 *ld_h = p.LD + ((long)hk * p.g.Tq + it.qrow0) * p.g.G;
+        // the first query row (of the sequence, tokens x heads) that sees this key
+        const long first = (long)packed_first_query(it.key0 + r, it.off, p.g.block) * p.g.G;
+        // this thread's row of P^T panel g: 8 chunks of 16 bytes, 128-byte swizzle
+        const uint32_t prow = smem_u32(sP) + g * PANEL + (r >> 3) * 1024 + (r & 7) * 128;
+        bool ok = true;
+        for (int t = 0; t < T; t++) {
+            if (!mbar_wait(bar + SREADY, t & 1, w)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // S^T of this half into registers, then its columns are free for S^T(t+1)
+            uint32_t sv[2][32];
+            tmem_ld32(lb + 64 * g, sv[0]);
+            tmem_ld32(lb + 64 * g + 32, sv[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(bar + CONSUMED);
+            const long q0 = (long)(it.qt0 + t) * p.g.rows + 64 * g;  // first query row of this half
+            const float2 *ldq = ld_h + q0;
+            const int nq = rows_of(t) - 64 * g;                       // rows of this half in the sequence (may be <= 0)
+            const int lo = (int)max(-1L, min(first - q0, 64L));       // rows of this half from lo on see the key
+            const bool full = !__any_sync(0xffffffffu, nq < 64 || lo > 0);
+            float pr[64];
+            if (full) p_row<true>(pr, sv, ldq, 0, 64, sl2);
+            else p_row<false>(pr, sv, ldq, lo, nq, sl2);
+            // dV/dK(t-1) and dP^T(t) done: the P^T buffer is free and dP^T(t) is in place
+            if (!mbar_wait(bar + WIN, t & 1, w)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // first part (queries 0-31 of this half), published before the second is formed
+            if (full) ds_row<true, 0, 2>(pr, ldq, 64, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            else ds_row<false, 0, 2>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            fence_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar + PDS);
+            if (full) ds_row<true, 2, 4>(pr, ldq, 64, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            else ds_row<false, 2, 4>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            fence_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar + PDS + 1);
+        }
+        if (ok && mbar_wait(bar + ACC, 0, w)) {
+            tc_fence_after();
+            store_half_row(lb + 384 + 64 * g, live ? krow : nullptr, p.scale * exp2f((float)-e));
+            store_half_row(lb + 256 + 64 * g, live ? vrow : nullptr, 1.0f);
+        }
+    }
+    teardown(tmem);
+}
+
+}  // namespace
+
+// Workspace: LD, then the two squared norms.
+size_t packed_bwd_workspace(const PackedGeom &p) { return round256((size_t)p.Tq * p.H * sizeof(float2)) + 256; }
+
+cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const void *out, long out_stride,
+                              const void *dout, long dout_stride, const float *lse, void *dq, long dq_stride,
+                              void *dk, long dk_stride, void *dv, long dv_stride, void *ws, cudaStream_t st,
+                              const char **why) {
+    if (g.Tq == 0 && g.Tk == 0) return cudaSuccess;
+    // a side without rows is never loaded: its maps get the other's
+    const void *q = g.Tq ? t.q : t.k, *d_o = g.Tq ? dout : t.v, *k = g.Tk ? t.k : t.q, *v = g.Tk ? t.v : dout;
+    PackedGeom gq = g;
+    if (!g.Tq) gq.Tq = g.Tk, gq.H = g.Hkv, gq.G = 1, gq.tpt = 128;
+    CUtensorMap mq, mdo, mk, mv;
+    const long krows = g.Tk ? g.Tk : g.Tq;
+    const int kheads = g.Tk ? g.Hkv : 1;
+    if (!packed_q_map(&mq, q, gq, g.Tq ? t.q_stride : t.k_stride, why) ||
+        !packed_q_map(&mdo, d_o, gq, g.Tq ? dout_stride : t.v_stride, why) ||
+        !packed_kv_map(&mk, k, krows, kheads, g.Tk ? t.k_stride : t.q_stride, why) ||
+        !packed_kv_map(&mv, v, krows, kheads, g.Tk ? t.v_stride : dout_stride, why))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_dq_kernel, pb::SMEM_ALLOC);
+    if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)packed_dkv_kernel, pb::SMEM_ALLOC);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 152;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    float2 *LD = static_cast<float2 *>(ws);
+    unsigned *norms = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
+    if (g.Tq) {
+        const long want = ((long)g.Tq * g.H + 15) / 16;
+        const unsigned grid = (unsigned)(want < 8L * sms ? want : 8L * sms);
+        auto rows = [&](auto kernel) {
+            kernel<<<grid, 256, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
+                                         static_cast<const char *>(dout), dout_stride * 2,
+                                         static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, norms);
+        };
+        if (t.qk_f16) {
+            e = cudaMemsetAsync(norms, 0, 2 * sizeof(unsigned), st);
+            if (e != cudaSuccess) return e;
+            rows(packed_bwd_rows_kernel<true>);
+        } else {
+            rows(packed_bwd_rows_kernel<false>);
+        }
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    PackedBwdParams p;
+    p.g = g;
+    p.plan = t.plan;
+    p.scale = (float)(1.0 / sqrt(128.0));
+    p.scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
+    p.LD = LD;
+    p.norms = t.qk_f16 && g.Tq ? norms : nullptr;
+    p.dq = static_cast<__nv_bfloat16 *>(dq), p.dk = static_cast<__nv_bfloat16 *>(dk);
+    p.dv = static_cast<__nv_bfloat16 *>(dv);
+    p.dq_stride = dq_stride, p.dk_stride = dk_stride, p.dv_stride = dv_stride;
+    // A/B formats: bits 7-9 and 10-12 (0 = fp16, 1 = bf16); bit 16: B MN-major
+    const uint32_t f16 = idesc_bf16_f32(128, 128, false) & ~((7u << 7) | (7u << 10));
+    const uint32_t bf16 = f16 | (1u << 7) | (1u << 10);
+    p.idesc_qk = t.qk_f16 ? f16 : bf16;                    // S = Q K^T
+    p.idesc_bf16 = bf16;                                   // dP = dO V^T
+    p.idesc_bf16_mn = bf16 | (1u << 16);                   // dV += P^T dO
+    p.idesc_ds_mn = (t.qk_f16 ? f16 : bf16) | (1u << 16);  // dQ += dS K, dK += dS^T Q
+    p.ds_f16 = t.qk_f16 ? 1 : 0;
+    p.wait_limit_ns = t.wait_limit_ns;
+    p.err = t.err;
+    if (g.Tq) {
+        packed_dq_kernel<<<(unsigned)((long)g.cap_q * g.Hkv), pb::THREADS, pb::SMEM_ALLOC, st>>>(mq, mdo, mk, mv, p);
+        e = cudaGetLastError();
+    }
+    if (g.Tk && e == cudaSuccess) {
+        packed_dkv_kernel<<<(unsigned)((long)g.cap_k * g.Hkv), pb::THREADS, pb::SMEM_ALLOC, st>>>(mq, mdo, mk, mv, p);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace k6

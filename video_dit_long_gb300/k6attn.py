@@ -25,7 +25,11 @@ SYMBOLS = ["k6attn_create", "k6attn_destroy", "k6attn_rope_tables", "k6attn_rope
            "k6attn_cross_forward", "k6attn_norm_rope_qk", "k6attn_row_bounds_bytes", "k6attn_row_bounds",
            "k6attn_attention_chunks_bounded", "k6attn_backward_workspace_bytes", "k6attn_backward",
            "k6attn_chunk_group", "k6attn_attention_chunk_groups", "k6attn_rope_split_heads",
-           "k6attn_lse_merge_heads", "k6attn_attention_chunk_groups_bounded"]
+           "k6attn_lse_merge_heads", "k6attn_attention_chunk_groups_bounded",
+           "k6attn_packed_norm_rope", "k6attn_packed_norm_rope_backward",
+           "k6attn_packed_norm_rope_backward_workspace_bytes", "k6attn_packed_plan_bytes", "k6attn_packed_plan",
+           "k6attn_packed_workspace_bytes", "k6attn_packed_forward", "k6attn_packed_backward_workspace_bytes",
+           "k6attn_packed_backward"]
 
 
 class K6Error(RuntimeError):
@@ -39,6 +43,19 @@ class Desc(ctypes.Structure):
                 ("grid_t", ctypes.c_int), ("grid_h", ctypes.c_int), ("grid_w", ctypes.c_int),
                 ("axis_dim", ctypes.c_int * 3), ("theta", ctypes.c_double), ("n_joint", ctypes.c_int),
                 ("joint_rope", ctypes.c_int)]
+
+
+class PackedBatch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("kv_heads", ctypes.c_int), ("mask_block", ctypes.c_int),
+                ("q_tokens", ctypes.c_long), ("k_tokens", ctypes.c_long)]
+
+
+class PackedPlan:
+    """A packed batch and its work list on the device (Handle.packed_plan)."""
+
+    def __init__(self, batch, buffer):
+        self.batch, self.buffer = batch, buffer
+        self.ref, self.ptr = ctypes.byref(batch), buffer.data_ptr()
 
 
 _lib = None
@@ -92,6 +109,17 @@ def load(build_if_missing: bool = True):
     L.k6attn_lse_merge_heads.argtypes = [P, P, P, I, I, P, P, P]
     L.k6attn_attention_chunk_groups_bounded.argtypes = [P, P, P, P, P, P, I, P, I, I, P, P, P]
     L.k6attn_seq2head_relayout.argtypes = [P, P, I, ctypes.c_long, I, I, I, I, I, P]
+    W, F, B = ctypes.c_long, ctypes.c_float, ctypes.POINTER(PackedBatch)
+    L.k6attn_packed_norm_rope.argtypes = [P, W, I, P, P, W, P, W, P, P, F, P, W, P, W, I, P]
+    L.k6attn_packed_norm_rope_backward.argtypes = [P, W, I, P, P, W, P, W, P, W, P, W, P, P, F, P, W, P, W, P, P, P, Z, P]
+    L.k6attn_packed_norm_rope_backward_workspace_bytes.argtypes = [P, W, I]
+    L.k6attn_packed_plan.argtypes = [P, B, P, P, P, Z, P]
+    L.k6attn_packed_forward.argtypes = [P, B, P, P, W, P, W, P, W, I, P, W, P, P, Z, P]
+    L.k6attn_packed_backward.argtypes = [P, B, P, P, W, P, W, P, W, I, P, W, P, W, P, P, W, P, W, P, W, P, Z, P]
+    for name in ("plan_bytes", "workspace_bytes", "backward_workspace_bytes"):
+        getattr(L, "k6attn_packed_" + name).argtypes = [P, B]
+    for name in ("plan_bytes", "workspace_bytes", "backward_workspace_bytes", "norm_rope_backward_workspace_bytes"):
+        getattr(L, "k6attn_packed_" + name).restype = Z
     L.k6attn_sync.argtypes = [P, P]
     L.k6attn_set_option.argtypes = [P, I, ctypes.c_longlong]
     L.k6attn_status_string.argtypes = [I]
@@ -102,7 +130,9 @@ def load(build_if_missing: bool = True):
                  "k6attn_attention_chunks", "k6attn_lse_merge", "k6attn_cross_forward", "k6attn_norm_rope_qk",
                  "k6attn_row_bounds", "k6attn_attention_chunks_bounded", "k6attn_attention_chunk_groups",
                  "k6attn_rope_split_heads", "k6attn_lse_merge_heads", "k6attn_attention_chunk_groups_bounded",
-                 "k6attn_seq2head_relayout", "k6attn_sync", "k6attn_set_option"):
+                 "k6attn_seq2head_relayout", "k6attn_sync", "k6attn_set_option", "k6attn_packed_norm_rope",
+                 "k6attn_packed_norm_rope_backward", "k6attn_packed_plan", "k6attn_packed_forward",
+                 "k6attn_packed_backward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -127,6 +157,53 @@ def _stream(stream):
     return ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
 
 
+# element types of the packed calls' tensors, by the library's code and by torch's name
+_DTYPES = {BF16: "bfloat16", F32: "float32", F16: "float16"}
+_CODES = {"torch.bfloat16": BF16, "torch.float32": F32, "torch.float16": F16}
+_NAMES = {}
+
+
+def _name(dtype):
+    """torch.float16 -> "float16", remembered (str() of a dtype costs more than the call it checks)."""
+    n = _NAMES.get(dtype)
+    if n is None:
+        n = _NAMES[dtype] = str(dtype).replace("torch.", "")
+    return n
+
+
+def _code(t):
+    c = _CODES.get("torch." + _name(t.dtype))
+    if c is None:
+        raise ValueError(f"element type {t.dtype} is not one of the library's")
+    return c
+
+
+def _rows(t, tokens, heads, d, dtype, what):
+    """(pointer, token stride) of a [tokens][heads][d] CUDA tensor whose heads and d are dense."""
+    if tuple(t.shape) != (tokens, heads, d) or _name(t.dtype) != dtype or not t.is_cuda:
+        raise ValueError(f"{what}: want a {dtype} CUDA tensor of shape {(tokens, heads, d)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{what}: heads and head dim must be dense (strides {st})")
+    return t.data_ptr(), st[0] if tokens > 1 else heads * d
+
+
+def _vec(t, n, what, dtype):
+    if t is None:
+        return None
+    if t.numel() != n or _name(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: want a dense {dtype} CUDA tensor of {n} values, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t.data_ptr()
+
+
+def _room(workspace):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 class Handle:
     """Owns a k6attn handle (rotary tables + device error word)."""
 
@@ -138,6 +215,11 @@ class Handle:
         _check(L.k6attn_create(ctypes.byref(self._desc), ctypes.byref(h)))
         self.h = h
         self.dtype = dtype
+
+    @classmethod
+    def for_packed(cls, H, d=128, dtype="bf16", axis_dim=(32, 48, 48), theta=10000.0):
+        """A handle for the packed calls, whose batches and positions come with each call."""
+        return cls(1, H, d, dtype, (1, 1, 1), 0, axis_dim, theta, 0)
 
     @classmethod
     def for_workload(cls, w, B=None):
@@ -285,6 +367,92 @@ class Handle:
     def lse_merge(self, part_o, part_lse, n_chunks, out, lse=None, stream=None):
         _check(load().k6attn_lse_merge(self.h, _ptr(part_o), _ptr(part_lse), int(n_chunks), _ptr(out), _ptr(lse),
                                        _stream(stream)))
+
+    # ---- packed sequences
+    def packed_norm_rope(self, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *, q_out, k_out, stream=None):
+        """Per-head QK-norm (with weights) and (t, h, w) rotation of q [T][H][d] and k [T][kv_heads][d], at
+        positions int32 [T][3], into q_out, k_out (the handle's type or, for bf16, fp16; may be q and k)."""
+        T, kv = int(q.shape[0]), int(k.shape[1])
+        D = self._desc
+        e = _DTYPES[D.dtype]
+        od = _code(q_out)
+        o = (od,) if od in (D.dtype, F16) else (D.dtype,)
+        _check(load().k6attn_packed_norm_rope(
+            self.h, T, kv, _vec(positions, 3 * T, "positions", "int32"),
+            *_rows(q, T, D.H, D.d, e, "q"), *_rows(k, T, kv, D.d, e, "k"),
+            _vec(q_weight, D.d, "q_weight", "float32"), _vec(k_weight, D.d, "k_weight", "float32"), eps,
+            *_rows(q_out, T, D.H, D.d, _DTYPES[o[0]], "q_out"), *_rows(k_out, T, kv, D.d, _DTYPES[o[0]], "k_out"),
+            od, _stream(stream)))
+
+    def packed_norm_rope_backward_workspace_bytes(self, tokens: int, kv_heads: int) -> int:
+        return load().k6attn_packed_norm_rope_backward_workspace_bytes(self.h, int(tokens), int(kv_heads))
+
+    def packed_norm_rope_backward(self, dq_out, dk_out, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *,
+                                  dq, dk, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+        """Gradients of packed_norm_rope: dq, dk (the handle's type) and, with weights, dq_weight, dk_weight (fp32)."""
+        T, kv = int(dq_out.shape[0]), int(dk_out.shape[1])
+        D = self._desc
+        e = _DTYPES[D.dtype]
+        none = (None, 0)
+        _check(load().k6attn_packed_norm_rope_backward(
+            self.h, T, kv, _vec(positions, 3 * T, "positions", "int32"),
+            *_rows(dq_out, T, D.H, D.d, e, "dq_out"), *_rows(dk_out, T, kv, D.d, e, "dk_out"),
+            *(none if q is None else _rows(q, T, D.H, D.d, e, "q")),
+            *(none if k is None else _rows(k, T, kv, D.d, e, "k")),
+            _vec(q_weight, D.d, "q_weight", "float32"), _vec(k_weight, D.d, "k_weight", "float32"), eps,
+            *_rows(dq, T, D.H, D.d, e, "dq"), *_rows(dk, T, kv, D.d, e, "dk"),
+            _vec(dq_weight, D.d, "dq_weight", "float32"), _vec(dk_weight, D.d, "dk_weight", "float32"),
+            *_room(workspace), _stream(stream)))
+
+    def packed_plan(self, cu_q, cu_k, q_tokens, k_tokens, kv_heads, mask_block=0, stream=None) -> PackedPlan:
+        """Plan attention over packed sequences: offsets cu_q, cu_k (int32, on the device; cu_k None = cu_q) into
+        q_tokens and k_tokens rows.  mask_block 0: full, 1: causal, F: causal by frames of F tokens."""
+        import torch
+        b = PackedBatch(int(cu_q.shape[0]) - 1, int(kv_heads), int(mask_block), int(q_tokens), int(k_tokens))
+        L = load()
+        n = L.k6attn_packed_plan_bytes(self.h, ctypes.byref(b))
+        if not n:
+            raise K6Error(ERR_INVALID_ARG, (L.k6attn_last_error() or b"").decode())
+        plan = PackedPlan(b, torch.empty(n, dtype=torch.uint8, device=cu_q.device))
+        self.packed_replan(plan, cu_q, cu_k, stream=stream)
+        return plan
+
+    def packed_replan(self, plan, cu_q, cu_k, stream=None):
+        """Make the plan anew for other offsets of a batch of the same size (in place: captured calls see it)."""
+        n = plan.batch.n_seq + 1
+        _check(load().k6attn_packed_plan(self.h, plan.ref, _vec(cu_q, n, "cu_q", "int32"),
+                                         _vec(cu_k, n, "cu_k", "int32"), plan.ptr, plan.buffer.numel(),
+                                         _stream(stream)))
+
+    def packed_workspace_bytes(self, plan) -> int:
+        return load().k6attn_packed_workspace_bytes(self.h, plan.ref)
+
+    def packed_forward(self, plan, q, k, v, out, lse=None, *, workspace=None, stream=None):
+        """Attention of a planned batch: q [Tq][H][d], k, v [Tk][kv_heads][d] (q, k bf16 or fp16, v bf16) into
+        out (bf16, as q) and lse (fp32 [H][Tq])."""
+        b = plan.batch
+        Tq, Tk, kv, H, d = b.q_tokens, b.k_tokens, b.kv_heads, self._desc.H, self._desc.d
+        qk = _code(q)
+        x = _DTYPES[qk] if qk in (BF16, F16) else "bfloat16"
+        _check(load().k6attn_packed_forward(
+            self.h, plan.ref, plan.ptr, *_rows(q, Tq, H, d, x, "q"), *_rows(k, Tk, kv, d, x, "k"),
+            *_rows(v, Tk, kv, d, "bfloat16", "v"), qk, *_rows(out, Tq, H, d, "bfloat16", "out"),
+            _vec(lse, H * Tq, "lse", "float32"), *_room(workspace), _stream(stream)))
+
+    def packed_backward_workspace_bytes(self, plan) -> int:
+        return load().k6attn_packed_backward_workspace_bytes(self.h, plan.ref)
+
+    def packed_backward(self, plan, q, k, v, out, dout, lse, dq, dk, dv, *, workspace, stream=None):
+        """Gradients dq, dk, dv (bf16) of packed_forward, from its out and lse and dout (bf16)."""
+        b = plan.batch
+        Tq, Tk, kv, H, d = b.q_tokens, b.k_tokens, b.kv_heads, self._desc.H, self._desc.d
+        qk, bf = _code(q), "bfloat16"
+        x = _DTYPES[qk] if qk in (BF16, F16) else bf
+        _check(load().k6attn_packed_backward(
+            self.h, plan.ref, plan.ptr, *_rows(q, Tq, H, d, x, "q"), *_rows(k, Tk, kv, d, x, "k"),
+            *_rows(v, Tk, kv, d, bf, "v"), qk, *_rows(out, Tq, H, d, bf, "out"), *_rows(dout, Tq, H, d, bf, "dout"),
+            _vec(lse, H * Tq, "lse", "float32"), *_rows(dq, Tq, H, d, bf, "dq"), *_rows(dk, Tk, kv, d, bf, "dk"),
+            *_rows(dv, Tk, kv, d, bf, "dv"), *_room(workspace), _stream(stream)))
 
     def sync(self, stream=None):
         _check(load().k6attn_sync(self.h, _stream(stream)))
