@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                         float a, b2;
                         f2_split(ffma2(f2(__uint_as_float(s[kk]), __uint_as_float(s[kk + 1])), scale2, negm2), a, b2);
                         const float p0 = ex2(a), p1 = ex2(b2);
-                        // P in bf16, the type of V (one MMA takes one type): 2^-9 of each term, the
+                        // P in bf16, the type of V (one MMA takes one type): 2^-8 of each term, the
                         // row sum keeps fp32
                         pk[k / 2] = pack_bf16x2(p0, p1);
                         acc[(k / 2) & 3] = fadd2(acc[(k / 2) & 3], f2(p0, p1));
