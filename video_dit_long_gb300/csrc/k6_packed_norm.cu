@@ -84,9 +84,10 @@ struct Rows {
 
 struct NormRopeArgs {
     long tokens;
-    int H, heads;                  // query heads; query and key heads together
-    int run;                       // heads of a token that one warp takes at a time
-    int runs;                      // runs of a token: ceil(heads / run)
+    int heads[2];                  // query heads, key heads
+    int run[2];                    // heads of a token that one warp takes at a time
+    int runs[2];                   // runs of a token: ceil(heads / run)
+    long units_q, units;           // runs over all tokens: of queries; and of keys behind them
     Rows x[2], z[2];               // [0] queries, [1] keys.  z: the output, or its gradient
     Rows dx[2];
     const int *positions;          // [tokens][3]
@@ -98,29 +99,45 @@ struct NormRopeArgs {
     int *err;
 };
 
-// The angles of a lane's pairs.  turns and axis are fixed for the lane.
+// cos and sin of the NP pairs from pair0 on, at a token's positions.  The
+// frequencies are re-read (L1) rather than kept: 2 NP registers less a lane.
 template <int NP>
-struct Angles {
-    unsigned long long turns[NP];
-    int axis[NP];
-    __device__ void init(const NormRopeArgs &a, int pair0) {
+__device__ __forceinline__ void cos_sin(const NormRopeArgs &a, long tok, int pair0, float (&c)[NP], float (&s)[NP]) {
+    const int p0 = __ldg(a.positions + 3 * tok), p1 = __ldg(a.positions + 3 * tok + 1),
+              p2 = __ldg(a.positions + 3 * tok + 2);
 #pragma unroll
-        for (int k = 0; k < NP; k++) {
-            turns[k] = __ldg(a.turns + pair0 + k);
-            axis[k] = pair0 + k < a.seg1 ? 0 : pair0 + k < a.seg2 ? 1 : 2;
-        }
+    for (int k = 0; k < NP; k++) {
+        const int p = pair0 + k < a.seg1 ? p0 : pair0 + k < a.seg2 ? p1 : p2;
+        const unsigned long long turns = __ldg(a.turns + pair0 + k);
+        const int top = (int)(((unsigned long long)(long long)p * turns) >> 32);  // in [-1/2, 1/2) turns
+        sincospif((float)top * 0x1p-31f, &s[k], &c[k]);
     }
-    __device__ void cos_sin(const NormRopeArgs &a, long tok, float (&c)[NP], float (&s)[NP]) const {
-        const int p0 = __ldg(a.positions + 3 * tok), p1 = __ldg(a.positions + 3 * tok + 1),
-                  p2 = __ldg(a.positions + 3 * tok + 2);
-#pragma unroll
-        for (int k = 0; k < NP; k++) {
-            const int p = axis[k] == 0 ? p0 : axis[k] == 1 ? p1 : p2;
-            const int top = (int)(((unsigned long long)(long long)p * turns[k]) >> 32);  // in [-1/2, 1/2) turns
-            sincospif((float)top * 0x1p-31f, &s[k], &c[k]);
-        }
-    }
+}
+
+// Unit u: which tensor, token, first head and end.
+struct Unit {
+    int t, h0, h1;
+    long tok;
 };
+__device__ __forceinline__ Unit unit_at(const NormRopeArgs &a, long u) {
+    Unit r;
+    r.t = u >= a.units_q;
+    if (r.t) u -= a.units_q;
+    r.tok = a.runs[r.t] == 1 ? u : u / a.runs[r.t];
+    r.h0 = (int)(u - r.tok * a.runs[r.t]) * a.run[r.t];
+    r.h1 = min(r.h0 + a.run[r.t], a.heads[r.t]);
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void load_weights(const float *w, int first, float (&v)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+        // the caller's weights are 4-byte aligned only
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[k + i] = __ldg(w + first + k + i);
+    }
+}
 
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -131,45 +148,35 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // D = head dim, T = element type of the rows, TO = of the output.
 template <typename T, typename TO, int D, bool NORM>
-__global__ void __launch_bounds__(256) packed_norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(256, 4) packed_norm_rope_kernel(const NormRopeArgs a) {
     constexpr int N = Row<T>::N, NP = N / 2;
     constexpr int LPH = D / N;       // lanes of a head row
     constexpr int HPW = 32 / LPH;    // heads a warp handles side by side
     constexpr int kU = 4;            // vectors in flight per lane
+    constexpr int ROW = D * sizeof(T);
     static_assert(sizeof(T) == sizeof(TO), "rows keep their element size");
     const int lane = threadIdx.x & 31, sub = lane % LPH, grp = lane / LPH;
     const long warp0 = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
     const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
-    Angles<NP> ang;
-    ang.init(a, sub * NP);
-    float wq[N], wk[N];
-    if constexpr (NORM) {
-#pragma unroll
-        for (int k = 0; k < N; k++) wq[k] = __ldg(a.w[0] + sub * N + k), wk[k] = __ldg(a.w[1] + sub * N + k);
-    }
     bool bad = false;
-    const long units = a.tokens * a.runs;
-    for (long u = warp0; u < units; u += nwarps) {
-        const long tok = a.runs == 1 ? u : u / a.runs;
-        const int h0 = (int)(u - tok * a.runs) * a.run;
-        const int h1 = min(h0 + a.run, a.heads);
-        const char *xq = a.x[0].base + tok * a.x[0].stride + sub * 16, *xk = a.x[1].base + tok * a.x[1].stride + sub * 16;
-        char *zq = a.z[0].base + tok * a.z[0].stride + sub * 16, *zk = a.z[1].base + tok * a.z[1].stride + sub * 16;
-        float c[NP], s[NP];
-        for (int hb = h0; hb < h1; hb += HPW * kU) {
+    for (long u = warp0; u < a.units; u += nwarps) {
+        const Unit un = unit_at(a, u);
+        const char *x0 = a.x[un.t].base + un.tok * a.x[un.t].stride + sub * 16;
+        char *z0 = a.z[un.t].base + un.tok * a.z[un.t].stride + sub * 16;
+        float c[NP], s[NP], w[N];
+        for (int hb = un.h0 + grp; hb - grp < un.h1; hb += HPW * kU) {
             uint4 raw[kU];
 #pragma unroll
             for (int i = 0; i < kU; i++) {
-                const int hh = hb + i * HPW + grp;
                 raw[i] = make_uint4(0, 0, 0, 0);
-                if (hh < h1)
-                    raw[i] = __ldcs(reinterpret_cast<const uint4 *>(hh < a.H ? xq + (long)hh * (D * sizeof(T))
-                                                                             : xk + (long)(hh - a.H) * (D * sizeof(T))));
+                if (hb + i * HPW < un.h1) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + (hb + i * HPW) * ROW));
             }
-            if (hb == h0) ang.cos_sin(a, tok, c, s);  // under the first loads
+            if (hb - grp == un.h0) {  // under the first loads
+                cos_sin<NP>(a, un.tok, sub * NP, c, s);
+                if constexpr (NORM) load_weights<N>(a.w[un.t], sub * N, w);
+            }
 #pragma unroll
             for (int i = 0; i < kU; i++) {
-                const int hh = hb + i * HPW + grp;
                 float x[N];
                 Row<T>::unpack(raw[i], x);
                 if constexpr (NORM) {
@@ -177,9 +184,8 @@ __global__ void __launch_bounds__(256) packed_norm_rope_kernel(const NormRopeArg
 #pragma unroll
                     for (int k = 0; k < N; k++) ss = fmaf(x[k], x[k], ss);
                     const float r = rsqrtf(lanes_sum<LPH>(ss) * (1.f / D) + a.eps);
-                    const bool isq = hh < a.H;
 #pragma unroll
-                    for (int k = 0; k < N; k++) x[k] *= r * (isq ? wq[k] : wk[k]);
+                    for (int k = 0; k < N; k++) x[k] *= r * w[k];
                 }
 #pragma unroll
                 for (int k = 0; k < NP; k++) {
@@ -187,13 +193,12 @@ __global__ void __launch_bounds__(256) packed_norm_rope_kernel(const NormRopeArg
                     x[2 * k] = re * c[k] - im * s[k];
                     x[2 * k + 1] = re * s[k] + im * c[k];
                 }
-                if (hh < h1) {
+                if (hb + i * HPW < un.h1) {
                     if constexpr (std::is_same<TO, __half>::value) {
 #pragma unroll
                         for (int k = 0; k < N; k++) bad |= !(fabsf(x[k]) < 65520.f);  // a finite half
                     }
-                    *reinterpret_cast<uint4 *>(hh < a.H ? zq + (long)hh * (D * sizeof(T))
-                                                        : zk + (long)(hh - a.H) * (D * sizeof(T))) = Row<TO>::pack(x);
+                    *reinterpret_cast<uint4 *>(z0 + (hb + i * HPW) * ROW) = Row<TO>::pack(x);
                 }
             }
         }
@@ -203,50 +208,60 @@ __global__ void __launch_bounds__(256) packed_norm_rope_kernel(const NormRopeArg
 
 // The gradient: dx, and this block's partial sums of dw in a.part[block][2][D].
 // A lane owns the same N dims of every head it meets, so dw is a running sum in
-// its registers; lanes and warps of the block are joined through shared memory
-// in a fixed order, and blocks by packed_norm_dw_kernel, so that the result
-// does not depend on timing.
+// its registers (first over the warp's units of queries, then over those of
+// keys); lanes and warps of the block are joined through shared memory in a
+// fixed order, and blocks by packed_norm_dw_kernel, so that the result does not
+// depend on timing.
 template <typename T, int D, bool NORM>
-__global__ void __launch_bounds__(256) packed_norm_rope_bwd_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(256, 3) packed_norm_rope_bwd_kernel(const NormRopeArgs a) {
     constexpr int N = Row<T>::N, NP = N / 2;
     constexpr int LPH = D / N, HPW = 32 / LPH;
     constexpr int kU = 2;
-    const int lane = threadIdx.x & 31, sub = lane % LPH, grp = lane / LPH;
+    constexpr int ROW = D * sizeof(T);
+    __shared__ float sum[8][2][D];
+    const int lane = threadIdx.x & 31, sub = lane % LPH, grp = lane / LPH, warp = threadIdx.x >> 5;
     const long warp0 = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
     const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
-    Angles<NP> ang;
-    ang.init(a, sub * NP);
-    float wq[N], wk[N], aq[N], ak[N];
+    float acc[N];
 #pragma unroll
-    for (int k = 0; k < N; k++) {
-        aq[k] = ak[k] = 0.f;
-        if constexpr (NORM) wq[k] = __ldg(a.w[0] + sub * N + k), wk[k] = __ldg(a.w[1] + sub * N + k);
-    }
-    const long units = a.tokens * a.runs;
-    for (long u = warp0; u < units; u += nwarps) {
-        const long tok = a.runs == 1 ? u : u / a.runs;
-        const int h0 = (int)(u - tok * a.runs) * a.run;
-        const int h1 = min(h0 + a.run, a.heads);
-        float c[NP], s[NP];
-        for (int hb = h0; hb < h1; hb += HPW * kU) {
+    for (int k = 0; k < N; k++) acc[k] = 0.f;
+    auto flush = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+#pragma unroll
+            for (int o = 16; o >= LPH; o >>= 1) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+            if (grp == 0) sum[warp][t][sub * N + k] = acc[k];
+            acc[k] = 0.f;
+        }
+    };
+    int cur = 0;  // the tensor that acc belongs to
+    for (long u = warp0; u < a.units; u += nwarps) {
+        const Unit un = unit_at(a, u);
+        if constexpr (NORM) {
+            if (un.t != cur) flush(0);
+        }
+        cur = un.t;
+        const char *x0 = a.x[un.t].base + un.tok * a.x[un.t].stride + sub * 16;
+        const char *z0 = a.z[un.t].base + un.tok * a.z[un.t].stride + sub * 16;
+        char *d0 = a.dx[un.t].base + un.tok * a.dx[un.t].stride + sub * 16;
+        float c[NP], s[NP], w[N];
+        for (int hb = un.h0 + grp; hb - grp < un.h1; hb += HPW * kU) {
             uint4 rx[kU], rg[kU];
 #pragma unroll
             for (int i = 0; i < kU; i++) {
-                const int hh = hb + i * HPW + grp;
-                const int t = hh < a.H ? 0 : 1;
-                const long off = (long)(t ? hh - a.H : hh) * (D * sizeof(T)) + sub * 16;
                 rx[i] = rg[i] = make_uint4(0, 0, 0, 0);
-                if (hh < h1) {
-                    rg[i] = __ldcs(reinterpret_cast<const uint4 *>(a.z[t].base + tok * a.z[t].stride + off));
-                    if constexpr (NORM)
-                        rx[i] = __ldcs(reinterpret_cast<const uint4 *>(a.x[t].base + tok * a.x[t].stride + off));
+                if (hb + i * HPW < un.h1) {
+                    rg[i] = __ldcs(reinterpret_cast<const uint4 *>(z0 + (hb + i * HPW) * ROW));
+                    if constexpr (NORM) rx[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + (hb + i * HPW) * ROW));
                 }
             }
-            if (hb == h0) ang.cos_sin(a, tok, c, s);
+            if (hb - grp == un.h0) {
+                cos_sin<NP>(a, un.tok, sub * NP, c, s);
+                if constexpr (NORM) load_weights<N>(a.w[un.t], sub * N, w);
+            }
 #pragma unroll
             for (int i = 0; i < kU; i++) {
-                const int hh = hb + i * HPW + grp;
-                const bool live = hh < h1, isq = hh < a.H;
+                const bool live = hb + i * HPW < un.h1;
                 float g[N];
                 Row<T>::unpack(rg[i], g);
 #pragma unroll
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(256) packed_norm_rope_bwd_kernel(const NormRop
 #pragma unroll
                     for (int k = 0; k < N; k++) {
                         ss = fmaf(x[k], x[k], ss);
-                        gx = fmaf(g[k] * (isq ? wq[k] : wk[k]), x[k], gx);
+                        gx = fmaf(g[k] * w[k], x[k], gx);
                     }
                     const float r = rsqrtf(lanes_sum<LPH>(ss) * (1.f / D) + a.eps);
                     const float m = lanes_sum<LPH>(gx) * (1.f / D) * r;  // mean of g x r
@@ -270,33 +285,21 @@ __global__ void __launch_bounds__(256) packed_norm_rope_bwd_kernel(const NormRop
 #pragma unroll
                         for (int k = 0; k < N; k++) {
                             const float xh = x[k] * r;
-                            if (isq) aq[k] = fmaf(g[k], xh, aq[k]);
-                            else ak[k] = fmaf(g[k], xh, ak[k]);
-                            g[k] = r * (g[k] * (isq ? wq[k] : wk[k]) - xh * m);
+                            acc[k] = fmaf(g[k], xh, acc[k]);
+                            g[k] = r * (g[k] * w[k] - xh * m);
                         }
                     }
                 }
-                if (live) {
-                    const int t = isq ? 0 : 1;
-                    *reinterpret_cast<uint4 *>(a.dx[t].base + tok * a.dx[t].stride +
-                                               (long)(t ? hh - a.H : hh) * (D * sizeof(T)) + sub * 16) =
-                        Row<T>::pack(g);
-                }
+                if (live) *reinterpret_cast<uint4 *>(d0 + (hb + i * HPW) * ROW) = Row<T>::pack(g);
             }
         }
     }
     if constexpr (NORM) {
-        __shared__ float sum[8][2][D];
-        const int warp = threadIdx.x >> 5;
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-#pragma unroll
-            for (int o = 16; o >= LPH; o >>= 1) {
-                aq[k] += __shfl_xor_sync(0xffffffffu, aq[k], o);
-                ak[k] += __shfl_xor_sync(0xffffffffu, ak[k], o);
-            }
-            if (grp == 0) sum[warp][0][sub * N + k] = aq[k], sum[warp][1][sub * N + k] = ak[k];
-        }
+        flush(cur);
+        // a warp that met one tensor only has nothing of the other
+        const bool both = cur == 1 && warp0 < a.units_q;
+        if (!both)
+            for (int i = lane; i < D; i += 32) sum[warp][cur ^ 1][i] = 0.f;
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * D; i += 256) {
             float v = 0.f;
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(1024) packed_norm_dw_kernel(const float *__res
 NormRopeArgs norm_args(const Geom &g, const PackedNormRope &p) {
     NormRopeArgs a = {};
     a.tokens = p.tokens;
-    a.H = g.H, a.heads = g.H + p.Hkv;
+    a.heads[0] = g.H, a.heads[1] = p.Hkv;
     for (int t = 0; t < 2; t++) {
         a.x[t] = {static_cast<char *>(const_cast<void *>(p.x[t])), p.x_stride[t] * g.elem};
         a.z[t] = {static_cast<char *>(p.z[t]), p.z_stride[t] * g.elem};
@@ -350,8 +353,12 @@ NormRopeArgs norm_args(const Geom &g, const PackedNormRope &p) {
 // with fewer, each warp takes one pass of `pass` heads, so that a few tokens
 // still spread over the SMs (the sin and cos are then computed once per pass).
 void choose_runs(NormRopeArgs &a, int pass, int sms) {
-    a.run = a.tokens >= 16L * sms ? (a.heads + pass - 1) / pass * pass : pass;
-    a.runs = (a.heads + a.run - 1) / a.run;
+    for (int t = 0; t < 2; t++) {
+        a.run[t] = a.tokens >= 16L * sms ? (a.heads[t] + pass - 1) / pass * pass : pass;
+        a.runs[t] = (a.heads[t] + a.run[t] - 1) / a.run[t];
+    }
+    a.units_q = a.tokens * a.runs[0];
+    a.units = a.units_q + a.tokens * a.runs[1];
 }
 
 int sm_count() {
@@ -363,11 +370,11 @@ int sm_count() {
 
 // Blocks of 256 threads: at most `per_sm` a SM, at most one unit per warp.
 long norm_blocks(const NormRopeArgs &a, int per_sm, int sms) {
-    const long want = (a.tokens * a.runs + 7) / 8, wave = (long)sms * per_sm;
+    const long want = (a.units + 7) / 8, wave = (long)sms * per_sm;
     return want < wave ? want : wave;
 }
 
-constexpr int BWD_BLOCKS_PER_SM = 4;
+constexpr int BWD_BLOCKS_PER_SM = 3;
 
 }  // namespace
 
