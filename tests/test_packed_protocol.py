@@ -7,8 +7,10 @@ Added to that model, in program order:
 - the producer issues an item's Q before its first K, once the last S of the
   item before is done;
 - the first S of an item waits for its Q;
-- the softmax groups finish an item's epilogue (after its last P.V) before they
-  look at the next item's S.
+- the softmax group that owns an item's last tile runs its epilogue (after the
+  last P.V and the other group's post) before it looks at a later tile; the
+  other group goes on at once;
+- the first P.V of an item waits for the epilogue before to have read O.
 Checked over sequences of items of 1-7 key tiles: every slot is freed by
 someone, no wait cycle, no wait that an earlier phase of its slot could match.
 """
@@ -26,7 +28,16 @@ def packed_model(Ts, q_first=True):
     for u, T in enumerate(Ts):
         last = first + T - 1
         deps[("S_release", first)].add(("Q", u))  # waited for before anything else of the item
-        deps[("epilogue", u)].add(("PV_done", last))
+        # tile n belongs to group n % 2; the group without the last tile posts after its own last one
+        deps[("read_O", u)] |= {("PV_done", last), ("P", last), ("post", u)}
+        deps[("post", u)].add(("P", last - 1) if T > 1 else ("left", u))
+        if last + 2 < N:
+            deps[("wake", last + 2)].add(("read_O", u))  # the owner's next tile
+        if u:  # posts and epilogues of a group come in order
+            other = (last - 1) % 2
+            earlier = [v for v in range(u) if (sum(Ts[:v + 1]) - 1) % 2 == other]
+            for v in earlier[-1:]:
+                deps[("post", u)].add(("read_O", v))
         if u:
             deps[("Q", u)].add(("S", first - 1))
             prev = max(idx[("K", first - 1)], idx[("V", first - 1)])
@@ -36,8 +47,8 @@ def packed_model(Ts, q_first=True):
             else:  # Q issued after the first two K tiles
                 deps[("Q", u)].add(("load", prev + min(2, T)))
                 deps[("load", prev + min(2, T) + 1)].add(("Q", u))
-            for n in range(first, first + T):
-                deps[("wake", n)].add(("epilogue", u - 1))
+            deps[("wait_O", first)].add(("read_O", u - 1))
+            deps[("PV", first)].add(("wait_O", first))
         first += T
     return loads, deps, consumer
 
@@ -55,6 +66,14 @@ def test_no_wait_can_match_an_earlier_phase():
             if i >= NSTAGE:
                 wait = ("wait_K" if kind == "K" else "wait_V", n)
                 assert consumer[i - NSTAGE] in ancestors(deps, wait), (Ts, loads[i], loads[i - NSTAGE])
+
+
+def test_no_item_is_posted_twice_ahead_of_an_epilogue():
+    """Two posts are kept, by item parity: item u's may be written once epilogue u - 2 has read its own."""
+    for Ts in CASES:
+        _, deps, _ = packed_model(Ts)
+        for u in range(2, len(Ts)):
+            assert ("read_O", u - 2) in ancestors(deps, ("post", u)), (Ts, u)
 
 
 def test_q_behind_the_first_k_tiles_would_deadlock():

@@ -239,6 +239,8 @@ k6attn_status k6attn_create(const k6attn_desc *desc, k6attn_t *out) {
     g.elem = d.dtype == K6ATTN_BF16 ? 2 : 4;
     g.dtype = d.dtype;
     cudaGetDevice(&h->device);
+    h->sms = 152;
+    cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
     RopeLayout L = rope_layout(g);
     h->table_bytes = (size_t)L.total * sizeof(float2);
     k6attn_status st = cuda_check(cudaMalloc(&h->err, sizeof(int)), "create: error word");

@@ -39,6 +39,7 @@ struct k6attn_handle {
     int strict_order = 0;
     int rotate_bf16 = 0;                // forward: rotated copies in bf16 instead of fp16
     int device = 0;
+    int sms = 0;                        // SMs of that device
 };
 
 namespace k6 {
@@ -176,10 +177,11 @@ struct PackedNormRope {
     long dx_stride[2];
     const float *w[2];                // [d] each, or null: rotation only
     float eps;
+    int sms;
     int *err;
 };
 cudaError_t launch_packed_norm_rope(const Geom &g, const PackedNormRope &p, k6attn_dtype out, cudaStream_t st);
-size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens);
+size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens, int sms);
 cudaError_t launch_packed_norm_rope_bwd(const Geom &g, const PackedNormRope &p, float *dq_w, float *dk_w, void *ws,
                                         cudaStream_t st);
 
@@ -191,10 +193,12 @@ struct PackedGeom {
     int Tq, Tk;                       // token rows of q and of k, v
     int tpt, rows;
     int cap_q, cap_k;                 // upper bounds: query tiles, 128-key tiles
-    int extra;                        // work items that splitting long key ranges may add, per key head
-    int cap_slots;                    // partial outputs per key head
+    int sms;                          // SMs, and so persistent CTAs of the forward kernel
+    int extra;                        // pieces that splitting long key ranges may add, per key head; 0: nothing to split
+    int cap_rows, cap_fwd;            // forward items per CTA; and in all
+    int cap_slots, cap_merge;         // partial outputs, split tiles
 };
-PackedGeom packed_geom(const Geom &g, const k6attn_packed &b);
+PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms);
 
 struct PackedPtrs {
     const void *q, *k, *v;

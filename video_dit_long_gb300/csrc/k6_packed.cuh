@@ -22,8 +22,8 @@ struct PackedHeader {
     unsigned magic;
     int n_seq, H, Hkv, block, Tq, Tk;  // what the plan was made for
     int n_fwd, n_merge, n_q, n_k;      // items in each list
-    int n_slots;
-    int chunk;                         // key tiles that one forward item takes at most
+    int stream;                        // forward items laid out per CTA (count[]), or one list for every key head
+    int slot_step;                     // partials of a split tile lie this far apart
     int q_lo, q_hi, k_lo, k_hi;        // token rows that belong to a sequence
     int bad;                           // the offsets are not ascending within the tokens: no list is valid
 };
@@ -32,7 +32,8 @@ static_assert(sizeof(PackedHeader) <= PACKED_HEADER_BYTES, "plan header");
 
 // One tile of query tokens over key tiles [kt0, kt1) of its sequence.
 struct __align__(16) PackedItem {
-    int tok0, n_tok;   // first token row of q, tokens (1 .. tpt)
+    int tok0;          // first token row of q
+    int n_tok_hk;      // tokens (1 .. tpt) in the low 8 bits, and (forward, per CTA) the key head above them
     int krow0, Lk;     // the sequence's first row of k, and its keys
     int pos0;          // key position of token tok0
     int kt0, kt1;
@@ -46,17 +47,18 @@ struct __align__(16) PackedKItem {
     int off;           // Lk - Lq
     int qt0, qt1;
 };
-// The partials [slot0, slot0 + n) of a split tile.
+// The n partials of a split tile of one key head, from slot0 on, slot_step apart.
 struct __align__(16) PackedMerge {
-    int tok0, n_tok, slot0, n;
+    int tok0, n_tok_hk, slot0, n;
 };
 
 struct PackedPlan {
     PackedHeader *head;
-    PackedItem *fwd;    // [cap_q + extra], heaviest first
+    int *count;         // [sms]: forward items of each CTA
+    PackedItem *fwd;    // [sms][cap_rows] items of each CTA, or [cap_q + extra] for every key head, heaviest first
     PackedItem *q;      // [cap_q], unsplit (backward), heaviest first
     PackedKItem *k;     // [cap_k], heaviest first
-    PackedMerge *merge; // [extra]
+    PackedMerge *merge; // [cap_merge]
 };
 
 static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const PackedGeom &p) {
@@ -64,8 +66,10 @@ static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const Pa
     char *b = static_cast<char *>(base);
     r.head = reinterpret_cast<PackedHeader *>(b);
     b += PACKED_HEADER_BYTES;
+    r.count = reinterpret_cast<int *>(b);
+    b += ((size_t)p.sms * sizeof(int) + 15) / 16 * 16;
     r.fwd = reinterpret_cast<PackedItem *>(b);
-    b += ((size_t)p.cap_q + p.extra) * sizeof(PackedItem);
+    b += (size_t)p.cap_fwd * sizeof(PackedItem);
     r.q = reinterpret_cast<PackedItem *>(b);
     b += (size_t)p.cap_q * sizeof(PackedItem);
     r.k = reinterpret_cast<PackedKItem *>(b);

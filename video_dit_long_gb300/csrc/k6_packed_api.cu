@@ -93,7 +93,7 @@ k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
     if (b->mask_block < 0 || b->mask_block >= (1 << 30))
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: mask_block must be in [0, 2^30)", fn);
     if (b->q_tokens >= (1L << 30) || b->k_tokens >= (1L << 30) || b->n_seq >= (1 << 24) ||
-        (b->q_tokens + b->n_seq) * h->g.H >= (1L << 31) || (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31))
+        (b->q_tokens + b->n_seq) * h->g.H >= (1L << 31) || (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31) || b->kv_heads >= (1 << 16))
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: batch too large", fn);
     return K6ATTN_OK;
 }
@@ -140,7 +140,7 @@ k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, con
     p.tokens = tokens, p.Hkv = kv_heads, p.positions = positions, p.turns = h->turns;
     p.x[0] = q, p.x_stride[0] = q_stride, p.x[1] = k, p.x_stride[1] = k_stride;
     p.z[0] = q_out, p.z_stride[0] = q_out_stride, p.z[1] = k_out, p.z_stride[1] = k_out_stride;
-    p.w[0] = q_weight, p.w[1] = k_weight, p.eps = eps, p.err = h->err;
+    p.w[0] = q_weight, p.w[1] = k_weight, p.eps = eps, p.sms = h->sms, p.err = h->err;
     return cuda_check(launch_packed_norm_rope(g, p, out_dtype, static_cast<cudaStream_t>(stream)),
                       "packed_norm_rope launch");
 }
@@ -148,7 +148,7 @@ k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, con
 size_t k6attn_packed_norm_rope_backward_workspace_bytes(k6attn_t h, long tokens, int kv_heads) {
     (void)kv_heads;
     if (!h || tokens < 1) return 0;
-    return packed_norm_rope_bwd_workspace(h->g, tokens);
+    return packed_norm_rope_bwd_workspace(h->g, tokens, h->sms);
 }
 
 k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *positions,
@@ -178,7 +178,7 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
         if ((s = check_rows(fn, grad[i])) != K6ATTN_OK || (s = check_rows(fn, in[i])) != K6ATTN_OK ||
             (s = check_rows(fn, out[i])) != K6ATTN_OK)
             return s;
-    const size_t need = norm ? packed_norm_rope_bwd_workspace(g, tokens) : 0;
+    const size_t need = norm ? packed_norm_rope_bwd_workspace(g, tokens, h->sms) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return set_error(K6ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
                          workspace ? workspace_bytes : (size_t)0);
@@ -208,7 +208,7 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
     p.z[0] = const_cast<void *>(dq_out), p.z_stride[0] = dq_out_stride;
     p.z[1] = const_cast<void *>(dk_out), p.z_stride[1] = dk_out_stride;
     p.dx[0] = dq, p.dx_stride[0] = dq_stride, p.dx[1] = dk, p.dx_stride[1] = dk_stride;
-    p.w[0] = q_weight, p.w[1] = k_weight, p.eps = eps, p.err = h->err;
+    p.w[0] = q_weight, p.w[1] = k_weight, p.eps = eps, p.sms = h->sms, p.err = h->err;
     return cuda_check(launch_packed_norm_rope_bwd(g, p, dq_weight, dk_weight, workspace,
                                                   static_cast<cudaStream_t>(stream)),
                       "packed_norm_rope_backward launch");
@@ -216,7 +216,7 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
 
 size_t k6attn_packed_plan_bytes(k6attn_t h, const k6attn_packed *batch) {
     if (check_batch("packed_plan_bytes", h, batch) != K6ATTN_OK) return 0;
-    return packed_plan_bytes(packed_geom(h->g, *batch));
+    return packed_plan_bytes(packed_geom(h->g, *batch, h->sms));
 }
 
 k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const int *cu_q, const int *cu_k, void *plan,
@@ -230,7 +230,7 @@ k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const i
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: cu_k may be null only where q and k have the same tokens", fn);
     if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: offsets must be 4-byte aligned", fn);
-    const PackedGeom g = packed_geom(h->g, *batch);
+    const PackedGeom g = packed_geom(h->g, *batch, h->sms);
     if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
     const size_t need = packed_plan_bytes(g);
     if (plan_bytes < need)
@@ -244,7 +244,7 @@ k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const i
 
 size_t k6attn_packed_workspace_bytes(k6attn_t h, const k6attn_packed *batch) {
     if (check_batch("packed_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
-    return packed_fwd_workspace(packed_geom(h->g, *batch));
+    return packed_fwd_workspace(packed_geom(h->g, *batch, h->sms));
 }
 
 k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,
@@ -257,7 +257,7 @@ k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, cons
     if (s != K6ATTN_OK) return s;
     if (qk_dtype != K6ATTN_BF16 && qk_dtype != K6ATTN_F16)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: q/k type must be BF16 or F16", fn);
-    const PackedGeom g = packed_geom(h->g, *batch);
+    const PackedGeom g = packed_geom(h->g, *batch, h->sms);
     if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
     const long wq = (long)g.H * 128, wk = (long)g.Hkv * 128;
     const size_t need = packed_fwd_workspace(g);
@@ -285,7 +285,7 @@ k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, cons
 
 size_t k6attn_packed_backward_workspace_bytes(k6attn_t h, const k6attn_packed *batch) {
     if (check_batch("packed_backward_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
-    return packed_bwd_workspace(packed_geom(h->g, *batch));
+    return packed_bwd_workspace(packed_geom(h->g, *batch, h->sms));
 }
 
 k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,
@@ -300,7 +300,7 @@ k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, con
     if (s != K6ATTN_OK) return s;
     if (qk_dtype != K6ATTN_BF16 && qk_dtype != K6ATTN_F16)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: q/k type must be BF16 or F16", fn);
-    const PackedGeom g = packed_geom(h->g, *batch);
+    const PackedGeom g = packed_geom(h->g, *batch, h->sms);
     if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
     const long wq = (long)g.H * 128, wk = (long)g.Hkv * 128;
     const size_t need = packed_bwd_workspace(g);

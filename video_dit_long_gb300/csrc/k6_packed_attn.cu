@@ -11,11 +11,9 @@
 // head (one TMA box of tokens x heads), so K and V are read once per key head,
 // and a single new token fills G rows of a tile instead of one.  A work item is
 // one such tile over a range of 128-key tiles.  The CTAs are persistent (one a
-// SM); each takes items of the plan's list in turn, key head slowest, so that
-// the CTAs running together share a head's K and V in L2.  Items of few query
-// tiles over many keys are split by the plan; their partials (fp32 O
-// normalised, lse in base 2) go to the workspace and packed_merge_kernel joins
-// them in key order.
+// SM) and walk the items that the plan gives them (k6_packed_plan.cu).  A tile
+// whose keys are cut into several items leaves partials (fp32 O normalised, lse
+// in base 2) in the workspace, which packed_merge_kernel joins in key order.
 //
 // Roles in a CTA (384 threads), shared memory (Q tile, six 32 KB K/V slots)
 // and tensor memory (three S/P buffers, O) are those of attn_tc_single_kernel:
@@ -26,8 +24,11 @@
 //            sequence's rows or unwritten memory lie: P is zero there, but
 //            0 * NaN is not;
 //   warps 0-7  two softmax groups on alternate tiles, one thread a row.
-// Warps 8-10 run ahead into the next item while the softmax groups finish one:
-// its first K/V tiles, Q and S are in place when they get there.
+// Items overlap: warps 8-10 run ahead into the next item (its Q, first K/V tiles
+// and S are in place early), and only the softmax group that owns an item's last
+// tile runs its epilogue; the other one posts its row sums and goes on to the
+// next item's first tile, which is its own.  The epilogue takes O into registers
+// first and hands the accumulator back (o_free) before it scales and stores.
 // All waits are bounded (DEV_TIMEOUT), as in the other kernels.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -50,11 +51,11 @@ constexpr int KP = BN / P_PARTS;
 constexpr int SMEM_Q = 0;
 constexpr int SMEM_KV = TILE;
 constexpr int SMEM_BAR = SMEM_KV + NSTAGE * TILE;
-// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, drain, pv_buf [S buffer],
-// m_ready [tile parity][warp], epi [warp], epi_done [warp]
-constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 2 + NSBUF + 8 + 4 + 4;
+// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain, pv_buf [S buffer],
+// m_ready [tile parity][warp], epi [item parity][warp]
+constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 3 + NSBUF + 8 + 8;
 constexpr int SMEM_XCH = (SMEM_BAR + NBAR * 8 + 8 + 15) & ~15;  // + TMEM address, abort flag
-constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) of each group
+constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) posted, of two items
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
 constexpr int THREADS = 384;
 // Register split (launch: 384 x 168 = 64512): 2*128*184 + 128*136 = 64512.
@@ -73,7 +74,7 @@ struct PackedFwdParams {
     __nv_bfloat16 *out;
     long out_stride;
     float *lse;                               // [H][Tq], or null
-    float *part_o, *part_lse;                 // [slot][Hkv][128][128], [slot][Hkv][128]
+    float *part_o, *part_lse;                 // [partial][128][128], [partial][128]
     uint32_t idesc_qk;
     unsigned long long wait_limit_ns;
     int *err;
@@ -93,6 +94,39 @@ __device__ __forceinline__ uint32_t v_load_at(int j, int T) {
 // exp2 of a difference from a maximum that may be -inf (nothing seen yet): 0 then.
 __device__ __forceinline__ float ex2_from(float m, float m_new) { return m == -INFINITY ? 0.f : ex2(m - m_new); }
 
+// The items of this CTA: its row of the plan's stretches, or every gridDim-th
+// (item, key head) of the sorted list, to and fro.
+struct Walk {
+    const PackedItem *list;
+    uint32_t rounds, n_items, units;  // n_items 0: list is this CTA's own
+    int slots;                        // partials that one slot number stands for (1, or one for every key head)
+    __device__ Walk(const PackedPlan &plan, const PackedGeom &g) {
+        list = plan.fwd;
+        slots = plan.head->slot_step;
+        if (plan.head->stream) {
+            list += (long)blockIdx.x * g.cap_rows;
+            n_items = units = 0;
+            rounds = blockIdx.x < (uint32_t)g.sms ? (uint32_t)plan.count[blockIdx.x] : 0;
+        } else {
+            n_items = (uint32_t)plan.head->n_fwd;
+            units = n_items * (uint32_t)g.Hkv;
+            rounds = (units + gridDim.x - 1) / gridDim.x;
+        }
+    }
+    __device__ bool at(uint32_t k, PackedItem &it, int &hk) const {
+        uint32_t i = k;
+        if (n_items) {
+            const uint32_t u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (u >= units) return false;
+            hk = (int)(u / n_items);
+            i = u - (uint32_t)hk * n_items;
+        }
+        it = list[i];
+        if (!n_items) hk = it.n_tok_hk >> 8;
+        return true;
+    }
+};
+
 __global__ void __launch_bounds__(pf::THREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PackedFwdParams p) {
@@ -107,9 +141,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
         return;
     }
-    const uint32_t n_items = (uint32_t)plan.head->n_fwd;
-    const uint32_t units = n_items * (uint32_t)p.g.Hkv;
-    if (blockIdx.x >= units) return;
+    const Walk walk(plan, p.g);
+    if (walk.rounds == 0) return;
 
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
     uint64_t *q_empty = q_full + 1;
@@ -118,12 +151,12 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     uint64_t *s_full = kv_empty + NSTAGE;
     uint64_t *p_part = s_full + NSBUF;     // [S buffer][part], 128 arrivals each
     uint64_t *o_final = p_part + NSBUF * P_PARTS;
-    uint64_t *drain = o_final + 1;
+    uint64_t *o_free = o_final + 1;        // the epilogue has O in registers (128 arrivals)
+    uint64_t *drain = o_free + 1;
     uint64_t *pv_buf = drain + 1;          // [S buffer]: P.V of the tile in that buffer done
     uint64_t *m_ready = pv_buf + NSBUF;    // [tile parity][warp % 4]: row max after the tile published
-    uint64_t *epi = m_ready + 8;           // [warp % 4]: both warps of a row pair posted (l, m)
-    uint64_t *epi_done = epi + 4;          // [warp % 4]: both warps of a row pair have read O
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(epi_done + 4);
+    uint64_t *epi = m_ready + 8;           // [item parity][warp % 4]: the group that left posted its (l, m)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(epi + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -140,11 +173,11 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         }
         for (int q = 0; q < NSBUF * P_PARTS; q++) mbar_init(&p_part[q], BM);
         mbar_init(o_final, 1);
+        mbar_init(o_free, BM);
         mbar_init(drain, 2);  // one commit per MMA issuer
-        for (int q = 0; q < 8; q++) mbar_init(&m_ready[q], 32);
-        for (int q = 0; q < 4; q++) {
-            mbar_init(&epi[q], 64);
-            mbar_init(&epi_done[q], 64);
+        for (int q = 0; q < 8; q++) {
+            mbar_init(&m_ready[q], 32);
+            mbar_init(&epi[q], 32);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -172,9 +205,10 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             uint32_t kv_idx = 0;  // K/V tile loads issued
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
-            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const int hk = (int)(u / n_items);
-                const PackedItem it = plan.fwd[u % n_items];
+            for (uint32_t k = 0; k < walk.rounds && ok; k++) {
+                PackedItem it;
+                int hk;
+                if (!walk.at(k, it, hk)) continue;
                 const int T = it.kt1 - it.kt0;
                 if (T <= 0) continue;
                 auto load = [&](const CUtensorMap *tm, int j) -> bool {
@@ -217,8 +251,10 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             uint32_t uc = 0;
             bool ok = true;
             uint32_t vslot[4] = {0, 0, 0, 0};  // warp 9: ring slot of V(m) at m % 4
-            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const PackedItem it = plan.fwd[u % n_items];
+            for (uint32_t k = 0; k < walk.rounds && ok; k++) {
+                PackedItem it;
+                int hk;
+                if (!walk.at(k, it, hk)) continue;
                 const int T = it.kt1 - it.kt0;
                 if (T <= 0) continue;
                 if (warp == 9) {
@@ -261,6 +297,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                         const uint32_t pb = tmem + (n % NSBUF) * BN;
                         for (int q = 0; q < P_PARTS && ok; q++) {
                             if (!(ok = mbar_wait_w(&p_part[(n % NSBUF) * P_PARTS + q], (n / NSBUF) & 1, w))) break;
+                            // the first product of an item overwrites O: the epilogue before has read it
+                            if (j == 0 && q == 0 && uc > 0 && !(ok = mbar_wait_w(o_free, (uc - 1) & 1, w))) break;
                             tc_fence_after();
 #pragma unroll
                             for (int kk = q * (KP / 16); kk < (q + 1) * (KP / 16); kk++)
@@ -295,22 +333,24 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tO = lane_base + O_COL;
         float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
-        float *xe = xm + BM;                                      // [group][row][l, m]
+        float *xe = xm + BM;                                      // [item parity][row][l, m]
         const float sl2 = p.scale_log2;
         uint32_t tile = 0, n_epi = 0, kv_idx = 0;
         bool ok = true;
-        for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const int hk = (int)(u / n_items);
-            const PackedItem it = plan.fwd[u % n_items];
+        for (uint32_t k = 0; k < walk.rounds && ok; k++) {
+            PackedItem it;
+            int hk;
+            if (!walk.at(k, it, hk)) continue;
             const int T = it.kt1 - it.kt0;
-            const bool live = rtok < it.n_tok && r < p.g.rows;
+            const bool live = rtok < (it.n_tok_hk & 255) && r < p.g.rows;
             const long tok = (long)it.tok0 + (live ? rtok : 0);
             const int head = hk * p.g.G + rhead;
-            __nv_bfloat16 *orow = p.out + tok * p.out_stride + (long)head * D + hf * (D / 2);
+            __nv_bfloat16 *orow = p.out + tok * p.out_stride + (long)head * D;
             if (T <= 0) {  // no key is seen by any row of the tile
                 if (live) {
 #pragma unroll
-                    for (int k = 0; k < D / 2; k += 8) *reinterpret_cast<uint4 *>(orow + k) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < D / 2; c += 8)
+                        *reinterpret_cast<uint4 *>(orow + hf * (D / 2) + c) = make_uint4(0, 0, 0, 0);
                     if (p.lse && hf == 0) p.lse[(long)head * p.g.Tq + tok] = -INFINITY;
                 }
                 continue;
@@ -422,58 +462,54 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 l_own += (a0 + a1) + (b0 + b1);
             }
             if (!ok) break;
-            // epilogue: the two groups combine their row sums, each writes half of O's
-            // columns; both have read O before either publishes the next item's P
-            if (!mbar_wait(o_final, n_epi & 1, w)) {
-                ok = false;
-                break;
-            }
-            xe[(hf * BM + r) * 2] = l_own;
-            xe[(hf * BM + r) * 2 + 1] = m_own;
-            mbar_arrive(&epi[wq]);
-            if (!mbar_wait(&epi[wq], n_epi & 1, w)) {
-                ok = false;
-                break;
-            }
-            const float l_oth = xe[((hf ^ 1) * BM + r) * 2], m_oth = xe[((hf ^ 1) * BM + r) * 2 + 1];
-            const float m_fin = fmaxf(m_own, m_oth);  // the max O is expressed in
-            const float l_tot = l_own * ex2_from(m_own, m_fin) + l_oth * ex2_from(m_oth, m_fin);
-            const bool none = l_tot == 0.f;
-            const float inv = none ? 0.f : 1.f / l_tot;
-            const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
-            tc_fence_after();
-            const long prow = ((long)it.slot * p.g.Hkv + hk) * BM + r;
-#pragma unroll
-            for (int cc = 0; cc < D / 64; cc++) {
-                uint32_t o[32];
-                tmem_ld32(tO + hf * (D / 2) + cc * 32, o);
-                tmem_ld_wait();
-                if (!live) continue;
-                float f[32];
-#pragma unroll
-                for (int k = 0; k < 32; k++) f[k] = none ? 0.f : __uint_as_float(o[k]) * inv;
-                if (it.slot >= 0) {
-                    float *dst = p.part_o + prow * D + hf * (D / 2) + cc * 32;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4 *>(dst + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4 *>(orow + cc * 32 + k) =
-                            make_uint4(pack_bf16x2(f[k], f[k + 1]), pack_bf16x2(f[k + 2], f[k + 3]),
-                                       pack_bf16x2(f[k + 4], f[k + 5]), pack_bf16x2(f[k + 6], f[k + 7]));
+            const uint32_t last = tile + T - 1, buf = n_epi & 1;
+            float *x = xe + (buf * BM + r) * 2;
+            uint64_t *posted = &epi[buf * 4 + wq];
+            if ((int)(last & 1) != hf) {
+                // the other group finishes the item.  Two items' posts are kept: this group cannot be two
+                // ahead of that epilogue, since each item's tiles but the first need the other's maxima.
+                x[0] = l_own, x[1] = m_own;
+                mbar_arrive(posted);
+            } else {
+                if (!mbar_wait(posted, (n_epi >> 1) & 1, w) || !mbar_wait(o_final, n_epi & 1, w)) {
+                    ok = false;
+                    break;
                 }
-            }
-            if (live && hf == 0) {
-                if (it.slot >= 0) p.part_lse[prow] = lse2;
-                else if (p.lse) p.lse[(long)head * p.g.Tq + tok] = lse2 * 0.69314718055994531f;
-            }
-            tc_fence_before();
-            mbar_arrive(&epi_done[wq]);
-            if (!mbar_wait(&epi_done[wq], n_epi & 1, w)) {
-                ok = false;
-                break;
+                tc_fence_after();
+                uint32_t o[D];
+#pragma unroll
+                for (int cc = 0; cc < D / 32; cc++)
+                    tmem_ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(o_free);
+                const float l_oth = x[0], m_oth = x[1];
+                const float m_fin = fmaxf(m_own, m_oth);  // the max O is expressed in
+                const float l_tot = l_own * ex2_from(m_own, m_fin) + l_oth * ex2_from(m_oth, m_fin);
+                const bool none = l_tot == 0.f;
+                const float inv = none ? 0.f : 1.f / l_tot;
+                const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < D; c++) o[c] = none ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+                    if (it.slot >= 0) {
+                        const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM + r;
+                        float *dst = p.part_o + prow * D;
+#pragma unroll
+                        for (int c = 0; c < D; c += 4)
+                            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        p.part_lse[prow] = lse2;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D; c += 8) {
+                            auto two = [&](int i) {
+                                return pack_bf16x2(__uint_as_float(o[c + i]), __uint_as_float(o[c + i + 1]));
+                            };
+                            *reinterpret_cast<uint4 *>(orow + c) = make_uint4(two(0), two(2), two(4), two(6));
+                        }
+                        if (p.lse) p.lse[(long)head * p.g.Tq + tok] = lse2 * 0.69314718055994531f;
+                    }
+                }
             }
             n_epi++;
             tile += T;
@@ -488,62 +524,59 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     }
 }
 
-// Joins the partials of the split tiles: one warp per (tile, key head, row),
+// Joins the partials of the split tiles: one warp per row of a split tile,
 //   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
 __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams p) {
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
     if (!packed_plan_ok(*plan.head, p.g)) return;  // the attention kernel reported it
     const int lane = threadIdx.x & 31;
-    const long warp0 = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
-    const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
-    const long rows = (long)plan.head->n_merge * p.g.Hkv * p.g.rows;
-    for (long x = warp0; x < rows; x += nwarps) {
-        const int r = (int)(x % p.g.rows);
-        const long y = x / p.g.rows;
-        const int hk = (int)(y % p.g.Hkv);
-        const PackedMerge m = plan.merge[y / p.g.Hkv];
-        if (r / p.g.G >= m.n_tok) continue;
-        const long base = ((long)m.slot0 * p.g.Hkv + hk) * 128 + r, step = (long)p.g.Hkv * 128;
-        float top = -INFINITY;
-        for (int c = lane; c < m.n; c += 32) top = fmaxf(top, p.part_lse[base + c * step]);
+    const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const uint32_t mi = x / (uint32_t)p.g.rows;
+    const int r = (int)(x - mi * (uint32_t)p.g.rows);
+    if (mi >= (uint32_t)plan.head->n_merge) return;
+    const PackedMerge m = plan.merge[mi];
+    if (r / p.g.G >= (m.n_tok_hk & 255)) return;
+    const long base = (long)m.slot0 * 128 + r, step = (long)plan.head->slot_step * 128;
+    constexpr int kU = 8;  // partials in flight
+    float top = -INFINITY;
+    for (int c = lane; c < m.n; c += 32) top = fmaxf(top, p.part_lse[base + c * step]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        for (int c = 0; c < m.n; c += 4) {
-            float4 o[4];
-            float l[4];
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int c = 0; c < m.n; c += kU) {
+        float4 o[kU];
+        float l[kU];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                l[i] = -INFINITY, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c + i < m.n) {
-                    l[i] = p.part_lse[base + (c + i) * step];
-                    o[i] = reinterpret_cast<const float4 *>(p.part_o + (base + (c + i) * step) * 128)[lane];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float f = ex2(l[i] - ref);
-                sum += f;
-                acc.x = fmaf(f, o[i].x, acc.x), acc.y = fmaf(f, o[i].y, acc.y);
-                acc.z = fmaf(f, o[i].z, acc.z), acc.w = fmaf(f, o[i].w, acc.w);
+        for (int i = 0; i < kU; i++) {
+            l[i] = -INFINITY, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + i < m.n) {
+                l[i] = p.part_lse[base + (c + i) * step];
+                o[i] = reinterpret_cast<const float4 *>(p.part_o + (base + (c + i) * step) * 128)[lane];
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const long tok = (long)m.tok0 + r / p.g.G;
-        const int head = hk * p.g.G + r % p.g.G;
-        *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head * 128 + lane * 4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (lane == 0 && p.lse)
-            p.lse[(long)head * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+        for (int i = 0; i < kU; i++) {
+            const float f = ex2(l[i] - ref);
+            sum += f;
+            acc.x = fmaf(f, o[i].x, acc.x), acc.y = fmaf(f, o[i].y, acc.y);
+            acc.z = fmaf(f, o[i].z, acc.z), acc.w = fmaf(f, o[i].w, acc.w);
+        }
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long tok = (long)m.tok0 + r / p.g.G;
+    const int head = (m.n_tok_hk >> 8) * p.g.G + r % p.g.G;
+    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head * 128 + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse)
+        p.lse[(long)head * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace
 
 size_t packed_fwd_workspace(const PackedGeom &p) {
-    const size_t rows = (size_t)p.cap_slots * p.Hkv * 128;
+    const size_t rows = (size_t)p.cap_slots * 128;
     return round256(rows * 128 * 4) + round256(rows * 4);
 }
 
@@ -565,7 +598,7 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.out_stride = out_stride;
     p.lse = lse;
-    const size_t rows = (size_t)g.cap_slots * g.Hkv * 128;
+    const size_t rows = (size_t)g.cap_slots * 128;
     p.part_o = static_cast<float *>(ws);
     p.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + round256(rows * 128 * 4));
     // Q.K^T operands: bf16 (A/B format 1) or fp16 (format 0)
@@ -573,14 +606,10 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     if (t.qk_f16) p.idesc_qk &= ~((7u << 7) | (7u << 10));
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long most = ((long)g.cap_q + g.extra) * g.Hkv;
-    packed_fwd_kernel<<<(unsigned)(most < sms ? most : sms), pf::THREADS, pf::SMEM_TOTAL, st>>>(mq, mk, mv, p);
+    packed_fwd_kernel<<<(unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st>>>(mq, mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || g.extra == 0) return e;
-    packed_merge_kernel<<<(unsigned)sms, 256, 0, st>>>(p);
+    packed_merge_kernel<<<(unsigned)(((long)g.cap_merge * g.rows + 7) / 8), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
     const int q4 = warp & 3, g = (warp >> 2) & 1;
     const int r = 32 * q4 + lane;
     const int rtok = r / p.g.G, rhead = r % p.g.G;
-    const bool live = warp < 8 && rtok < it.n_tok && r < p.g.rows;
+    const bool live = warp < 8 && rtok < it.n_tok_hk && r < p.g.rows;
     const long tok = (long)it.tok0 + (live ? rtok : 0);
     __nv_bfloat16 *drow = p.dq + tok * p.dq_stride + (long)(hk * p.g.G + rhead) * D + 64 * g;
     if (T <= 0) {  // no key is seen by any row of the tile
@@ -763,9 +763,7 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     cudaError_t e = set_max_dynamic_smem((const void *)packed_dq_kernel, pb::SMEM_ALLOC);
     if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)packed_dkv_kernel, pb::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = g.sms;
     float2 *LD = static_cast<float2 *>(ws);
     unsigned *norms = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
     if (g.Tq) {

@@ -76,6 +76,9 @@ struct Row<float> {
     }
 };
 
+// Blocks of 256 threads resident on an SM: what the registers are bounded to, and the grid.
+constexpr int FWD_BLOCKS_PER_SM = 4, BWD_BLOCKS_PER_SM = 3;
+
 // Token rows of one tensor: `base`, and bytes from one token to the next.
 struct Rows {
     char *base;
@@ -148,7 +151,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // D = head dim, T = element type of the rows, TO = of the output.
 template <typename T, typename TO, int D, bool NORM>
-__global__ void __launch_bounds__(256, 4) packed_norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kernel(const NormRopeArgs a) {
     constexpr int N = Row<T>::N, NP = N / 2;
     constexpr int LPH = D / N;       // lanes of a head row
     constexpr int HPW = 32 / LPH;    // heads a warp handles side by side
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(256, 4) packed_norm_rope_kernel(const NormRope
 // fixed order, and blocks by packed_norm_dw_kernel, so that the result does not
 // depend on timing.
 template <typename T, int D, bool NORM>
-__global__ void __launch_bounds__(256, 3) packed_norm_rope_bwd_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(256, BWD_BLOCKS_PER_SM) packed_norm_rope_bwd_kernel(const NormRopeArgs a) {
     constexpr int N = Row<T>::N, NP = N / 2;
     constexpr int LPH = D / N, HPW = 32 / LPH;
     constexpr int kU = 2;
@@ -361,37 +364,26 @@ void choose_runs(NormRopeArgs &a, int pass, int sms) {
     a.units = a.units_q + a.tokens * a.runs[1];
 }
 
-int sm_count() {
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // Blocks of 256 threads: at most `per_sm` a SM, at most one unit per warp.
 long norm_blocks(const NormRopeArgs &a, int per_sm, int sms) {
     const long want = (a.units + 7) / 8, wave = (long)sms * per_sm;
     return want < wave ? want : wave;
 }
 
-constexpr int BWD_BLOCKS_PER_SM = 3;
-
 }  // namespace
 
-size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens) {
+size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens, int sms) {
     if (tokens <= 0) return 0;
-    return (size_t)sm_count() * BWD_BLOCKS_PER_SM * 2 * g.d * sizeof(float);
+    return (size_t)sms * BWD_BLOCKS_PER_SM * 2 * g.d * sizeof(float);
 }
 
 cudaError_t launch_packed_norm_rope(const Geom &g, const PackedNormRope &p, k6attn_dtype out, cudaStream_t st) {
     if (p.tokens == 0) return cudaSuccess;
     NormRopeArgs a = norm_args(g, p);
-    const int sms = sm_count();
+    const int sms = p.sms;
     auto launch = [&](auto kernel, int vec) {
         choose_runs(a, 4 * 32 * vec / g.d, sms);
-        int per_sm = 1;
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 256, 0);
-        kernel<<<(unsigned)norm_blocks(a, per_sm > 0 ? per_sm : 1, sms), 256, 0, st>>>(a);
+        kernel<<<(unsigned)norm_blocks(a, FWD_BLOCKS_PER_SM, sms), 256, 0, st>>>(a);
     };
     const bool norm = p.w[0] != nullptr;
     if (g.dtype == K6ATTN_F32 && g.d == 128)
@@ -420,7 +412,7 @@ cudaError_t launch_packed_norm_rope_bwd(const Geom &g, const PackedNormRope &p, 
     }
     NormRopeArgs a = norm_args(g, p);
     a.part = static_cast<float *>(ws);
-    const int sms = sm_count();
+    const int sms = p.sms;
     long blocks = 0;
     auto launch = [&](auto kernel, int vec) {
         choose_runs(a, 2 * 32 * vec / g.d, sms);

@@ -1,27 +1,35 @@
 // k6_packed_plan.cu -- lays out the work of packed attention on the device, once
-// per batch: lists of query tiles and key tiles from the sequences' offsets,
-// heaviest first, with long key ranges of few query tiles split so that the
-// GPU's SMs share them.  The offsets stay on the device, so a batch can be
-// planned inside a captured graph; a layer stack reuses the plan.
+// per batch.  The offsets stay on the device, so a batch can be planned inside a
+// captured graph; a layer stack reuses the plan.
 //
-// Three blocks, one list each: forward items (with splits), unsplit query
-// tiles (backward dq) and key tiles (backward dk/dv).  Warps stride over
-// sequences, lanes over a sequence's tiles; a counting sort by work in 256
-// classes orders the items.  The order within a class, and so which SM runs an
-// item and which slot holds a partial, may differ between runs; every item
-// writes rows of its own and partials are joined in key order, so results do
-// not.
+// Three blocks, one list each: forward items, unsplit query tiles (backward dq)
+// and key tiles (backward dk/dv).  Warps stride over sequences, lanes over a
+// sequence's tiles.
+//
+// Forward, up to STREAM_MOST key tiles per SM: every unit (a query tile of one
+// key head) costs its key tiles plus ITEM_COST; the units of the batch, end to
+// end, are cut into one stretch per SM, so that all SMs finish together
+// whatever the lengths: a stretch may begin or end inside a unit, whose
+// partials are then joined.  A cut that would leave a piece of less than
+// MIN_PIECE tiles moves to the unit's border.  Larger batches: one list of
+// query tiles per key head, heaviest first (a counting sort by work), which the
+// CTAs walk to and fro, one head after another, so that CTAs running together
+// share a head's K and V in L2; only units longer than the SMs' share are cut.
+// The other two lists are sorted alike.
+//
+// The order inside a class of equal work, and so which SM runs an item and
+// which slot holds a partial, may differ between runs; every item writes rows
+// of its own and partials are joined in key order, so results do not.
 #include "k6_packed.cuh"
 
 namespace k6 {
 
-// Key tiles below which a range is never split: a piece should outlast the
-// start and the join of a work item.
-constexpr int MIN_CHUNK = 4;
-// Work items aimed at, per SM, when long ranges are split.
-constexpr int ITEMS_PER_SM = 2;
+constexpr int MIN_PIECE = 4;       // key tiles of a piece at least
+constexpr int ITEM_COST = 3;       // start and end of an item, in key tiles
+constexpr int STREAM_MOST = 256;   // cost per SM up to which the batch is cut into one stretch per SM
+constexpr int STREAM_SEQS = 1024;  // and sequences
 
-PackedGeom packed_geom(const Geom &g, const k6attn_packed &b) {
+PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
     PackedGeom p;
     p.n_seq = b.n_seq;
     p.H = g.H, p.Hkv = b.kv_heads, p.G = g.H / b.kv_heads, p.block = b.mask_block;
@@ -31,23 +39,28 @@ PackedGeom packed_geom(const Geom &g, const k6attn_packed &b) {
     // sum of ceil(L / n) <= floor(T / n) + sequences
     p.cap_q = p.Tq / p.tpt + p.n_seq;
     p.cap_k = p.Tk / 128 + p.n_seq;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // no sequence has more than MIN_CHUNK key tiles: nothing to split
-    p.extra = p.Tk > MIN_CHUNK * 128 ? (ITEMS_PER_SM * sms + p.Hkv - 1) / p.Hkv : 0;
-    p.cap_slots = 2 * p.extra;
+    p.sms = sms;
+    // both pieces of a cut have MIN_PIECE tiles: nothing to cut below twice that
+    p.extra = p.Tk > (2 * MIN_PIECE - 1) * 128 ? (sms + p.Hkv - 1) / p.Hkv : 0;
+    // one cut per SM at most; or, per key head, n < 2 tiles / chunk pieces of each unit longer than chunk
+    p.cap_slots = p.extra ? 2 * (p.extra * p.Hkv > sms ? p.extra * p.Hkv : sms) : 0;
+    p.cap_merge = p.cap_slots / 2;
+    // a stretch of cost q, after its ends moved by MIN_PIECE + ITEM_COST at most, holds units of cost > ITEM_COST
+    const long most = ((long)p.cap_q * p.Hkv * ((p.Tk + 127) / 128 + 1 + ITEM_COST) + sms - 1) / sms;
+    p.cap_rows = (int)(most < STREAM_MOST ? most : STREAM_MOST) / (ITEM_COST + 1) + 8;
+    const long list = (long)p.cap_q + p.extra, rows = (long)sms * p.cap_rows;
+    p.cap_fwd = (int)(list > rows ? list : rows);
     return p;
 }
 
 size_t packed_plan_bytes(const PackedGeom &p) {
     const PackedPlan at = packed_plan_at(nullptr, p);
-    return reinterpret_cast<size_t>(at.merge) + (size_t)p.extra * sizeof(PackedMerge);
+    return reinterpret_cast<size_t>(at.merge) + (size_t)p.cap_merge * sizeof(PackedMerge);
 }
 
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32, CLASSES = 256;
+constexpr int THREADS = 1024, WARPS = THREADS / 32, CLASSES = 256, MAX_SMS = 512;
 
 enum List { FWD, QTILES, KTILES };
 
@@ -88,6 +101,10 @@ struct Shared {
     int bad, total;
     unsigned long long work;
     int slots, merges;
+    // stretches: first unit and item count of each CTA; cost and tiles of the sequences before each one
+    int first[MAX_SMS], items[MAX_SMS];
+    int cost[STREAM_SEQS + 1], tiles[STREAM_SEQS + 1];
+    int warp_sum[WARPS];
 };
 
 template <List LIST>
@@ -110,7 +127,7 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         __syncthreads();
         // extra * chunk >= work, so that the pieces beyond one per tile number at most extra
         const unsigned long long c = (sh.work + p.extra - 1) / p.extra;
-        chunk = c < (1u << 30) ? max(MIN_CHUNK, (int)c) : 1 << 30;
+        chunk = c < (1u << 30) ? max(2 * MIN_PIECE, (int)c) : 1 << 30;
     }
     for (int s = warp; s < p.n_seq; s += WARPS) {
         const Seq q = sequence<LIST>(p, cu_q, cu_k, s);
@@ -158,13 +175,15 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
             int i = atomicAdd(&sh.at[work_class((hi - lo) / n, most)], n);
             PackedItem it;
             it.tok0 = q.q0 + t * p.tpt;
-            it.n_tok = min(p.tpt, q.Lq - t * p.tpt);
+            it.n_tok_hk = min(p.tpt, q.Lq - t * p.tpt);
             it.krow0 = q.k0, it.Lk = q.Lk;
             it.pos0 = t * p.tpt + q.Lk - q.Lq;
             int slot = -1;
             if (n > 1) {
                 slot = atomicAdd(&sh.slots, n);
-                plan.merge[atomicAdd(&sh.merges, 1)] = {it.tok0, it.n_tok, slot, n};
+                const int m = atomicAdd(&sh.merges, p.Hkv);
+                for (int hk = 0; hk < p.Hkv; hk++)
+                    plan.merge[m + hk] = {it.tok0, it.n_tok_hk | hk << 8, slot * p.Hkv + hk, n};
             }
             for (int c = 0; c < n; c++, i++) {  // pieces of equal length, to within a tile
                 it.kt0 = (int)((long)hi * c / n), it.kt1 = (int)((long)hi * (c + 1) / n);
@@ -176,14 +195,148 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
     __syncthreads();
     if (threadIdx.x == 0) {
         if (LIST == FWD) {
-            plan.head->n_fwd = sh.total, plan.head->n_merge = sh.merges, plan.head->n_slots = sh.slots;
-            plan.head->chunk = chunk;
+            plan.head->n_fwd = sh.total, plan.head->n_merge = sh.merges;
+            plan.head->stream = 0, plan.head->slot_step = p.Hkv;
         } else if (LIST == QTILES) {
             plan.head->n_q = sh.total;
         } else {
             plan.head->n_k = sh.total;
         }
     }
+}
+
+// The batch cut into one stretch per SM.  False (the same for all threads): too
+// large, nothing was written.
+__device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int *cu_k, const PackedPlan &plan,
+                                Shared &sh) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (p.n_seq > STREAM_SEQS || p.sms > MAX_SMS) return false;
+    // cost and tiles of each sequence, then of those before it
+    unsigned long long all = 0;
+    for (int s = warp; s < p.n_seq; s += WARPS) {
+        const Seq q = sequence<FWD>(p, cu_q, cu_k, s);
+        unsigned long long c = 0;
+        for (int t = lane; t < q.tiles; t += 32) {
+            int lo, hi;
+            range<FWD>(p, q, t, lo, hi);
+            c += max(hi, 1) + ITEM_COST;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        all += c;
+        if (lane == 0) {  // a sum beyond the limit below is never used
+            sh.cost[s] = (int)(c < (1ull << 30) ? c : 1ull << 30);
+            sh.tiles[s] = q.tiles;
+        }
+    }
+    if (lane == 0) atomicAdd(&sh.work, all);
+    __syncthreads();
+    const unsigned long long total = sh.work * (unsigned long long)p.Hkv;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.work = 0;  // the sorted list counts anew
+    if (total > (unsigned long long)p.sms * STREAM_MOST) {
+        __syncthreads();
+        return false;
+    }
+    {  // exclusive sums over the sequences: one thread each (STREAM_SEQS threads)
+        const int s = threadIdx.x;
+        const int c = s < p.n_seq ? sh.cost[s] : 0, n = s < p.n_seq ? sh.tiles[s] : 0;
+        for (int pass = 0; pass < 2; pass++) {
+            const int mine = pass ? n : c;
+            int upto = mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) sh.warp_sum[warp] = upto;
+            __syncthreads();
+            int before = 0;
+            for (int w = 0; w < warp; w++) before += sh.warp_sum[w];
+            (pass ? sh.tiles : sh.cost)[s] = before + upto - mine;
+            if (s == THREADS - 1) (pass ? sh.tiles : sh.cost)[STREAM_SEQS] = before + upto;
+            __syncthreads();
+        }
+    }
+    const int head_cost = sh.cost[STREAM_SEQS], head_tiles = sh.tiles[STREAM_SEQS];  // of one key head
+    const int Q = max(MIN_PIECE, ((int)total + p.sms - 1) / p.sms);
+    for (int c = threadIdx.x; c < p.sms; c += THREADS) sh.first[c] = 1 << 30, sh.items[c] = 0;
+    __syncthreads();
+    // pass 0: the unit that each stretch begins with; pass 1: the items
+    for (int pass = 0; pass < 2; pass++) {
+        for (int s = warp; s < p.n_seq; s += WARPS) {
+            const Seq q = sequence<FWD>(p, cu_q, cu_k, s);
+            int run = sh.cost[s];
+            for (int t0 = 0; t0 < q.tiles; t0 += 32) {
+                const int t = t0 + lane;
+                int lo = 0, work = 0, cost = 0;
+                if (t < q.tiles) {
+                    range<FWD>(p, q, t, lo, work);
+                    cost = max(work, 1) + ITEM_COST;
+                }
+                int upto = cost;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                const int at = run + upto - cost;
+                run += __shfl_sync(0xffffffffu, upto, 31);
+                if (t >= q.tiles) continue;
+                for (int hk = 0; hk < p.Hkv; hk++) {
+                    const int a = hk * head_cost + at, b = a + cost, unit = hk * head_tiles + sh.tiles[s] + t;
+                    const int c0 = (a + Q - 1) / Q, c1 = min(p.sms, (b + Q - 1) / Q);  // borders in [a, b): [c0, c1)
+                    // tile at which border c cuts the unit, moved to its ends where a piece would be too short
+                    auto cut = [&](int c) {
+                        const int x = max(0, c * Q - a - ITEM_COST);
+                        return x < MIN_PIECE ? 0 : work - x < MIN_PIECE ? work : x;
+                    };
+                    if (pass == 0) {
+                        for (int c = c0; c < c1; c++) sh.first[c] = unit + (cut(c) >= max(work, 1) ? 1 : 0);
+                        continue;
+                    }
+                    int owner = min(p.sms - 1, a / Q), n = 1;
+                    for (int c = c0; c < c1; c++) {
+                        const int x = cut(c);
+                        if (x == 0) owner = c;
+                        else if (x < work) n++;
+                    }
+                    PackedItem it;
+                    it.tok0 = q.q0 + t * p.tpt;
+                    it.n_tok_hk = min(p.tpt, q.Lq - t * p.tpt) | hk << 8;
+                    it.krow0 = q.k0, it.Lk = q.Lk;
+                    it.pos0 = t * p.tpt + q.Lk - q.Lq;
+                    int slot = -1;
+                    if (n > 1) {
+                        slot = atomicAdd(&sh.slots, n);
+                        plan.merge[atomicAdd(&sh.merges, 1)] = {it.tok0, it.n_tok_hk, slot, n};
+                    }
+                    int from = 0, piece = 0;
+                    for (int c = c0; c <= c1; c++) {
+                        int x = work;
+                        if (c < c1) {
+                            x = cut(c);
+                            if (x == 0 || x >= work) continue;
+                        }
+                        // the piece [from, x) belongs to `owner`; the border c begins the next one
+                        const int k = unit - sh.first[owner];
+                        it.kt0 = from, it.kt1 = x;
+                        it.slot = n > 1 ? slot + piece : -1;
+                        if (k >= 0 && k < p.cap_rows) {
+                            plan.fwd[(long)owner * p.cap_rows + k] = it;
+                            atomicMax(&sh.items[owner], k + 1);
+                        }
+                        from = x, piece++, owner = c;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < p.sms; c += THREADS) plan.count[c] = sh.items[c];
+    if (threadIdx.x == 0) {
+        plan.head->n_fwd = 0, plan.head->n_merge = sh.merges;
+        plan.head->stream = 1, plan.head->slot_step = 1;
+    }
+    return true;
 }
 
 __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p, const int *__restrict__ cu_q,
@@ -210,8 +363,9 @@ __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p
         if (bad) atomicCAS(err, DEV_OK, DEV_PLAN);
     }
     if (bad) return;
-    if (blockIdx.x == 0) build<FWD>(p, cu_q, cu_k, plan, sh);
-    else if (blockIdx.x == 1) build<QTILES>(p, cu_q, cu_k, plan, sh);
+    if (blockIdx.x == 0) {
+        if (!build_stretches(p, cu_q, cu_k, plan, sh)) build<FWD>(p, cu_q, cu_k, plan, sh);
+    } else if (blockIdx.x == 1) build<QTILES>(p, cu_q, cu_k, plan, sh);
     else build<KTILES>(p, cu_q, cu_k, plan, sh);
 }
 
