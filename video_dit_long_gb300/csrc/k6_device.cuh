@@ -29,6 +29,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// In a kernel launched with launch_after (k6_internal.h): wait until the kernel
+// before it in the stream has completed and its writes are visible.  Every
+// thread of such a kernel runs this first, so that the kernel never completes
+// before the one it follows.
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {

@@ -161,6 +161,25 @@ cudaError_t launch_attn_bwd(const Geom &g, bool qk_f16, const void *q, const voi
                             float *dk, float *dv, float *djk, float *djv, unsigned long long wait_limit_ns, int *err,
                             cudaStream_t st, const char **why);
 
+// Launch `kernel` so that its blocks may be placed while the kernel before it in
+// the stream drains (programmatic dependent launch): the kernel calls
+// wait_previous_kernel() first.  Saves most of a launch's latency.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                         Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- packed sequences (k6_packed_*.cu) ----
 
 // Per-head norm and rotation of packed token rows; strides in elements between tokens.

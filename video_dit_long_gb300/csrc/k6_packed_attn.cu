@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 // Joins the partials of the split tiles: one warp per row of a split tile,
 //   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
 __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams p) {
+    wait_previous_kernel();
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
     if (!packed_plan_ok(*plan.head, p.g)) return;  // the attention kernel reported it
     const int lane = threadIdx.x & 31;
@@ -609,8 +610,7 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     packed_fwd_kernel<<<(unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st>>>(mq, mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || g.extra == 0) return e;
-    packed_merge_kernel<<<(unsigned)(((long)g.cap_merge * g.rows + 7) / 8), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 7) / 8), 256, 0, st, p);
 }
 
 }  // namespace k6

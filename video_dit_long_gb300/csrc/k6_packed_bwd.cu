@@ -5,12 +5,12 @@
 //   dV = P^T dO,   dQ = dS K / sqrt(d),   dK = dS^T Q / sqrt(d),
 // dK and dV summed over the G query heads of a key head inside the accumulator:
 // a tile of query rows holds 128 / G tokens of all G heads (one TMA box), so
-// the sum over heads is part of the product over rows.  Both kernels are those
-// of the joint-sequence backward (one stationary 128-row tile per CTA, the
+// the sum over heads is part of the product over rows.  The two kinds of item
+// are those of the joint-sequence backward (one stationary 128-row tile per CTA, the
 // other side streamed by TMA; warps 0-7 form P and dS, warp 8 copies, warp 9
 // issues the MMAs), walking the plan's lists: query tiles over the key tiles
 // below their limit (dq), key tiles over the query tiles that see them
-// (dk, dv), heaviest first.  Each output row is written by one CTA: no atomics,
+// (dk, dv), heaviest first, in one grid.  Each output row is written by one CTA: no atomics,
 // the same bits every run.
 //
 // Streamed tiles that reach past their sequence hold another sequence's rows
@@ -48,7 +48,9 @@ struct PackedBwdParams {
     const void *plan;
     float scale_log2, scale;                // log2(e)/sqrt(d), 1/sqrt(d)
     const float2 *LD;                       // [Hkv][Tq * G] {lse * log2(e), D}; lse = +inf for a row that sees nothing
-    const unsigned *norms;                  // max |dO_i|^2, max |v_j|^2 (float bits), or null: dS is not scaled
+    const float *norms;                     // [2][n_norms]: parts of max |dO_i|^2 and max |v_j|^2, or null: no scale
+    int n_norms;
+    uint32_t dkv_blocks;                    // blocks of key tiles, ahead of those of query tiles
     __nv_bfloat16 *dq, *dk, *dv;
     long dq_stride, dk_stride, dv_stride;
     uint32_t idesc_qk, idesc_bf16, idesc_bf16_mn, idesc_ds_mn;
@@ -97,9 +99,19 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
 }
 
 // The power of two that dS is carried with: 2^e, 2 max|dO| max|v| 2^e in (2^14, 2^15].
+// A whole warp.
 __device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
     if (!p.norms) return 0;
-    const float a = __uint_as_float(p.norms[0]), b = __uint_as_float(p.norms[1]);
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x & 31; i < p.n_norms; i += 32) {
+        a = fmaxf(a, p.norms[i]);
+        b = fmaxf(b, p.norms[p.n_norms + i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+    }
     // the product of the squares may leave fp32: add exponents instead
     if (!(a > 0.f) || !(b > 0.f)) return 60;  // all zero, or squares below fp32
     const int e = 14 - (int)ceilf(0.5f * (log2f(a) + log2f(b)));
@@ -108,81 +120,105 @@ __device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
 
 // -------------------------------------------------------------- pre-pass
 
-// LD of every query row of the sequences, and for fp16 q/k the largest squared
-// row norms of dO and v (finite ones: a row that is not makes its own results
-// NaN, whatever the scale).  Half a warp (16 lanes x 8 elements) covers one row.
+// LD of every query row of the sequences, and for fp16 q/k each block's largest
+// squared row norms of dO and v (finite ones: a row that is not makes its own
+// results NaN, whatever the scale) in norms[2][gridDim].  Half a warp (16 lanes x
+// 8 elements) covers one row, kU rows in flight.  Bound by HBM.
 template <bool NORMS>
 __global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g, const void *plan_base,
                                                               const char *out, long out_stride, const char *dout,
                                                               long dout_stride, const char *v, long v_stride,
                                                               const float *__restrict__ lse, float2 *__restrict__ LD,
-                                                              unsigned *norms) {
+                                                              float *norms) {
+    constexpr int kU = 4;
     const int lane = threadIdx.x & 31, sub = lane & 15;
-    const long warp = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5;
-    const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
+    const uint32_t half = (uint32_t)((blockIdx.x * blockDim.x + threadIdx.x) >> 4);
+    const uint32_t halves = (uint32_t)(gridDim.x * blockDim.x) >> 4;
     const PackedPlan plan = packed_plan_at(const_cast<void *>(plan_base), g);
-    if (!packed_plan_ok(*plan.head, g)) return;  // the next kernels report it
+    if (!packed_plan_ok(*plan.head, g)) return;  // the next kernel reports it
     const int q_lo = plan.head->q_lo, k_lo = plan.head->k_lo;
-    const long rows = (long)(plan.head->q_hi - q_lo) * g.H;
-    const long vrows = NORMS ? (long)(plan.head->k_hi - k_lo) * g.Hkv : 0;
+    // the host keeps tokens * heads below 2^31
+    const uint32_t rows = (uint32_t)(plan.head->q_hi - q_lo) * (uint32_t)g.H;
+    const uint32_t vrows = NORMS ? (uint32_t)(plan.head->k_hi - k_lo) * (uint32_t)g.Hkv : 0;
     float top_do = 0.f, top_v = 0.f;
-    for (long r0 = warp * 2; r0 < rows; r0 += nwarps * 2) {
-        const long r = r0 + (lane >> 4);
-        const long rr = r < rows ? r : rows - 1;
-        const long t0 = rr / g.H;
-        const int h = (int)(rr - t0 * g.H);
-        const long tok = q_lo + t0;
-        const uint4 a = reinterpret_cast<const uint4 *>(out + tok * out_stride + (long)h * 256)[sub];
-        const uint4 b = reinterpret_cast<const uint4 *>(dout + tok * dout_stride + (long)h * 256)[sub];
-        const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a);
-        const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(&b);
-        float s = 0.f, q = 0.f;
+    // both halves of a warp run the same number of rounds (the shuffles need all lanes)
+    for (uint32_t base = 0; base < rows; base += halves * kU) {
+        uint4 a[kU], b[kU];
+        uint32_t tok[kU], h[kU];
+        float l[kU];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const float2 fx = __bfloat1622float2(x[k]), fy = __bfloat1622float2(y[k]);
-            s = fmaf(fx.x, fy.x, s);
-            s = fmaf(fx.y, fy.y, s);
-            if (NORMS) q = fmaf(fy.x, fy.x, fmaf(fy.y, fy.y, q));
+        for (int i = 0; i < kU; i++) {
+            const uint32_t r = base + i * halves + half;
+            const bool in = r < rows;
+            tok[i] = in ? r / (uint32_t)g.H : 0;
+            h[i] = in ? r - tok[i] * (uint32_t)g.H : 0;
+            tok[i] += q_lo;
+            a[i] = reinterpret_cast<const uint4 *>(out + (long)tok[i] * out_stride + (long)h[i] * 256)[sub];
+            b[i] = reinterpret_cast<const uint4 *>(dout + (long)tok[i] * dout_stride + (long)h[i] * 256)[sub];
+            l[i] = sub == 0 ? lse[(long)h[i] * g.Tq + tok[i]] : 0.f;
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o, 16);
-            if (NORMS) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
-        }
-        if (r < rows) {
-            const float l = sub == 0 ? lse[(long)h * g.Tq + tok] : 0.f;
-            if (sub == 0)
-                LD[((long)(h / g.G) * g.Tq + tok) * g.G + h % g.G] =
-                    make_float2(l == -INFINITY ? INFINITY : l * pb::LOG2E, s);
-            // a row that sees nothing has no say in the scale
-            if (NORMS && sub == 0 && l > -INFINITY && q < INFINITY) top_do = fmaxf(top_do, q);
+        for (int i = 0; i < kU; i++) {
+            const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
+            const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(&b[i]);
+            float s = 0.f, q = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 fx = __bfloat1622float2(x[k]), fy = __bfloat1622float2(y[k]);
+                s = fmaf(fx.x, fy.x, s);
+                s = fmaf(fx.y, fy.y, s);
+                if (NORMS) q = fmaf(fy.x, fy.x, fmaf(fy.y, fy.y, q));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+                if (NORMS) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
+            }
+            if (base + i * halves + half < rows && sub == 0) {
+                LD[((long)(h[i] / g.G) * g.Tq + tok[i]) * g.G + h[i] % g.G] =
+                    make_float2(l[i] == -INFINITY ? INFINITY : l[i] * pb::LOG2E, s);
+                // a row that sees nothing has no say in the scale
+                if (NORMS && l[i] > -INFINITY && q < INFINITY) top_do = fmaxf(top_do, q);
+            }
         }
     }
     if constexpr (NORMS) {
-        for (long r0 = warp * 2; r0 < vrows; r0 += nwarps * 2) {
-            const long r = r0 + (lane >> 4) < vrows ? r0 + (lane >> 4) : vrows - 1;
-            const long t0 = r / g.Hkv;
-            const uint4 a = reinterpret_cast<const uint4 *>(v + (k_lo + t0) * v_stride + (r - t0 * g.Hkv) * 256)[sub];
-            const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a);
-            float q = 0.f;
+        for (uint32_t base = 0; base < vrows; base += halves * kU) {
+            uint4 a[kU];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float2 f = __bfloat1622float2(x[k]);
-                q = fmaf(f.x, f.x, fmaf(f.y, f.y, q));
+            for (int i = 0; i < kU; i++) {
+                const uint32_t r = base + i * halves + half < vrows ? base + i * halves + half : 0;
+                const uint32_t t = r / (uint32_t)g.Hkv;
+                a[i] = reinterpret_cast<const uint4 *>(v + (long)(k_lo + t) * v_stride +
+                                                       (long)(r - t * (uint32_t)g.Hkv) * 256)[sub];
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
-            if (q < INFINITY) top_v = fmaxf(top_v, q);
+            for (int i = 0; i < kU; i++) {
+                const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
+                float q = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float2 f = __bfloat1622float2(x[k]);
+                    q = fmaf(f.x, f.x, fmaf(f.y, f.y, q));
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
+                if (q < INFINITY) top_v = fmaxf(top_v, q);
+            }
         }
+        __shared__ float tops[2][8];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             top_do = fmaxf(top_do, __shfl_xor_sync(0xffffffffu, top_do, o));
             top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
         }
-        // bits of non-negative floats order as integers: a maximum does not depend on the order
-        if (lane == 0) {
-            if (top_do > 0.f) atomicMax(norms, __float_as_uint(top_do));
-            if (top_v > 0.f) atomicMax(norms + 1, __float_as_uint(top_v));
+        if (lane == 0) tops[0][threadIdx.x >> 5] = top_do, tops[1][threadIdx.x >> 5] = top_v;
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; w++) m = fmaxf(m, tops[threadIdx.x][w]);
+            norms[threadIdx.x * gridDim.x + blockIdx.x] = m;
         }
     }
 }
@@ -303,23 +339,12 @@ __device__ __forceinline__ void dq_row(uint32_t lb, int g, int buf, int rel, flo
     }
 }
 
-__global__ void __launch_bounds__(pb::THREADS, 1)
-    packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const PackedBwdParams p) {
+// One query tile of one key head (the whole block).
+__device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, const CUtensorMap &tm_do,
+                                        const CUtensorMap &tm_k, const CUtensorMap &tm_v, const PackedBwdParams &p,
+                                        const PackedItem &it, int hk) {
     using namespace pb;
     using namespace dqk;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
-    if (!packed_plan_ok(*plan.head, p.g)) {
-        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
-        return;
-    }
-    const uint32_t n_items = (uint32_t)plan.head->n_q;
-    if (blockIdx.x >= n_items * (uint32_t)p.g.Hkv) return;
-    const int hk = (int)(blockIdx.x / n_items);
-    const PackedItem it = plan.q[blockIdx.x % n_items];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int T = it.kt1;
     // rows: lane quarter q4, key half g
@@ -512,23 +537,12 @@ constexpr int STAT = 0, QFULL = 1, DOFULL = 3, QEMPTY = 5, DOEMPTY = 7, SREADY =
               WIN = 13, ACC = 14, DRAIN = 15, NB = 16;  // PDS, PDS + 1: the two parts of a tile's P^T / dS^T
 }
 
-__global__ void __launch_bounds__(pb::THREADS, 1)
-    packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const PackedBwdParams p) {
+// One key tile of one key head (the whole block).
+__device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q, const CUtensorMap &tm_do,
+                                         const CUtensorMap &tm_k, const CUtensorMap &tm_v, const PackedBwdParams &p,
+                                         const PackedKItem &it, int hk) {
     using namespace pb;
     using namespace dkvk;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
-    if (!packed_plan_ok(*plan.head, p.g)) {
-        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
-        return;
-    }
-    const uint32_t n_items = (uint32_t)plan.head->n_k;
-    if (blockIdx.x >= n_items * (uint32_t)p.g.Hkv) return;
-    const int hk = (int)(blockIdx.x / n_items);
-    const PackedKItem it = plan.k[blockIdx.x % n_items];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int T = it.qt1 - it.qt0;
     // rows: key row r, query half g
@@ -738,10 +752,41 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
     teardown(tmem);
 }
 
+// Key tiles first (their steps are the longer ones), query tiles behind them:
+// one grid, so that the GPU drains once.
+__global__ void __launch_bounds__(pb::THREADS, 1)
+    packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PackedBwdParams p) {
+    wait_previous_kernel();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    if (!packed_plan_ok(*plan.head, p.g)) {
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+        return;
+    }
+    const bool keys = blockIdx.x < p.dkv_blocks;
+    const uint32_t u = keys ? blockIdx.x : blockIdx.x - p.dkv_blocks;
+    const uint32_t n_items = (uint32_t)(keys ? plan.head->n_k : plan.head->n_q);
+    if (u >= n_items * (uint32_t)p.g.Hkv) return;
+    const int hk = (int)(u / n_items);
+    if (keys) dkv_item(smem, tm_q, tm_do, tm_k, tm_v, p, plan.k[u - (uint32_t)hk * n_items], hk);
+    else dq_item(smem, tm_q, tm_do, tm_k, tm_v, p, plan.q[u - (uint32_t)hk * n_items], hk);
+}
+
 }  // namespace
 
-// Workspace: LD, then the two squared norms.
-size_t packed_bwd_workspace(const PackedGeom &p) { return round256((size_t)p.Tq * p.H * sizeof(float2)) + 256; }
+// Blocks of the pre-pass: each leaves two norms, which every block of the main kernel reads.
+static unsigned rows_blocks(const PackedGeom &g) {
+    const long want = ((long)g.Tq * g.H + 63) / 64;
+    return (unsigned)(want < 4L * g.sms ? want : 4L * g.sms);
+}
+
+// Workspace: LD, then the blocks' squared norms.
+size_t packed_bwd_workspace(const PackedGeom &p) {
+    return round256((size_t)p.Tq * p.H * sizeof(float2)) + round256((size_t)p.sms * 4 * 2 * sizeof(float));
+}
 
 cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const void *out, long out_stride,
                               const void *dout, long dout_stride, const float *lse, void *dq, long dq_stride,
@@ -760,27 +805,19 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
         !packed_kv_map(&mk, k, krows, kheads, g.Tk ? t.k_stride : t.q_stride, why) ||
         !packed_kv_map(&mv, v, krows, kheads, g.Tk ? t.v_stride : dout_stride, why))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem((const void *)packed_dq_kernel, pb::SMEM_ALLOC);
-    if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)packed_dkv_kernel, pb::SMEM_ALLOC);
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_bwd_kernel, pb::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    const int sms = g.sms;
     float2 *LD = static_cast<float2 *>(ws);
-    unsigned *norms = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
+    float *norms = reinterpret_cast<float *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
+    const unsigned n_rows = rows_blocks(g);
     if (g.Tq) {
-        const long want = ((long)g.Tq * g.H + 15) / 16;
-        const unsigned grid = (unsigned)(want < 8L * sms ? want : 8L * sms);
         auto rows = [&](auto kernel) {
-            kernel<<<grid, 256, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
-                                         static_cast<const char *>(dout), dout_stride * 2,
-                                         static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, norms);
+            kernel<<<n_rows, 256, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
+                                           static_cast<const char *>(dout), dout_stride * 2,
+                                           static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, norms);
         };
-        if (t.qk_f16) {
-            e = cudaMemsetAsync(norms, 0, 2 * sizeof(unsigned), st);
-            if (e != cudaSuccess) return e;
-            rows(packed_bwd_rows_kernel<true>);
-        } else {
-            rows(packed_bwd_rows_kernel<false>);
-        }
+        if (t.qk_f16) rows(packed_bwd_rows_kernel<true>);
+        else rows(packed_bwd_rows_kernel<false>);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -791,6 +828,7 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     p.scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
     p.LD = LD;
     p.norms = t.qk_f16 && g.Tq ? norms : nullptr;
+    p.n_norms = (int)n_rows;
     p.dq = static_cast<__nv_bfloat16 *>(dq), p.dk = static_cast<__nv_bfloat16 *>(dk);
     p.dv = static_cast<__nv_bfloat16 *>(dv);
     p.dq_stride = dq_stride, p.dk_stride = dk_stride, p.dv_stride = dv_stride;
@@ -804,15 +842,9 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     p.ds_f16 = t.qk_f16 ? 1 : 0;
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
-    if (g.Tq) {
-        packed_dq_kernel<<<(unsigned)((long)g.cap_q * g.Hkv), pb::THREADS, pb::SMEM_ALLOC, st>>>(mq, mdo, mk, mv, p);
-        e = cudaGetLastError();
-    }
-    if (g.Tk && e == cudaSuccess) {
-        packed_dkv_kernel<<<(unsigned)((long)g.cap_k * g.Hkv), pb::THREADS, pb::SMEM_ALLOC, st>>>(mq, mdo, mk, mv, p);
-        e = cudaGetLastError();
-    }
-    return e;
+    p.dkv_blocks = g.Tk ? (uint32_t)((long)g.cap_k * g.Hkv) : 0;
+    const uint32_t blocks = p.dkv_blocks + (g.Tq ? (uint32_t)((long)g.cap_q * g.Hkv) : 0);
+    return launch_after(packed_bwd_kernel, blocks, pb::THREADS, pb::SMEM_ALLOC, st, mq, mdo, mk, mv, p);
 }
 
 }  // namespace k6

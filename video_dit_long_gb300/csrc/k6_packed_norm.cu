@@ -315,12 +315,14 @@ __global__ void __launch_bounds__(256, BWD_BLOCKS_PER_SM) packed_norm_rope_bwd_k
 
 // dw[t][e] = sum over blocks of part[block][t][e], in a fixed order.  One block
 // per 32 columns; a warp per slice of the blocks, its lanes the columns.
-__global__ void __launch_bounds__(1024) packed_norm_dw_kernel(const float *__restrict__ part, int blocks, int D,
+__global__ void __launch_bounds__(1024) packed_norm_dw_kernel(const float *part, int blocks, int D,
                                                               float *__restrict__ dq_w, float *__restrict__ dk_w) {
+    wait_previous_kernel();
     __shared__ float sum[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float v = 0.f;
+#pragma unroll 8
     for (int b = warp; b < blocks; b += 32) v += part[(long)b * 2 * D + col];
     sum[warp][lane] = v;
     __syncthreads();
@@ -430,8 +432,7 @@ cudaError_t launch_packed_norm_rope_bwd(const Geom &g, const PackedNormRope &p, 
              : launch(packed_norm_rope_bwd_kernel<__nv_bfloat16, 128, false>, 8);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !norm) return e;
-    packed_norm_dw_kernel<<<2 * g.d / 32, 1024, 0, st>>>(a.part, (int)blocks, g.d, dq_w, dk_w);
-    return cudaGetLastError();
+    return launch_after(packed_norm_dw_kernel, 2 * g.d / 32, 1024, 0, st, a.part, (int)blocks, g.d, dq_w, dk_w);
 }
 
 }  // namespace k6

@@ -157,50 +157,50 @@ def _stream(stream):
     return ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
 
 
-# element types of the packed calls' tensors, by the library's code and by torch's name
-_DTYPES = {BF16: "bfloat16", F32: "float32", F16: "float16"}
-_CODES = {"torch.bfloat16": BF16, "torch.float32": F32, "torch.float16": F16}
-_NAMES = {}
+# element types of the packed calls' tensors: torch's by the library's code, and back (filled at the first handle)
+_DTYPES, _CODES = {}, {}
 
 
-def _name(dtype):
-    """torch.float16 -> "float16", remembered (str() of a dtype costs more than the call it checks)."""
-    n = _NAMES.get(dtype)
-    if n is None:
-        n = _NAMES[dtype] = str(dtype).replace("torch.", "")
-    return n
+def _torch_types():
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({BF16: torch.bfloat16, F32: torch.float32, F16: torch.float16, "int32": torch.int32})
+        _CODES.update({torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16})
+    return torch
 
 
 def _code(t):
-    c = _CODES.get("torch." + _name(t.dtype))
+    c = _CODES.get(t.dtype)
     if c is None:
         raise ValueError(f"element type {t.dtype} is not one of the library's")
     return c
 
 
-def _rows(t, tokens, heads, d, dtype, what):
-    """(pointer, token stride) of a [tokens][heads][d] CUDA tensor whose heads and d are dense."""
-    if tuple(t.shape) != (tokens, heads, d) or _name(t.dtype) != dtype or not t.is_cuda:
-        raise ValueError(f"{what}: want a {dtype} CUDA tensor of shape {(tokens, heads, d)}, got {t.dtype} "
+def _rows(t, shape, dtype, device, what):
+    """(pointer, token stride) of a [tokens][heads][d] tensor on `device` whose heads and d are dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what}: want a {dtype} tensor of shape {shape} on cuda:{device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    if st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{what}: heads and head dim must be dense (strides {st})")
-    return t.data_ptr(), st[0] if tokens > 1 else heads * d
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _vec(t, n, what, dtype):
+def _vec(t, n, dtype, device, what):
     if t is None:
         return None
-    if t.numel() != n or _name(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: want a dense {dtype} CUDA tensor of {n} values, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: want a dense {dtype} tensor of {n} values on cuda:{device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _room(workspace):
+def _room(workspace, device):
     if workspace is None:
         return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a dense tensor on cuda:{device}, got one on {workspace.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -215,6 +215,9 @@ class Handle:
         _check(L.k6attn_create(ctypes.byref(self._desc), ctypes.byref(h)))
         self.h = h
         self.dtype = dtype
+        torch = _torch_types()  # the packed calls check their tensors' device and type
+        self._dev = torch.cuda.current_device()
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     @classmethod
     def for_packed(cls, H, d=128, dtype="bf16", axis_dim=(32, 48, 48), theta=10000.0):
@@ -369,20 +372,29 @@ class Handle:
                                        _stream(stream)))
 
     # ---- packed sequences
+    def _packed(self, stream):
+        """(device index, stream) of a packed call: the handle's device, its current stream unless one is given."""
+        if stream is None and self._raw_stream is not None:  # torch.cuda.current_stream without its object
+            return self._dev, self._raw_stream(self._dev)
+        return self._dev, _stream(stream)
+
     def packed_norm_rope(self, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *, q_out, k_out, stream=None):
         """Per-head QK-norm (with weights) and (t, h, w) rotation of q [T][H][d] and k [T][kv_heads][d], at
         positions int32 [T][3], into q_out, k_out (the handle's type or, for bf16, fp16; may be q and k)."""
-        T, kv = int(q.shape[0]), int(k.shape[1])
+        dev, st = self._packed(stream)
         D = self._desc
-        e = _DTYPES[D.dtype]
+        d, T, kv = D.d, q.shape[0], k.shape[1]
+        sq, sk, e, f32 = (T, D.H, d), (T, kv, d), _DTYPES[D.dtype], _DTYPES[F32]
         od = _code(q_out)
-        o = (od,) if od in (D.dtype, F16) else (D.dtype,)
+        o = q_out.dtype
+        pq, lq = _rows(q, sq, e, dev, "q")
+        pk, lk = _rows(k, sk, e, dev, "k")
+        poq, loq = _rows(q_out, sq, o, dev, "q_out")
+        pok, lok = _rows(k_out, sk, o, dev, "k_out")
         _check(load().k6attn_packed_norm_rope(
-            self.h, T, kv, _vec(positions, 3 * T, "positions", "int32"),
-            *_rows(q, T, D.H, D.d, e, "q"), *_rows(k, T, kv, D.d, e, "k"),
-            _vec(q_weight, D.d, "q_weight", "float32"), _vec(k_weight, D.d, "k_weight", "float32"), eps,
-            *_rows(q_out, T, D.H, D.d, _DTYPES[o[0]], "q_out"), *_rows(k_out, T, kv, D.d, _DTYPES[o[0]], "k_out"),
-            od, _stream(stream)))
+            self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pq, lq, pk, lk,
+            _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, poq, loq, pok, lok,
+            od, st))
 
     def packed_norm_rope_backward_workspace_bytes(self, tokens: int, kv_heads: int) -> int:
         return load().k6attn_packed_norm_rope_backward_workspace_bytes(self.h, int(tokens), int(kv_heads))
@@ -390,25 +402,27 @@ class Handle:
     def packed_norm_rope_backward(self, dq_out, dk_out, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *,
                                   dq, dk, dq_weight=None, dk_weight=None, workspace=None, stream=None):
         """Gradients of packed_norm_rope: dq, dk (the handle's type) and, with weights, dq_weight, dk_weight (fp32)."""
-        T, kv = int(dq_out.shape[0]), int(dk_out.shape[1])
+        dev, st = self._packed(stream)
         D = self._desc
-        e = _DTYPES[D.dtype]
-        none = (None, 0)
+        d, T, kv = D.d, dq_out.shape[0], dk_out.shape[1]
+        sq, sk, e, f32 = (T, D.H, d), (T, kv, d), _DTYPES[D.dtype], _DTYPES[F32]
+        pgq, lgq = _rows(dq_out, sq, e, dev, "dq_out")
+        pgk, lgk = _rows(dk_out, sk, e, dev, "dk_out")
+        pq, lq = (None, 0) if q is None else _rows(q, sq, e, dev, "q")
+        pk, lk = (None, 0) if k is None else _rows(k, sk, e, dev, "k")
+        pdq, ldq = _rows(dq, sq, e, dev, "dq")
+        pdk, ldk = _rows(dk, sk, e, dev, "dk")
+        ws, nws = _room(workspace, dev)
         _check(load().k6attn_packed_norm_rope_backward(
-            self.h, T, kv, _vec(positions, 3 * T, "positions", "int32"),
-            *_rows(dq_out, T, D.H, D.d, e, "dq_out"), *_rows(dk_out, T, kv, D.d, e, "dk_out"),
-            *(none if q is None else _rows(q, T, D.H, D.d, e, "q")),
-            *(none if k is None else _rows(k, T, kv, D.d, e, "k")),
-            _vec(q_weight, D.d, "q_weight", "float32"), _vec(k_weight, D.d, "k_weight", "float32"), eps,
-            *_rows(dq, T, D.H, D.d, e, "dq"), *_rows(dk, T, kv, D.d, e, "dk"),
-            _vec(dq_weight, D.d, "dq_weight", "float32"), _vec(dk_weight, D.d, "dk_weight", "float32"),
-            *_room(workspace), _stream(stream)))
+            self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pgq, lgq, pgk, lgk, pq, lq, pk,
+            lk, _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, pdq, ldq, pdk,
+            ldk, _vec(dq_weight, d, f32, dev, "dq_weight"), _vec(dk_weight, d, f32, dev, "dk_weight"), ws, nws, st))
 
     def packed_plan(self, cu_q, cu_k, q_tokens, k_tokens, kv_heads, mask_block=0, stream=None) -> PackedPlan:
         """Plan attention over packed sequences: offsets cu_q, cu_k (int32, on the device; cu_k None = cu_q) into
         q_tokens and k_tokens rows.  mask_block 0: full, 1: causal, F: causal by frames of F tokens."""
-        import torch
-        b = PackedBatch(int(cu_q.shape[0]) - 1, int(kv_heads), int(mask_block), int(q_tokens), int(k_tokens))
+        torch = _torch_types()
+        b = PackedBatch(int(cu_q.numel()) - 1, int(kv_heads), int(mask_block), int(q_tokens), int(k_tokens))
         L = load()
         n = L.k6attn_packed_plan_bytes(self.h, ctypes.byref(b))
         if not n:
@@ -419,10 +433,10 @@ class Handle:
 
     def packed_replan(self, plan, cu_q, cu_k, stream=None):
         """Make the plan anew for other offsets of a batch of the same size (in place: captured calls see it)."""
-        n = plan.batch.n_seq + 1
-        _check(load().k6attn_packed_plan(self.h, plan.ref, _vec(cu_q, n, "cu_q", "int32"),
-                                         _vec(cu_k, n, "cu_k", "int32"), plan.ptr, plan.buffer.numel(),
-                                         _stream(stream)))
+        dev, st = self._packed(stream)
+        n, i32 = plan.batch.n_seq + 1, _DTYPES["int32"]
+        _check(load().k6attn_packed_plan(self.h, plan.ref, _vec(cu_q, n, i32, dev, "cu_q"),
+                                         _vec(cu_k, n, i32, dev, "cu_k"), plan.ptr, plan.buffer.numel(), st))
 
     def packed_workspace_bytes(self, plan) -> int:
         return load().k6attn_packed_workspace_bytes(self.h, plan.ref)
@@ -430,29 +444,38 @@ class Handle:
     def packed_forward(self, plan, q, k, v, out, lse=None, *, workspace=None, stream=None):
         """Attention of a planned batch: q [Tq][H][d], k, v [Tk][kv_heads][d] (q, k bf16 or fp16, v bf16) into
         out (bf16, as q) and lse (fp32 [H][Tq])."""
-        b = plan.batch
-        Tq, Tk, kv, H, d = b.q_tokens, b.k_tokens, b.kv_heads, self._desc.H, self._desc.d
-        qk = _code(q)
-        x = _DTYPES[qk] if qk in (BF16, F16) else "bfloat16"
+        dev, st = self._packed(stream)
+        b, D, bf = plan.batch, self._desc, _DTYPES[BF16]
+        sq, sk, x = (b.q_tokens, D.H, D.d), (b.k_tokens, b.kv_heads, D.d), q.dtype
+        pq, lq = _rows(q, sq, x, dev, "q")
+        pk, lk = _rows(k, sk, x, dev, "k")
+        pv, lv = _rows(v, sk, bf, dev, "v")
+        po, lo = _rows(out, sq, bf, dev, "out")
+        ws, nws = _room(workspace, dev)
         _check(load().k6attn_packed_forward(
-            self.h, plan.ref, plan.ptr, *_rows(q, Tq, H, d, x, "q"), *_rows(k, Tk, kv, d, x, "k"),
-            *_rows(v, Tk, kv, d, "bfloat16", "v"), qk, *_rows(out, Tq, H, d, "bfloat16", "out"),
-            _vec(lse, H * Tq, "lse", "float32"), *_room(workspace), _stream(stream)))
+            self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo,
+            _vec(lse, D.H * b.q_tokens, _DTYPES[F32], dev, "lse"), ws, nws, st))
 
     def packed_backward_workspace_bytes(self, plan) -> int:
         return load().k6attn_packed_backward_workspace_bytes(self.h, plan.ref)
 
     def packed_backward(self, plan, q, k, v, out, dout, lse, dq, dk, dv, *, workspace, stream=None):
         """Gradients dq, dk, dv (bf16) of packed_forward, from its out and lse and dout (bf16)."""
-        b = plan.batch
-        Tq, Tk, kv, H, d = b.q_tokens, b.k_tokens, b.kv_heads, self._desc.H, self._desc.d
-        qk, bf = _code(q), "bfloat16"
-        x = _DTYPES[qk] if qk in (BF16, F16) else bf
+        dev, st = self._packed(stream)
+        b, D, bf = plan.batch, self._desc, _DTYPES[BF16]
+        sq, sk, x = (b.q_tokens, D.H, D.d), (b.k_tokens, b.kv_heads, D.d), q.dtype
+        pq, lq = _rows(q, sq, x, dev, "q")
+        pk, lk = _rows(k, sk, x, dev, "k")
+        pv, lv = _rows(v, sk, bf, dev, "v")
+        po, lo = _rows(out, sq, bf, dev, "out")
+        pg, lg = _rows(dout, sq, bf, dev, "dout")
+        pdq, ldq = _rows(dq, sq, bf, dev, "dq")
+        pdk, ldk = _rows(dk, sk, bf, dev, "dk")
+        pdv, ldv = _rows(dv, sk, bf, dev, "dv")
+        ws, nws = _room(workspace, dev)
         _check(load().k6attn_packed_backward(
-            self.h, plan.ref, plan.ptr, *_rows(q, Tq, H, d, x, "q"), *_rows(k, Tk, kv, d, x, "k"),
-            *_rows(v, Tk, kv, d, bf, "v"), qk, *_rows(out, Tq, H, d, bf, "out"), *_rows(dout, Tq, H, d, bf, "dout"),
-            _vec(lse, H * Tq, "lse", "float32"), *_rows(dq, Tq, H, d, bf, "dq"), *_rows(dk, Tk, kv, d, bf, "dk"),
-            *_rows(dv, Tk, kv, d, bf, "dv"), *_room(workspace), _stream(stream)))
+            self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo, pg, lg,
+            _vec(lse, D.H * b.q_tokens, _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st))
 
     def sync(self, stream=None):
         _check(load().k6attn_sync(self.h, _stream(stream)))
