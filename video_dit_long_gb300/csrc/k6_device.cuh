@@ -35,6 +35,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 // before the one it follows.
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Let the next kernel of the stream, if it is launched with launch_after, place
+// its blocks from now on.
+__device__ __forceinline__ void launch_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {

@@ -15,20 +15,21 @@
 // whose keys are cut into several items leaves partials (fp32 O normalised, lse
 // in base 2) in the workspace, which packed_merge_kernel joins in key order.
 //
-// Roles in a CTA (384 threads), shared memory (Q tile, six 32 KB K/V slots)
-// and tensor memory (three S/P buffers, O) are those of attn_tc_single_kernel:
-//   warp 8   TMA: K and V tiles in the order K_0 K_1 V_0 K_2 V_1 ..., and the
-//            item's Q tile, which waits for the last S of the item before;
+// Roles in a CTA (512 threads), shared memory (two Q tiles, five 32 KB K/V slots)
+// and tensor memory (three S/P buffers, O) follow attn_tc_single_kernel:
+//   warp 8   TMA: the item's Q tile, then its K and V tiles in the order
+//            K_0 K_1 V_0 K_2 V_1 ...;
 //   warp 9   S(n) = Q K_n^T;   warp 10   O += P(n) V_n, and the zeroing of the
 //            rows of V behind the sequence's last key, where another
 //            sequence's rows or unwritten memory lie: P is zero there, but
 //            0 * NaN is not;
-//   warps 0-7  two softmax groups on alternate tiles, one thread a row.
-// Items overlap: warps 8-10 run ahead into the next item (its Q, first K/V tiles
-// and S are in place early), and only the softmax group that owns an item's last
-// tile runs its epilogue; the other one posts its row sums and goes on to the
-// next item's first tile, which is its own.  The epilogue takes O into registers
-// first and hands the accumulator back (o_free) before it scales and stores.
+//   warps 0-7  two softmax groups on alternate tiles, one thread a row;
+//   warps 12-15  the epilogue: joins the groups' row sums, takes O out of tensor
+//            memory (handing it back before storing), turns the rows in the
+//            item's Q buffer and stores them.
+// Items overlap: every role but the last runs on into the next item while the
+// epilogue finishes one.  (With the epilogue in the softmax groups an item cost
+// 3.4 us beyond its tiles: 1 warp a scheduler runs its serial code slowly.)
 // All waits are bounded (DEV_TIMEOUT), as in the other kernels.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,24 +44,29 @@ namespace pf {
 constexpr int D = 128, BM = 128, BN = 128;
 constexpr int PANEL = BM * 64 * 2;
 constexpr int TILE = 2 * PANEL;
-constexpr int NSTAGE = 6;                     // K/V slots: even, so that inside an item a slot keeps one kind
+// Five K/V slots and two Q buffers: the next item's Q is in place before the last S of this one.  (Six
+// slots and one Q buffer, as in the joint kernel, cost 3.2 us an item beyond its tiles: the next Q could
+// only be asked for when the last S had read the present one.)
+constexpr int NSTAGE = 5;
+constexpr int NQ = 2;
 constexpr int KAHEAD = 2;                     // K runs two tiles ahead of V
 constexpr int NSBUF = 3;                      // S/P buffers in tensor memory
 constexpr int P_PARTS = 2;
 constexpr int KP = BN / P_PARTS;
 constexpr int SMEM_Q = 0;
-constexpr int SMEM_KV = TILE;
+constexpr int SMEM_KV = NQ * TILE;
 constexpr int SMEM_BAR = SMEM_KV + NSTAGE * TILE;
-// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain, pv_buf [S buffer],
-// m_ready [tile parity][warp], epi [item parity][warp]
-constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 3 + NSBUF + 8 + 8;
+// q_full, q_empty [Q buffer], kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain,
+// posted, sums_free, pv_buf [S buffer], m_ready [tile parity][warp]
+constexpr int NBAR = 2 * NQ + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 5 + NSBUF + 8;
 constexpr int SMEM_XCH = (SMEM_BAR + NBAR * 8 + 8 + 15) & ~15;  // + TMEM address, abort flag
-constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) posted, of two items
+constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) of each group
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
-constexpr int THREADS = 384;
-// Register split (launch: 384 x 168 = 64512): 2*128*184 + 128*136 = 64512.
+constexpr int THREADS = 512;
+// Register split (launch: 512 x 128 = 65536): 2*128*184 + 128*64 + 128*80 = 65536.
 constexpr int REGS_SOFTMAX = 184;
-constexpr int REGS_CONTROL = 136;
+constexpr int REGS_CONTROL = 64;
+constexpr int REGS_EPILOGUE = 80;
 constexpr int TMEM_COLS = 512;
 constexpr int O_COL = NSBUF * BN;
 constexpr float RESCALE_THRESHOLD = 8.0f;     // log2 units: O is rescaled when the max grows past 2^8
@@ -76,6 +82,7 @@ struct PackedFwdParams {
     float *lse;                               // [H][Tq], or null
     float *part_o, *part_lse;                 // [partial][128][128], [partial][128]
     uint32_t idesc_qk;
+    uint32_t inv_g;                           // ceil(2^16 / G): (row * inv_g) >> 16 == row / G for row < 128
     unsigned long long wait_limit_ns;
     int *err;
 };
@@ -102,11 +109,12 @@ struct Walk {
     int slots;                        // partials that one slot number stands for (1, or one for every key head)
     __device__ Walk(const PackedPlan &plan, const PackedGeom &g) {
         list = plan.fwd;
+        const int mine = plan.count[blockIdx.x];  // beside the header: no wait between the two (the grid is g.sms)
         slots = plan.head->slot_step;
         if (plan.head->stream) {
             list += (long)blockIdx.x * g.cap_rows;
             n_items = units = 0;
-            rounds = blockIdx.x < (uint32_t)g.sms ? (uint32_t)plan.count[blockIdx.x] : 0;
+            rounds = (uint32_t)mine;
         } else {
             n_items = (uint32_t)plan.head->n_fwd;
             units = n_items * (uint32_t)g.Hkv;
@@ -132,6 +140,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                       const __grid_constant__ CUtensorMap tm_v, const PackedFwdParams p) {
     using namespace pf;
     extern __shared__ __align__(1024) uint8_t smem[];
+    launch_next_kernel();
+    wait_previous_kernel();
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
         if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_LAYOUT);
@@ -145,24 +155,27 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     if (walk.rounds == 0) return;
 
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
-    uint64_t *q_empty = q_full + 1;
-    uint64_t *kv_full = q_empty + 1;
+    uint64_t *q_empty = q_full + NQ;
+    uint64_t *kv_full = q_empty + NQ;
     uint64_t *kv_empty = kv_full + NSTAGE;
     uint64_t *s_full = kv_empty + NSTAGE;
     uint64_t *p_part = s_full + NSBUF;     // [S buffer][part], 128 arrivals each
     uint64_t *o_final = p_part + NSBUF * P_PARTS;
     uint64_t *o_free = o_final + 1;        // the epilogue has O in registers (128 arrivals)
     uint64_t *drain = o_free + 1;
-    uint64_t *pv_buf = drain + 1;          // [S buffer]: P.V of the tile in that buffer done
+    uint64_t *posted = drain + 1;          // both softmax groups posted an item's (l, m)
+    uint64_t *sums_free = posted + 1;      // the epilogue has read them
+    uint64_t *pv_buf = sums_free + 1;      // [S buffer]: P.V of the tile in that buffer done
     uint64_t *m_ready = pv_buf + NSBUF;    // [tile parity][warp % 4]: row max after the tile published
-    uint64_t *epi = m_ready + 8;           // [item parity][warp % 4]: the group that left posted its (l, m)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(epi + 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(m_ready + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        for (int b = 0; b < NQ; b++) {
+            mbar_init(&q_full[b], 1);
+            mbar_init(&q_empty[b], BM);  // the epilogue, which stages the output in the Q buffer, frees it
+        }
         for (int s = 0; s < NSTAGE; s++) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -175,10 +188,9 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         mbar_init(o_final, 1);
         mbar_init(o_free, BM);
         mbar_init(drain, 2);  // one commit per MMA issuer
-        for (int q = 0; q < 8; q++) {
-            mbar_init(&m_ready[q], 32);
-            mbar_init(&epi[q], 32);
-        }
+        mbar_init(posted, 2 * BM);
+        mbar_init(sums_free, BM);
+        for (int q = 0; q < 8; q++) mbar_init(&m_ready[q], 32);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -192,7 +204,10 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
 
-    if (warp >= 8) {
+    float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
+    float *xe = xm + BM;                                      // [group][row][l, m]
+
+    if (warp >= 8 && warp < 12) {
         regs_decrease<REGS_CONTROL>();
         if (warp == 8) {
             // -------------------------------------------------- TMA producer
@@ -224,20 +239,22 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                     kv_idx++;
                     return true;
                 };
-                // Q once the last S of the item before has read its tile; ahead of the first K tiles, since
-                // the slot of K_1 may hold a V that is only freed at this item's first S
-                if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) break;
+                // Q ahead of the first K tiles, since the slot of K_1 may hold a V that is only freed at this
+                // item's first S; its buffer is free once the item before the last has stored its output from it
+                const uint32_t qb = uc % NQ;
+                if (!(ok = mbar_wait_w(&q_empty[qb], ((uc / NQ) & 1) ^ 1, w))) break;
                 if (leader) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)p.g.rows * 256u);
-                    tma_load_4d(smem + SMEM_Q, &tm_q, q_full, 0, hk * p.g.G, it.tok0, 0);
-                    tma_load_4d(smem + SMEM_Q + PANEL, &tm_q, q_full, 64, hk * p.g.G, it.tok0, 0);
+                    uint8_t *dst = smem + SMEM_Q + qb * TILE;
+                    mbar_arrive_expect_tx(&q_full[qb], (uint32_t)p.g.rows * 256u);
+                    tma_load_4d(dst, &tm_q, &q_full[qb], 0, hk * p.g.G, it.tok0, 0);
+                    tma_load_4d(dst + PANEL, &tm_q, &q_full[qb], 64, hk * p.g.G, it.tok0, 0);
                 }
                 uc++;
                 for (int t = 0; t < KAHEAD && t < T && ok; t++) ok = load(&tm_k, t);
                 for (int j = 0; j < T && ok; j++) ok = load(&tm_v, j) && (j + KAHEAD >= T || load(&tm_k, j + KAHEAD));
             }
             // every copy issued lands before the CTA can exit
-            if (uc > 0) mbar_drain(q_full, (uc - 1) & 1, DRAIN_NS);
+            for (uint32_t i = uc > NQ ? uc - NQ : 0; i < uc; i++) mbar_drain(&q_full[i % NQ], (i / NQ) & 1, DRAIN_NS);
             for (uint32_t idx = kv_idx > NSTAGE ? kv_idx - NSTAGE : 0; idx < kv_idx; idx++)
                 mbar_drain(&kv_full[idx % NSTAGE], (idx / NSTAGE) & 1, DRAIN_NS);
         } else if (warp == 9 || warp == 10) {
@@ -258,7 +275,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 const int T = it.kt1 - it.kt0;
                 if (T <= 0) continue;
                 if (warp == 9) {
-                    ok = mbar_wait_w(q_full, uc & 1, w);
+                    ok = mbar_wait_w(&q_full[uc % NQ], (uc / NQ) & 1, w);
+                    const uint64_t qd = dq0 + ((uint64_t)((uc % NQ) * TILE) >> 4);
                     for (int t = 0; t < T && ok; t++) {
                         const uint32_t n = tile + t;
                         const uint32_t kidx = kv_idx + k_load_at(t);
@@ -273,11 +291,10 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; kk++) {
                             const uint64_t off = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
-                            mma_ss_w(tmem + (n % NSBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
+                            mma_ss_w(tmem + (n % NSBUF) * BN, qd + off, kb + off, p.idesc_qk, kk > 0);
                         }
                         tc_commit_w(&s_full[n % NSBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
                     }
-                    if (ok) tc_commit_w(q_empty);
                 } else {
                     for (int j = 0; j < T && ok; j++) {
                         const uint32_t n = tile + j;
@@ -319,42 +336,130 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             mbar_drain(drain, 0, DRAIN_NS);
         }
         __syncwarp();
+    } else if (warp >= 12) {
+        regs_decrease<REGS_EPILOGUE>();
+        // ------------------------------------ epilogue (thread = row = TMEM lane)
+        const int wq = warp % 4;
+        const int r = 32 * wq + lane;
+        const int rtok = r / p.g.G, rhead = r - rtok * p.g.G;  // this row's token of a tile and head of a group
+        const uint32_t tO = tmem + ((uint32_t)(32 * wq) << 16) + O_COL;
+        // the row that this lane stores first (16 lanes a row), and its place in a tile
+        const int srow = 32 * wq + lane / 16;
+        const int stok = srow / p.g.G, shead = srow - stok * p.g.G;
+        uint32_t n_epi = 0;
+        bool ok = true;
+        for (uint32_t k = 0; k < walk.rounds && ok; k++) {
+            PackedItem it;
+            int hk;
+            if (!walk.at(k, it, hk)) continue;
+            const int n_tok = it.n_tok_hk & 255;
+            const bool live = rtok < n_tok && r < p.g.rows;
+            float *lse = p.lse ? p.lse + (long)(hk * p.g.G + rhead) * p.g.Tq + it.tok0 + rtok : nullptr;
+            if (it.kt1 <= it.kt0) {  // no key is seen by any row of the tile
+                if (live) {
+                    __nv_bfloat16 *dst =
+                        p.out + ((long)it.tok0 + rtok) * p.out_stride + (long)(hk * p.g.G + rhead) * D;
+#pragma unroll
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
+                    if (lse) *lse = -INFINITY;
+                }
+                continue;
+            }
+            if (!(ok = mbar_wait(posted, n_epi & 1, w))) break;
+            const float l0 = xe[r * 2], m0 = xe[r * 2 + 1], l1 = xe[(BM + r) * 2], m1 = xe[(BM + r) * 2 + 1];
+            mbar_arrive(sums_free);
+            const float m_fin = fmaxf(m0, m1);  // the max O is expressed in
+            const float l_tot = l0 * ex2_from(m0, m_fin) + l1 * ex2_from(m1, m_fin);
+            const bool none = l_tot == 0.f;  // the row sees nothing
+            const float inv = none ? 0.f : 1.f / l_tot;
+            const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
+            if (!(ok = mbar_wait(o_final, n_epi & 1, w))) break;
+            tc_fence_after();
+            // A thread holds a row; 32 lanes storing to 32 rows at a time would be slow.  The warp turns its
+            // rows in its part of the item's Q buffer (S is done with it) and stores whole rows, 16 lanes a
+            // row; 16-byte chunks swizzled against bank conflicts.  A partial is stored in two halves of 64
+            // fp32 columns.
+            uint8_t *mine = smem + SMEM_Q + (n_epi % NQ) * TILE + wq * 32 * 256;
+            auto chunk = [&](int row, int c) {
+                return reinterpret_cast<uint4 *>(mine + row * 256 + (((c & 8) | ((c ^ row) & 7)) << 4));
+            };
+            const bool part = it.slot >= 0;
+            const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM;
+            // two rows a step: (tok, head) of the row, and its offset in `dst`
+            auto store = [&](char *dst, long tok_bytes, int head_bytes) {
+                __syncwarp();
+                int tk = stok, hd = shead;
+                char *d = dst + stok * tok_bytes + shead * head_bytes + (lane % 16) * 16;
+#pragma unroll 8
+                for (int i = 0; i < 16; i++) {
+                    const uint4 u = *chunk(2 * i + lane / 16, lane % 16);
+                    if (tk < n_tok && srow + 2 * i < p.g.rows) *reinterpret_cast<uint4 *>(d) = u;
+                    hd += 2, d += 2 * head_bytes;
+                    while (hd >= p.g.G) hd -= p.g.G, tk++, d += tok_bytes - p.g.G * head_bytes;
+                }
+                __syncwarp();
+            };
+#pragma unroll
+            for (int cc = 0; cc < D / 32; cc++) {
+                uint32_t o[32];
+                tmem_ld32(tO + cc * 32, o);
+                tmem_ld_wait();
+                if (cc + 1 == D / 32) {  // O is out of tensor memory
+                    tc_fence_before();
+                    mbar_arrive(o_free);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c++) o[c] = none ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+                if (part) {
+#pragma unroll
+                    for (int c = 0; c < 8; c++)
+                        *chunk(lane, (cc & 1) * 8 + c) = make_uint4(o[c * 4], o[c * 4 + 1], o[c * 4 + 2], o[c * 4 + 3]);
+                    if (cc & 1)
+                        store(reinterpret_cast<char *>(p.part_o + prow * D) + (cc >> 1) * 256, p.g.G * (long)(D * 4), D * 4);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        auto two = [&](int i) {
+                            return pack_bf16x2(__uint_as_float(o[c * 8 + i]), __uint_as_float(o[c * 8 + i + 1]));
+                        };
+                        *chunk(lane, cc * 4 + c) = make_uint4(two(0), two(2), two(4), two(6));
+                    }
+                }
+            }
+            if (!part)
+                store(reinterpret_cast<char *>(p.out + (long)it.tok0 * p.out_stride + (long)hk * p.g.G * D),
+                      p.out_stride * 2, D * 2);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next Q lands there
+            mbar_arrive(&q_empty[n_epi % NQ]);
+            if (live) {
+                if (part) p.part_lse[prow + r] = lse2;
+                else if (lse) *lse = lse2 * 0.69314718055994531f;
+            }
+            n_epi++;
+        }
     } else {
         regs_increase<REGS_SOFTMAX>();
-        // ------------------------------------ softmax / epilogue (group hf)
+        // ------------------------------------ softmax (group hf)
         // Group hf takes the tiles n with n % 2 == hf, whole rows (thread = row =
         // TMEM lane).  The groups share the row's running max through shared
         // memory (m_ready); O is rescaled in tensor memory only when a tile's max
         // exceeds it by 2^8.  Each group keeps the row sum of its own tiles, in
-        // the max it last saw; the epilogue combines the two.
+        // the max it last saw, and posts it for the epilogue.
         const int hf = warp / 4, wq = warp % 4;
         const int r = threadIdx.x % BM;
-        const int rtok = r / p.g.G, rhead = r % p.g.G;  // this row's token of a tile and head of a group
+        const int rtok = r / p.g.G;  // this row's token of a tile
         const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tO = lane_base + O_COL;
-        float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
-        float *xe = xm + BM;                                      // [item parity][row][l, m]
         const float sl2 = p.scale_log2;
-        uint32_t tile = 0, n_epi = 0, kv_idx = 0;
+        uint32_t tile = 0, n_item = 0, kv_idx = 0;
         bool ok = true;
         for (uint32_t k = 0; k < walk.rounds && ok; k++) {
             PackedItem it;
             int hk;
             if (!walk.at(k, it, hk)) continue;
             const int T = it.kt1 - it.kt0;
+            if (T <= 0) continue;
             const bool live = rtok < (it.n_tok_hk & 255) && r < p.g.rows;
-            const long tok = (long)it.tok0 + (live ? rtok : 0);
-            const int head = hk * p.g.G + rhead;
-            __nv_bfloat16 *orow = p.out + tok * p.out_stride + (long)head * D;
-            if (T <= 0) {  // no key is seen by any row of the tile
-                if (live) {
-#pragma unroll
-                    for (int c = 0; c < D / 2; c += 8)
-                        *reinterpret_cast<uint4 *>(orow + hf * (D / 2) + c) = make_uint4(0, 0, 0, 0);
-                    if (p.lse && hf == 0) p.lse[(long)head * p.g.Tq + tok] = -INFINITY;
-                }
-                continue;
-            }
             // keys this row sees; rows past the tile's tokens see what the sequence has (their results are dropped)
             const int lim = live ? packed_limit(it.pos0 + rtok, it.Lk, p.g.block) : it.Lk;
             float m_run = -INFINITY;  // the row max in force after the latest tile
@@ -462,56 +567,15 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 l_own += (a0 + a1) + (b0 + b1);
             }
             if (!ok) break;
-            const uint32_t last = tile + T - 1, buf = n_epi & 1;
-            float *x = xe + (buf * BM + r) * 2;
-            uint64_t *posted = &epi[buf * 4 + wq];
-            if ((int)(last & 1) != hf) {
-                // the other group finishes the item.  Two items' posts are kept: this group cannot be two
-                // ahead of that epilogue, since each item's tiles but the first need the other's maxima.
-                x[0] = l_own, x[1] = m_own;
-                mbar_arrive(posted);
-            } else {
-                if (!mbar_wait(posted, (n_epi >> 1) & 1, w) || !mbar_wait(o_final, n_epi & 1, w)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint32_t o[D];
-#pragma unroll
-                for (int cc = 0; cc < D / 32; cc++)
-                    tmem_ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
-                tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(o_free);
-                const float l_oth = x[0], m_oth = x[1];
-                const float m_fin = fmaxf(m_own, m_oth);  // the max O is expressed in
-                const float l_tot = l_own * ex2_from(m_own, m_fin) + l_oth * ex2_from(m_oth, m_fin);
-                const bool none = l_tot == 0.f;
-                const float inv = none ? 0.f : 1.f / l_tot;
-                const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
-                if (live) {
-#pragma unroll
-                    for (int c = 0; c < D; c++) o[c] = none ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
-                    if (it.slot >= 0) {
-                        const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM + r;
-                        float *dst = p.part_o + prow * D;
-#pragma unroll
-                        for (int c = 0; c < D; c += 4)
-                            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-                        p.part_lse[prow] = lse2;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < D; c += 8) {
-                            auto two = [&](int i) {
-                                return pack_bf16x2(__uint_as_float(o[c + i]), __uint_as_float(o[c + i + 1]));
-                            };
-                            *reinterpret_cast<uint4 *>(orow + c) = make_uint4(two(0), two(2), two(4), two(6));
-                        }
-                        if (p.lse) p.lse[(long)head * p.g.Tq + tok] = lse2 * 0.69314718055994531f;
-                    }
-                }
+            // post the row sum of this group's tiles, once the epilogue has read the item before's
+            if (n_item > 0 && !mbar_wait(sums_free, (n_item - 1) & 1, w)) {
+                ok = false;
+                break;
             }
-            n_epi++;
+            xe[(hf * BM + r) * 2] = l_own;
+            xe[(hf * BM + r) * 2 + 1] = m_own;
+            mbar_arrive(posted);
+            n_item++;
             tile += T;
             kv_idx += 2 * T;
         }
@@ -527,25 +591,22 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 // Joins the partials of the split tiles: one warp per row of a split tile,
 //   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
 __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams p) {
+    launch_next_kernel();
     wait_previous_kernel();
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
-    if (!packed_plan_ok(*plan.head, p.g)) return;  // the attention kernel reported it
     const int lane = threadIdx.x & 31;
     const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const uint32_t mi = x / (uint32_t)p.g.rows;
     const int r = (int)(x - mi * (uint32_t)p.g.rows);
-    if (mi >= (uint32_t)plan.head->n_merge) return;
-    const PackedMerge m = plan.merge[mi];
+    if (mi >= (uint32_t)p.g.cap_merge) return;
+    const PackedMerge m = plan.merge[mi];  // beside the header: no wait between the two
+    const PackedHeader head = *plan.head;
+    if (!packed_plan_ok(head, p.g) || mi >= (uint32_t)head.n_merge) return;  // the attention kernel reported a bad plan
     if (r / p.g.G >= (m.n_tok_hk & 255)) return;
-    const long base = (long)m.slot0 * 128 + r, step = (long)plan.head->slot_step * 128;
+    const long base = (long)m.slot0 * 128 + r, step = (long)head.slot_step * 128;
     constexpr int kU = 8;  // partials in flight
-    float top = -INFINITY;
-    for (int c = lane; c < m.n; c += 32) top = fmaxf(top, p.part_lse[base + c * step]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
+    float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
     for (int c = 0; c < m.n; c += kU) {
         float4 o[kU];
         float l[kU];
@@ -557,6 +618,14 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
                 o[i] = reinterpret_cast<const float4 *>(p.part_o + (base + (c + i) * step) * 128)[lane];
             }
         }
+        float m_new = top;
+#pragma unroll
+        for (int i = 0; i < kU; i++) m_new = fmaxf(m_new, l[i]);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float old = ex2(top - ref);  // 0 from -inf
+        top = m_new;
+        sum *= old;
+        acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
 #pragma unroll
         for (int i = 0; i < kU; i++) {
             const float f = ex2(l[i] - ref);
@@ -567,11 +636,11 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long tok = (long)m.tok0 + r / p.g.G;
-    const int head = (m.n_tok_hk >> 8) * p.g.G + r % p.g.G;
-    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head * 128 + lane * 4) =
+    const int head_q = (m.n_tok_hk >> 8) * p.g.G + r % p.g.G;
+    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head_q * 128 + lane * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0 && p.lse)
-        p.lse[(long)head * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+        p.lse[(long)head_q * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -605,10 +674,10 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     // Q.K^T operands: bf16 (A/B format 1) or fp16 (format 0)
     p.idesc_qk = idesc_bf16_f32(128, 128, false);
     if (t.qk_f16) p.idesc_qk &= ~((7u << 7) | (7u << 10));
+    p.inv_g = (65536u + (uint32_t)g.G - 1) / (uint32_t)g.G;
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
-    packed_fwd_kernel<<<(unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st>>>(mq, mk, mv, p);
-    e = cudaGetLastError();
+    e = launch_after(packed_fwd_kernel, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
     if (e != cudaSuccess || g.extra == 0) return e;
     return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 7) / 8), 256, 0, st, p);
 }

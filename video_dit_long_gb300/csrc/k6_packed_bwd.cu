@@ -55,6 +55,7 @@ struct PackedBwdParams {
     long dq_stride, dk_stride, dv_stride;
     uint32_t idesc_qk, idesc_bf16, idesc_bf16_mn, idesc_ds_mn;
     int ds_f16;
+    uint32_t inv_g;                         // ceil(2^16 / G): (row * inv_g) >> 16 == row / G for row < 128
     unsigned long long wait_limit_ns;
     int *err;
 };
@@ -277,25 +278,34 @@ __device__ __forceinline__ void mma_k(uint32_t d, uint64_t a, uint64_t b, uint32
     mma_ss_w(d, a + off, b + off, idesc, kk > 0);
 }
 
-// 64 columns of this thread's TMEM lane, times `scale`, as bf16 to dst (null: read only).
-__device__ __forceinline__ void store_half_row(uint32_t taddr, __nv_bfloat16 *dst, float scale) {
+// 64 columns of this warp's 32 TMEM lanes (rows), times `scale`, as bf16: row i
+// of the warp goes to dst(i) (null: not stored).  The warp turns its rows in
+// `mine` (4 KB of shared memory that no MMA or copy uses any more) so that eight
+// lanes store a row's 128 bytes, instead of 32 lanes 32 rows.
+template <typename Dst>
+__device__ __forceinline__ void store_rows(uint32_t taddr, uint8_t *mine, int lane, float scale, Dst dst) {
+    auto chunk = [&](int row, int c) { return reinterpret_cast<uint4 *>(mine + row * 128 + (((c ^ row) & 7) << 4)); };
 #pragma unroll
-    for (int c = 0; c < 2; c++) {
+    for (int h = 0; h < 2; h++) {
         uint32_t o[32];
-        tmem_ld32(taddr + c * 32, o);
+        tmem_ld32(taddr + h * 32, o);
         tmem_ld_wait();
-        if (dst) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                uint4 u;
-                u.x = pack_bf16x2(__uint_as_float(o[k]) * scale, __uint_as_float(o[k + 1]) * scale);
-                u.y = pack_bf16x2(__uint_as_float(o[k + 2]) * scale, __uint_as_float(o[k + 3]) * scale);
-                u.z = pack_bf16x2(__uint_as_float(o[k + 4]) * scale, __uint_as_float(o[k + 5]) * scale);
-                u.w = pack_bf16x2(__uint_as_float(o[k + 6]) * scale, __uint_as_float(o[k + 7]) * scale);
-                *reinterpret_cast<uint4 *>(dst + c * 32 + k) = u;
-            }
+        for (int c = 0; c < 4; c++) {
+            auto two = [&](int i) {
+                return pack_bf16x2(__uint_as_float(o[c * 8 + i]) * scale, __uint_as_float(o[c * 8 + i + 1]) * scale);
+            };
+            *chunk(lane, h * 4 + c) = make_uint4(two(0), two(2), two(4), two(6));
         }
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int row = 4 * i + lane / 8;
+        __nv_bfloat16 *d = dst(row);
+        if (d) *reinterpret_cast<uint4 *>(d + (lane % 8) * 8) = *chunk(row, lane % 8);
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void zero_half_row(__nv_bfloat16 *dst) {
@@ -461,7 +471,13 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         }
         if (ok && mbar_wait(bar + ACC, 0, w)) {
             tc_fence_after();
-            store_half_row(lb + 256 + 64 * g, live ? drow : nullptr, p.scale * exp2f((float)-e));
+            store_rows(lb + 256 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), [&](int i) {
+                const int rr = 32 * q4 + i;
+                const int tk = (int)(((uint32_t)rr * p.inv_g) >> 16);  // rr / G
+                return tk < it.n_tok_hk && rr < p.g.rows
+                           ? p.dq + ((long)it.tok0 + tk) * p.dq_stride + (long)(hk * p.g.G + rr - tk * p.g.G) * D + 64 * g
+                           : nullptr;
+            });
         }
     }
     teardown(tmem);
@@ -745,8 +761,14 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         }
         if (ok && mbar_wait(bar + ACC, 0, w)) {
             tc_fence_after();
-            store_half_row(lb + 384 + 64 * g, live ? krow : nullptr, p.scale * exp2f((float)-e));
-            store_half_row(lb + 256 + 64 * g, live ? vrow : nullptr, 1.0f);
+            auto row_of = [&](__nv_bfloat16 *base, long stride) {
+                return [=](int i) {
+                    const int rr = 32 * q4 + i;
+                    return rr < it.n_key ? base + ((long)it.krow0 + rr) * stride + (long)hk * D + 64 * g : nullptr;
+                };
+            };
+            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), row_of(p.dk, p.dk_stride));
+            store_rows(lb + 256 + 64 * g, smem + warp * 4096, lane, 1.0f, row_of(p.dv, p.dv_stride));
         }
     }
     teardown(tmem);
@@ -840,6 +862,7 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     p.idesc_bf16_mn = bf16 | (1u << 16);                   // dV += P^T dO
     p.idesc_ds_mn = (t.qk_f16 ? f16 : bf16) | (1u << 16);  // dQ += dS K, dK += dS^T Q
     p.ds_f16 = t.qk_f16 ? 1 : 0;
+    p.inv_g = (65536u + (uint32_t)g.G - 1) / (uint32_t)g.G;
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
     p.dkv_blocks = g.Tk ? (uint32_t)((long)g.cap_k * g.Hkv) : 0;
