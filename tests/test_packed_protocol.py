@@ -1,11 +1,11 @@
 """Host-side model of the waits of the packed attention kernel
 (k6_packed_attn.cu): a persistent CTA that runs one item after another, the K/V
-ring of the joint kernel (modelled in test_ring_protocol.py; five slots here)
-carried from item to item, and two Q buffers that the items take in turn.
+ring of the joint kernel (modelled in test_ring_protocol.py) carried from item
+to item, and one Q buffer that an item's first S waits for.
 
 Added to that model, in program order:
-- the producer issues an item's Q before its first K, once the item two before
-  has stored its output, which it stages in that Q buffer;
+- the producer issues an item's Q before its first K, once the last S of the
+  item before is done;
 - the first S of an item waits for its Q;
 - each softmax group posts its row sums after its last tile of an item, once the
   epilogue has read those of the item before, and goes on at once;
@@ -17,20 +17,17 @@ someone, no wait cycle, no wait that an earlier phase of its slot could match.
 """
 import itertools
 
-from .test_ring_protocol import acyclic, ancestors, model
-
-NSTAGE, NQ = 5, 2   # the kernel's ring slots and Q buffers
+from .test_ring_protocol import NSTAGE, acyclic, ancestors, model
 
 CASES = [list(Ts) for k in range(1, 5) for Ts in itertools.product((1, 2, 3, 4, 5, 7), repeat=k)] + \
     [[1] * 12, [2] * 9, [3] * 7, [17, 1, 17], [1, 2, 1, 2, 1, 2, 1], [6, 6, 6, 6]]
 
 
-def packed_model(Ts, q_first=True, nq=NQ):
-    loads, idx, deps, consumer, N = model(Ts, 2, NSTAGE)
-    first, firsts = 0, []
+def packed_model(Ts, q_first=True):
+    loads, idx, deps, consumer, N = model(Ts, 2)
+    first = 0
     for u, T in enumerate(Ts):
         last = first + T - 1
-        firsts.append(first)
         deps[("S_release", first)].add(("Q", u))  # waited for before anything else of the item
         deps[("stored", u)].add(("read_O", u))
         # tile n belongs to group n % 2; a group without a tile of the item posts all the same
@@ -47,8 +44,7 @@ def packed_model(Ts, q_first=True, nq=NQ):
             deps[("read_sums", u)].add(("stored", u - 1))
         deps[("read_O", u)] |= {("PV_done", last), ("read_sums", u)}
         if u:
-            if u >= nq:
-                deps[("Q", u)].add(("stored", u - nq))
+            deps[("Q", u)].add(("S", first - 1))
             prev = max(idx[("K", first - 1)], idx[("V", first - 1)])
             if q_first:
                 deps[("Q", u)].add(("load", prev))

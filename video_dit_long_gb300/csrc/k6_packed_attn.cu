@@ -15,7 +15,7 @@
 // whose keys are cut into several items leaves partials (fp32 O normalised, lse
 // in base 2) in the workspace, which packed_merge_kernel joins in key order.
 //
-// Roles in a CTA (512 threads), shared memory (two Q tiles, five 32 KB K/V slots)
+// Roles in a CTA (512 threads), shared memory (Q tile, six 32 KB K/V slots)
 // and tensor memory (three S/P buffers, O) follow attn_tc_single_kernel:
 //   warp 8   TMA: the item's Q tile, then its K and V tiles in the order
 //            K_0 K_1 V_0 K_2 V_1 ...;
@@ -25,8 +25,7 @@
 //            0 * NaN is not;
 //   warps 0-7  two softmax groups on alternate tiles, one thread a row;
 //   warps 12-15  the epilogue: joins the groups' row sums, takes O out of tensor
-//            memory (handing it back before storing), turns the rows in the
-//            item's Q buffer and stores them.
+//            memory (handing it back before storing) and stores it.
 // Items overlap: every role but the last runs on into the next item while the
 // epilogue finishes one.  (With the epilogue in the softmax groups an item cost
 // 3.4 us beyond its tiles: 1 warp a scheduler runs its serial code slowly.)
@@ -44,29 +43,28 @@ namespace pf {
 constexpr int D = 128, BM = 128, BN = 128;
 constexpr int PANEL = BM * 64 * 2;
 constexpr int TILE = 2 * PANEL;
-// Five K/V slots and two Q buffers: the next item's Q is in place before the last S of this one.  (Six
-// slots and one Q buffer, as in the joint kernel, cost 3.2 us an item beyond its tiles: the next Q could
-// only be asked for when the last S had read the present one.)
-constexpr int NSTAGE = 5;
-constexpr int NQ = 2;
+// Six K/V slots: K(n) takes K(n-3)'s slot, whose release is two tiles back.  (With five, and a second Q buffer
+// in the sixth's place, K(n) waited for V(n-4): its load was only asked for at S(n-1), and the load's 1,000 to
+// 1,500 cycles set the pace, 1,550 cycles a tile.)
+constexpr int NSTAGE = 6;
 constexpr int KAHEAD = 2;                     // K runs two tiles ahead of V
 constexpr int NSBUF = 3;                      // S/P buffers in tensor memory
 constexpr int P_PARTS = 2;
 constexpr int KP = BN / P_PARTS;
 constexpr int SMEM_Q = 0;
-constexpr int SMEM_KV = NQ * TILE;
+constexpr int SMEM_KV = TILE;
 constexpr int SMEM_BAR = SMEM_KV + NSTAGE * TILE;
-// q_full, q_empty [Q buffer], kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain,
+// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain,
 // posted, sums_free, pv_buf [S buffer], m_ready [tile parity][warp]
-constexpr int NBAR = 2 * NQ + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 5 + NSBUF + 8;
+constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 5 + NSBUF + 8;
 constexpr int SMEM_XCH = (SMEM_BAR + NBAR * 8 + 8 + 15) & ~15;  // + TMEM address, abort flag
 constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) of each group
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
 constexpr int THREADS = 512;
-// Register split (launch: 512 x 128 = 65536): 2*128*184 + 128*64 + 128*80 = 65536.
-constexpr int REGS_SOFTMAX = 184;
+// Register split (launch: 512 x 128 = 65536): 2*128*176 + 128*64 + 128*96 = 65536.
+constexpr int REGS_SOFTMAX = 176;
 constexpr int REGS_CONTROL = 64;
-constexpr int REGS_EPILOGUE = 80;
+constexpr int REGS_EPILOGUE = 96;
 constexpr int TMEM_COLS = 512;
 constexpr int O_COL = NSBUF * BN;
 constexpr float RESCALE_THRESHOLD = 8.0f;     // log2 units: O is rescaled when the max grows past 2^8
@@ -82,7 +80,7 @@ struct PackedFwdParams {
     float *lse;                               // [H][Tq], or null
     float *part_o, *part_lse;                 // [partial][128][128], [partial][128]
     uint32_t idesc_qk;
-    uint32_t inv_g;                           // ceil(2^16 / G): (row * inv_g) >> 16 == row / G for row < 128
+    int wide;                                 // rows of out are 32-byte aligned
     unsigned long long wait_limit_ns;
     int *err;
 };
@@ -135,6 +133,13 @@ struct Walk {
     }
 };
 
+// 32 bytes in one store.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 __global__ void __launch_bounds__(pf::THREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PackedFwdParams p) {
@@ -155,8 +160,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     if (walk.rounds == 0) return;
 
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
-    uint64_t *q_empty = q_full + NQ;
-    uint64_t *kv_full = q_empty + NQ;
+    uint64_t *q_empty = q_full + 1;
+    uint64_t *kv_full = q_empty + 1;
     uint64_t *kv_empty = kv_full + NSTAGE;
     uint64_t *s_full = kv_empty + NSTAGE;
     uint64_t *p_part = s_full + NSBUF;     // [S buffer][part], 128 arrivals each
@@ -172,10 +177,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
-        for (int b = 0; b < NQ; b++) {
-            mbar_init(&q_full[b], 1);
-            mbar_init(&q_empty[b], BM);  // the epilogue, which stages the output in the Q buffer, frees it
-        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int s = 0; s < NSTAGE; s++) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -239,22 +242,20 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                     kv_idx++;
                     return true;
                 };
-                // Q ahead of the first K tiles, since the slot of K_1 may hold a V that is only freed at this
-                // item's first S; its buffer is free once the item before the last has stored its output from it
-                const uint32_t qb = uc % NQ;
-                if (!(ok = mbar_wait_w(&q_empty[qb], ((uc / NQ) & 1) ^ 1, w))) break;
+                // Q once the last S of the item before has read its tile; ahead of the first K tiles, since
+                // the slot of K_1 may hold a V that is only freed at this item's first S
+                if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) break;
                 if (leader) {
-                    uint8_t *dst = smem + SMEM_Q + qb * TILE;
-                    mbar_arrive_expect_tx(&q_full[qb], (uint32_t)p.g.rows * 256u);
-                    tma_load_4d(dst, &tm_q, &q_full[qb], 0, hk * p.g.G, it.tok0, 0);
-                    tma_load_4d(dst + PANEL, &tm_q, &q_full[qb], 64, hk * p.g.G, it.tok0, 0);
+                    mbar_arrive_expect_tx(q_full, (uint32_t)p.g.rows * 256u);
+                    tma_load_4d(smem + SMEM_Q, &tm_q, q_full, 0, hk * p.g.G, it.tok0, 0);
+                    tma_load_4d(smem + SMEM_Q + PANEL, &tm_q, q_full, 64, hk * p.g.G, it.tok0, 0);
                 }
                 uc++;
                 for (int t = 0; t < KAHEAD && t < T && ok; t++) ok = load(&tm_k, t);
                 for (int j = 0; j < T && ok; j++) ok = load(&tm_v, j) && (j + KAHEAD >= T || load(&tm_k, j + KAHEAD));
             }
             // every copy issued lands before the CTA can exit
-            for (uint32_t i = uc > NQ ? uc - NQ : 0; i < uc; i++) mbar_drain(&q_full[i % NQ], (i / NQ) & 1, DRAIN_NS);
+            if (uc > 0) mbar_drain(q_full, (uc - 1) & 1, DRAIN_NS);
             for (uint32_t idx = kv_idx > NSTAGE ? kv_idx - NSTAGE : 0; idx < kv_idx; idx++)
                 mbar_drain(&kv_full[idx % NSTAGE], (idx / NSTAGE) & 1, DRAIN_NS);
         } else if (warp == 9 || warp == 10) {
@@ -275,8 +276,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 const int T = it.kt1 - it.kt0;
                 if (T <= 0) continue;
                 if (warp == 9) {
-                    ok = mbar_wait_w(&q_full[uc % NQ], (uc / NQ) & 1, w);
-                    const uint64_t qd = dq0 + ((uint64_t)((uc % NQ) * TILE) >> 4);
+                    ok = mbar_wait_w(q_full, uc & 1, w);
                     for (int t = 0; t < T && ok; t++) {
                         const uint32_t n = tile + t;
                         const uint32_t kidx = kv_idx + k_load_at(t);
@@ -291,10 +291,11 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; kk++) {
                             const uint64_t off = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
-                            mma_ss_w(tmem + (n % NSBUF) * BN, qd + off, kb + off, p.idesc_qk, kk > 0);
+                            mma_ss_w(tmem + (n % NSBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
                         }
                         tc_commit_w(&s_full[n % NSBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
                     }
+                    if (ok) tc_commit_w(q_empty);
                 } else {
                     for (int j = 0; j < T && ok; j++) {
                         const uint32_t n = tile + j;
@@ -343,9 +344,6 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         const int r = 32 * wq + lane;
         const int rtok = r / p.g.G, rhead = r - rtok * p.g.G;  // this row's token of a tile and head of a group
         const uint32_t tO = tmem + ((uint32_t)(32 * wq) << 16) + O_COL;
-        // the row that this lane stores first (16 lanes a row), and its place in a tile
-        const int srow = 32 * wq + lane / 16;
-        const int stok = srow / p.g.G, shead = srow - stok * p.g.G;
         uint32_t n_epi = 0;
         bool ok = true;
         for (uint32_t k = 0; k < walk.rounds && ok; k++) {
@@ -375,64 +373,58 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             const float lse2 = none ? -INFINITY : m_fin + log2f(l_tot);
             if (!(ok = mbar_wait(o_final, n_epi & 1, w))) break;
             tc_fence_after();
-            // A thread holds a row; 32 lanes storing to 32 rows at a time would be slow.  The warp turns its
-            // rows in its part of the item's Q buffer (S is done with it) and stores whole rows, 16 lanes a
-            // row; 16-byte chunks swizzled against bank conflicts.  A partial is stored in two halves of 64
-            // fp32 columns.
-            uint8_t *mine = smem + SMEM_Q + (n_epi % NQ) * TILE + wq * 32 * 256;
-            auto chunk = [&](int row, int c) {
-                return reinterpret_cast<uint4 *>(mine + row * 256 + (((c & 8) | ((c ^ row) & 7)) << 4));
-            };
+            // each thread stores its row, a 32-byte sector at a time
             const bool part = it.slot >= 0;
-            const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM;
-            // two rows a step: (tok, head) of the row, and its offset in `dst`
-            auto store = [&](char *dst, long tok_bytes, int head_bytes) {
-                __syncwarp();
-                int tk = stok, hd = shead;
-                char *d = dst + stok * tok_bytes + shead * head_bytes + (lane % 16) * 16;
-#pragma unroll 8
-                for (int i = 0; i < 16; i++) {
-                    const uint4 u = *chunk(2 * i + lane / 16, lane % 16);
-                    if (tk < n_tok && srow + 2 * i < p.g.rows) *reinterpret_cast<uint4 *>(d) = u;
-                    hd += 2, d += 2 * head_bytes;
-                    while (hd >= p.g.G) hd -= p.g.G, tk++, d += tok_bytes - p.g.G * head_bytes;
+            const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM + r;
+            if (part) {
+                float *dst = p.part_o + prow * D;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; cc++) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + cc * 32, o);
+                    tmem_ld_wait();
+                    if (cc + 1 == D / 32) {  // O is out of tensor memory
+                        tc_fence_before();
+                        mbar_arrive(o_free);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; c++) o[c] = none ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
+                    if (live) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) st_global_32(dst + cc * 32 + c, &o[c]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            };
+            } else {
+                uint32_t b[D / 2];  // the row as bf16
 #pragma unroll
-            for (int cc = 0; cc < D / 32; cc++) {
-                uint32_t o[32];
-                tmem_ld32(tO + cc * 32, o);
-                tmem_ld_wait();
-                if (cc + 1 == D / 32) {  // O is out of tensor memory
-                    tc_fence_before();
-                    mbar_arrive(o_free);
+                for (int cc = 0; cc < D / 32; cc++) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + cc * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2)
+                        b[(cc * 32 + c) / 2] = none ? 0u
+                                                    : pack_bf16x2(__uint_as_float(o[c]) * inv,
+                                                                  __uint_as_float(o[c + 1]) * inv);
                 }
+                tc_fence_before();
+                mbar_arrive(o_free);  // O is out of tensor memory
+                if (live) {
+                    __nv_bfloat16 *dst =
+                        p.out + ((long)it.tok0 + rtok) * p.out_stride + (long)(hk * p.g.G + rhead) * D;
+                    if (p.wide) {
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = none ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
-                if (part) {
+                        for (int c = 0; c < D / 2; c += 8) st_global_32(dst + 2 * c, &b[c]);
+                    } else {  // rows are 16-byte aligned only
 #pragma unroll
-                    for (int c = 0; c < 8; c++)
-                        *chunk(lane, (cc & 1) * 8 + c) = make_uint4(o[c * 4], o[c * 4 + 1], o[c * 4 + 2], o[c * 4 + 3]);
-                    if (cc & 1)
-                        store(reinterpret_cast<char *>(p.part_o + prow * D) + (cc >> 1) * 256, p.g.G * (long)(D * 4), D * 4);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        auto two = [&](int i) {
-                            return pack_bf16x2(__uint_as_float(o[c * 8 + i]), __uint_as_float(o[c * 8 + i + 1]));
-                        };
-                        *chunk(lane, cc * 4 + c) = make_uint4(two(0), two(2), two(4), two(6));
+                        for (int c = 0; c < D / 2; c += 4)
+                            *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(b[c], b[c + 1], b[c + 2], b[c + 3]);
                     }
                 }
             }
-            if (!part)
-                store(reinterpret_cast<char *>(p.out + (long)it.tok0 * p.out_stride + (long)hk * p.g.G * D),
-                      p.out_stride * 2, D * 2);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next Q lands there
-            mbar_arrive(&q_empty[n_epi % NQ]);
             if (live) {
-                if (part) p.part_lse[prow + r] = lse2;
+                if (part) p.part_lse[prow] = lse2;
                 else if (lse) *lse = lse2 * 0.69314718055994531f;
             }
             n_epi++;
@@ -674,7 +666,7 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     // Q.K^T operands: bf16 (A/B format 1) or fp16 (format 0)
     p.idesc_qk = idesc_bf16_f32(128, 128, false);
     if (t.qk_f16) p.idesc_qk &= ~((7u << 7) | (7u << 10));
-    p.inv_g = (65536u + (uint32_t)g.G - 1) / (uint32_t)g.G;
+    p.wide = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && out_stride * 2 % 32 == 0) ? 1 : 0;
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
     e = launch_after(packed_fwd_kernel, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
