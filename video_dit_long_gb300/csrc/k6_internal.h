@@ -215,6 +215,7 @@ struct PackedGeom {
     int sms;                          // SMs, and so persistent CTAs of the forward kernel
     int extra;                        // pieces that splitting long key ranges may add, per key head; 0: nothing to split
     int cap_rows, cap_fwd;            // forward items per CTA; and in all
+    long cap_sched;                   // (item, key head) pairs of the sorted list, in whole rounds of the SMs
     int cap_slots, cap_merge;         // partial outputs, split tiles
 };
 PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms);

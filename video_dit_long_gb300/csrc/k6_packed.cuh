@@ -56,6 +56,7 @@ struct PackedPlan {
     PackedHeader *head;
     int *count;         // [sms]: forward items of each CTA
     PackedItem *fwd;    // [sms][cap_rows] items of each CTA, or [cap_q + extra] for every key head, heaviest first
+    int *sched;         // sorted list: [round][sms] the (key head * n_fwd + item) of each CTA, or -1
     PackedItem *q;      // [cap_q], unsplit (backward), heaviest first
     PackedKItem *k;     // [cap_k], heaviest first
     PackedMerge *merge; // [cap_merge]
@@ -70,6 +71,8 @@ static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const Pa
     b += ((size_t)p.sms * sizeof(int) + 15) / 16 * 16;
     r.fwd = reinterpret_cast<PackedItem *>(b);
     b += (size_t)p.cap_fwd * sizeof(PackedItem);
+    r.sched = reinterpret_cast<int *>(b);
+    b += ((size_t)p.cap_sched * sizeof(int) + 15) / 16 * 16;
     r.q = reinterpret_cast<PackedItem *>(b);
     b += (size_t)p.cap_q * sizeof(PackedItem);
     r.k = reinterpret_cast<PackedKItem *>(b);

@@ -92,6 +92,7 @@ k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: more than 128 query heads per key head", fn);
     if (b->mask_block < 0 || b->mask_block >= (1 << 30))
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: mask_block must be in [0, 2^30)", fn);
+    if (h->sms > 512) return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: more than 512 SMs", fn);
     if (b->q_tokens >= (1L << 30) || b->k_tokens >= (1L << 30) || b->n_seq >= (1 << 24) ||
         (b->q_tokens + b->n_seq) * h->g.H >= (1L << 31) || (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31) || b->kv_heads >= (1 << 16))
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: batch too large", fn);

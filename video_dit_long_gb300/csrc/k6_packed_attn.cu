@@ -99,36 +99,37 @@ __device__ __forceinline__ uint32_t v_load_at(int j, int T) {
 // exp2 of a difference from a maximum that may be -inf (nothing seen yet): 0 then.
 __device__ __forceinline__ float ex2_from(float m, float m_new) { return m == -INFINITY ? 0.f : ex2(m - m_new); }
 
-// The items of this CTA: its row of the plan's stretches, or every gridDim-th
-// (item, key head) of the sorted list, to and fro.
+// The items of this CTA: its row of the plan's stretches, or its column of the
+// schedule of (item, key head) pairs.
 struct Walk {
     const PackedItem *list;
-    uint32_t rounds, n_items, units;  // n_items 0: list is this CTA's own
-    int slots;                        // partials that one slot number stands for (1, or one for every key head)
+    const int *sched;   // null: list is this CTA's own
+    uint32_t rounds, n_items;
+    int slots;          // partials that one slot number stands for (1, or one for every key head)
     __device__ Walk(const PackedPlan &plan, const PackedGeom &g) {
         list = plan.fwd;
         const int mine = plan.count[blockIdx.x];  // beside the header: no wait between the two (the grid is g.sms)
         slots = plan.head->slot_step;
+        n_items = (uint32_t)plan.head->n_fwd;
         if (plan.head->stream) {
             list += (long)blockIdx.x * g.cap_rows;
-            n_items = units = 0;
+            sched = nullptr;
             rounds = (uint32_t)mine;
         } else {
-            n_items = (uint32_t)plan.head->n_fwd;
-            units = n_items * (uint32_t)g.Hkv;
-            rounds = (units + gridDim.x - 1) / gridDim.x;
+            sched = plan.sched + blockIdx.x;
+            rounds = (n_items * (uint32_t)g.Hkv + gridDim.x - 1) / gridDim.x;
         }
     }
     __device__ bool at(uint32_t k, PackedItem &it, int &hk) const {
         uint32_t i = k;
-        if (n_items) {
-            const uint32_t u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (u >= units) return false;
-            hk = (int)(u / n_items);
-            i = u - (uint32_t)hk * n_items;
+        if (sched) {
+            const int u = sched[(long)k * gridDim.x];
+            if (u < 0) return false;
+            hk = (int)((uint32_t)u / n_items);
+            i = (uint32_t)u - (uint32_t)hk * n_items;
         }
         it = list[i];
-        if (!n_items) hk = it.n_tok_hk >> 8;
+        if (!sched) hk = it.n_tok_hk >> 8;
         return true;
     }
 };
