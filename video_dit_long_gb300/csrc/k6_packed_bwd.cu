@@ -6,7 +6,7 @@
 // dK and dV summed over the G query heads of a key head inside the accumulator:
 // a tile of query rows holds 128 / G tokens of all G heads (one TMA box), so
 // the sum over heads is part of the product over rows.  The two kinds of item
-// are those of the joint-sequence backward (one stationary 128-row tile per CTA, the
+// follow the joint-sequence backward (one stationary 128-row tile per CTA, the
 // other side streamed by TMA; warps 0-7 form P and dS, warp 8 copies, warp 9
 // issues the MMAs), walking the plan's lists: query tiles over the key tiles
 // below their limit (dq), key tiles over the query tiles that see them
@@ -79,12 +79,6 @@ __device__ __forceinline__ void tmem_ld16_here(uint32_t taddr, uint32_t (&r)[16]
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8_here(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // 2^x in program order, so the exps of a row pass run before the wait that follows them.
 __device__ __forceinline__ float ex2_in_order(float x) {
     float y;
@@ -315,29 +309,33 @@ __device__ __forceinline__ void zero_half_row(__nv_bfloat16 *dst) {
 
 // ------------------------------------------------------------------ dq kernel
 //
-// smem tiles: Q 0, dO 1, K slots 2-4, V slots 5-6.  Tensor memory: S 0-127,
-// dP 128-255, dQ 256-383, dS buffers 384-447 and 448-511.
+// smem tiles: Q 0, dO 1, K slots 2-4, V slots 5-6.  Tensor memory: S buffers
+// 0-127 and 128-255 (dS over each half's first 32 columns), dP 256-383, dQ
+// 384-511.  With two S buffers the MMAs of a step (dP(t+1), dQ(t), S(t+2)) and
+// the row pass (P(t+1) from S(t+1), then dS(t+1) once dP(t+1) is there) run side
+// by side; with one, and S and dP both awaited before a row pass, a step took
+// 2,580 cycles instead of SS-operand reads' 1,750.
 
 namespace dqk {
-constexpr int STAT = 0, KFULL = 1, KEMPTY = 4, VFULL = 7, VEMPTY = 9, SFULL = 11, DSFULL = 12, ACC = 13,
-              DRAIN = 14, NB = 15;
+constexpr int STAT = 0, KFULL = 1, KEMPTY = 4, VFULL = 7, VEMPTY = 9, SFULL = 11, DPFULL = 13, DSFULL = 14, ACC = 15,
+              DRAIN = 16, NB = 17;
 }
 
-// Row pass of the dq kernel: dS of one query row and 64 keys (half g) from S and
-// dP in tensor memory into dS buffer `buf`; keys from rel on get dS = 0 (MASKED).
+// Row pass of the dq kernel, second half: dS of one query row and 64 keys from P
+// in registers and dP in tensor memory, to `ds_at`; keys from rel on get dS = 0
+// (MASKED).
 template <bool MASKED>
-__device__ __forceinline__ void dq_row(uint32_t lb, int g, int buf, int rel, float2 ld, float sl2, int ds_f16) {
+__device__ __forceinline__ void dq_row(const float (&pr)[64], uint32_t dp_at, uint32_t ds_at, int rel, float d,
+                                       int ds_f16) {
 #pragma unroll
     for (int c = 0; c < 2; c++) {
-        uint32_t sv[32], pv[32], ds[16];
-        tmem_ld32(lb + 64 * g + 32 * c, sv);
-        tmem_ld32(lb + 128 + 64 * g + 32 * c, pv);
+        uint32_t pv[32], ds[16];
+        tmem_ld32(dp_at + 32 * c, pv);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(sv[k]), sl2, -ld.x));
-            const float p1 = ex2(fmaf(__uint_as_float(sv[k + 1]), sl2, -ld.x));
-            float d0 = p0 * (__uint_as_float(pv[k]) - ld.y), d1 = p1 * (__uint_as_float(pv[k + 1]) - ld.y);
+            float d0 = pr[32 * c + k] * (__uint_as_float(pv[k]) - d);
+            float d1 = pr[32 * c + k + 1] * (__uint_as_float(pv[k + 1]) - d);
             if (MASKED) {
                 if (32 * c + k >= rel) d0 = 0.f;
                 if (32 * c + k + 1 >= rel) d1 = 0.f;
@@ -345,7 +343,7 @@ __device__ __forceinline__ void dq_row(uint32_t lb, int g, int buf, int rel, flo
             // dS in K's type (one MMA takes one type): 2^-8 (bf16) or 2^-11 (fp16) of each term
             ds[k / 2] = pack_ds(d0, d1, ds_f16);
         }
-        tmem_st16(lb + 384 + 64 * buf + 32 * g + 16 * c, ds);
+        tmem_st16(ds_at + 16 * c, ds);
     }
 }
 
@@ -368,7 +366,7 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         if (live) zero_half_row(drow);
         return;
     }
-    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 1, 1};
+    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 1, 1};
     uint64_t *bar;
     volatile int *abort_flag;
     const uint32_t tmem = setup<NB>(smem, counts, bar, abort_flag);
@@ -404,44 +402,49 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         for (int t = nv > 2 ? nv - 2 : 0; t < nv; t++) mbar_drain(bar + VFULL + (t & 1), (t >> 1) & 1, DRAIN_NS);
         __syncwarp();
     } else if (warp == 9) {
-        const uint32_t tS = tmem, tP = tmem + 128, tA = tmem + 256, tDS = tmem + 384;
+        const uint32_t tS = tmem, tP = tmem + 256, tA = tmem + 384;
         const uint64_t dq_ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t ddo = smem_desc_sw128(smem_u32(sDO), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), 16, 1024);
         const uint64_t dkmn = smem_desc_sw128(smem_u32(sK), PANEL, 1024);
-        // S(t) = Q K^T and dP(t) = dO V^T, two interleaved chains; then free the
-        // V slot and publish S/dP (each commit also covers every earlier MMA).
-        auto issue_sdp = [&](int t) -> bool {
-            const int ks = t % 3, vs = t & 1;
+        auto issue_s = [&](int t) -> bool {  // S(t) = Q K^T into buffer t & 1
+            const int ks = t % 3;
             if (!mbar_wait_w(bar + KFULL + ks, (t / 3) & 1, w)) return false;
             // keys behind the sequence enter dQ += dS K times zero
             if (it.Lk - t * BM < BM) zero_rows(sK + ks * TILE, it.Lk - t * BM, lane);
-            if (!mbar_wait_w(bar + VFULL + vs, (t >> 1) & 1, w)) return false;
             tc_fence_after();
-            const uint64_t kd = dk0 + (uint64_t)((ks * TILE) >> 4), vd = dv0 + (uint64_t)((vs * TILE) >> 4);
+            const uint64_t kd = dk0 + (uint64_t)((ks * TILE) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk++) {
-                mma_k(tS, dq_, kd, p.idesc_qk, kk);
-                mma_k(tP, ddo, vd, p.idesc_bf16, kk);
-            }
-            tc_commit_w(bar + VEMPTY + vs);
-            tc_commit_w(bar + SFULL);
+            for (int kk = 0; kk < D / 16; kk++) mma_k(tS + (t & 1) * 128, dq_, kd, p.idesc_qk, kk);
+            tc_commit_w(bar + SFULL + (t & 1));
             return true;
         };
-        bool ok = mbar_wait_w(bar + STAT, 0, w) && issue_sdp(0);
+        auto issue_dp = [&](int t) -> bool {  // dP(t) = dO V^T
+            const int vs = t & 1;
+            if (!mbar_wait_w(bar + VFULL + vs, (t >> 1) & 1, w)) return false;
+            tc_fence_after();
+            const uint64_t vd = dv0 + (uint64_t)((vs * TILE) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) mma_k(tP, ddo, vd, p.idesc_bf16, kk);
+            tc_commit_w(bar + VEMPTY + vs);
+            tc_commit_w(bar + DPFULL);
+            return true;
+        };
+        bool ok = mbar_wait_w(bar + STAT, 0, w) && issue_s(0) && issue_dp(0) && (T < 2 || issue_s(1));
         for (int t = 0; t < T && ok; t++) {
-            // the row pass has read S(t)/dP(t) and written dS(t) to buffer t & 1
+            // the row pass has read dP(t) and written dS(t) over S(t)
             if (!(ok = mbar_wait_w(bar + DSFULL, t & 1, w))) break;
             tc_fence_after();
-            if (t + 1 < T && !(ok = issue_sdp(t + 1))) break;
+            if (t + 1 < T && !(ok = issue_dp(t + 1))) break;
             const uint64_t kmn = dkmn + (uint64_t)(((t % 3) * TILE) >> 4);
-            const uint32_t ads = tDS + (t & 1) * 64;
+            const uint32_t ads = tS + (t & 1) * 128;
 #pragma unroll
             for (int kk = 0; kk < BM / 16; kk++)
-                mma_ts_w(tA, ads + kk * 8, kmn + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
+                mma_ts_w(tA, ads + (kk >> 2) * 64 + (kk & 3) * 8, kmn + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
                          (t > 0 || kk > 0) ? 1u : 0u);  // dQ += dS K
             tc_commit_w(bar + KEMPTY + t % 3);
+            if (t + 2 < T && !(ok = issue_s(t + 2))) break;  // MMAs of a thread run in order: dS(t) has been read
         }
         if (ok) tc_commit_w(bar + ACC);
         tc_commit_w(bar + DRAIN);
@@ -457,21 +460,36 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         const float sl2 = p.scale_log2;
         bool ok = true;
         for (int t = 0; t < T; t++) {
-            if (!mbar_wait(bar + SFULL, t & 1, w)) {
+            if (!mbar_wait(bar + SFULL + (t & 1), (t >> 1) & 1, w)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t mine = lb + 128 * (t & 1) + 64 * g;  // this half's columns of S(t), and its dS(t)
+            float pr[64];
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t sv[32];
+                tmem_ld32(mine + 32 * c, sv);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; k++) pr[32 * c + k] = ex2_in_order(fmaf(__uint_as_float(sv[k]), sl2, -ld.x));
+            }
+            if (!mbar_wait(bar + DPFULL, t & 1, w)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const int rel = lim - t * BM - 64 * g;  // columns below rel of this half are seen
-            if (__any_sync(0xffffffffu, rel < 64)) dq_row<true>(lb, g, t & 1, rel, ld, sl2, p.ds_f16);
-            else dq_row<false>(lb, g, t & 1, rel, ld, sl2, p.ds_f16);
+            if (__any_sync(0xffffffffu, rel < 64)) dq_row<true>(pr, lb + 256 + 64 * g, mine, rel, ld.y, p.ds_f16);
+            else dq_row<false>(pr, lb + 256 + 64 * g, mine, rel, ld.y, p.ds_f16);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(bar + DSFULL);
         }
         if (ok && mbar_wait(bar + ACC, 0, w)) {
             tc_fence_after();
-            store_rows(lb + 256 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), [&](int i) {
+            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), [&](int i) {
                 const int rr = 32 * q4 + i;
                 const int tk = (int)(((uint32_t)rr * p.inv_g) >> 16);  // rr / G
                 return tk < it.n_tok_hk && rr < p.g.rows
@@ -507,15 +525,14 @@ __device__ __forceinline__ void p_row(float (&pr)[64], const uint32_t (&sv)[2][3
     }
 }
 
-// dS^T = P (dP^T - D) over 16-query chunks [C0, C1) of the 64 columns at taddr
-// (each chunk's dS^T lands on columns already read), times `sc`, and P rounded
-// to bf16 into this thread's row of the swizzled P^T panel at prow.
-template <bool FULL, int C0, int C1>
+// dS^T = P (dP^T - D) of the 64 columns at taddr, times `sc`, into this thread's
+// row of the swizzled dS^T panel at prow.
+template <bool FULL>
 __device__ __forceinline__ void ds_row(const float (&pr)[64], const float2 *ldq, int nq, uint32_t taddr,
                                        uint32_t prow, int r, int ds_f16, float sc) {
 #pragma unroll
-    for (int c = C0; c < C1; c++) {
-        uint32_t pv[16], ds[8], pk[8];
+    for (int c = 0; c < 4; c++) {
+        uint32_t pv[16], ds[8];
         tmem_ld16_here(taddr + 16 * c, pv);
         tmem_ld_wait();
 #pragma unroll
@@ -529,28 +546,29 @@ __device__ __forceinline__ void ds_row(const float (&pr)[64], const float2 *ldq,
                 de[e] = pr[j] * (__uint_as_float(pv[k + e]) - dd);
             }
             ds[k / 2] = ds_f16 ? pack_ds(de[0] * sc, de[1] * sc, true) : pack_ds(de[0], de[1], false);
-            pk[k / 2] = pack_bf16x2(pr[16 * c + k], pr[16 * c + k + 1]);
         }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const int chunk = 2 * c + i;  // 16-byte chunk of the 128-byte row
-            st_shared_16(prow + ((chunk ^ (r & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            st_shared_16(prow + ((chunk ^ (r & 7)) << 4), ds[4 * i], ds[4 * i + 1], ds[4 * i + 2], ds[4 * i + 3]);
         }
-        tmem_st8_here(taddr + 8 * c, ds);
     }
 }
 
 // ----------------------------------------------------------------- dkv kernel
 //
-// smem tiles: K 0, V 1, ring slot s: Q 2+2s, dO 3+2s; P^T 6.  Tensor memory:
-// S^T 0-127, dP^T 128-255 (dS^T over it), dV 256-383, dK 384-511.  The schedule
-// of the MMA warp (S^T(i+1) under the row pass of tile i, P^T/dS^T published in
-// two parts, dP^T(i+1) after the last dK(i) step that reads dS^T(i)) is that of
-// bwd_dkv_kernel.
+// smem tiles: K 0, V 1, ring slot s: Q 2+2s, dO 3+2s; dS^T 6.  Tensor memory:
+// S^T 0-127 (P^T over each half's first 32 columns), dP^T 128-255, dV 256-383,
+// dK 384-511.  A step: P^T(t) is published as soon as S^T(t) is read, so that
+// dV(t) and behind it S^T(t+1) run under the second half of the row pass
+// (dS^T(t) from dP^T(t)); that half published, dP^T(t+1) and dK(t) follow under
+// the next row pass.  (With dS^T over dP^T and P^T in shared memory, as in
+// bwd_dkv_kernel, dP^T(t+1) had to wait for dK(t) and the row pass for both: a
+// step took 3,550 cycles.)
 
 namespace dkvk {
-constexpr int STAT = 0, QFULL = 1, DOFULL = 3, QEMPTY = 5, DOEMPTY = 7, SREADY = 9, CONSUMED = 10, PDS = 11,
-              WIN = 13, ACC = 14, DRAIN = 15, NB = 16;  // PDS, PDS + 1: the two parts of a tile's P^T / dS^T
+constexpr int STAT = 0, QFULL = 1, DOFULL = 3, QEMPTY = 5, DOEMPTY = 7, SREADY = 9, DPREADY = 10, PREADY = 11,
+              DSREADY = 12, DSFREE = 13, ACC = 14, DRAIN = 15, NB = 16;
 }
 
 // One key tile of one key head (the whole block).
@@ -574,7 +592,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         }
         return;
     }
-    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 256, 256, 1, 1, 1};
+    const int counts[NB] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 256, 1, 1, 1};
     uint64_t *bar;
     volatile int *abort_flag;
     // rows that a copy of g.rows rows does not reach stay zero
@@ -587,7 +605,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
     }
     const uint32_t tmem = setup<NB>(smem, counts, bar, abort_flag);
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
-    uint8_t *sK = smem, *sV = smem + TILE, *sRing = smem + 2 * TILE, *sP = smem + 6 * TILE;
+    uint8_t *sK = smem, *sV = smem + TILE, *sRing = smem + 2 * TILE, *sDS = smem + 6 * TILE;
     // query rows of tile t (of the item's T) that belong to the sequence
     auto rows_of = [&](int t) { return min(p.g.rows, (it.Lq - (it.qt0 + t) * p.g.tpt) * p.g.G); };
 
@@ -626,7 +644,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), 16, 1024);
         const uint64_t dring = smem_desc_sw128(smem_u32(sRing), 16, 1024);
         const uint64_t dring_mn = smem_desc_sw128(smem_u32(sRing), PANEL, 1024);
-        const uint64_t dp = smem_desc_sw128(smem_u32(sP), 16, 1024);
+        const uint64_t dds = smem_desc_sw128(smem_u32(sDS), 16, 1024);
         // descriptor of tile `which` (0 Q, 1 dO) of the ring slot of tile t
         auto slot = [&](uint64_t base, int t, int which) {
             return base + (uint64_t)(((2 * (t & 1) + which) * TILE) >> 4);
@@ -651,57 +669,41 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk++) mma_k(tP, dv0, slot(dring, 0, 1), p.idesc_bf16, kk);  // dP^T = V dO^T
-            tc_commit_w(bar + WIN);
+            tc_commit_w(bar + DPREADY);
         }
         for (int t = 0; t < T && ok; t++) {
-            // the row pass has read S^T(t): S^T(t+1) may overwrite its columns
-            if (!(ok = mbar_wait_w(bar + CONSUMED, t & 1, w))) break;
-            tc_fence_after();
             const bool next = t + 1 < T;
-            if (next) {
+            // P^T(t) is in tensor memory
+            if (!(ok = mbar_wait_w(bar + PREADY, t & 1, w))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BM / 16; kk++)  // dV += P^T dO; K-step kk covers queries 16 kk .. 16 kk + 15
+                mma_ts_w(tV, tS + (kk >> 2) * 64 + (kk & 3) * 8, slot(dring_mn, t, 1) + (uint64_t)((kk * 16 * 128) >> 4),
+                         p.idesc_bf16_mn, (t > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_w(bar + DOEMPTY + (t & 1));  // dO(t): dP^T(t) and dV(t) done
+            if (next) {  // MMAs of a thread run in order: S^T(t+1) overwrites P^T(t) behind dV(t)
                 if (!(ok = wait_q(t + 1))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk++) mma_k(tS, dk0, slot(dring, t + 1, 0), p.idesc_qk, kk);
                 tc_commit_w(bar + SREADY);
             }
-            // the first part of P^T(t) is in shared memory and of dS^T(t) over dP^T(t)
-            if (!(ok = mbar_wait_w(bar + PDS, t & 1, w))) break;
+            // dS^T(t) is in shared memory, dP^T(t) read
+            if (!(ok = mbar_wait_w(bar + DSREADY, t & 1, w))) break;
             if (next && !(ok = wait_do(t + 1))) break;
             tc_fence_after();
-            const uint32_t acc = t > 0 ? 1u : 0u;
-            // K-step kk covers queries 16 kk .. 16 kk + 15: the first part holds kk 0, 1, 4, 5
-            auto dv_step = [&](int kk) {  // dV += P^T dO
-                const uint64_t poff = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
-                mma_ss_w(tV, dp + poff, slot(dring_mn, t, 1) + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_bf16_mn,
-                         acc | (kk > 0 ? 1u : 0u));
-            };
-            auto dk_step = [&](int kk) {  // dK += dS^T Q
-                mma_ts_w(tK, tP + (kk >> 2) * 64 + (kk & 3) * 8,
+            if (next) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) mma_k(tP, dv0, slot(dring, t + 1, 1), p.idesc_bf16, kk);  // dP^T(t+1)
+                tc_commit_w(bar + DPREADY);
+            }
+#pragma unroll
+            for (int kk = 0; kk < BM / 16; kk++)  // dK += dS^T Q
+                mma_ss_w(tK, dds + ((uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4),
                          slot(dring_mn, t, 0) + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
-                         acc | (kk > 0 ? 1u : 0u));
-            };
-            constexpr int part0[4] = {0, 1, 4, 5}, part1[4] = {2, 3, 6, 7};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                dk_step(part0[i]);
-                dv_step(part0[i]);
-            }
-            if (!(ok = mbar_wait_w(bar + PDS + 1, t & 1, w))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                dk_step(part1[i]);
-                if (i < 2) dv_step(part1[i]);
-            }
+                         (t > 0 || kk > 0) ? 1u : 0u);
             tc_commit_w(bar + QEMPTY + (t & 1));  // Q(t): S^T(t) and dK(t) done
-#pragma unroll
-            for (int kk = 0; kk < D / 16; kk++) {
-                if (next) mma_k(tP, dv0, slot(dring, t + 1, 1), p.idesc_bf16, kk);  // dP^T(t+1)
-                if (kk < 2) dv_step(part1[2 + kk]);
-            }
-            tc_commit_w(bar + DOEMPTY + (t & 1));  // dO(t): dP^T(t) and dV(t) done
-            tc_commit_w(bar + WIN);
+            tc_commit_w(bar + DSFREE);
         }
         if (ok) tc_commit_w(bar + ACC);
         tc_commit_w(bar + DRAIN);
@@ -715,8 +717,8 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         const float2 *ld_h = p.LD + ((long)hk * p.g.Tq + it.qrow0) * p.g.G;
         // the first query row (of the sequence, tokens x heads) that sees this key
         const long first = (long)packed_first_query(it.key0 + r, it.off, p.g.block) * p.g.G;
-        // this thread's row of P^T panel g: 8 chunks of 16 bytes, 128-byte swizzle
-        const uint32_t prow = smem_u32(sP) + g * PANEL + (r >> 3) * 1024 + (r & 7) * 128;
+        // this thread's row of dS^T panel g: 8 chunks of 16 bytes, 128-byte swizzle
+        const uint32_t prow = smem_u32(sDS) + g * PANEL + (r >> 3) * 1024 + (r & 7) * 128;
         bool ok = true;
         for (int t = 0; t < T; t++) {
             if (!mbar_wait(bar + SREADY, t & 1, w)) {
@@ -724,13 +726,10 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
                 break;
             }
             tc_fence_after();
-            // S^T of this half into registers, then its columns are free for S^T(t+1)
             uint32_t sv[2][32];
             tmem_ld32(lb + 64 * g, sv[0]);
             tmem_ld32(lb + 64 * g + 32, sv[1]);
             tmem_ld_wait();
-            tc_fence_before();
-            mbar_arrive(bar + CONSUMED);
             const long q0 = (long)(it.qt0 + t) * p.g.rows + 64 * g;  // first query row of this half
             const float2 *ldq = ld_h + q0;
             const int nq = rows_of(t) - 64 * g;                       // rows of this half in the sequence (may be <= 0)
@@ -739,25 +738,26 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
             float pr[64];
             if (full) p_row<true>(pr, sv, ldq, 0, nq, sl2);
             else p_row<false>(pr, sv, ldq, lo, nq, sl2);
-            // dV/dK(t-1) and dP^T(t) done: the P^T buffer is free and dP^T(t) is in place
-            if (!mbar_wait(bar + WIN, t & 1, w)) {
+            {  // P^T(t), rounded to bf16 (dO's type; one MMA takes one type), over this half's columns of S^T(t)
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) pk[k / 2] = pack_bf16x2(pr[k], pr[k + 1]);
+                tmem_st32(lb + 64 * g, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar + PREADY);
+            // dP^T(t) is in place, and dK(t-1) has read the dS^T buffer
+            if (!mbar_wait(bar + DPREADY, t & 1, w) || (t > 0 && !mbar_wait(bar + DSFREE, (t - 1) & 1, w))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            // first part (queries 0-31 of this half), published before the second is formed
-            if (full) ds_row<true, 0, 2>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
-            else ds_row<false, 0, 2>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            if (full) ds_row<true>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            else ds_row<false>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
             fence_async_smem();
-            tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(bar + PDS);
-            if (full) ds_row<true, 2, 4>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
-            else ds_row<false, 2, 4>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
-            fence_async_smem();
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(bar + PDS + 1);
+            mbar_arrive(bar + DSREADY);
         }
         if (ok && mbar_wait(bar + ACC, 0, w)) {
             tc_fence_after();
