@@ -38,7 +38,9 @@ constexpr int PANEL = BM * 64 * 2;
 constexpr int TILE = 2 * PANEL;
 constexpr int THREADS = 320;                // warps 0-7 rows, 8 TMA, 9 MMA + TMEM
 constexpr int SMEM_DATA = 7 * TILE;
-constexpr int SMEM_ALLOC = SMEM_DATA + 256 + 1024;  // barriers, TMEM slot, abort flag, alignment
+constexpr int SMEM_LD = SMEM_DATA + 256;    // barriers, TMEM slot and abort flag before it
+constexpr int SMEM_ALLOC = SMEM_LD + 2 * 2 * BM * 4;  // lse and D of two tiles of query rows (dk/dv)
+static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 }  // namespace pb
@@ -501,51 +503,47 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
     teardown(tmem);
 }
 
-// A tile of 128 / G tokens x G heads leaves 128 mod G rows empty (2 for G = 3,
-// at most 8 for G <= 12), and so every tile ends in dead rows: the row pass
-// without masks guards its last TAIL columns instead of calling such a tile
-// ragged (G = 3, 25,920 tokens by frames: 14.4 ms with every tile ragged).
-constexpr int TAIL = 8;
-
-// Row pass of the dk/dv kernel: P of one key row and 64 queries from S^T in
-// registers.  Queries outside [lo, nq) get P = 0 (FULL: all below 64 - TAIL are seen).
-template <bool FULL>
-__device__ __forceinline__ void p_row(float (&pr)[64], const uint32_t (&sv)[2][32], const float2 *ldq, int lo, int nq,
-                                      float sl2) {
+// Row pass of the dk/dv kernel, first half: P of one key row and 64 queries from
+// S^T in registers; sx holds the queries' lse (+inf for rows that are none).
+// Queries below lo do not see the key: P = 0 (MASKED).
+template <bool MASKED>
+__device__ __forceinline__ void p_row(float (&pr)[64], const uint32_t (&sv)[2][32], const float *sx, int lo, float sl2) {
 #pragma unroll
-    for (int c = 0; c < 2; c++) {
+    for (int c = 0; c < 16; c++) {
+        const float4 x = *reinterpret_cast<const float4 *>(sx + 4 * c);
+        const float l2[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int k = 0; k < 32; k++) {
-            const int j = 32 * c + k;
-            const float l2 = ((FULL && j < 64 - TAIL) || j < nq) ? ldq[j].x : INFINITY;
-            pr[j] = ex2_in_order(fmaf(__uint_as_float(sv[c][k]), sl2, -l2));
-            if (!FULL && !(j >= lo && j < nq)) pr[j] = 0.f;
+        for (int k = 0; k < 4; k++) {
+            const int j = 4 * c + k;
+            pr[j] = ex2_in_order(fmaf(__uint_as_float(sv[j / 32][j % 32]), sl2, -l2[k]));
+            if (MASKED && j < lo) pr[j] = 0.f;
         }
-        asm volatile("" ::: "memory");  // one half's loads at a time (register pressure)
     }
 }
 
-// dS^T = P (dP^T - D) of the 64 columns at taddr, times `sc`, into this thread's
-// row of the swizzled dS^T panel at prow.
-template <bool FULL>
-__device__ __forceinline__ void ds_row(const float (&pr)[64], const float2 *ldq, int nq, uint32_t taddr,
-                                       uint32_t prow, int r, int ds_f16, float sc) {
+// Second half: dS^T = P (dP^T - D) of the 64 columns at taddr, times `sc`, into
+// this thread's row of the swizzled dS^T panel at prow; sd holds the queries' D.
+__device__ __forceinline__ void ds_row(const float (&pr)[64], const float *sd, uint32_t taddr, uint32_t prow, int r,
+                                       int ds_f16, float sc) {
 #pragma unroll
     for (int c = 0; c < 4; c++) {
         uint32_t pv[16], ds[8];
         tmem_ld16_here(taddr + 16 * c, pv);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-            float de[2];
+        for (int k = 0; k < 16; k += 4) {
+            const float4 d = *reinterpret_cast<const float4 *>(sd + 16 * c + k);
+            float de[4] = {__uint_as_float(pv[k]) - d.x, __uint_as_float(pv[k + 1]) - d.y,
+                           __uint_as_float(pv[k + 2]) - d.z, __uint_as_float(pv[k + 3]) - d.w};
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int j = 16 * c + k + e;
-                // plain load: the clobber of the tensor-memory load above keeps it in this chunk
-                const float dd = ((FULL && j < 64 - TAIL) || j < nq) ? ldq[j].y : 0.f;
-                de[e] = pr[j] * (__uint_as_float(pv[k + e]) - dd);
+            for (int e = 0; e < 4; e++) de[e] *= pr[16 * c + k + e];
+            if (ds_f16) {
+                ds[k / 2] = pack_ds(de[0] * sc, de[1] * sc, true);
+                ds[k / 2 + 1] = pack_ds(de[2] * sc, de[3] * sc, true);
+            } else {
+                ds[k / 2] = pack_ds(de[0], de[1], false);
+                ds[k / 2 + 1] = pack_ds(de[2], de[3], false);
             }
-            ds[k / 2] = ds_f16 ? pack_ds(de[0] * sc, de[1] * sc, true) : pack_ds(de[0], de[1], false);
         }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -603,11 +601,22 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         }
         fence_async_smem();
     }
+    // query rows of tile t (of the item's T) that belong to the sequence
+    auto rows_of = [&](int t) { return min(p.g.rows, (it.Lq - (it.qt0 + t) * p.g.tpt) * p.g.G); };
+    // {lse, D} of row i of tile t: P is 0 in a row that is none (its rows of Q and dO are zero, its D finite)
+    const float2 *ld_h = p.LD + ((long)hk * p.g.Tq + it.qrow0) * p.g.G;
+    auto row_ld = [&](int t, int i) {
+        return t < T && i < rows_of(t) ? ld_h[(long)(it.qt0 + t) * p.g.rows + i] : make_float2(INFINITY, 0.f);
+    };
+    // the queries' lse and D, [tile parity][lse, D][128]: warps 0-3 bring the next tile's
+    float *sLD = reinterpret_cast<float *>(smem + SMEM_LD);
+    if (threadIdx.x < BM) {
+        const float2 v = row_ld(0, threadIdx.x);
+        sLD[threadIdx.x] = v.x, sLD[BM + threadIdx.x] = v.y;
+    }
     const uint32_t tmem = setup<NB>(smem, counts, bar, abort_flag);
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
     uint8_t *sK = smem, *sV = smem + TILE, *sRing = smem + 2 * TILE, *sDS = smem + 6 * TILE;
-    // query rows of tile t (of the item's T) that belong to the sequence
-    auto rows_of = [&](int t) { return min(p.g.rows, (it.Lq - (it.qt0 + t) * p.g.tpt) * p.g.G); };
 
     if (warp == 8) {
         const bool leader = elect_one();
@@ -714,7 +723,6 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         const float sl2 = p.scale_log2;
         const int e = ds_exponent(p);
         const float sc = exp2f((float)e);
-        const float2 *ld_h = p.LD + ((long)hk * p.g.Tq + it.qrow0) * p.g.G;
         // the first query row (of the sequence, tokens x heads) that sees this key
         const long first = (long)packed_first_query(it.key0 + r, it.off, p.g.block) * p.g.G;
         // this thread's row of dS^T panel g: 8 chunks of 16 bytes, 128-byte swizzle
@@ -731,13 +739,26 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
             tmem_ld32(lb + 64 * g + 32, sv[1]);
             tmem_ld_wait();
             const long q0 = (long)(it.qt0 + t) * p.g.rows + 64 * g;  // first query row of this half
-            const float2 *ldq = ld_h + q0;
-            const int nq = rows_of(t) - 64 * g;                       // rows of this half in the sequence (may be <= 0)
             const int lo = (int)max(-1L, min(first - q0, 64L));       // rows of this half from lo on see the key
-            const bool full = !__any_sync(0xffffffffu, nq < 64 - TAIL || lo > 0);
+            // the tile's {lse, D}, written before its writers' P^T(t-1) arrivals
+            if (t > 0 && !mbar_wait(bar + PREADY, (t - 1) & 1, w)) {
+                ok = false;
+                break;
+            }
+            const float *sx = sLD + (t & 1) * 2 * BM + 64 * g;
+            float2 nx = make_float2(0.f, 0.f);
+            if (g == 0) nx = row_ld(t + 1, r);
             float pr[64];
-            if (full) p_row<true>(pr, sv, ldq, 0, nq, sl2);
-            else p_row<false>(pr, sv, ldq, lo, nq, sl2);
+            if (__any_sync(0xffffffffu, lo > 0)) p_row<true>(pr, sv, sx, lo, sl2);
+            else p_row<false>(pr, sv, sx, lo, sl2);
+            if (g == 0) {  // the other buffer was last read in step t-1, before its readers' dS^T(t-1) arrivals
+                float *at = sLD + ((t + 1) & 1) * 2 * BM + r;
+                if (t > 0 && !mbar_wait(bar + DSREADY, (t - 1) & 1, w)) {
+                    ok = false;
+                    break;
+                }
+                at[0] = nx.x, at[BM] = nx.y;
+            }
             {  // P^T(t), rounded to bf16 (dO's type; one MMA takes one type), over this half's columns of S^T(t)
                 uint32_t pk[32];
 #pragma unroll
@@ -753,8 +774,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
                 break;
             }
             tc_fence_after();
-            if (full) ds_row<true>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
-            else ds_row<false>(pr, ldq, nq, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
+            ds_row(pr, sx + BM, lb + 128 + 64 * g, prow, r, p.ds_f16, sc);
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(bar + DSREADY);
@@ -781,8 +801,11 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const PackedBwdParams p) {
     wait_previous_kernel();
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
+        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_LAYOUT);
+        return;
+    }
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
     if (!packed_plan_ok(*plan.head, p.g)) {
         if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
