@@ -699,20 +699,21 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
             }
             // dS^T(t) is in shared memory, dP^T(t) read
             if (!(ok = mbar_wait_w(bar + DSREADY, t & 1, w))) break;
-            if (next && !(ok = wait_do(t + 1))) break;
             tc_fence_after();
-            if (next) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; kk++) mma_k(tP, dv0, slot(dring, t + 1, 1), p.idesc_bf16, kk);  // dP^T(t+1)
-                tc_commit_w(bar + DPREADY);
-            }
-#pragma unroll
-            for (int kk = 0; kk < BM / 16; kk++)  // dK += dS^T Q
+            for (int kk = 0; kk < BM / 16; kk++)  // dK += dS^T Q; ahead of dP^T(t+1), since Q(t+2) waits for its slot
                 mma_ss_w(tK, dds + ((uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4),
                          slot(dring_mn, t, 0) + (uint64_t)((kk * 16 * 128) >> 4), p.idesc_ds_mn,
                          (t > 0 || kk > 0) ? 1u : 0u);
             tc_commit_w(bar + QEMPTY + (t & 1));  // Q(t): S^T(t) and dK(t) done
             tc_commit_w(bar + DSFREE);
+            if (next) {
+                if (!(ok = wait_do(t + 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) mma_k(tP, dv0, slot(dring, t + 1, 1), p.idesc_bf16, kk);  // dP^T(t+1)
+                tc_commit_w(bar + DPREADY);
+            }
         }
         if (ok) tc_commit_w(bar + ACC);
         tc_commit_w(bar + DRAIN);
