@@ -56,6 +56,7 @@ class PackedPlan:
     def __init__(self, batch, buffer):
         self.batch, self.buffer = batch, buffer
         self.ref, self.ptr = ctypes.byref(batch), buffer.data_ptr()
+        self.q_tokens, self.k_tokens, self.kv_heads = batch.q_tokens, batch.k_tokens, batch.kv_heads
 
 
 _lib = None
@@ -181,16 +182,16 @@ def _rows(t, shape, dtype, device, what):
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what}: want a {dtype} tensor of shape {shape} on cuda:{device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    if st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"{what}: heads and head dim must be dense (strides {st})")
-    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+    a, b, c = t.stride()
+    if c != 1 or (b != shape[2] and shape[1] > 1):
+        raise ValueError(f"{what}: heads and head dim must be dense (strides {(a, b, c)})")
+    return t.data_ptr(), a if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _vec(t, n, dtype, device, what):
     if t is None:
         return None
-    if t.numel() != n or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what}: want a dense {dtype} tensor of {n} values on cuda:{device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -214,8 +215,10 @@ class Handle:
         h = ctypes.c_void_p()
         _check(L.k6attn_create(ctypes.byref(self._desc), ctypes.byref(h)))
         self.h = h
+        self._lib, self._H, self._d = L, H, d
         self.dtype = dtype
-        torch = _torch_types()  # the packed calls check their tensors' device and type
+        torch = _torch_types()
+        self._elem = _DTYPES[self._desc.dtype]  # the packed calls check their tensors' device and type
         self._dev = torch.cuda.current_device()
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -382,19 +385,20 @@ class Handle:
         """Per-head QK-norm (with weights) and (t, h, w) rotation of q [T][H][d] and k [T][kv_heads][d], at
         positions int32 [T][3], into q_out, k_out (the handle's type or, for bf16, fp16; may be q and k)."""
         dev, st = self._packed(stream)
-        D = self._desc
-        d, T, kv = D.d, q.shape[0], k.shape[1]
-        sq, sk, e, f32 = (T, D.H, d), (T, kv, d), _DTYPES[D.dtype], _DTYPES[F32]
+        d, T, kv = self._d, q.size(0), k.size(1)
+        sq, sk, e, f32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32]
         od = _code(q_out)
         o = q_out.dtype
         pq, lq = _rows(q, sq, e, dev, "q")
         pk, lk = _rows(k, sk, e, dev, "k")
         poq, loq = _rows(q_out, sq, o, dev, "q_out")
         pok, lok = _rows(k_out, sk, o, dev, "k_out")
-        _check(load().k6attn_packed_norm_rope(
+        s = self._lib.k6attn_packed_norm_rope(
             self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pq, lq, pk, lk,
             _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, poq, loq, pok, lok,
-            od, st))
+            od, st)
+        if s:
+            _check(s)
 
     def packed_norm_rope_backward_workspace_bytes(self, tokens: int, kv_heads: int) -> int:
         return load().k6attn_packed_norm_rope_backward_workspace_bytes(self.h, int(tokens), int(kv_heads))
@@ -403,9 +407,8 @@ class Handle:
                                   dq, dk, dq_weight=None, dk_weight=None, workspace=None, stream=None):
         """Gradients of packed_norm_rope: dq, dk (the handle's type) and, with weights, dq_weight, dk_weight (fp32)."""
         dev, st = self._packed(stream)
-        D = self._desc
-        d, T, kv = D.d, dq_out.shape[0], dk_out.shape[1]
-        sq, sk, e, f32 = (T, D.H, d), (T, kv, d), _DTYPES[D.dtype], _DTYPES[F32]
+        d, T, kv = self._d, dq_out.size(0), dk_out.size(1)
+        sq, sk, e, f32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32]
         pgq, lgq = _rows(dq_out, sq, e, dev, "dq_out")
         pgk, lgk = _rows(dk_out, sk, e, dev, "dk_out")
         pq, lq = (None, 0) if q is None else _rows(q, sq, e, dev, "q")
@@ -413,10 +416,12 @@ class Handle:
         pdq, ldq = _rows(dq, sq, e, dev, "dq")
         pdk, ldk = _rows(dk, sk, e, dev, "dk")
         ws, nws = _room(workspace, dev)
-        _check(load().k6attn_packed_norm_rope_backward(
+        s = self._lib.k6attn_packed_norm_rope_backward(
             self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pgq, lgq, pgk, lgk, pq, lq, pk,
             lk, _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, pdq, ldq, pdk,
-            ldk, _vec(dq_weight, d, f32, dev, "dq_weight"), _vec(dk_weight, d, f32, dev, "dk_weight"), ws, nws, st))
+            ldk, _vec(dq_weight, d, f32, dev, "dq_weight"), _vec(dk_weight, d, f32, dev, "dk_weight"), ws, nws, st)
+        if s:
+            _check(s)
 
     def packed_plan(self, cu_q, cu_k, q_tokens, k_tokens, kv_heads, mask_block=0, stream=None) -> PackedPlan:
         """Plan attention over packed sequences: offsets cu_q, cu_k (int32, on the device; cu_k None = cu_q) into
@@ -445,16 +450,18 @@ class Handle:
         """Attention of a planned batch: q [Tq][H][d], k, v [Tk][kv_heads][d] (q, k bf16 or fp16, v bf16) into
         out (bf16, as q) and lse (fp32 [H][Tq])."""
         dev, st = self._packed(stream)
-        b, D, bf = plan.batch, self._desc, _DTYPES[BF16]
-        sq, sk, x = (b.q_tokens, D.H, D.d), (b.k_tokens, b.kv_heads, D.d), q.dtype
+        H, d, bf = self._H, self._d, _DTYPES[BF16]
+        sq, sk, x = (plan.q_tokens, H, d), (plan.k_tokens, plan.kv_heads, d), q.dtype
         pq, lq = _rows(q, sq, x, dev, "q")
         pk, lk = _rows(k, sk, x, dev, "k")
         pv, lv = _rows(v, sk, bf, dev, "v")
         po, lo = _rows(out, sq, bf, dev, "out")
         ws, nws = _room(workspace, dev)
-        _check(load().k6attn_packed_forward(
+        s = self._lib.k6attn_packed_forward(
             self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo,
-            _vec(lse, D.H * b.q_tokens, _DTYPES[F32], dev, "lse"), ws, nws, st))
+            _vec(lse, H * plan.q_tokens, _DTYPES[F32], dev, "lse"), ws, nws, st)
+        if s:
+            _check(s)
 
     def packed_backward_workspace_bytes(self, plan) -> int:
         return load().k6attn_packed_backward_workspace_bytes(self.h, plan.ref)
@@ -462,8 +469,8 @@ class Handle:
     def packed_backward(self, plan, q, k, v, out, dout, lse, dq, dk, dv, *, workspace, stream=None):
         """Gradients dq, dk, dv (bf16) of packed_forward, from its out and lse and dout (bf16)."""
         dev, st = self._packed(stream)
-        b, D, bf = plan.batch, self._desc, _DTYPES[BF16]
-        sq, sk, x = (b.q_tokens, D.H, D.d), (b.k_tokens, b.kv_heads, D.d), q.dtype
+        H, d, bf = self._H, self._d, _DTYPES[BF16]
+        sq, sk, x = (plan.q_tokens, H, d), (plan.k_tokens, plan.kv_heads, d), q.dtype
         pq, lq = _rows(q, sq, x, dev, "q")
         pk, lk = _rows(k, sk, x, dev, "k")
         pv, lv = _rows(v, sk, bf, dev, "v")
@@ -473,9 +480,11 @@ class Handle:
         pdk, ldk = _rows(dk, sk, bf, dev, "dk")
         pdv, ldv = _rows(dv, sk, bf, dev, "dv")
         ws, nws = _room(workspace, dev)
-        _check(load().k6attn_packed_backward(
+        s = self._lib.k6attn_packed_backward(
             self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo, pg, lg,
-            _vec(lse, D.H * b.q_tokens, _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st))
+            _vec(lse, H * plan.q_tokens, _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st)
+        if s:
+            _check(s)
 
     def sync(self, stream=None):
         _check(load().k6attn_sync(self.h, _stream(stream)))
