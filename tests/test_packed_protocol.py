@@ -1,38 +1,87 @@
 """Host-side model of the waits of the packed attention kernel
-(k6_packed_attn.cu): a persistent CTA that runs one item after another, the K/V
-ring of the joint kernel (modelled in test_ring_protocol.py) carried from item
-to item, and one Q buffer that an item's first S waits for.
+(k6_packed_attn.cu): a persistent CTA that runs one item after another.
 
-Added to that model, in program order:
-- the producer issues an item's Q before its first K, once the last S of the
-  item before is done;
-- the first S of an item waits for its Q;
-- each softmax group posts its row sums after its last tile of an item, once the
-  epilogue has read those of the item before, and goes on at once;
-- the epilogue reads both posts, waits for the item's last P.V, takes O and
-  stores it, one item after another;
-- the first P.V of an item waits for the epilogue before to have read O.
-Checked over sequences of items of 1-7 key tiles: every slot is freed by
-someone, no wait cycle, no wait that an earlier phase of its slot could match.
+In program order, as a dependency graph over the items' key tiles n:
+- one producer loads an item's first K, then its Q (once the last S of the item
+  before is done), then its other K tiles, K(n) into slot n % 3; another loads
+  V(n) into slot n % 3 of a ring of its own;
+- the Q.K^T warp issues S(n) once K(n) has landed and the softmax has read
+  S(n-2), whose buffer it takes;
+- tile n belongs to softmax group n % 2, which frees K(n)'s slot when it sees
+  S(n), waits for the maximum after tile n-1, reads S(n), posts its own maximum,
+  and writes P(n) once P(n-2).V, which read the same buffer, is done (and
+  P(n-1).V, where it rescales the output);
+- the P.V warp issues P(n).V once V(n) has landed and P(n) is there; V(n)'s slot
+  is freed when it is done; the first of an item also waits until the epilogue
+  has taken the output of the item before;
+- each group posts its row sums after its last tile of an item, once the
+  epilogue has read those of the item before;
+- the epilogue reads both posts, waits for the item's last P.V and takes O.
+Checked over sequences of items: no wait cycle, and no wait that an earlier phase
+of its barrier could match.
 """
+import collections
 import itertools
 
-from .test_ring_protocol import NSTAGE, acyclic, ancestors, model
+from .test_ring_protocol import acyclic, ancestors
+
+SLOTS = 3
 
 CASES = [list(Ts) for k in range(1, 5) for Ts in itertools.product((1, 2, 3, 4, 5, 7), repeat=k)] + \
     [[1] * 12, [2] * 9, [3] * 7, [17, 1, 17], [1, 2, 1, 2, 1, 2, 1], [6, 6, 6, 6]]
 
 
-def packed_model(Ts, q_first=True):
-    loads, idx, deps, consumer, N = model(Ts, 2)
-    first = 0
+def packed_model(Ts, k_before_q=1):
+    deps = collections.defaultdict(set)
+    N = sum(Ts)
+    first = [sum(Ts[:u]) for u in range(len(Ts))]
+    item_of = {n: u for u, T in enumerate(Ts) for n in range(first[u], first[u] + T)}
+    order = []  # of the K and Q producer
     for u, T in enumerate(Ts):
-        last = first + T - 1
-        deps[("S_release", first)].add(("Q", u))  # waited for before anything else of the item
-        deps[("stored", u)].add(("read_O", u))
-        # tile n belongs to group n % 2; a group without a tile of the item posts all the same
+        ks = [("load_K", n) for n in range(first[u], first[u] + T)]
+        order += ks[:k_before_q] + [("Q", u)] + ks[k_before_q:]
+    for a, b in zip(order, order[1:]):
+        deps[b].add(a)
+    for n in range(N):
+        u = item_of[n]
+        at_start = n == first[u]
+        if n:
+            deps[("load_V", n)].add(("load_V", n - 1))
+        if n >= SLOTS:
+            deps[("load_K", n)].add(("wake", n - SLOTS))
+            deps[("load_V", n)].add(("PV_done", n - SLOTS))
+        # Q.K^T warp
+        if n:
+            deps[("wait_K", n)].add(("S", n - 1))
+        if n >= 2:
+            deps[("wait_K", n)].add(("read_S", n - 2))
+        if at_start:
+            deps[("wait_K", n)].add(("Q", u))
+        deps[("S", n)] |= {("wait_K", n), ("load_K", n)}
+        # softmax group n % 2
+        deps[("wake", n)].add(("S", n))
+        if n >= 2:
+            deps[("wake", n)].add(("P", n - 2))
+        deps[("read_S", n)] |= {("wake", n)} | ({("max", n - 1)} if n else set())
+        deps[("max", n)].add(("read_S", n))
+        deps[("P", n)].add(("max", n))
+        if n >= 2:
+            deps[("P", n)].add(("PV_done", n - 2))
+        if not at_start:
+            deps[("P", n)].add(("PV_done", n - 1))
+        # P.V warp
+        if n:
+            deps[("wait_V", n)].add(("PV", n - 1))
+        deps[("PV", n)] |= {("wait_V", n), ("load_V", n), ("P", n)}
+        if at_start and u:
+            deps[("PV", n)].add(("read_O", u - 1))
+        deps[("PV_done", n)].add(("PV", n))
+    for u, T in enumerate(Ts):
+        last = first[u] + T - 1
+        if u:
+            deps[("Q", u)].add(("S", first[u] - 1))
         for g in (0, 1):
-            mine = [n for n in range(first, first + T) if n % 2 == g]
+            mine = [n for n in range(first[u], last + 1) if n % 2 == g]
             if mine:
                 deps[("post", u, g)].add(("P", mine[-1]))
             if u:
@@ -41,38 +90,35 @@ def packed_model(Ts, q_first=True):
                     deps[("wake", n)].add(("post", u - 1, g))
             deps[("read_sums", u)].add(("post", u, g))
         if u:
-            deps[("read_sums", u)].add(("stored", u - 1))
+            deps[("read_sums", u)].add(("read_O", u - 1))
         deps[("read_O", u)] |= {("PV_done", last), ("read_sums", u)}
-        if u:
-            deps[("Q", u)].add(("S", first - 1))
-            prev = max(idx[("K", first - 1)], idx[("V", first - 1)])
-            if q_first:
-                deps[("Q", u)].add(("load", prev))
-                deps[("load", prev + 1)].add(("Q", u))
-            else:  # Q issued after the first two K tiles
-                deps[("Q", u)].add(("load", prev + min(2, T)))
-                deps[("load", prev + min(2, T) + 1)].add(("Q", u))
-            deps[("wait_O", first)].add(("read_O", u - 1))
-            deps[("PV", first)].add(("wait_O", first))
-        first += T
-    return loads, deps, consumer
+    return deps, N
 
 
 def test_no_wait_cycle_over_items():
     for Ts in CASES:
-        _, deps, _ = packed_model(Ts)
-        assert acyclic(deps), Ts
+        assert acyclic(packed_model(Ts)[0]), Ts
 
 
 def test_no_wait_can_match_an_earlier_phase():
+    """A barrier's phase is told by its parity, so its completion before must be known when a wait starts."""
     for Ts in CASES:
-        loads, deps, consumer = packed_model(Ts)
-        for i, (kind, n) in enumerate(loads):
-            if i >= NSTAGE:
-                wait = ("wait_K" if kind == "K" else "wait_V", n)
-                assert consumer[i - NSTAGE] in ancestors(deps, wait), (Ts, loads[i], loads[i - NSTAGE])
+        deps, N = packed_model(Ts)
+        for n in range(N):
+            if n >= SLOTS:  # K and V slots: the consumer's use of the load before
+                assert ("S", n - SLOTS) in ancestors(deps, ("wait_K", n)), (Ts, n)
+                assert ("PV", n - SLOTS) in ancestors(deps, ("wait_V", n)), (Ts, n)
+            if n >= 3:
+                # a group waits for P(n-2).V in turn; where it rescales it then waits for P(n-1).V, whose
+                # barrier's completion before is P(n-3).V
+                assert ("PV", n - 3) in ancestors(deps, ("PV_done", n - 2)), (Ts, n)
 
 
-def test_q_behind_the_first_k_tiles_would_deadlock():
-    # a K of a later item takes the slot of a V that only that item's first S frees, which waits for its Q
-    assert not all(acyclic(packed_model(Ts, q_first=False)[1]) for Ts in CASES)
+def test_two_k_tiles_ahead_of_q_would_deadlock_in_a_two_slot_ring():
+    """The order matters: a K ahead of its item's Q may need a slot that a later tile frees only after that Q."""
+    global SLOTS
+    SLOTS, was = 2, SLOTS
+    try:
+        assert not all(acyclic(packed_model(Ts, k_before_q=3)[0]) for Ts in CASES)
+    finally:
+        SLOTS = was

@@ -15,10 +15,9 @@
 // whose keys are cut into several items leaves partials (fp32 O normalised, lse
 // in base 2) in the workspace, which packed_merge_kernel joins in key order.
 //
-// Roles in a CTA (512 threads), shared memory (Q tile, six 32 KB K/V slots)
-// and tensor memory (three S/P buffers, O) follow attn_tc_single_kernel:
-//   warp 8   TMA: the item's Q tile, then its K and V tiles in the order
-//            K_0 K_1 V_0 K_2 V_1 ...;
+// Roles in a CTA (512 threads), shared memory (Q tile, three K and three V tiles of
+// 32 KB) and tensor memory (S 2 x 128 columns, P 2 x 64, O 128):
+//   warp 8   TMA of the item's Q tile and its K tiles;   warp 11   of V tiles;
 //   warp 9   S(n) = Q K_n^T;   warp 10   O += P(n) V_n, and the zeroing of the
 //            rows of V behind the sequence's last key, where another
 //            sequence's rows or unwritten memory lie: P is zero there, but
@@ -43,20 +42,22 @@ namespace pf {
 constexpr int D = 128, BM = 128, BN = 128;
 constexpr int PANEL = BM * 64 * 2;
 constexpr int TILE = 2 * PANEL;
-// Six K/V slots: K(n) takes K(n-3)'s slot, whose release is two tiles back.  (With five, and a second Q buffer
-// in the sixth's place, K(n) waited for V(n-4): its load was only asked for at S(n-1), and the load's 1,000 to
-// 1,500 cycles set the pace, 1,550 cycles a tile.)
-constexpr int NSTAGE = 6;
-constexpr int KAHEAD = 2;                     // K runs two tiles ahead of V
-constexpr int NSBUF = 3;                      // S/P buffers in tensor memory
+// Three slots each for K and V, each kind with a producer warp of its own: K(n) takes K(n-3)'s slot as soon as
+// S(n-3) is done, V(n) takes V(n-3)'s when P(n-3).V is.
+constexpr int NSLOT = 3;
+// S and P have tensor memory of their own, two buffers each: S(n) may be issued when the softmax has read S(n-2).
+// (With P over S in three buffers S(n) waited for P(n-3).V, and the chain P(n) -> P(n).V -> S(n+3) -> softmax set
+// a pace of 1,500 cycles a tile, half as much again as the products take.)
+constexpr int NBUF = 2;
 constexpr int P_PARTS = 2;
 constexpr int KP = BN / P_PARTS;
 constexpr int SMEM_Q = 0;
 constexpr int SMEM_KV = TILE;
-constexpr int SMEM_BAR = SMEM_KV + NSTAGE * TILE;
-// q_full, q_empty, kv_full, kv_empty, s_full, p_part [S buffer][part], o_final, o_free, drain,
-// posted, sums_free, pv_buf [S buffer], m_ready [tile parity][warp]
-constexpr int NBAR = 2 + 2 * NSTAGE + NSBUF + NSBUF * P_PARTS + 5 + NSBUF + 8;
+constexpr int SMEM_V = SMEM_KV + NSLOT * TILE;
+constexpr int SMEM_BAR = SMEM_V + NSLOT * TILE;
+// q_full, q_empty, k_full, k_empty, v_full, v_empty [slot], s_full, s_free [buffer], p_part [buffer][part], o_final,
+// o_free, drain, posted, sums_free, pv_buf [buffer], m_ready [tile parity][warp]
+constexpr int NBAR = 2 + 4 * NSLOT + 2 * NBUF + NBUF * P_PARTS + 5 + NBUF + 8;
 constexpr int SMEM_XCH = (SMEM_BAR + NBAR * 8 + 8 + 15) & ~15;  // + TMEM address, abort flag
 constexpr int SMEM_TOTAL = SMEM_XCH + (BM + 2 * 2 * BM) * 4;    // row max; (l, m) of each group
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory plan exceeds the per-CTA limit");
@@ -66,7 +67,8 @@ constexpr int REGS_SOFTMAX = 176;
 constexpr int REGS_CONTROL = 64;
 constexpr int REGS_EPILOGUE = 96;
 constexpr int TMEM_COLS = 512;
-constexpr int O_COL = NSBUF * BN;
+constexpr int P_COL = NBUF * BN;              // P buffers: 64 columns each
+constexpr int O_COL = P_COL + NBUF * BN / 2;
 constexpr float RESCALE_THRESHOLD = 8.0f;     // log2 units: O is rescaled when the max grows past 2^8
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 }  // namespace pf
@@ -86,15 +88,6 @@ struct PackedFwdParams {
 };
 
 namespace {
-
-// Index of K_t's and V_j's load within an item of T tiles: K_0 K_1, then V_j
-// followed by K_{j+2} while there is one.
-__device__ __forceinline__ uint32_t k_load_at(int t) { return t < pf::KAHEAD ? t : 2 * t - pf::KAHEAD + 1; }
-__device__ __forceinline__ uint32_t v_load_at(int j, int T) {
-    const int lead = T < pf::KAHEAD ? T : pf::KAHEAD;
-    const int more = T > pf::KAHEAD ? T - pf::KAHEAD : 0;
-    return lead + j + (j < more ? j : more);
-}
 
 // exp2 of a difference from a maximum that may be -inf (nothing seen yet): 0 then.
 __device__ __forceinline__ float ex2_from(float m, float m_new) { return m == -INFINITY ? 0.f : ex2(m - m_new); }
@@ -162,17 +155,20 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
     uint64_t *q_empty = q_full + 1;
-    uint64_t *kv_full = q_empty + 1;
-    uint64_t *kv_empty = kv_full + NSTAGE;
-    uint64_t *s_full = kv_empty + NSTAGE;
-    uint64_t *p_part = s_full + NSBUF;     // [S buffer][part], 128 arrivals each
-    uint64_t *o_final = p_part + NSBUF * P_PARTS;
+    uint64_t *k_full = q_empty + 1;
+    uint64_t *k_empty = k_full + NSLOT;
+    uint64_t *v_full = k_empty + NSLOT;
+    uint64_t *v_empty = v_full + NSLOT;
+    uint64_t *s_full = v_empty + NSLOT;
+    uint64_t *s_free = s_full + NBUF;      // the softmax has read S (128 arrivals)
+    uint64_t *p_part = s_free + NBUF;      // [buffer][part], 128 arrivals each
+    uint64_t *o_final = p_part + NBUF * P_PARTS;
     uint64_t *o_free = o_final + 1;        // the epilogue has O in registers (128 arrivals)
     uint64_t *drain = o_free + 1;
     uint64_t *posted = drain + 1;          // both softmax groups posted an item's (l, m)
     uint64_t *sums_free = posted + 1;      // the epilogue has read them
-    uint64_t *pv_buf = sums_free + 1;      // [S buffer]: P.V of the tile in that buffer done
-    uint64_t *m_ready = pv_buf + NSBUF;    // [tile parity][warp % 4]: row max after the tile published
+    uint64_t *pv_buf = sums_free + 1;      // [buffer]: P.V of the P in that buffer done
+    uint64_t *m_ready = pv_buf + NBUF;    // [tile parity][warp % 4]: row max after the tile published
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(m_ready + 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -180,15 +176,18 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int s = 0; s < NSTAGE; s++) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
+        for (int i = 0; i < NSLOT; i++) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
-        for (int b = 0; b < NSBUF; b++) {
+        for (int b = 0; b < NBUF; b++) {
             mbar_init(&s_full[b], 1);
+            mbar_init(&s_free[b], BM);
             mbar_init(&pv_buf[b], 1);
         }
-        for (int q = 0; q < NSBUF * P_PARTS; q++) mbar_init(&p_part[q], BM);
+        for (int q = 0; q < NBUF * P_PARTS; q++) mbar_init(&p_part[q], BM);
         mbar_init(o_final, 1);
         mbar_init(o_free, BM);
         mbar_init(drain, 2);  // one commit per MMA issuer
@@ -213,15 +212,17 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 
     if (warp >= 8 && warp < 12) {
         regs_decrease<REGS_CONTROL>();
-        if (warp == 8) {
-            // -------------------------------------------------- TMA producer
+        if (warp == 8 || warp == 11) {
+            // ------------------------------------- TMA producers: K and Q (8), V (11)
             const bool leader = elect_one();
+            const CUtensorMap *tm = warp == 8 ? &tm_k : &tm_v;
+            uint64_t *full = warp == 8 ? k_full : v_full, *empty = warp == 8 ? k_empty : v_empty;
+            uint8_t *ring = smem + (warp == 8 ? SMEM_KV : SMEM_V);
             if (leader) {
-                prefetch_tmap(&tm_q);
-                prefetch_tmap(&tm_k);
-                prefetch_tmap(&tm_v);
+                prefetch_tmap(tm);
+                if (warp == 8) prefetch_tmap(&tm_q);
             }
-            uint32_t kv_idx = 0;  // K/V tile loads issued
+            uint32_t n = 0;       // tiles loaded
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
             for (uint32_t k = 0; k < walk.rounds && ok; k++) {
@@ -230,46 +231,43 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 if (!walk.at(k, it, hk)) continue;
                 const int T = it.kt1 - it.kt0;
                 if (T <= 0) continue;
-                auto load = [&](const CUtensorMap *tm, int j) -> bool {
-                    const uint32_t slot = kv_idx % NSTAGE;
-                    if (!mbar_wait_w(&kv_empty[slot], ((kv_idx / NSTAGE) & 1) ^ 1, w)) return false;
+                for (int j = 0; j < T && ok; j++, n++) {
+                    const uint32_t slot = n % NSLOT;
+                    if (!(ok = mbar_wait_w(&empty[slot], ((n / NSLOT) & 1) ^ 1, w))) break;
                     if (leader) {
-                        uint8_t *dst = smem + SMEM_KV + slot * TILE;
+                        uint8_t *dst = ring + slot * TILE;
                         const int row = it.krow0 + (it.kt0 + j) * BN;
-                        mbar_arrive_expect_tx(&kv_full[slot], TILE);
-                        tma_load_4d(dst, tm, &kv_full[slot], 0, hk, row, 0);
-                        tma_load_4d(dst + PANEL, tm, &kv_full[slot], 64, hk, row, 0);
+                        mbar_arrive_expect_tx(&full[slot], TILE);
+                        tma_load_4d(dst, tm, &full[slot], 0, hk, row, 0);
+                        tma_load_4d(dst + PANEL, tm, &full[slot], 64, hk, row, 0);
                     }
-                    kv_idx++;
-                    return true;
-                };
-                // Q once the last S of the item before has read its tile; ahead of the first K tiles, since
-                // the slot of K_1 may hold a V that is only freed at this item's first S
-                if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) break;
-                if (leader) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)p.g.rows * 256u);
-                    tma_load_4d(smem + SMEM_Q, &tm_q, q_full, 0, hk * p.g.G, it.tok0, 0);
-                    tma_load_4d(smem + SMEM_Q + PANEL, &tm_q, q_full, 64, hk * p.g.G, it.tok0, 0);
+                    if (j == 0 && warp == 8) {  // Q once the last S of the item before has read its tile
+                        if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) {
+                            n++;  // this tile's load was issued
+                            break;
+                        }
+                        if (leader) {
+                            mbar_arrive_expect_tx(q_full, (uint32_t)p.g.rows * 256u);
+                            tma_load_4d(smem + SMEM_Q, &tm_q, q_full, 0, hk * p.g.G, it.tok0, 0);
+                            tma_load_4d(smem + SMEM_Q + PANEL, &tm_q, q_full, 64, hk * p.g.G, it.tok0, 0);
+                        }
+                        uc++;
+                    }
                 }
-                uc++;
-                for (int t = 0; t < KAHEAD && t < T && ok; t++) ok = load(&tm_k, t);
-                for (int j = 0; j < T && ok; j++) ok = load(&tm_v, j) && (j + KAHEAD >= T || load(&tm_k, j + KAHEAD));
             }
             // every copy issued lands before the CTA can exit
             if (uc > 0) mbar_drain(q_full, (uc - 1) & 1, DRAIN_NS);
-            for (uint32_t idx = kv_idx > NSTAGE ? kv_idx - NSTAGE : 0; idx < kv_idx; idx++)
-                mbar_drain(&kv_full[idx % NSTAGE], (idx / NSTAGE) & 1, DRAIN_NS);
+            for (uint32_t i = n > NSLOT ? n - NSLOT : 0; i < n; i++)
+                mbar_drain(&full[i % NSLOT], (i / NSLOT) & 1, DRAIN_NS);
         } else if (warp == 9 || warp == 10) {
             // ------------------------------------------------- MMA issuers
             const uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
-            const uint32_t sKV = smem_u32(smem + SMEM_KV);
-            const uint64_t dq0 = smem_desc_sw128(smem_u32(smem + SMEM_Q), 16, 1024);  // Q / K: K-major
-            const uint64_t dv0 = smem_desc_sw128(sKV, PANEL, 1024);                   // V: MN-major
-            uint32_t kv_idx = 0;  // K/V loads of earlier items
-            uint32_t tile = 0;    // K/V tiles of earlier items
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(smem + SMEM_Q), 16, 1024);     // Q / K: K-major
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + SMEM_KV), 16, 1024);
+            const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + SMEM_V), PANEL, 1024);  // V: MN-major
+            uint32_t tile = 0;    // key tiles of earlier items
             uint32_t uc = 0;
             bool ok = true;
-            uint32_t vslot[4] = {0, 0, 0, 0};  // warp 9: ring slot of V(m) at m % 4
             for (uint32_t k = 0; k < walk.rounds && ok; k++) {
                 PackedItem it;
                 int hk;
@@ -279,32 +277,27 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 if (warp == 9) {
                     ok = mbar_wait_w(q_full, uc & 1, w);
                     for (int t = 0; t < T && ok; t++) {
-                        const uint32_t n = tile + t;
-                        const uint32_t kidx = kv_idx + k_load_at(t);
-                        vslot[n % 4] = (kv_idx + v_load_at(t, T)) % NSTAGE;
-                        if (n >= NSBUF) {  // S(n)'s buffer held P(n-3): its P.V is done, and V(n-3)'s slot free
-                            if (!(ok = mbar_wait_w(&pv_buf[n % NSBUF], (n / NSBUF - 1) & 1, w))) break;
-                            if (lane == 0) mbar_arrive(&kv_empty[vslot[(n - NSBUF) % 4]]);
-                        }
-                        if (!(ok = mbar_wait_w(&kv_full[kidx % NSTAGE], (kidx / NSTAGE) & 1, w))) break;
+                        const uint32_t n = tile + t, slot = n % NSLOT;
+                        // S(n) takes the buffer of S(n-2), which the softmax has read
+                        if (n >= NBUF && !(ok = mbar_wait_w(&s_free[n % NBUF], (n / NBUF - 1) & 1, w))) break;
+                        if (!(ok = mbar_wait_w(&k_full[slot], (n / NSLOT) & 1, w))) break;
                         tc_fence_after();
-                        const uint64_t kb = dq0 + ((uint64_t)(SMEM_KV - SMEM_Q + (kidx % NSTAGE) * TILE) >> 4);
+                        const uint64_t kb = dk0 + ((uint64_t)(slot * TILE) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; kk++) {
                             const uint64_t off = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
-                            mma_ss_w(tmem + (n % NSBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
+                            mma_ss_w(tmem + (n % NBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
                         }
-                        tc_commit_w(&s_full[n % NSBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
+                        tc_commit_w(&s_full[n % NBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
                     }
                     if (ok) tc_commit_w(q_empty);
                 } else {
                     for (int j = 0; j < T && ok; j++) {
-                        const uint32_t n = tile + j;
-                        const uint32_t vidx = kv_idx + v_load_at(j, T);
-                        if (!(ok = mbar_wait_w(&kv_full[vidx % NSTAGE], (vidx / NSTAGE) & 1, w))) break;
+                        const uint32_t n = tile + j, slot = n % NSLOT;
+                        if (!(ok = mbar_wait_w(&v_full[slot], (n / NSLOT) & 1, w))) break;
                         const int valid = it.Lk - (it.kt0 + j) * BN;
                         if (valid < BN) {  // rows behind the sequence's last key: zero (P is)
-                            uint8_t *v = smem + SMEM_KV + (vidx % NSTAGE) * TILE;
+                            uint8_t *v = smem + SMEM_V + slot * TILE;
                             for (int c = valid * 8 + lane; c < BN * 8; c += 32) {
                                 *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
                                 *reinterpret_cast<uint4 *>(v + PANEL + c * 16) = make_uint4(0, 0, 0, 0);
@@ -312,10 +305,10 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
                         }
-                        const uint64_t vb = dv0 + ((uint64_t)((vidx % NSTAGE) * TILE) >> 4);
-                        const uint32_t pb = tmem + (n % NSBUF) * BN;
+                        const uint64_t vb = dv0 + ((uint64_t)(slot * TILE) >> 4);
+                        const uint32_t pb = tmem + P_COL + (n % NBUF) * (BN / 2);
                         for (int q = 0; q < P_PARTS && ok; q++) {
-                            if (!(ok = mbar_wait_w(&p_part[(n % NSBUF) * P_PARTS + q], (n / NSBUF) & 1, w))) break;
+                            if (!(ok = mbar_wait_w(&p_part[(n % NBUF) * P_PARTS + q], (n / NBUF) & 1, w))) break;
                             // the first product of an item overwrites O: the epilogue before has read it
                             if (j == 0 && q == 0 && uc > 0 && !(ok = mbar_wait_w(o_free, (uc - 1) & 1, w))) break;
                             tc_fence_after();
@@ -325,11 +318,11 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                                          (j > 0 || kk > 0) ? 1u : 0u);
                         }
                         if (!ok) break;
-                        tc_commit_w(&pv_buf[n % NSBUF]);
+                        tc_commit_w(&v_empty[slot]);
+                        tc_commit_w(&pv_buf[n % NBUF]);
                         if (j + 1 == T) tc_commit_w(o_final);
                     }
                 }
-                kv_idx += 2 * T;
                 tile += T;
                 uc++;
             }
@@ -444,7 +437,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tO = lane_base + O_COL;
         const float sl2 = p.scale_log2;
-        uint32_t tile = 0, n_item = 0, kv_idx = 0;
+        uint32_t tile = 0, n_item = 0;
         bool ok = true;
         for (uint32_t k = 0; k < walk.rounds && ok; k++) {
             PackedItem it;
@@ -461,13 +454,13 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             for (int j = 0; j < T; j++) {
                 const uint32_t n = tile + j;
                 if ((int)(n & 1) != hf) continue;
-                const uint32_t tS = lane_base + (n % NSBUF) * BN;
-                if (!mbar_wait(&s_full[n % NSBUF], (n / NSBUF) & 1, w)) {
+                const uint32_t tS = lane_base + (n % NBUF) * BN, tP = lane_base + P_COL + (n % NBUF) * (BN / 2);
+                if (!mbar_wait(&s_full[n % NBUF], (n / NBUF) & 1, w)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (r == 0) mbar_arrive(&kv_empty[(kv_idx + k_load_at(j)) % NSTAGE]);  // K(n) read
+                if (r == 0) mbar_arrive(&k_empty[n % NSLOT]);  // K(n) read
                 if (n > 0) {  // the max after tile n-1, every phase waited for in turn
                     if (!mbar_wait(&m_ready[((n - 1) & 1) * 4 + wq], ((n - 1) >> 1) & 1, w)) {
                         ok = false;
@@ -480,6 +473,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 for (int cc = 0; cc < BN / 32; cc++)
                     tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[cc * 32]));
                 tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(&s_free[n % NBUF]);  // S(n+2) may take the buffer
                 const int rel = lim - (it.kt0 + j) * BN;  // columns below rel are seen
                 if (__any_sync(0xffffffffu, rel < BN)) {
 #pragma unroll
@@ -531,10 +526,17 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                         pk[k / 2] = pack_bf16x2(p0, p1);
                         acc[(k / 2) & 3] = fadd2(acc[(k / 2) & 3], f2(p0, p1));
                     }
-                    tmem_st_cols<KP / 2>(tS + q * (KP / 2), pk);
+                    if (q == 0 && n >= NBUF) {  // P(n) takes the buffer of P(n-2)
+                        if (!mbar_wait(&pv_buf[n % NBUF], (n / NBUF - 1) & 1, w)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    tmem_st_cols<KP / 2>(tP + q * (KP / 2), pk);
                     if (q == 0 && rescale) {
                         // O holds P.V of tiles < n once P(n-1).V is done; rescale it before P(n).V
-                        if (!mbar_wait(&pv_buf[(n - 1) % NSBUF], ((n - 1) / NSBUF) & 1, w)) {
+                        if (!mbar_wait(&pv_buf[(n - 1) % NBUF], ((n - 1) / NBUF) & 1, w)) {
                             ok = false;
                             break;
                         }
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    mbar_arrive(&p_part[(n % NSBUF) * P_PARTS + q]);
+                    mbar_arrive(&p_part[(n % NBUF) * P_PARTS + q]);
                 }
                 if (!ok) break;
                 float a0, a1, b0, b1;
@@ -570,7 +572,6 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             mbar_arrive(posted);
             n_item++;
             tile += T;
-            kv_idx += 2 * T;
         }
     }
     tc_fence_before();
