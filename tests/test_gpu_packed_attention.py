@@ -107,6 +107,84 @@ def test_many_short_sequences():
     Batch(lens, lens, 3, 1, 1, seed=5).forward().check()
 
 
+def test_more_sequences_than_one_block_plans():
+    """Past 1,024 sequences the batch is not cut into stretches but dealt out from a sorted list; a long key range of a
+    few queries among them is split all the same."""
+    g = torch.Generator().manual_seed(1)
+    q = torch.randint(0, 9, (1500,), generator=g).tolist()
+    k = [x + (x % 3) for x in q]
+    q[700], k[700] = 2, 20_000
+    q[3], k[3] = 300, 310
+    b = Batch(q, k, 4, 2, 1, seed=17).forward().check()
+    first = b.out.clone(), b.lse.clone()
+    b.h.packed_replan(b.plan, b.cu_q, b.cu_k)
+    b.forward().h.sync()
+    assert torch.equal(first[0], b.out) and torch.equal(first[1], b.lse)
+
+
+def test_a_batch_too_large_for_stretches():
+    """40 x 512 tokens of 24 heads: more than 256 key tiles a SM, dealt out by load; checked against its own parts."""
+    lens = [512] * 30 + [9000]
+    b = Batch(lens, lens, 24, 24, 1, seed=18)
+    b.forward().h.sync()
+    part = slice(b.pad + 512 * 7, b.pad + 512 * 8)
+    ref, rl, bo, bl = R.attention(b.q[part], b.k[part], b.v[part], [512], [512], 1)
+    R.assert_within(b.out[part], ref, bo, "out")
+    R.assert_within(b.lse[:, part], rl, bl, "lse")
+    last = slice(b.pad + 512 * 30, b.pad + 512 * 30 + 9000)
+    h = 17  # one head of the long sequence, its last 100 queries
+    ref, rl, bo, bl = R.attention(b.q[last, h:h + 1][-100:], b.k[last, h:h + 1], b.v[last, h:h + 1], [100], [9000], 1)
+    R.assert_within(b.out[last, h:h + 1][-100:], ref, bo, "out")
+    assert bool((b.out[:b.pad] == 7.0).all()) and bool(b.out[b.pad:-b.pad].isfinite().all())
+
+
+def test_no_query_rows_or_no_key_rows():
+    from video_dit_long_gb300 import k6attn as K
+    h = K.Handle.for_packed(4)
+    cu = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = lambda n, heads, t=torch.bfloat16: torch.full((n, heads, 128), 3.0, dtype=t, device="cuda")  # noqa: E731
+    p = h.packed_plan(cu(0, 0), cu(0, 5), 0, 5, 2)
+    h.packed_forward(p, e(0, 4), e(5, 2), e(5, 2), e(0, 4), torch.empty((4, 0), device="cuda"))
+    ws = torch.empty(h.packed_backward_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    dk, dv = e(5, 2), e(5, 2)
+    h.packed_backward(p, e(0, 4), e(5, 2), e(5, 2), e(0, 4), e(0, 4), torch.empty((4, 0), device="cuda"), e(0, 4), dk, dv,
+                      workspace=ws)
+    h.sync()
+    assert not dk.any() and not dv.any()
+    p = h.packed_plan(cu(0, 5), cu(0, 0), 5, 0, 2)
+    out, lse = e(5, 4), torch.zeros((4, 5), device="cuda")
+    h.packed_forward(p, e(5, 4), e(0, 2), e(0, 2), out, lse)
+    ws = torch.empty(h.packed_backward_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    dq = e(5, 4)
+    h.packed_backward(p, e(5, 4), e(0, 2), e(0, 2), out, e(5, 4), lse, dq, e(0, 2), e(0, 2), workspace=ws)
+    h.sync()
+    assert not out.any() and bool((lse == -float("inf")).all()) and not dq.any()
+    p = h.packed_plan(cu(0, 0), None, 0, 0, 2)
+    h.packed_forward(p, e(0, 4), e(0, 2), e(0, 2), e(0, 4))
+    h.sync()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """One plan, two streams, a workspace each."""
+    a, b = Batch([3, 200], [6000, 200], 8, 4, 1, seed=19), Batch([3, 200], [6000, 200], 8, 4, 1, seed=20)
+    a.forward().h.sync()
+    b.forward().h.sync()
+    want = a.out.clone(), b.out.clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s, x in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                x.out.fill_(7.0)
+                x.h.packed_forward(a.plan, x.q, x.k, x.v, x.out, x.lse, workspace=x.ws)
+    torch.cuda.synchronize()
+    a.h.sync()
+    b.h.sync()
+    for x, y in zip((a, b), want):
+        n = slice(x.pad, x.out.shape[0] - x.pad)
+        assert torch.equal(x.out[n], y[n])
+
+
 def test_parts_of_a_fused_projection():
     Batch([150, 60], [150, 60], 6, 2, 1, qk="bf16", seed=6, fused=True).forward().check()
 

@@ -136,6 +136,24 @@ def test_a_captured_backward_with_an_eager_one_alive():
             assert torch.equal(x, y)
 
 
+def test_many_sequences():
+    g = torch.Generator().manual_seed(2)
+    lens = torch.randint(0, 30, (1300,), generator=g).tolist()
+    check(backward(Batch(lens, lens, 3, 1, 1, seed=32).forward()))
+
+
+def test_a_wait_limit_of_zero_gives_up():
+    b = Batch([90, 200], [90, 200], 4, 2, 1, seed=33).forward()
+    b.h.sync()
+    b.h.set_option(b.K.OPT_WAIT_LIMIT_NS, 0)
+    backward(b)
+    with pytest.raises(b.K.K6Error) as e:
+        b.h.sync()
+    assert e.value.status == b.K.ERR_TIMEOUT
+    b.h.set_option(b.K.OPT_WAIT_LIMIT_NS, 2_000_000_000)
+    check(backward(b))
+
+
 def test_workspace_and_plan_refusals():
     b = backward(Batch([90], [90], 4, 2, 1, seed=31).forward())
     K = b.K
