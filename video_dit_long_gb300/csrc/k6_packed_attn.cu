@@ -99,7 +99,7 @@ struct Walk {
     const int *sched;   // null: list is this CTA's own
     uint32_t rounds, n_items;
     int slots;          // partials that one slot number stands for (1, or one for every key head)
-    __device__ Walk(const PackedPlan &plan, const PackedGeom &g) {
+    __device__ Walk(const PackedPlan &plan, const PackedGeom &g, bool ok) {
         list = plan.fwd;
         const int mine = plan.count[blockIdx.x];  // beside the header: no wait between the two (the grid is g.sms)
         slots = plan.head->slot_step;
@@ -112,6 +112,7 @@ struct Walk {
             sched = plan.sched + blockIdx.x;
             rounds = (n_items * (uint32_t)g.Hkv + gridDim.x - 1) / gridDim.x;
         }
+        if (!ok) rounds = 0;
     }
     __device__ bool at(uint32_t k, PackedItem &it, int &hk) const {
         uint32_t i = k;
@@ -140,19 +141,12 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     using namespace pf;
     extern __shared__ __align__(1024) uint8_t smem[];
     launch_next_kernel();
-    wait_previous_kernel();
-    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
+        wait_previous_kernel();
         if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_LAYOUT);
         return;
     }
-    if (!packed_plan_ok(*plan.head, p.g)) {
-        if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
-        return;
-    }
-    const Walk walk(plan, p.g);
-    if (walk.rounds == 0) return;
-
+    // barriers and tensor memory are set up while the kernel before this one drains
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + SMEM_BAR);
     uint64_t *q_empty = q_full + 1;
     uint64_t *k_full = q_empty + 1;
@@ -205,6 +199,11 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    wait_previous_kernel();
+    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
+    const bool plan_ok = packed_plan_ok(*plan.head, p.g);
+    if (!plan_ok && threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+    const Walk walk(plan, p.g, plan_ok);  // nothing to walk under a plan that is not this batch's
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
 
     float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
@@ -582,14 +581,17 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     }
 }
 
-// Joins the partials of the split tiles: one warp per row of a split tile,
+// Joins the partials of the split tiles: half a warp per row of a split tile,
+// 32 bytes a lane,
 //   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
+// All rows fit the GPU at once, so that the kernel is two reads deep: the
+// partial's place, then its data.
 __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams p) {
     launch_next_kernel();
     wait_previous_kernel();
     const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
-    const int lane = threadIdx.x & 31;
-    const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 15;
+    const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 4;
     const uint32_t mi = x / (uint32_t)p.g.rows;
     const int r = (int)(x - mi * (uint32_t)p.g.rows);
     if (mi >= (uint32_t)p.g.cap_merge) return;
@@ -598,18 +600,21 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
     if (!packed_plan_ok(head, p.g) || mi >= (uint32_t)head.n_merge) return;  // the attention kernel reported a bad plan
     if (r / p.g.G >= (m.n_tok_hk & 255)) return;
     const long base = (long)m.slot0 * 128 + r, step = (long)head.slot_step * 128;
-    constexpr int kU = 8;  // partials in flight
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kU = 4;  // partials in flight
+    float top = -INFINITY, sum = 0.f, acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) acc[e] = 0.f;
     for (int c = 0; c < m.n; c += kU) {
-        float4 o[kU];
+        float4 o[kU][2];
         float l[kU];
 #pragma unroll
         for (int i = 0; i < kU; i++) {
-            l[i] = -INFINITY, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            l[i] = -INFINITY, o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c + i < m.n) {
-                l[i] = p.part_lse[base + (c + i) * step];
-                o[i] = reinterpret_cast<const float4 *>(p.part_o + (base + (c + i) * step) * 128)[lane];
+                const long row = base + (c + i) * step;
+                l[i] = p.part_lse[row];
+                o[i][0] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane];
+                o[i][1] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane + 1];
             }
         }
         float m_new = top;
@@ -619,20 +624,23 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
         const float old = ex2(top - ref);  // 0 from -inf
         top = m_new;
         sum *= old;
-        acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+#pragma unroll
+        for (int e = 0; e < 8; e++) acc[e] *= old;
 #pragma unroll
         for (int i = 0; i < kU; i++) {
             const float f = ex2(l[i] - ref);
             sum += f;
-            acc.x = fmaf(f, o[i].x, acc.x), acc.y = fmaf(f, o[i].y, acc.y);
-            acc.z = fmaf(f, o[i].z, acc.z), acc.w = fmaf(f, o[i].w, acc.w);
+            const float v[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
+#pragma unroll
+            for (int e = 0; e < 8; e++) acc[e] = fmaf(f, v[e], acc[e]);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long tok = (long)m.tok0 + r / p.g.G;
     const int head_q = (m.n_tok_hk >> 8) * p.g.G + r % p.g.G;
-    *reinterpret_cast<uint2 *>(p.out + tok * p.out_stride + (long)head_q * 128 + lane * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint4 *>(p.out + tok * p.out_stride + (long)head_q * 128 + lane * 8) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
     if (lane == 0 && p.lse)
         p.lse[(long)head_q * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
@@ -673,7 +681,7 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     p.err = t.err;
     e = launch_after(packed_fwd_kernel, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
     if (e != cudaSuccess || g.extra == 0) return e;
-    return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 7) / 8), 256, 0, st, p);
+    return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 15) / 16), 256, 0, st, p);
 }
 
 }  // namespace k6
