@@ -468,6 +468,9 @@ k6attn_status k6attn_forward_static_scratch(k6attn_t h, const void *q, const voi
  *   y = x / sqrt(mean over d (x^2) + eps) * weight     (weights fp32 [d], one
  *       for q and one for k; both NULL: y = x, eps unused),
  *   pair (2i, 2i+1) of axis a's segment turns by p_a * theta^(-2i / axis_dim[a]).
+ * cu, n_seq: as for k6attn_packed_plan, offsets whose first and last bound the
+ *       tokens [cu[0], cu[n_seq]) of the sequences: the rows of other tokens are
+ *       neither read nor written, and enter no sum; cu NULL: all `tokens` rows.
  * A token with positions (0, 0, 0) is not rotated.  Statistics and angles are
  * fp32 or finer, each output element is rounded once.  q, k, q_out, k_out:
  * [tokens][H][d] and [tokens][kv_heads][d]; q and k of the handle's type,
@@ -484,12 +487,14 @@ k6attn_status k6attn_forward_static_scratch(k6attn_t h, const void *q, const voi
  * pointer and stride), dk dk_out.  workspace: at least
  * k6attn_packed_norm_rope_backward_workspace_bytes (0 without weights).
  */
-k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, const int *positions, const void *q,
+k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, const int *cu, int n_seq,
+                                      const int *positions, const void *q,
                                       long q_stride, const void *k, long k_stride, const float *q_weight,
                                       const float *k_weight, float eps, void *q_out, long q_out_stride, void *k_out,
                                       long k_out_stride, k6attn_dtype out_dtype, void *stream);
 size_t k6attn_packed_norm_rope_backward_workspace_bytes(k6attn_t h, long tokens, int kv_heads);
-k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *positions,
+k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *cu, int n_seq,
+                                               const int *positions,
                                                const void *dq_out, long dq_out_stride, const void *dk_out,
                                                long dk_out_stride, const void *q, long q_stride, const void *k,
                                                long k_stride, const float *q_weight, const float *k_weight, float eps,

@@ -123,7 +123,7 @@ def test_more_sequences_than_one_block_plans():
 
 
 def test_a_batch_too_large_for_stretches():
-    """40 x 512 tokens of 24 heads: more than 256 key tiles a SM, dealt out by load; checked against its own parts."""
+    """30 sequences of 512 tokens and one of 9,000, 24 heads: more than 256 key tiles a SM, dealt out by load; checked against its own parts."""
     lens = [512] * 30 + [9000]
     b = Batch(lens, lens, 24, 24, 1, seed=18)
     b.forward().h.sync()
@@ -341,3 +341,30 @@ def test_refusals():
     with pytest.raises(K.K6Error) as e:  # the output over an input
         h.packed_forward(b.plan, b.out, b.k.to(torch.bfloat16), b.v, b.out, b.lse, workspace=b.ws)
     assert e.value.status == K.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("as_pointer", [False, True])
+def test_a_plan_made_on_a_stream_of_its_own(as_pointer):
+    """The plan's memory belongs to the stream that is given: work still running on the current one cannot reach it."""
+    from video_dit_long_gb300 import k6attn as K
+    H, kv, L = 2, 1, 200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((L, n, 128), generator=g, device="cuda").to(torch.bfloat16) for n in (H, kv, kv))
+    cu = torch.tensor([0, 80, L], dtype=torch.int32, device="cuda")
+    h = K.Handle.for_packed(H)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    plan = h.packed_plan(cu, None, L, L, kv, 1)
+    h.packed_forward(plan, q, k, v, want, workspace=torch.empty(h.packed_workspace_bytes(plan), dtype=torch.uint8,
+                                                                device="cuda"))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    room = torch.empty(plan.buffer.numel(), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        room.random_(0, 255)  # on the current stream; freed while it runs
+        del room
+        s = side.cuda_stream if as_pointer else side
+        mine = h.packed_plan(cu, None, L, L, kv, 1, stream=s)
+        h.packed_forward(mine, q, k, v, out, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"), stream=s)
+        h.sync(s)
+        assert torch.equal(out, want)
+        room = torch.empty(plan.buffer.numel(), dtype=torch.uint8, device="cuda")

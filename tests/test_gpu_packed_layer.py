@@ -109,3 +109,46 @@ def test_a_captured_layer_follows_new_lengths():
         assert torch.equal(layer.out, want.out) and torch.equal(d, wd)
         assert torch.equal(layer.dq_weight, want.dq_weight) and torch.equal(layer.dk_weight, want.dk_weight)
     assert keep[0].out.isfinite().all() and keep[1].isfinite().all()
+
+
+def test_rows_behind_a_padded_batch_enter_nothing():
+    """A batch padded with NaN, then one of fewer tokens in the same buffers: padding rows are left as they were, and
+    the weights' gradients are those of the batch alone, to the bit."""
+    from video_dit_long_gb300 import k6attn as K
+    from video_dit_long_gb300.packed import PackedAttention, PackedBatch
+    H, kv, T = 4, 2, 300
+    g = torch.Generator(device="cuda").manual_seed(47)
+    qkv = torch.randn((T, (H + 2 * kv) * 128), generator=g, device="cuda").to(torch.bfloat16)
+    dout = torch.randn((T, H, 128), generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(0, 60, (T, 3), generator=g, device="cuda").to(torch.int32)
+    wq, wk = torch.ones(128, device="cuda"), torch.ones(128, device="cuda")
+    h = K.Handle.for_packed(H)
+    given = torch.tensor([0, 120, 280], dtype=torch.int32, device="cuda")
+    batch = PackedBatch(h, given, T, kv, 1)
+    layer = PackedAttention(batch, wq, wk)
+    for offsets in ([0, 120, 280], [3, 50, 90], [7, 7, 7]):
+        lo, hi = offsets[0], offsets[-1]
+        x, dy, d = (t.clone() for t in (qkv, dout, torch.full_like(qkv, 7.0)))
+        for t in (x, dy):
+            t[:lo], t[hi:] = float("nan"), float("nan")
+        batch.set_offsets(torch.tensor(offsets, dtype=torch.int32))
+        layer.forward(x, pos)
+        layer.backward(dy, x, pos, d)
+        h.sync()
+        assert (d[:lo] == 7).all() and (d[hi:] == 7).all()
+        alone = PackedAttention(PackedBatch(h, [b - a for a, b in zip(offsets, offsets[1:])], T, kv, 1), wq, wk)
+        # the same rows at the same places, other rows zero
+        z, dz, want = torch.zeros_like(qkv), torch.zeros_like(dout), torch.zeros_like(qkv)
+        z[:hi - lo], dz[:hi - lo] = qkv[lo:hi], dout[lo:hi]
+        p = torch.zeros_like(pos)
+        p[:hi - lo] = pos[lo:hi]
+        alone.forward(z, p)
+        alone.backward(dz, z, p, want)
+        h.sync()
+        assert torch.equal(d[lo:hi], want[:hi - lo]) and torch.equal(layer.out[lo:hi], alone.out[:hi - lo])
+        # sums over the tokens in another order: fp32, n <= T H terms of the same sign structure
+        for a, b in ((layer.dq_weight, alone.dq_weight), (layer.dk_weight, alone.dk_weight)):
+            assert a.isfinite().all()
+            assert (a - b).abs().max() <= 2.0 ** -12 * max(1.0, float(b.abs().max()))
+    assert given.tolist() == [0, 120, 280]  # the caller's own
+    assert not layer.dq_weight.any() and not layer.dk_weight.any()  # of no token

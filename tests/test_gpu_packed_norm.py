@@ -176,3 +176,62 @@ def test_out_of_range_and_nan():
     h.packed_norm_rope(x[:, :2], x[:, 2:4], pos, wq, wk, q_out=o, k_out=o2)
     h.sync()
     assert bool(o[1, 0].isnan().all()) and int(o.isnan().sum()) == 128 and not o2.isnan().any()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("lo,hi", [(0, 5), (2, 40), (39, 40), (17, 17), (9, 3)])
+def test_offsets_bound_the_tokens(dtype, d, lo, hi):
+    """With offsets only the tokens between the first and the last are read and written: the others may hold NaN, and
+    the results are those of the same tokens alone."""
+    from video_dit_long_gb300 import k6attn as K
+    T, H, kv, axes = 40, 3, 1, {128: (32, 48, 48), 64: (16, 24, 24)}[d]
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, gq, gk = (torch.randn((T, n, d), generator=g, device="cuda").to(t) for n in (H, kv, H, kv))
+    pos = torch.randint(-9, 90, (T, 3), generator=g, device="cuda").to(torch.int32)
+    wq, wk = (torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    h = K.Handle.for_packed(H, d, dtype, axes)
+    cu = torch.tensor([lo, min(lo, hi), hi], dtype=torch.int32, device="cuda")
+    room = lambda n: torch.empty(h.packed_norm_rope_backward_workspace_bytes(n, kv), dtype=torch.uint8,  # noqa: E731
+                                 device="cuda")
+
+    def both(sel, offsets):
+        n = q[sel].shape[0]
+        a = [x[sel].clone() for x in (q, k, gq, gk)]
+        if offsets is not None:
+            for x in a:
+                x[:lo], x[max(lo, hi):] = float("nan"), float("nan")
+        o = [torch.full_like(x, 7.0) for x in a]
+        dw = [torch.full((d,), 9.0, device="cuda") for _ in range(2)]
+        h.packed_norm_rope(a[0], a[1], pos[sel], wq, wk, q_out=o[0], k_out=o[1], offsets=offsets)
+        h.packed_norm_rope_backward(a[2], a[3], a[0], a[1], pos[sel], wq, wk, dq=o[2], dk=o[3], dq_weight=dw[0],
+                                    dk_weight=dw[1], workspace=room(n), offsets=offsets)
+        h.sync()
+        return o, dw
+
+    got, dw = both(slice(0, T), cu)
+    want, dw1 = both(slice(lo, max(lo, hi)), None)
+    for a, b in zip(got, want):
+        assert torch.equal(a[lo:max(lo, hi)], b)
+        assert (a[:lo] == 7).all() and (a[max(lo, hi):] == 7).all()
+    # at most 120 fp32 terms, in another order: n 2^-24 (sum of their sizes) for each of the two, terms below 30
+    for a, b in zip(dw, dw1):
+        assert (a - b).abs().max() <= 2 * 120 * 2.0 ** -24 * 120 * 30
+
+
+def test_shapes_of_positions_and_offsets_are_checked():
+    from video_dit_long_gb300 import k6attn as K
+    T = 8
+    h = K.Handle.for_packed(2)
+    x = torch.zeros((T, 4, 128), dtype=torch.bfloat16, device="cuda")
+    o = torch.empty_like(x)
+    call = lambda pos, **kw: h.packed_norm_rope(x[:, :2], x[:, 2:], pos, q_out=o[:, :2], k_out=o[:, 2:], **kw)  # noqa: E731
+    pos = torch.zeros((T, 3), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        call(pos.view(3, T))
+    with pytest.raises(ValueError):
+        call(pos, offsets=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(K.K6Error):
+        call(pos, offsets=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(K.K6Error):
+        call(pos, offsets=o.view(torch.int32).view(-1)[:2])  # an output

@@ -17,10 +17,10 @@ def lib():
 
 def test_a_null_handle_is_refused_by_every_call(lib):
     b = ctypes.byref(K.PackedBatch(2, 2, 1, 100, 100))
-    assert lib.k6attn_packed_norm_rope(None, 4, 2, P, P, 512, P, 256, P, P, 1e-6, P, 512, P, 256, K.F16,
-                                       None) == K.ERR_INVALID_ARG
-    assert lib.k6attn_packed_norm_rope_backward(None, 4, 2, P, P, 512, P, 256, P, 512, P, 256, P, P, 1e-6, P, 512, P,
-                                                256, P, P, P, 1 << 20, None) == K.ERR_INVALID_ARG
+    assert lib.k6attn_packed_norm_rope(None, 4, 2, None, 0, P, P, 512, P, 256, P, P, 1e-6, P, 512, P, 256,
+                                       K.F16, None) == K.ERR_INVALID_ARG
+    assert lib.k6attn_packed_norm_rope_backward(None, 4, 2, P, 2, P, P, 512, P, 256, P, 512, P, 256, P, P, 1e-6,
+                                                P, 512, P, 256, P, P, P, 1 << 20, None) == K.ERR_INVALID_ARG
     assert lib.k6attn_packed_plan(None, b, P, P, P, 1 << 20, None) == K.ERR_INVALID_ARG
     assert lib.k6attn_packed_forward(None, b, P, P, 512, P, 256, P, 256, K.F16, P, 512, P, P, 1 << 20,
                                      None) == K.ERR_INVALID_ARG

@@ -186,6 +186,8 @@ cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned bloc
 struct PackedNormRope {
     long tokens;
     int Hkv;
+    const int *cu;                    // [n_seq + 1] offsets that bound the tokens, or null: all of them
+    int n_seq;
     const int *positions;             // [tokens][3]
     const unsigned long long *turns;  // the handle's rotary frequencies
     const void *x[2];                 // [0] queries, [1] keys (the norm's inputs; unused by the backward pass without norm)

@@ -59,8 +59,8 @@ Rows flat(const char *name, const void *p, size_t bytes) {
     return {name, p, p && bytes ? 1 : 0, (long)bytes, (long)bytes, 1};
 }
 
-k6attn_status check_norm(const char *fn, k6attn_t h, long tokens, int kv_heads, const int *positions,
-                         const float *q_weight, const float *k_weight, float eps) {
+k6attn_status check_norm(const char *fn, k6attn_t h, long tokens, int kv_heads, const int *cu, int n_seq,
+                         const int *positions, const float *q_weight, const float *k_weight, float eps) {
     k6attn_status s = check_handle(fn, h);
     if (s != K6ATTN_OK) return s;
     if (tokens < 0 || kv_heads < 1)
@@ -69,12 +69,14 @@ k6attn_status check_norm(const char *fn, k6attn_t h, long tokens, int kv_heads, 
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: %ld tokens of %d + %d heads are too many", fn, tokens, h->g.H,
                          kv_heads);
     if (tokens > 0 && !positions) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null positions", fn);
+    if (cu && (n_seq < 1 || n_seq >= (1 << 24)))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: n_seq must be in [1, 2^24) with offsets", fn);
     if ((q_weight == nullptr) != (k_weight == nullptr))
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: give both norm weights, or neither", fn);
     if (!(eps >= 0.f)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
     if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(q_weight) |
-         reinterpret_cast<uintptr_t>(k_weight)) & 3)
-        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: positions and weights must be 4-byte aligned", fn);
+         reinterpret_cast<uintptr_t>(k_weight) | reinterpret_cast<uintptr_t>(cu)) & 3)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: offsets, positions and weights must be 4-byte aligned", fn);
     return K6ATTN_OK;
 }
 
@@ -94,13 +96,13 @@ k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: mask_block must be in [0, 2^30)", fn);
     if (h->sms > 512) return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: more than 512 SMs", fn);
     if (b->q_tokens >= (1L << 30) || b->k_tokens >= (1L << 30) || b->n_seq >= (1 << 24) ||
-        (b->q_tokens + b->n_seq) * h->g.H >= (1L << 31) || (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31) || b->kv_heads >= (1 << 16))
+        b->kv_heads >= (1 << 16) || (b->q_tokens + b->n_seq) * h->g.H >= (1L << 31) ||
+        (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31))
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: batch too large", fn);
     return K6ATTN_OK;
 }
 
-k6attn_status check_plan(const char *fn, const PackedGeom &g, const void *plan) {
-    (void)g;
+k6attn_status check_plan(const char *fn, const void *plan) {
     if (!plan || !aligned16(plan))
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null plan, or one that is not 16-byte aligned", fn);
     return K6ATTN_OK;
@@ -110,13 +112,14 @@ k6attn_status check_plan(const char *fn, const PackedGeom &g, const void *plan) 
 
 extern "C" {
 
-k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, const int *positions, const void *q,
+k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, const int *cu, int n_seq,
+                                      const int *positions, const void *q,
                                       long q_stride, const void *k, long k_stride, const float *q_weight,
                                       const float *k_weight, float eps, void *q_out, long q_out_stride, void *k_out,
                                       long k_out_stride, k6attn_dtype out_dtype, void *stream) {
     const char *fn = "packed_norm_rope";
     clear_error();
-    k6attn_status s = check_norm(fn, h, tokens, kv_heads, positions, q_weight, k_weight, eps);
+    k6attn_status s = check_norm(fn, h, tokens, kv_heads, cu, n_seq, positions, q_weight, k_weight, eps);
     if (s != K6ATTN_OK) return s;
     const Geom &g = h->g;
     if (out_dtype != g.dtype && !(g.dtype == K6ATTN_BF16 && out_dtype == K6ATTN_F16))
@@ -133,12 +136,13 @@ k6attn_status k6attn_packed_norm_rope(k6attn_t h, long tokens, int kv_heads, con
         const Rows others[] = {in[1 - i], in_place ? flat("", nullptr, 0) : in[i],
                                flat("the positions", positions, (size_t)tokens * 12),
                                flat("a weight", q_weight, q_weight ? g.d * 4 : 0),
-                               flat("a weight", k_weight, k_weight ? g.d * 4 : 0)};
-        if ((s = check_apart(fn, out + i, 1, others, 5)) != K6ATTN_OK) return s;
+                               flat("a weight", k_weight, k_weight ? g.d * 4 : 0),
+                               flat("the offsets", cu, cu ? ((size_t)n_seq + 1) * 4 : 0)};
+        if ((s = check_apart(fn, out + i, 1, others, 6)) != K6ATTN_OK) return s;
     }
     if ((s = check_apart(fn, out, 2, nullptr, 0)) != K6ATTN_OK) return s;
     PackedNormRope p = {};
-    p.tokens = tokens, p.Hkv = kv_heads, p.positions = positions, p.turns = h->turns;
+    p.tokens = tokens, p.Hkv = kv_heads, p.cu = cu, p.n_seq = n_seq, p.positions = positions, p.turns = h->turns;
     p.x[0] = q, p.x_stride[0] = q_stride, p.x[1] = k, p.x_stride[1] = k_stride;
     p.z[0] = q_out, p.z_stride[0] = q_out_stride, p.z[1] = k_out, p.z_stride[1] = k_out_stride;
     p.w[0] = q_weight, p.w[1] = k_weight, p.eps = eps, p.sms = h->sms, p.err = h->err;
@@ -152,7 +156,8 @@ size_t k6attn_packed_norm_rope_backward_workspace_bytes(k6attn_t h, long tokens,
     return packed_norm_rope_bwd_workspace(h->g, tokens, h->sms);
 }
 
-k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *positions,
+k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_heads, const int *cu, int n_seq,
+                                               const int *positions,
                                                const void *dq_out, long dq_out_stride, const void *dk_out,
                                                long dk_out_stride, const void *q, long q_stride, const void *k,
                                                long k_stride, const float *q_weight, const float *k_weight, float eps,
@@ -161,7 +166,7 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
                                                void *stream) {
     const char *fn = "packed_norm_rope_backward";
     clear_error();
-    k6attn_status s = check_norm(fn, h, tokens, kv_heads, positions, q_weight, k_weight, eps);
+    k6attn_status s = check_norm(fn, h, tokens, kv_heads, cu, n_seq, positions, q_weight, k_weight, eps);
     if (s != K6ATTN_OK) return s;
     const Geom &g = h->g;
     const bool norm = q_weight != nullptr;
@@ -194,17 +199,18 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
                           out[1],
                           flat("the positions", positions, (size_t)tokens * 12),
                           flat("a weight", q_weight, norm ? g.d * 4 : 0),
-                          flat("a weight", k_weight, norm ? g.d * 4 : 0)};
-    if ((s = check_apart(fn, wide, 3, fixed, 9)) != K6ATTN_OK) return s;
+                          flat("a weight", k_weight, norm ? g.d * 4 : 0),
+                          flat("the offsets", cu, cu ? ((size_t)n_seq + 1) * 4 : 0)};
+    if ((s = check_apart(fn, wide, 3, fixed, 10)) != K6ATTN_OK) return s;
     for (int i = 0; i < 2; i++) {
         const bool in_place = out[i].p == grad[i].p && out[i].stride == grad[i].stride;
         const Rows others[] = {in[0], in[1], grad[1 - i], in_place ? flat("", nullptr, 0) : grad[i], fixed[6], fixed[7],
-                               fixed[8]};
-        if ((s = check_apart(fn, out + i, 1, others, 7)) != K6ATTN_OK) return s;
+                               fixed[8], fixed[9]};
+        if ((s = check_apart(fn, out + i, 1, others, 8)) != K6ATTN_OK) return s;
     }
     if ((s = check_apart(fn, out, 2, nullptr, 0)) != K6ATTN_OK) return s;
     PackedNormRope p = {};
-    p.tokens = tokens, p.Hkv = kv_heads, p.positions = positions, p.turns = h->turns;
+    p.tokens = tokens, p.Hkv = kv_heads, p.cu = cu, p.n_seq = n_seq, p.positions = positions, p.turns = h->turns;
     p.x[0] = q, p.x_stride[0] = q_stride, p.x[1] = k, p.x_stride[1] = k_stride;
     p.z[0] = const_cast<void *>(dq_out), p.z_stride[0] = dq_out_stride;
     p.z[1] = const_cast<void *>(dk_out), p.z_stride[1] = dk_out_stride;
@@ -232,7 +238,7 @@ k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const i
     if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: offsets must be 4-byte aligned", fn);
     const PackedGeom g = packed_geom(h->g, *batch, h->sms);
-    if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
     const size_t need = packed_plan_bytes(g);
     if (plan_bytes < need)
         return set_error(K6ATTN_ERR_WORKSPACE, "%s: plan of %zu bytes needed, %zu given", fn, need, plan_bytes);
@@ -259,7 +265,7 @@ k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, cons
     if (qk_dtype != K6ATTN_BF16 && qk_dtype != K6ATTN_F16)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: q/k type must be BF16 or F16", fn);
     const PackedGeom g = packed_geom(h->g, *batch, h->sms);
-    if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
     const long wq = (long)g.H * 128, wk = (long)g.Hkv * 128;
     const size_t need = packed_fwd_workspace(g);
     if (need && (!workspace || workspace_bytes < need))
@@ -302,7 +308,7 @@ k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, con
     if (qk_dtype != K6ATTN_BF16 && qk_dtype != K6ATTN_F16)
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: q/k type must be BF16 or F16", fn);
     const PackedGeom g = packed_geom(h->g, *batch, h->sms);
-    if ((s = check_plan(fn, g, plan)) != K6ATTN_OK) return s;
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
     const long wq = (long)g.H * 128, wk = (long)g.Hkv * 128;
     const size_t need = packed_bwd_workspace(g);
     if (!workspace || workspace_bytes < need)

@@ -111,6 +111,8 @@ struct NormRopeArgs {
     Rows x[2], z[2];               // [0] queries, [1] keys.  z: the output, or its gradient
     Rows dx[2];
     const int *positions;          // [tokens][3]
+    const int *cu;                 // [n_seq + 1] offsets: only the tokens between the first and the last; or null
+    int n_seq;
     const unsigned long long *turns;
     int seg1, seg2;                // first pair of the h and w axes
     const float *w[2];             // [d] each, or null: no norm
@@ -132,6 +134,13 @@ __device__ __forceinline__ void cos_sin(const NormRopeArgs &a, long tok, int pai
         const int top = (int)(((unsigned long long)(long long)p * turns) >> 32);  // in [-1/2, 1/2) turns
         sincospif((float)top * 0x1p-31f, &s[k], &c[k]);
     }
+}
+
+// The tokens that belong to a sequence, [r[0], r[1]), where offsets say.  The whole block.
+__device__ __forceinline__ void token_range(const NormRopeArgs &a, int (&r)[2]) {
+    if (!a.cu) return;
+    if (threadIdx.x == 0) r[0] = __ldg(a.cu), r[1] = __ldg(a.cu + a.n_seq);
+    __syncthreads();
 }
 
 // Unit u: which tensor, token, first head and end.
@@ -168,8 +177,11 @@ __global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kerne
     const int lane = threadIdx.x & 31, sub = lane % LPH, grp = lane / LPH;
     const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
     float top = 0.f;
+    __shared__ int range[2];
+    token_range(a, range);
     for (long u = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5; u < a.units; u += nwarps) {
         const Unit un = unit_at(a, u);
+        if (a.cu && (un.tok < range[0] || un.tok >= range[1])) continue;  // padding: whatever it holds
         const char *x0 = a.x[un.t].base + un.tok * a.x[un.t].stride + sub * 16;
         char *z0 = a.z[un.t].base + un.tok * a.z[un.t].stride + sub * 16;
         // z = r (x0 p0 - x1 p1, x0 p2 + x1 p3) for each pair, p the weights times cos and sin
@@ -267,8 +279,11 @@ __global__ void __launch_bounds__(256, BWD_BLOCKS_PER_SM) packed_norm_rope_bwd_k
         }
     };
     int met = 0;  // the tensor that acc belongs to
+    __shared__ int range[2];
+    token_range(a, range);
     for (long u = warp0; u < a.units; u += nwarps) {
         const Unit un = unit_at(a, u);
+        if (a.cu && (un.tok < range[0] || un.tok >= range[1])) continue;  // padding: whatever it holds
         const char *x0 = a.x[un.t].base + un.tok * a.x[un.t].stride + sub * 16;
         const char *z0 = a.z[un.t].base + un.tok * a.z[un.t].stride + sub * 16;
         char *d0 = a.dx[un.t].base + un.tok * a.dx[un.t].stride + sub * 16;
@@ -387,6 +402,7 @@ NormRopeArgs norm_args(const Geom &g, const PackedNormRope &p) {
         a.w[t] = p.w[t];
     }
     a.positions = p.positions;
+    a.cu = p.cu, a.n_seq = p.n_seq;
     a.turns = p.turns;
     a.seg1 = g.axis_dim[0] / 2;
     a.seg2 = (g.axis_dim[0] + g.axis_dim[1]) / 2;

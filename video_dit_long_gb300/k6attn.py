@@ -111,8 +111,9 @@ def load(build_if_missing: bool = True):
     L.k6attn_attention_chunk_groups_bounded.argtypes = [P, P, P, P, P, P, I, P, I, I, P, P, P]
     L.k6attn_seq2head_relayout.argtypes = [P, P, I, ctypes.c_long, I, I, I, I, I, P]
     W, F, B = ctypes.c_long, ctypes.c_float, ctypes.POINTER(PackedBatch)
-    L.k6attn_packed_norm_rope.argtypes = [P, W, I, P, P, W, P, W, P, P, F, P, W, P, W, I, P]
-    L.k6attn_packed_norm_rope_backward.argtypes = [P, W, I, P, P, W, P, W, P, W, P, W, P, P, F, P, W, P, W, P, P, P, Z, P]
+    L.k6attn_packed_norm_rope.argtypes = [P, W, I, P, I, P, P, W, P, W, P, P, F, P, W, P, W, I, P]
+    L.k6attn_packed_norm_rope_backward.argtypes = [P, W, I, P, I, P, P, W, P, W, P, W, P, W, P, P, F, P, W, P, W, P,
+                                                   P, P, Z, P]
     L.k6attn_packed_norm_rope_backward_workspace_bytes.argtypes = [P, W, I]
     L.k6attn_packed_plan.argtypes = [P, B, P, P, P, Z, P]
     L.k6attn_packed_forward.argtypes = [P, B, P, P, W, P, W, P, W, I, P, W, P, P, Z, P]
@@ -158,6 +159,14 @@ def _stream(stream):
     return ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
 
 
+def _torch_stream(stream, device):
+    """The stream of a call as torch's object, or None for the current one."""
+    if stream is None:
+        return None
+    import torch
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
 # element types of the packed calls' tensors: torch's by the library's code, and back (filled at the first handle)
 _DTYPES, _CODES = {}, {}
 
@@ -188,11 +197,11 @@ def _rows(t, shape, dtype, device, what):
     return t.data_ptr(), a if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _vec(t, n, dtype, device, what):
+def _vec(t, shape, dtype, device, what):
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{what}: want a dense {dtype} tensor of {n} values on cuda:{device}, got {t.dtype} "
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: want a dense {dtype} tensor of shape {shape} on cuda:{device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -381,12 +390,15 @@ class Handle:
             return self._dev, self._raw_stream(self._dev)
         return self._dev, _stream(stream)
 
-    def packed_norm_rope(self, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *, q_out, k_out, stream=None):
+    def packed_norm_rope(self, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *, q_out, k_out, offsets=None,
+                         stream=None):
         """Per-head QK-norm (with weights) and (t, h, w) rotation of q [T][H][d] and k [T][kv_heads][d], at
-        positions int32 [T][3], into q_out, k_out (the handle's type or, for bf16, fp16; may be q and k)."""
+        positions int32 [T][3], into q_out, k_out (the handle's type or, for bf16, fp16; may be q and k).  With
+        a batch's offsets (int32, on the device) rows before the first and from the last on are left alone."""
         dev, st = self._packed(stream)
         d, T, kv = self._d, q.size(0), k.size(1)
-        sq, sk, e, f32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32]
+        sq, sk, e, f32, i32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32], _DTYPES["int32"]
+        n = 1 if offsets is None else offsets.numel()
         od = _code(q_out)
         o = q_out.dtype
         pq, lq = _rows(q, sq, e, dev, "q")
@@ -394,9 +406,10 @@ class Handle:
         poq, loq = _rows(q_out, sq, o, dev, "q_out")
         pok, lok = _rows(k_out, sk, o, dev, "k_out")
         s = self._lib.k6attn_packed_norm_rope(
-            self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pq, lq, pk, lk,
-            _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, poq, loq, pok, lok,
-            od, st)
+            self.h, T, kv, _vec(offsets, (n,), i32, dev, "offsets"), n - 1,
+            _vec(positions, (T, 3), i32, dev, "positions"), pq, lq, pk, lk,
+            _vec(q_weight, (d,), f32, dev, "q_weight"), _vec(k_weight, (d,), f32, dev, "k_weight"), eps, poq, loq, pok,
+            lok, od, st)
         if s:
             _check(s)
 
@@ -404,11 +417,12 @@ class Handle:
         return load().k6attn_packed_norm_rope_backward_workspace_bytes(self.h, int(tokens), int(kv_heads))
 
     def packed_norm_rope_backward(self, dq_out, dk_out, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, *,
-                                  dq, dk, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+                                  dq, dk, dq_weight=None, dk_weight=None, workspace=None, offsets=None, stream=None):
         """Gradients of packed_norm_rope: dq, dk (the handle's type) and, with weights, dq_weight, dk_weight (fp32)."""
         dev, st = self._packed(stream)
         d, T, kv = self._d, dq_out.size(0), dk_out.size(1)
-        sq, sk, e, f32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32]
+        sq, sk, e, f32, i32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32], _DTYPES["int32"]
+        n = 1 if offsets is None else offsets.numel()
         pgq, lgq = _rows(dq_out, sq, e, dev, "dq_out")
         pgk, lgk = _rows(dk_out, sk, e, dev, "dk_out")
         pq, lq = (None, 0) if q is None else _rows(q, sq, e, dev, "q")
@@ -417,9 +431,11 @@ class Handle:
         pdk, ldk = _rows(dk, sk, e, dev, "dk")
         ws, nws = _room(workspace, dev)
         s = self._lib.k6attn_packed_norm_rope_backward(
-            self.h, T, kv, _vec(positions, 3 * T, _DTYPES["int32"], dev, "positions"), pgq, lgq, pgk, lgk, pq, lq, pk,
-            lk, _vec(q_weight, d, f32, dev, "q_weight"), _vec(k_weight, d, f32, dev, "k_weight"), eps, pdq, ldq, pdk,
-            ldk, _vec(dq_weight, d, f32, dev, "dq_weight"), _vec(dk_weight, d, f32, dev, "dk_weight"), ws, nws, st)
+            self.h, T, kv, _vec(offsets, (n,), i32, dev, "offsets"), n - 1,
+            _vec(positions, (T, 3), i32, dev, "positions"), pgq, lgq, pgk, lgk, pq, lq, pk, lk,
+            _vec(q_weight, (d,), f32, dev, "q_weight"), _vec(k_weight, (d,), f32, dev, "k_weight"), eps, pdq, ldq, pdk,
+            ldk, _vec(dq_weight, (d,), f32, dev, "dq_weight"), _vec(dk_weight, (d,), f32, dev, "dk_weight"), ws, nws,
+            st)
         if s:
             _check(s)
 
@@ -432,7 +448,8 @@ class Handle:
         n = L.k6attn_packed_plan_bytes(self.h, ctypes.byref(b))
         if not n:
             raise K6Error(ERR_INVALID_ARG, (L.k6attn_last_error() or b"").decode())
-        plan = PackedPlan(b, torch.empty(n, dtype=torch.uint8, device=cu_q.device))
+        with torch.cuda.stream(_torch_stream(stream, self._dev)):  # memory of the stream that writes it first
+            plan = PackedPlan(b, torch.empty(n, dtype=torch.uint8, device=cu_q.device))
         self.packed_replan(plan, cu_q, cu_k, stream=stream)
         return plan
 
@@ -440,8 +457,8 @@ class Handle:
         """Make the plan anew for other offsets of a batch of the same size (in place: captured calls see it)."""
         dev, st = self._packed(stream)
         n, i32 = plan.batch.n_seq + 1, _DTYPES["int32"]
-        _check(load().k6attn_packed_plan(self.h, plan.ref, _vec(cu_q, n, i32, dev, "cu_q"),
-                                         _vec(cu_k, n, i32, dev, "cu_k"), plan.ptr, plan.buffer.numel(), st))
+        _check(load().k6attn_packed_plan(self.h, plan.ref, _vec(cu_q, (n,), i32, dev, "cu_q"),
+                                         _vec(cu_k, (n,), i32, dev, "cu_k"), plan.ptr, plan.buffer.numel(), st))
 
     def packed_workspace_bytes(self, plan) -> int:
         return load().k6attn_packed_workspace_bytes(self.h, plan.ref)
@@ -459,7 +476,7 @@ class Handle:
         ws, nws = _room(workspace, dev)
         s = self._lib.k6attn_packed_forward(
             self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo,
-            _vec(lse, H * plan.q_tokens, _DTYPES[F32], dev, "lse"), ws, nws, st)
+            _vec(lse, (H, plan.q_tokens), _DTYPES[F32], dev, "lse"), ws, nws, st)
         if s:
             _check(s)
 
@@ -482,7 +499,7 @@ class Handle:
         ws, nws = _room(workspace, dev)
         s = self._lib.k6attn_packed_backward(
             self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo, pg, lg,
-            _vec(lse, H * plan.q_tokens, _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st)
+            _vec(lse, (H, plan.q_tokens), _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st)
         if s:
             _check(s)
 

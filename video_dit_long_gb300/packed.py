@@ -31,8 +31,8 @@ class PackedBatch:
         import torch
         self.handle, self.tokens, self.kv_heads = handle, int(tokens), int(kv_heads)
         if not isinstance(lens, torch.Tensor):
-            lens = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
-        self.offsets = lens
+            lens = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+        self.offsets = torch.empty_like(lens, device=handle._dev).copy_(lens)  # its own: set_offsets writes to it
         self.plan = handle.packed_plan(self.offsets, None, self.tokens, self.tokens, self.kv_heads, mask_block)
 
     def set_offsets(self, offsets):
@@ -53,10 +53,10 @@ class PackedAttention:
         T, H, kv, d = batch.tokens, self.h._H, batch.kv_heads, self.h._d
         self.H, self.kv, self.d = H, kv, d
         t = torch.float16 if qk == "f16" else torch.bfloat16
-        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.h._dev)  # noqa: E731
         self.q, self.k = new(T, H, d, dtype=t), new(T, kv, d, dtype=t)
-        self.out, self.lse = torch.zeros((T, H, d), dtype=torch.bfloat16, device="cuda"), new(H, T, dtype=torch.float32)
-        self.dq, self.dk = torch.zeros_like(self.out), torch.zeros((T, kv, d), dtype=torch.bfloat16, device="cuda")
+        self.out, self.lse = new(T, H, d).zero_(), new(H, T, dtype=torch.float32)
+        self.dq, self.dk = new(T, H, d), new(T, kv, d)
         self.dq_weight, self.dk_weight = torch.empty_like(q_weight), torch.empty_like(k_weight)
         room = max(self.h.packed_workspace_bytes(batch.plan), self.h.packed_backward_workspace_bytes(batch.plan),
                    self.h.packed_norm_rope_backward_workspace_bytes(T, kv))
@@ -70,18 +70,19 @@ class PackedAttention:
     def forward(self, qkv, positions):
         """qkv bf16, positions int32 [tokens][3]; returns out [tokens][H][d] (bf16; rows outside the sequences stay)."""
         q, k, v = self.parts(qkv)
-        self.h.packed_norm_rope(q, k, positions, self.q_weight, self.k_weight, self.eps, q_out=self.q, k_out=self.k)
+        self.h.packed_norm_rope(q, k, positions, self.q_weight, self.k_weight, self.eps, q_out=self.q, k_out=self.k,
+                                offsets=self.batch.offsets)
         self.h.packed_forward(self.batch.plan, self.q, self.k, v, self.out, self.lse, workspace=self.workspace)
         return self.out
 
     def backward(self, dout, qkv, positions, dqkv):
-        """The gradients of qkv into dqkv (as qkv; rows outside the sequences get none of v and zero of q and k) and
-        of the norm's weights; returns (dq_weight, dk_weight)."""
+        """The gradients of qkv into dqkv (as qkv; rows outside the sequences stay, and enter nothing) and of the
+        norm's weights; returns (dq_weight, dk_weight)."""
         q, k, v = self.parts(qkv)
         dq, dk, dv = self.parts(dqkv)
         self.h.packed_backward(self.batch.plan, self.q, self.k, v, self.out, dout, self.lse, self.dq, self.dk, dv,
                                workspace=self.workspace)
         self.h.packed_norm_rope_backward(self.dq, self.dk, q, k, positions, self.q_weight, self.k_weight, self.eps,
                                          dq=dq, dk=dk, dq_weight=self.dq_weight, dk_weight=self.dk_weight,
-                                         workspace=self.workspace)
+                                         workspace=self.workspace, offsets=self.batch.offsets)
         return self.dq_weight, self.dk_weight
