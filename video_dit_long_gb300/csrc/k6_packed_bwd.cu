@@ -22,6 +22,12 @@
 // |dS| <= 2 max|dO| max|v|, and the kernels carry dS times the power of two that
 // brings this bound to 2^15; the epilogue takes it out again (exact).  bf16 q/k
 // need none.
+//
+// Seven products are executed for the five of the formulas (S and dP in both
+// kinds of item), so that nothing is summed across CTAs.  25,920 tokens causal by
+// frames of 1,620, 24/8 heads, on one GB300: 11.0 ms, 1.39 PFLOP/s executed, 80 %
+// of a long product's; 3,152 + 1,081 + 257 + 77 + 1 tokens, 24/24 heads: 440 us,
+// 5.5 us an item beyond its steps.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -315,8 +321,11 @@ __device__ __forceinline__ void zero_half_row(__nv_bfloat16 *dst) {
 // 0-127 and 128-255 (dS over each half's first 32 columns), dP 256-383, dQ
 // 384-511.  With two S buffers the MMAs of a step (dP(t+1), dQ(t), S(t+2)) and
 // the row pass (P(t+1) from S(t+1), then dS(t+1) once dP(t+1) is there) run side
-// by side; with one, and S and dP both awaited before a row pass, a step took
-// 2,580 cycles instead of SS-operand reads' 1,750.
+// by side: 2,330 cycles a step, of which its products take 1,536 and shared
+// memory (their operands and the copies) some 1,800.  (One S buffer, and S and dP
+// both awaited before a row pass: 2,580.  Q and dO in tensor memory and steps of
+// 64 keys, for the room: 3,100, since a product of N = 64 takes as long as one of
+// 128.)
 
 namespace dqk {
 constexpr int STAT = 0, KFULL = 1, KEMPTY = 4, VFULL = 7, VEMPTY = 9, SFULL = 11, DPFULL = 13, DSFULL = 14, ACC = 15,
@@ -559,8 +568,8 @@ __device__ __forceinline__ void ds_row(const float (&pr)[64], const float *sd, u
 // S^T 0-127 (P^T over each half's first 32 columns), dP^T 128-255, dV 256-383,
 // dK 384-511.  A step: P^T(t) is published as soon as S^T(t) is read, so that
 // dV(t) and behind it S^T(t+1) run under the second half of the row pass
-// (dS^T(t) from dP^T(t)); that half published, dP^T(t+1) and dK(t) follow under
-// the next row pass.  (With dS^T over dP^T and P^T in shared memory, as in
+// (dS^T(t) from dP^T(t)); that half published, dK(t) and dP^T(t+1) follow under
+// the next row pass: 3,100 cycles a step, its products 2,048.  (With dS^T over dP^T and P^T in shared memory, as in
 // bwd_dkv_kernel, dP^T(t+1) had to wait for dK(t) and the row pass for both: a
 // step took 3,550 cycles.)
 
