@@ -368,3 +368,35 @@ def test_a_plan_made_on_a_stream_of_its_own(as_pointer):
         h.sync(s)
         assert torch.equal(out, want)
         room = torch.empty(plan.buffer.numel(), dtype=torch.uint8, device="cuda")
+
+
+def off16(t):
+    """A copy of t whose first element lies 16 bytes behind a 32-byte boundary."""
+    n, skip = t.numel(), 16 // t.element_size()
+    x = torch.empty(n + skip, dtype=t.dtype, device="cuda")[skip:].view(t.shape)
+    assert n == 0 or x.data_ptr() % 32 == 16
+    return x.copy_(t)
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [([1, 1, 3], [5000, 300, 4097]), ([130, 60], [130, 60])])
+def test_everything_sixteen_byte_aligned_only(q_lens, k_lens):
+    """The alignment that the library asks for, on every tensor and workspace, split key ranges included."""
+    want = Batch(q_lens, k_lens, 4, 2, 1, seed=61).forward()
+    b = Batch(q_lens, k_lens, 4, 2, 1, seed=61)
+    b.q, b.k, b.v, b.out, b.lse, b.ws = (off16(x) for x in (b.q, b.k, b.v, b.out, b.lse, b.ws))
+    b.plan.buffer = off16(b.plan.buffer)
+    b.plan.ptr = b.plan.buffer.data_ptr()
+    b.forward().check()
+    assert torch.equal(b.out[3:-3], want.out[3:-3]) and torch.equal(b.lse[:, 3:-3], want.lse[:, 3:-3])
+    grads = []
+    for x in (want, b):
+        o = [torch.zeros_like(x.q, dtype=torch.bfloat16), torch.zeros_like(x.v), torch.zeros_like(x.v)]
+        room = torch.empty(x.h.packed_backward_workspace_bytes(x.plan), dtype=torch.uint8, device="cuda")
+        dout = x.dout
+        if x is b:
+            o, room, dout = [off16(y) for y in o], off16(room), off16(dout)
+        x.h.packed_backward(x.plan, x.q, x.k, x.v, x.out, dout, x.lse, *o, workspace=room)
+        x.h.sync()
+        grads.append([y[3:-3] for y in o])
+    for x, y in zip(*grads):
+        assert torch.equal(x, y)

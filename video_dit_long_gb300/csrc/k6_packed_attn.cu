@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
 
 size_t packed_fwd_workspace(const PackedGeom &p) {
     const size_t rows = (size_t)p.cap_slots * 128;
-    return round256(rows * 128 * 4) + round256(rows * 4);
+    return rows ? round256(rows * 128 * 4) + round256(rows * 4) + 256 : 0;  // 256: see launch_packed_fwd
 }
 
 cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *out, long out_stride, float *lse,
@@ -678,8 +678,10 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     p.out_stride = out_stride;
     p.lse = lse;
     const size_t rows = (size_t)g.cap_slots * 128;
-    p.part_o = static_cast<float *>(ws);
-    p.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + round256(rows * 128 * 4));
+    // partial rows are stored 32 bytes at a time; the caller's workspace may be 16-byte aligned only
+    char *at = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31);
+    p.part_o = reinterpret_cast<float *>(at);
+    p.part_lse = reinterpret_cast<float *>(at + round256(rows * 128 * 4));
     // Q.K^T operands: bf16 (A/B format 1) or fp16 (format 0)
     p.idesc_qk = idesc_bf16_f32(128, 128, false);
     if (t.qk_f16) p.idesc_qk &= ~((7u << 7) | (7u << 10));
