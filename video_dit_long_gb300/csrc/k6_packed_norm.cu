@@ -23,8 +23,8 @@
 // 16-byte vector each, so its sum of squares is 4 (5) shuffles; a warp takes a
 // run of a token's heads, computes its pairs' sin and cos once per run, and has
 // several vectors a lane in flight.  52,360 tokens on one GB300: forward 24/8
-// heads to fp16 143 us (6.0 TB/s, 88 % of a copy's), backward 24/24 heads 290 us
-// (6.7 TB/s, 98 %).
+// heads to fp16 145 us (5.9 TB/s, 87 % of a copy's), backward 24/24 heads 294 us
+// (6.6 TB/s, 97 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
