@@ -400,3 +400,27 @@ def test_everything_sixteen_byte_aligned_only(q_lens, k_lens):
         grads.append([y[3:-3] for y in o])
     for x, y in zip(*grads):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("Hkv", [4, 1])
+def test_a_plan_of_a_smaller_batch_is_reported_and_nothing_is_written(Hkv):
+    """A call whose batch has more sequences, tokens and split tiles than the plan it is given was made for: its lists
+    would lie behind the end of that plan, in memory that holds anything."""
+    small, big = Batch([1], [1], 4, 4, 1, seed=62), Batch([1, 200], [9000, 5000], 4, Hkv, 1, seed=63)
+    assert small.plan.buffer.numel() < big.plan.buffer.numel() and big.ws.numel() > 0
+    room = torch.full_like(big.plan.buffer, 255)
+    room[:small.plan.buffer.numel()] = small.plan.buffer
+    p = big.K.PackedPlan(big.plan.batch, room)
+    big.h.packed_forward(p, big.q, big.k, big.v, big.out, big.lse, workspace=big.ws)
+    with pytest.raises(big.K.K6Error) as e:
+        big.h.sync()
+    assert e.value.status == big.K.ERR_INVALID_ARG
+    assert bool((big.out == 7.0).all()) and bool((big.lse == 7.0).all())
+    grads = [torch.full(x.shape, 7.0, dtype=torch.bfloat16, device="cuda") for x in (big.q, big.k, big.v)]
+    ws = torch.empty(big.h.packed_backward_workspace_bytes(big.plan), dtype=torch.uint8, device="cuda")
+    big.h.packed_backward(p, big.q, big.k, big.v, big.out, big.dout, big.lse, *grads, workspace=ws)
+    with pytest.raises(big.K.K6Error) as e:
+        big.h.sync()
+    assert e.value.status == big.K.ERR_INVALID_ARG
+    assert all(bool((x == 7.0).all()) for x in grads)
+    big.forward().check()  # its own plan still serves

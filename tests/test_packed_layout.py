@@ -1,0 +1,65 @@
+"""Where a plan's parts lie in its buffer, from the library's own host code: what
+a kernel reads of a plan before its header has shown whose it is must lie in
+every plan, also in one of a smaller batch."""
+import itertools
+import os
+import subprocess
+
+import pytest
+
+from video_dit_long_gb300 import build as B
+
+SOURCE = r"""
+#include <cstdio>
+#include "k6_packed.cuh"
+// lines of: H kv_heads n_seq q_tokens k_tokens sms
+int main() {
+    int H, kv, n, sms;
+    long q, k;
+    while (scanf("%d %d %d %ld %ld %d", &H, &kv, &n, &q, &k, &sms) == 6) {
+        k6::Geom g = {};
+        g.H = H, g.d = 128;
+        const k6attn_packed b = {n, kv, 1, q, k};
+        const k6::PackedGeom p = k6::packed_geom(g, b, sms);
+        const k6::PackedPlan at = k6::packed_plan_at(nullptr, p);
+        printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d\n", k6::packed_plan_bytes(p), k6::packed_plan_common_bytes(sms),
+               (size_t)at.count, (size_t)at.merge, (size_t)at.fwd, (size_t)at.sched, (size_t)at.q, (size_t)at.k,
+               sizeof(k6::PackedMerge), p.cap_merge);
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def program(tmp_path_factory):
+    lib = B.build()
+    d = tmp_path_factory.mktemp("layout")
+    (d / "layout.cu").write_text(SOURCE)
+    cmd = [B.NVCC, *B.ARCH, "-std=c++17", "-I", B.INCLUDE, "-I", B.CSRC, str(d / "layout.cu"), "-o", str(d / "layout"), lib,
+           "-Xlinker", "-rpath," + os.path.dirname(lib)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return str(d / "layout")
+
+
+CASES = [(H, kv, n, q, k, sms)
+         for (H, kv), (n, q, k), sms in itertools.product(
+             [(1, 1), (4, 2), (24, 1), (24, 8), (24, 24), (128, 1)],
+             [(1, 0, 1), (1, 1, 1), (3, 208, 208), (12, 12, 150000), (2, 864, 13824), (1, 25920, 25920), (2000, 9000, 9000)],
+             [152, 7, 512])]
+
+
+def test_every_plan_holds_what_is_read_before_its_header_is_checked(program):
+    text = "\n".join(" ".join(map(str, c)) for c in CASES)
+    out = subprocess.run([program], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(out) == len(CASES)
+    common = {}
+    for c, line in zip(CASES, out):
+        size, shared, count, merge, fwd, sched, q, k, each, cap = map(int, line.split())
+        sms = c[-1]
+        # the same places in every plan of a GPU: header, counts, the first `sms` split tiles
+        assert common.setdefault(sms, (shared, count, merge)) == (shared, count, merge)
+        assert count == 256 and merge >= count + 4 * sms and merge % 16 == 0
+        assert merge + sms * each == shared <= size, c
+        # and room for all of this batch's split tiles, in front of the lists whose places depend on the batch
+        assert merge + max(cap, sms) * each <= fwd <= sched <= q <= k <= size, c

@@ -55,12 +55,26 @@ struct __align__(16) PackedMerge {
 struct PackedPlan {
     PackedHeader *head;
     int *count;         // [sms]: forward items of each CTA
+    PackedMerge *merge; // [packed_merge_rows]
     PackedItem *fwd;    // [sms][cap_rows] items of each CTA, or [cap_q + extra] for every key head, heaviest first
     int *sched;         // sorted list: [round][sms] the (key head * n_fwd + item) of each CTA, or -1
     PackedItem *q;      // [cap_q], unsplit (backward), heaviest first
     PackedKItem *k;     // [cap_k], heaviest first
-    PackedMerge *merge; // [cap_merge]
 };
+
+// Split tiles a plan has room for: one per SM at least, whatever the batch.
+static inline __host__ __device__ int packed_merge_rows(const PackedGeom &p) {
+    return p.cap_merge > p.sms ? p.cap_merge : p.sms;
+}
+
+// The start of every plan on a GPU of `sms` SMs, of any batch: the header, the
+// CTAs' counts and the first `sms` split tiles.  A kernel may read this much, and
+// no more, before the header has told it that the plan is its batch's: the lists
+// behind it lie where the batch's sizes put them, and a plan of a smaller batch
+// ends before a larger one's.
+static inline __host__ __device__ size_t packed_plan_common_bytes(int sms) {
+    return PACKED_HEADER_BYTES + ((size_t)sms * sizeof(int) + 15) / 16 * 16 + (size_t)sms * sizeof(PackedMerge);
+}
 
 static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const PackedGeom &p) {
     PackedPlan r;
@@ -69,6 +83,8 @@ static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const Pa
     b += PACKED_HEADER_BYTES;
     r.count = reinterpret_cast<int *>(b);
     b += ((size_t)p.sms * sizeof(int) + 15) / 16 * 16;
+    r.merge = reinterpret_cast<PackedMerge *>(b);
+    b += (size_t)packed_merge_rows(p) * sizeof(PackedMerge);
     r.fwd = reinterpret_cast<PackedItem *>(b);
     b += (size_t)p.cap_fwd * sizeof(PackedItem);
     r.sched = reinterpret_cast<int *>(b);
@@ -76,8 +92,6 @@ static inline __host__ __device__ PackedPlan packed_plan_at(void *base, const Pa
     r.q = reinterpret_cast<PackedItem *>(b);
     b += (size_t)p.cap_q * sizeof(PackedItem);
     r.k = reinterpret_cast<PackedKItem *>(b);
-    b += (size_t)p.cap_k * sizeof(PackedKItem);
-    r.merge = reinterpret_cast<PackedMerge *>(b);
     return r;
 }
 

@@ -108,7 +108,7 @@ struct Walk {
     int slots;          // partials that one slot number stands for (1, or one for every key head)
     __device__ Walk(const PackedPlan &plan, const PackedGeom &g, bool ok) {
         list = plan.fwd;
-        const int mine = plan.count[blockIdx.x];  // beside the header: no wait between the two (the grid is g.sms)
+        const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
         slots = plan.head->slot_step;
         n_items = (uint32_t)plan.head->n_fwd;
         if (plan.head->stream) {
@@ -602,9 +602,14 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
     const uint32_t mi = x / (uint32_t)p.g.rows;
     const int r = (int)(x - mi * (uint32_t)p.g.rows);
     if (mi >= (uint32_t)p.g.cap_merge) return;
-    const PackedMerge m = plan.merge[mi];  // beside the header: no wait between the two
+    // the first p.g.sms split tiles lie in every plan (packed_plan_common_bytes): read beside the header, with no wait
+    // between the two; those behind them only once the header has shown that the plan is this batch's
+    const bool early = mi < (uint32_t)p.g.sms;
+    PackedMerge m;
+    if (early) m = plan.merge[mi];
     const PackedHeader head = *plan.head;
     if (!packed_plan_ok(head, p.g) || mi >= (uint32_t)head.n_merge) return;  // the attention kernel reported a bad plan
+    if (!early) m = plan.merge[mi];
     if (r / p.g.G >= (m.n_tok_hk & 255)) return;
     const long base = (long)m.slot0 * 128 + r, step = (long)head.slot_step * 128;
     constexpr int kU = 4;  // partials in flight

@@ -63,7 +63,7 @@ PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
 
 size_t packed_plan_bytes(const PackedGeom &p) {
     const PackedPlan at = packed_plan_at(nullptr, p);
-    return reinterpret_cast<size_t>(at.merge) + (size_t)p.cap_merge * sizeof(PackedMerge);
+    return reinterpret_cast<size_t>(at.k) + (size_t)p.cap_k * sizeof(PackedKItem);
 }
 
 namespace {
