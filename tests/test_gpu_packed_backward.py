@@ -171,3 +171,9 @@ def test_workspace_and_plan_refusals():
     with pytest.raises(K.K6Error) as e:
         b.h.sync()
     assert e.value.status == K.ERR_INVALID_ARG and bool((b.dq == 7.0).all())
+
+
+@pytest.mark.parametrize("qk", ["f16", "bf16"])
+@pytest.mark.parametrize("block", [0, 1])
+def test_few_queries_over_long_caches(qk, block):
+    check(backward(Batch([3, 1, 8], [9000, 20000, 4097], 8, 4, block, qk=qk, seed=34).forward()))

@@ -1,6 +1,8 @@
-"""Where a plan's parts lie in its buffer, from the library's own host code: what
-a kernel reads of a plan before its header has shown whose it is must lie in
-every plan, also in one of a smaller batch."""
+"""Host-side sizes of the packed calls, from the library's own code.
+
+Where a plan's parts lie in its buffer: what a kernel reads of a plan before its
+header has shown whose it is must lie in every plan, also in one of a smaller
+batch.  And the blocks of the backward pass's pre-pass."""
 import itertools
 import os
 import subprocess
@@ -22,9 +24,10 @@ int main() {
         const k6attn_packed b = {n, kv, 1, q, k};
         const k6::PackedGeom p = k6::packed_geom(g, b, sms);
         const k6::PackedPlan at = k6::packed_plan_at(nullptr, p);
-        printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d\n", k6::packed_plan_bytes(p), k6::packed_plan_common_bytes(sms),
+        printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d %u %u\n", k6::packed_plan_bytes(p), k6::packed_plan_common_bytes(sms),
                (size_t)at.count, (size_t)at.merge, (size_t)at.fwd, (size_t)at.sched, (size_t)at.q, (size_t)at.k,
-               sizeof(k6::PackedMerge), p.cap_merge);
+               sizeof(k6::PackedMerge), p.cap_merge, k6::packed_bwd_rows_blocks(p, true),
+               k6::packed_bwd_rows_blocks(p, false));
     }
 }
 """
@@ -49,13 +52,17 @@ CASES = [(H, kv, n, q, k, sms)
              [152, 7, 512])]
 
 
-def test_every_plan_holds_what_is_read_before_its_header_is_checked(program):
-    text = "\n".join(" ".join(map(str, c)) for c in CASES)
+def sizes(program, cases):
+    text = "\n".join(" ".join(map(str, c)) for c in cases)
     out = subprocess.run([program], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
-    assert len(out) == len(CASES)
+    assert len(out) == len(cases)
+    return [list(map(int, line.split())) for line in out]
+
+
+def test_every_plan_holds_what_is_read_before_its_header_is_checked(program):
     common = {}
-    for c, line in zip(CASES, out):
-        size, shared, count, merge, fwd, sched, q, k, each, cap = map(int, line.split())
+    for c, got in zip(CASES, sizes(program, CASES)):
+        size, shared, count, merge, fwd, sched, q, k, each, cap = got[:10]
         sms = c[-1]
         # the same places in every plan of a GPU: header, counts, the first `sms` split tiles
         assert common.setdefault(sms, (shared, count, merge)) == (shared, count, merge)
@@ -63,3 +70,11 @@ def test_every_plan_holds_what_is_read_before_its_header_is_checked(program):
         assert merge + sms * each == shared <= size, c
         # and room for all of this batch's split tiles, in front of the lists whose places depend on the batch
         assert merge + max(cap, sms) * each <= fwd <= sched <= q <= k <= size, c
+
+
+def test_the_pre_pass_of_few_queries_over_long_caches_fills_the_gpu(program):
+    """With fp16 q and k it takes the norms of every row of v, whatever the number of queries."""
+    for H, kv, k in ((24, 4, 134000), (8, 1, 52360), (24, 24, 9000)):
+        (got,) = sizes(program, [(H, kv, 3, 12, k, 152)])
+        assert got[10] >= 2 * 152, (H, kv, k, got[10])
+        assert 1 <= got[11] <= got[10]

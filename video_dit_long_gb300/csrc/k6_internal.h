@@ -240,6 +240,7 @@ cudaError_t launch_packed_fwd(const PackedGeom &p, const PackedPtrs &t, void *ou
                               void *ws, cudaStream_t st, const char **why);
 
 size_t packed_bwd_workspace(const PackedGeom &p);
+unsigned packed_bwd_rows_blocks(const PackedGeom &p, bool norms);  // of the backward pass's pre-pass
 cudaError_t launch_packed_bwd(const PackedGeom &p, const PackedPtrs &t, const void *out, long out_stride,
                               const void *dout, long dout_stride, const float *lse, void *dq, long dq_stride,
                               void *dk, long dk_stride, void *dv, long dv_stride, void *ws, cudaStream_t st,

@@ -832,9 +832,11 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
 
 }  // namespace
 
-// Blocks of the pre-pass: each leaves two norms, which every block of the main kernel reads.
-static unsigned rows_blocks(const PackedGeom &g) {
-    const long want = ((long)g.Tq * g.H + 63) / 64;
+// Blocks of the pre-pass, from the longer of its two reads (with norms it takes all of v too, which a few new
+// tokens over long caches have far more of): each leaves two norms, which every block of the main kernel reads.
+unsigned packed_bwd_rows_blocks(const PackedGeom &g, bool norms) {
+    const long q = (long)g.Tq * g.H, v = norms ? (long)g.Tk * g.Hkv : 0;
+    const long want = ((q > v ? q : v) + 63) / 64;
     return (unsigned)(want < 4L * g.sms ? want : 4L * g.sms);
 }
 
@@ -864,7 +866,7 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     if (e != cudaSuccess) return e;
     float2 *LD = static_cast<float2 *>(ws);
     float *norms = reinterpret_cast<float *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
-    const unsigned n_rows = rows_blocks(g);
+    const unsigned n_rows = packed_bwd_rows_blocks(g, t.qk_f16);
     if (g.Tq) {
         auto rows = [&](auto kernel) {
             kernel<<<n_rows, 256, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
