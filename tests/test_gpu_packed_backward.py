@@ -177,3 +177,20 @@ def test_workspace_and_plan_refusals():
 @pytest.mark.parametrize("block", [0, 1])
 def test_few_queries_over_long_caches(qk, block):
     check(backward(Batch([3, 1, 8], [9000, 20000, 4097], 8, 4, block, qk=qk, seed=34).forward()))
+
+
+@pytest.mark.parametrize("qk", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** 66, 2.0 ** 100])
+@pytest.mark.parametrize("block", [0, 1])
+def test_gradients_whose_squares_leave_fp32(qk, size, block):
+    """bf16 holds dout whose squared norm is 0 or infinite in fp32."""
+    b = Batch([300, 40], [300, 40], 6, 2, block, qk=qk, seed=35).forward()
+    b.dout = (b.dout.float() * size).to(torch.bfloat16)
+    check(backward(b))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** 66])
+def test_values_whose_squares_leave_fp32(size):
+    b = Batch([200, 40], [200, 40], 4, 2, 1, seed=36)
+    b.v = (b.v.float() * size).to(torch.bfloat16)
+    check(backward(b.forward()))

@@ -56,7 +56,7 @@ struct PackedBwdParams {
     const void *plan;
     float scale_log2, scale;                // log2(e)/sqrt(d), 1/sqrt(d)
     const float2 *LD;                       // [Hkv][Tq * G] {lse * log2(e), D}; lse = +inf for a row that sees nothing
-    const float *norms;                     // [2][n_norms]: parts of max |dO_i|^2 and max |v_j|^2, or null: no scale
+    const float *norms;                     // [2][n_norms]: log2 of parts of max |dO_i| and max |v_j|, or null: no scale
     int n_norms;
     uint32_t dkv_blocks;                    // blocks of key tiles, ahead of those of query tiles
     __nv_bfloat16 *dq, *dk, *dv;
@@ -101,11 +101,34 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
                  : "memory");
 }
 
-// The power of two that dS is carried with: 2^e, 2 max|dO| max|v| 2^e in (2^14, 2^15].
-// A whole warp.
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// log2 of the 2-norm of a row of 128 bf16 values, 8 in each lane (`x`) of half a
+// warp, whose squares sum to `q`: -inf for zeros, inf or NaN where the row is
+// not finite.  Squares leave fp32's range long before bf16 values do: where they
+// come near its ends they are summed again from scaled values.
+__device__ __forceinline__ float log2_norm(float q, const uint4 &x, int lane) {
+    if (q >= 0x1p-80f && q <= 0x1p120f) return 0.5f * log2f(q);
+    const int shift = q > 1.f ? -70 : 70;
+    const float by = pow2(shift);
+    const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x);
+    q = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 f = __bfloat1622float2(v[k]);
+        q = fmaf(f.x * by, f.x * by, fmaf(f.y * by, f.y * by, q));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffu << (lane & 16), q, o, 16);
+    return 0.5f * log2f(q) - (float)shift;
+}
+
+// The power of two that dS is carried with: 2^e, 2 max|dO| max|v| 2^e in (2^14, 2^15], |e| <= 100 (gradients of
+// 2^-100 and 2^100 are far outside what else fp32 holds of them).  A whole warp.
 __device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
     if (!p.norms) return 0;
-    float a = 0.f, b = 0.f;
+    float a = -INFINITY, b = -INFINITY;
     for (int i = threadIdx.x & 31; i < p.n_norms; i += 32) {
         a = fmaxf(a, p.norms[i]);
         b = fmaxf(b, p.norms[p.n_norms + i]);
@@ -115,16 +138,13 @@ __device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
     }
-    // the product of the squares may leave fp32: add exponents instead
-    if (!(a > 0.f) || !(b > 0.f)) return 60;  // all zero, or squares below fp32
-    const int e = 14 - (int)ceilf(0.5f * (log2f(a) + log2f(b)));
-    return max(-60, min(60, e));
+    return (int)fmaxf(-100.f, fminf(100.f, 14.f - ceilf(a + b)));  // 100 where all of either is zero
 }
 
 // -------------------------------------------------------------- pre-pass
 
-// LD of every query row of the sequences, and for fp16 q/k each block's largest
-// squared row norms of dO and v (finite ones: a row that is not makes its own
+// LD of every query row of the sequences, and for fp16 q/k log2 of each block's
+// largest row norms of dO and v (finite ones: a row that is not makes its own
 // results NaN, whatever the scale) in norms[2][gridDim].  Half a warp (16 lanes x
 // 8 elements) covers one row, kU rows in flight.  Bound by HBM.
 template <bool NORMS>
@@ -143,7 +163,7 @@ __global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g
     // the host keeps tokens * heads below 2^31
     const uint32_t rows = (uint32_t)(plan.head->q_hi - q_lo) * (uint32_t)g.H;
     const uint32_t vrows = NORMS ? (uint32_t)(plan.head->k_hi - k_lo) * (uint32_t)g.Hkv : 0;
-    float top_do = 0.f, top_v = 0.f;
+    float top_do = -INFINITY, top_v = -INFINITY;
     // both halves of a warp run the same number of rounds (the shuffles need all lanes)
     for (uint32_t base = 0; base < rows; base += halves * kU) {
         uint4 a[kU], b[kU];
@@ -177,11 +197,12 @@ __global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g
                 s += __shfl_xor_sync(0xffffffffu, s, o, 16);
                 if (NORMS) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
             }
+            const float n = NORMS ? log2_norm(q, b[i], lane) : 0.f;
             if (base + i * halves + half < rows && sub == 0) {
                 LD[((long)(h[i] / g.G) * g.Tq + tok[i]) * g.G + h[i] % g.G] =
                     make_float2(l[i] == -INFINITY ? INFINITY : l[i] * pb::LOG2E, s);
                 // a row that sees nothing has no say in the scale
-                if (NORMS && l[i] > -INFINITY && q < INFINITY) top_do = fmaxf(top_do, q);
+                if (NORMS && l[i] > -INFINITY && n < INFINITY) top_do = fmaxf(top_do, n);
             }
         }
     }
@@ -206,7 +227,8 @@ __global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g
                 }
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
-                if (q < INFINITY) top_v = fmaxf(top_v, q);
+                const float n = log2_norm(q, a[i], lane);
+                if (n < INFINITY) top_v = fmaxf(top_v, n);
             }
         }
         __shared__ float tops[2][8];
@@ -218,7 +240,7 @@ __global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g
         if (lane == 0) tops[0][threadIdx.x >> 5] = top_do, tops[1][threadIdx.x >> 5] = top_v;
         __syncthreads();
         if (threadIdx.x < 2) {
-            float m = 0.f;
+            float m = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 8; w++) m = fmaxf(m, tops[threadIdx.x][w]);
             norms[threadIdx.x * gridDim.x + blockIdx.x] = m;
@@ -500,7 +522,7 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         }
         if (ok && mbar_wait(bar + ACC, 0, w)) {
             tc_fence_after();
-            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), [&](int i) {
+            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * pow2(-e), [&](int i) {
                 const int rr = 32 * q4 + i;
                 const int tk = (int)(((uint32_t)rr * p.inv_g) >> 16);  // rr / G
                 return tk < it.n_tok_hk && rr < p.g.rows
@@ -732,7 +754,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
         const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
         const float sl2 = p.scale_log2;
         const int e = ds_exponent(p);
-        const float sc = exp2f((float)e);
+        const float sc = pow2(e);
         // the first query row (of the sequence, tokens x heads) that sees this key
         const long first = (long)packed_first_query(it.key0 + r, it.off, p.g.block) * p.g.G;
         // this thread's row of dS^T panel g: 8 chunks of 16 bytes, 128-byte swizzle
@@ -797,7 +819,7 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
                     return rr < it.n_key ? base + ((long)it.krow0 + rr) * stride + (long)hk * D + 64 * g : nullptr;
                 };
             };
-            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * exp2f((float)-e), row_of(p.dk, p.dk_stride));
+            store_rows(lb + 384 + 64 * g, smem + warp * 4096, lane, p.scale * pow2(-e), row_of(p.dk, p.dk_stride));
             store_rows(lb + 256 + 64 * g, smem + warp * 4096, lane, 1.0f, row_of(p.dv, p.dv_stride));
         }
     }
@@ -840,7 +862,7 @@ unsigned packed_bwd_rows_blocks(const PackedGeom &g, bool norms) {
     return (unsigned)(want < 4L * g.sms ? want : 4L * g.sms);
 }
 
-// Workspace: LD, then the blocks' squared norms.
+// Workspace: LD, then the blocks' norms.
 size_t packed_bwd_workspace(const PackedGeom &p) {
     return round256((size_t)p.Tq * p.H * sizeof(float2)) + round256((size_t)p.sms * 4 * 2 * sizeof(float));
 }
