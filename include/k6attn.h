@@ -566,9 +566,13 @@ k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, cons
  * their key head.  dout must be finite.  Gradients overlap no input and one
  * another nowhere.  The same bits in every run.  workspace: at least
  * k6attn_packed_backward_workspace_bytes.
- * P is rounded to bf16 and dS to qk_dtype before their products (for F16, dS is
- * carried times a power of two that follows max |dout| and max |v|, so that
- * small gradients do not vanish); products accumulate in fp32.
+ * P is rounded to bf16 and dS to qk_dtype before their products, which
+ * accumulate in fp32.  For F16 each row of dq and of dk has its dS carried times
+ * a power of two of its own, from the largest |dout_i| |v_j| and
+ * |dout_i . out_i| that enter the row, so that small gradients keep their
+ * precision beside large ones: dS keeps fp16's 11 bits down to 2^-28 of twice
+ * that largest, and loses them below.  The scale follows products |dout| |v| from
+ * 2^-86 to 2^114.  The gradients of a sequence depend on no other one.
  */
 size_t k6attn_packed_backward_workspace_bytes(k6attn_t h, const k6attn_packed *batch);
 k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,

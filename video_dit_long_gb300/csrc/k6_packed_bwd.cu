@@ -18,9 +18,13 @@
 // memory before they enter a product over rows, since 0 * NaN is not 0.
 //
 // fp16 q/k: dS must have K's and Q's type, and gradients are often far below
-// fp16's 2^-24.  The pre-pass takes max |dO_i| and max |v_j|, which bound
-// |dS| <= 2 max|dO| max|v|, and the kernels carry dS times the power of two that
-// brings this bound to 2^15; the epilogue takes it out again (exact).  bf16 q/k
+// fp16's 2^-24.  |dS_ij| <= |dO_i| |v_j| + |D_i|, so each row of an accumulator is
+// carried times a power of two of its own that brings this bound to 2^15, and the
+// epilogue takes it out again (exact): a row of dQ takes |dO_i|, |D_i| and the
+// largest |v_j| of its key tiles; a row of dK takes |v_j| and the largest |dO_i|
+// and |D_i| of the queries that see its key.  So a small gradient keeps its bits
+// beside large ones, and a sequence's gradients do not depend on the others.  The
+// pre-pass leaves the logarithms of these norms by row, token and tile.  bf16 q/k
 // need none.
 //
 // Seven products are executed for the five of the formulas (S and dP in both
@@ -51,13 +55,23 @@ constexpr unsigned long long DRAIN_NS = 1000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 }  // namespace pb
 
+// log2 of norms, for the scale of dS (fp16 q/k; null pointers otherwise): -inf for
+// zeros, for rows that see nothing (they have no say) and for rows that are not
+// finite (which make their own results NaN, whatever the scale).
+struct PackedTops {
+    float *row;    // [Hkv][Tq * G]: |dO_i|
+    float2 *tok;   // [Hkv][Tq]: the largest {|dO_i|, |D_i|} of a token's G rows
+    float2 *tile;  // [Hkv][Tq]: the same of a query tile's rows, at its first token
+    float *key;    // [Hkv][Tk]: |v_j|
+    float *ktile;  // [Hkv][Tk]: the largest |v_j| of a key tile, at its first key
+};
+
 struct PackedBwdParams {
     PackedGeom g;
     const void *plan;
     float scale_log2, scale;                // log2(e)/sqrt(d), 1/sqrt(d)
     const float2 *LD;                       // [Hkv][Tq * G] {lse * log2(e), D}; lse = +inf for a row that sees nothing
-    const float *norms;                     // [2][n_norms]: log2 of parts of max |dO_i| and max |v_j|, or null: no scale
-    int n_norms;
+    PackedTops tops;
     uint32_t dkv_blocks;                    // blocks of key tiles, ahead of those of query tiles
     __nv_bfloat16 *dq, *dk, *dv;
     long dq_stride, dk_stride, dv_stride;
@@ -104,146 +118,199 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// log2 of the 2-norm of a row of 128 bf16 values, 8 in each lane (`x`) of half a
-// warp, whose squares sum to `q`: -inf for zeros, inf or NaN where the row is
-// not finite.  Squares leave fp32's range long before bf16 values do: where they
-// come near its ends they are summed again from scaled values.
-__device__ __forceinline__ float log2_norm(float q, const uint4 &x, int lane) {
-    if (q >= 0x1p-80f && q <= 0x1p120f) return 0.5f * log2f(q);
-    const int shift = q > 1.f ? -70 : 70;
-    const float by = pow2(shift);
-    const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x);
-    q = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const float2 f = __bfloat1622float2(v[k]);
-        q = fmaf(f.x * by, f.x * by, fmaf(f.y * by, f.y * by, q));
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffu << (lane & 16), q, o, 16);
-    return 0.5f * log2f(q) - (float)shift;
+// Four rows of 16 lanes each (half a warp) summed side by side: two steps leave
+// lane `sub` with a part of row sub / 4, and the steps 2 and 1 of the sum to go.
+__device__ __forceinline__ float fold(float lo, float hi, bool up, int o) {
+    return (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, o);
+}
+__device__ __forceinline__ float fold_rows(const float (&x)[4], int sub) {
+    return fold(fold(x[0], x[2], sub & 8, 8), fold(x[1], x[3], sub & 8, 8), sub & 4, 4);
 }
 
-// The power of two that dS is carried with: 2^e, 2 max|dO| max|v| 2^e in (2^14, 2^15], |e| <= 100 (gradients of
-// 2^-100 and 2^100 are far outside what else fp32 holds of them).  A whole warp.
-__device__ __forceinline__ int ds_exponent(const PackedBwdParams &p) {
-    if (!p.norms) return 0;
-    float a = -INFINITY, b = -INFINITY;
-    for (int i = threadIdx.x & 31; i < p.n_norms; i += 32) {
-        a = fmaxf(a, p.norms[i]);
-        b = fmaxf(b, p.norms[p.n_norms + i]);
-    }
+// log2 of the squared 2-norms of four rows of 128 bf16 values, 8 in each lane
+// (`x`) of half a warp: lane `sub` holds the sum `q` of row sub / 4's squares and
+// gets its logarithm: -inf for zeros, inf or NaN where the row is not finite.
+// Squares leave fp32's range long before bf16 values do: where one comes near its
+// ends, the rows are summed again from scaled values.  A whole warp.
+__device__ __forceinline__ float log2_squares(float q, const uint4 (&x)[4], int lane) {
+    float log_q = log2f(q);
+    if (__any_sync(0xffffffffu, !(q >= 0x1p-80f && q <= 0x1p120f))) {
+        const int row = (lane & 15) >> 2, first = lane & 16;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        for (int i = 0; i < 4; i++) {
+            const float was = __shfl_sync(0xffffffffu, q, first + 4 * i);
+            const int shift = was > 1.f ? -70 : 70;
+            const float by = pow2(shift);
+            const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x[i]);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = __bfloat1622float2(v[k]);
+                sum = fmaf(f.x * by, f.x * by, fmaf(f.y * by, f.y * by, sum));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (row == i && !(q >= 0x1p-80f && q <= 0x1p120f)) log_q = log2f(sum) - 2.f * (float)shift;
+        }
     }
-    return (int)fmaxf(-100.f, fminf(100.f, 14.f - ceilf(a + b)));  // 100 where all of either is zero
+    return log_q;
 }
+
+// The power of two 2^e that a row of dS is carried with: twice 2^top, the bound of
+// its elements, times 2^e in (2^14, 2^15].  |e| <= 100: gradients of 2^-100 and
+// 2^100 are far outside what else fp32 holds of them.
+__device__ __forceinline__ int ds_exponent(float top) {
+    return (int)fmaxf(-100.f, fminf(100.f, 14.f - ceilf(top)));  // 100 where all is zero
+}
+
+// Floats (no NaN) as integers of the same order, for atomicMax; its own inverse.
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // -------------------------------------------------------------- pre-pass
 
-// LD of every query row of the sequences, and for fp16 q/k log2 of each block's
-// largest row norms of dO and v (finite ones: a row that is not makes its own
-// results NaN, whatever the scale) in norms[2][gridDim].  Half a warp (16 lanes x
-// 8 elements) covers one row, kU rows in flight.  Bound by HBM.
+// LD of every query row of the sequences, and for fp16 q/k the tops.  A block takes
+// one query tile of a key head after another (128 rows at most), then key tiles:
+// half a warp (16 lanes x 8 elements) has four rows in flight, whose sums and
+// logarithms it takes side by side, so that all rows of a tile are under way at
+// once.  A token's and a tile's largest are found in shared memory, two tiles'
+// entries in turn, so that a tile costs one barrier.  Bound by HBM: 25,920 tokens,
+// 24/8 heads, 64 us with bf16 q/k, 82 with fp16 (a block of 256 threads, two
+// passes a tile and logarithms row by row: 127).
+constexpr int ROWS_THREADS = 512;
+
 template <bool NORMS>
-__global__ void __launch_bounds__(256) packed_bwd_rows_kernel(const PackedGeom g, const void *plan_base,
-                                                              const char *out, long out_stride, const char *dout,
-                                                              long dout_stride, const char *v, long v_stride,
-                                                              const float *__restrict__ lse, float2 *__restrict__ LD,
-                                                              float *norms) {
-    constexpr int kU = 4;
-    const int lane = threadIdx.x & 31, sub = lane & 15;
-    const uint32_t half = (uint32_t)((blockIdx.x * blockDim.x + threadIdx.x) >> 4);
-    const uint32_t halves = (uint32_t)(gridDim.x * blockDim.x) >> 4;
+__global__ void __launch_bounds__(ROWS_THREADS, 2)
+    packed_bwd_rows_kernel(const PackedGeom g, const void *plan_base, const char *out, long out_stride,
+                           const char *dout, long dout_stride, const char *v, long v_stride,
+                           const float *__restrict__ lse, float2 *__restrict__ LD, const PackedTops tops) {
+    constexpr int HALVES = ROWS_THREADS / 16;
+    __shared__ int best[2][2][128];  // [tile's turn][|dO|, |D|][token], or [turn][0][key]: ordered
+    const int lane = threadIdx.x & 31, sub = lane & 15, half = threadIdx.x >> 4;
+    const int mine = (sub >> 2) * HALVES + half;  // the row, of those in flight, whose sums this lane gets
     const PackedPlan plan = packed_plan_at(const_cast<void *>(plan_base), g);
     if (!packed_plan_ok(*plan.head, g)) return;  // the next kernel reports it
-    const int q_lo = plan.head->q_lo, k_lo = plan.head->k_lo;
+    const uint32_t n_q = (uint32_t)plan.head->n_q, n_k = (uint32_t)plan.head->n_k;
     // the host keeps tokens * heads below 2^31
-    const uint32_t rows = (uint32_t)(plan.head->q_hi - q_lo) * (uint32_t)g.H;
-    const uint32_t vrows = NORMS ? (uint32_t)(plan.head->k_hi - k_lo) * (uint32_t)g.Hkv : 0;
-    float top_do = -INFINITY, top_v = -INFINITY;
-    // both halves of a warp run the same number of rounds (the shuffles need all lanes)
-    for (uint32_t base = 0; base < rows; base += halves * kU) {
-        uint4 a[kU], b[kU];
-        uint32_t tok[kU], h[kU];
-        float l[kU];
-#pragma unroll
-        for (int i = 0; i < kU; i++) {
-            const uint32_t r = base + i * halves + half;
-            const bool in = r < rows;
-            tok[i] = in ? r / (uint32_t)g.H : 0;
-            h[i] = in ? r - tok[i] * (uint32_t)g.H : 0;
-            tok[i] += q_lo;
-            a[i] = reinterpret_cast<const uint4 *>(out + (long)tok[i] * out_stride + (long)h[i] * 256)[sub];
-            b[i] = reinterpret_cast<const uint4 *>(dout + (long)tok[i] * dout_stride + (long)h[i] * 256)[sub];
-            l[i] = sub == 0 ? lse[(long)h[i] * g.Tq + tok[i]] : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kU; i++) {
-            const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
-            const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(&b[i]);
-            float s = 0.f, q = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float2 fx = __bfloat1622float2(x[k]), fy = __bfloat1622float2(y[k]);
-                s = fmaf(fx.x, fy.x, s);
-                s = fmaf(fx.y, fy.y, s);
-                if (NORMS) q = fmaf(fy.x, fy.x, fmaf(fy.y, fy.y, q));
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, o, 16);
-                if (NORMS) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
-            }
-            const float n = NORMS ? log2_norm(q, b[i], lane) : 0.f;
-            if (base + i * halves + half < rows && sub == 0) {
-                LD[((long)(h[i] / g.G) * g.Tq + tok[i]) * g.G + h[i] % g.G] =
-                    make_float2(l[i] == -INFINITY ? INFINITY : l[i] * pb::LOG2E, s);
-                // a row that sees nothing has no say in the scale
-                if (NORMS && l[i] > -INFINITY && n < INFINITY) top_do = fmaxf(top_do, n);
-            }
-        }
-    }
+    const uint32_t q_units = n_q * (uint32_t)g.Hkv, units = q_units + (NORMS ? n_k * (uint32_t)g.Hkv : 0);
     if constexpr (NORMS) {
-        for (uint32_t base = 0; base < vrows; base += halves * kU) {
-            uint4 a[kU];
+        for (int i = threadIdx.x; i < 512; i += ROWS_THREADS) (&best[0][0][0])[i] = ordered(-INFINITY);
+        __syncthreads();
+    }
+    int turn = 0;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        int n;    // tokens or keys of the tile
+        long at;  // [Hkv][Tq] or [Hkv][Tk] index of its first
+        const bool keys = u >= q_units;
+        if (!keys) {
+            const int hk = (int)(u / n_q);
+            const PackedItem it = plan.q[u - (uint32_t)hk * n_q];
+            n = it.n_tok_hk, at = (long)hk * g.Tq + it.tok0;
+            const int rows = n * g.G;
+            for (int base = 0; base < rows; base += HALVES * 4) {
+                uint4 a[4], b[4];
 #pragma unroll
-            for (int i = 0; i < kU; i++) {
-                const uint32_t r = base + i * halves + half < vrows ? base + i * halves + half : 0;
-                const uint32_t t = r / (uint32_t)g.Hkv;
-                a[i] = reinterpret_cast<const uint4 *>(v + (long)(k_lo + t) * v_stride +
-                                                       (long)(r - t * (uint32_t)g.Hkv) * 256)[sub];
+                for (int i = 0; i < 4; i++) {
+                    const int r = min(base + i * HALVES + half, rows - 1);
+                    const int t = r / g.G, h = hk * g.G + r - t * g.G;
+                    a[i] = reinterpret_cast<const uint4 *>(out + (long)(it.tok0 + t) * out_stride + (long)h * 256)[sub];
+                    b[i] = reinterpret_cast<const uint4 *>(dout + (long)(it.tok0 + t) * dout_stride + (long)h * 256)[sub];
+                }
+                const int r = min(base + mine, rows - 1), t = r / g.G;
+                const float l = lse[(long)(hk * g.G + r - t * g.G) * g.Tq + it.tok0 + t];
+                float s[4], q[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
+                    const __nv_bfloat162 *y = reinterpret_cast<const __nv_bfloat162 *>(&b[i]);
+                    s[i] = q[i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 fx = __bfloat1622float2(x[k]), fy = __bfloat1622float2(y[k]);
+                        s[i] = fmaf(fx.x, fy.x, s[i]);
+                        s[i] = fmaf(fx.y, fy.y, s[i]);
+                        if (NORMS) q[i] = fmaf(fy.x, fy.x, fmaf(fy.y, fy.y, q[i]));
+                    }
+                }
+                float d = fold_rows(s, sub);
+                d += __shfl_xor_sync(0xffffffffu, d, 2);
+                d += __shfl_xor_sync(0xffffffffu, d, 1);
+                float top = 0.f;
+                if constexpr (NORMS) {
+                    float x = fold_rows(q, sub);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    top = 0.5f * log2_squares(x, b, lane);
+                }
+                if (base + mine < rows && (sub & 3) == 0) {
+                    const bool none = l == -INFINITY;  // the row sees nothing
+                    LD[at * g.G + r] = make_float2(none ? INFINITY : l * pb::LOG2E, d);
+                    if constexpr (NORMS) {
+                        const float log_d = log2f(fabsf(d));
+                        const bool has_do = !none && top < INFINITY, has_d = !none && log_d < INFINITY;
+                        tops.row[at * g.G + r] = has_do ? top : -INFINITY;
+                        if (has_do) atomicMax(&best[turn][0][t], ordered(top));
+                        if (has_d) atomicMax(&best[turn][1][t], ordered(log_d));
+                    }
+                }
             }
+        } else {
+            const int hk = (int)((u - q_units) / n_k);
+            const PackedKItem it = plan.k[u - q_units - (uint32_t)hk * n_k];
+            n = it.n_key, at = (long)hk * g.Tk + it.krow0;
+            for (int base = 0; base < n; base += HALVES * 4) {
+                uint4 a[4];
 #pragma unroll
-            for (int i = 0; i < kU; i++) {
-                const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
-                float q = 0.f;
+                for (int i = 0; i < 4; i++) {
+                    const int r = min(base + i * HALVES + half, n - 1);
+                    a[i] = reinterpret_cast<const uint4 *>(v + (long)(it.krow0 + r) * v_stride + (long)hk * 256)[sub];
+                }
+                float q[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float2 f = __bfloat1622float2(x[k]);
-                    q = fmaf(f.x, f.x, fmaf(f.y, f.y, q));
+                for (int i = 0; i < 4; i++) {
+                    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&a[i]);
+                    q[i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 f = __bfloat1622float2(x[k]);
+                        q[i] = fmaf(f.x, f.x, fmaf(f.y, f.y, q[i]));
+                    }
+                }
+                float x = fold_rows(q, sub);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                float top = 0.5f * log2_squares(x, a, lane);
+                if (!(top < INFINITY)) top = -INFINITY;
+                if (base + mine < n && (sub & 3) == 0) {
+                    tops.key[at + base + mine] = top;
+                    best[turn][0][base + mine] = ordered(top);
+                }
+            }
+        }
+        if constexpr (NORMS) {
+            __syncthreads();
+            if (threadIdx.x < 32) {
+                float2 m = make_float2(-INFINITY, -INFINITY);
+                for (int t = lane; t < n; t += 32) {
+                    const float2 x = make_float2(unordered(best[turn][0][t]), unordered(best[turn][1][t]));
+                    best[turn][0][t] = best[turn][1][t] = ordered(-INFINITY);  // next written behind the next barrier
+                    if (!keys) tops.tok[at + t] = x;
+                    m = make_float2(fmaxf(m.x, x.x), fmaxf(m.y, x.y));
                 }
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o, 16);
-                const float n = log2_norm(q, a[i], lane);
-                if (n < INFINITY) top_v = fmaxf(top_v, n);
+                for (int o = 16; o > 0; o >>= 1) {
+                    m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+                    m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+                }
+                if (lane == 0) {
+                    if (keys) tops.ktile[at] = m.x;
+                    else tops.tile[at] = m;
+                }
             }
-        }
-        __shared__ float tops[2][8];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            top_do = fmaxf(top_do, __shfl_xor_sync(0xffffffffu, top_do, o));
-            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
-        }
-        if (lane == 0) tops[0][threadIdx.x >> 5] = top_do, tops[1][threadIdx.x >> 5] = top_v;
-        __syncthreads();
-        if (threadIdx.x < 2) {
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < 8; w++) m = fmaxf(m, tops[threadIdx.x][w]);
-            norms[threadIdx.x * gridDim.x + blockIdx.x] = m;
+            turn ^= 1;
         }
     }
 }
@@ -485,10 +552,19 @@ __device__ __forceinline__ void dq_item(uint8_t *smem, const CUtensorMap &tm_q, 
         __syncwarp();
     } else {
         const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
-        const int e = ds_exponent(p);
+        int e = 0;
         const int lim = live ? packed_limit(it.pos0 + rtok, it.Lk, p.g.block) : it.Lk;
         float2 ld = make_float2(INFINITY, 0.f);
-        if (live) ld = p.LD[((long)hk * p.g.Tq + tok) * p.g.G + rhead];
+        const long at = ((long)hk * p.g.Tq + tok) * p.g.G + rhead;
+        if (live) ld = p.LD[at];
+        if (p.tops.row) {
+            const float top = live ? p.tops.row[at] : -INFINITY;
+            float v = -INFINITY;  // the largest |v_j| of the item's keys
+            for (int t = lane; t < T; t += 32) v = fmaxf(v, p.tops.ktile[(long)hk * p.g.Tk + it.krow0 + t * BM]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            e = ds_exponent(fmaxf(top + v, log2f(fabsf(ld.y))));
+        }
         ld.x -= (float)e;  // P, and with it dS, is carried times 2^e
         const float sl2 = p.scale_log2;
         bool ok = true;
@@ -582,6 +658,64 @@ __device__ __forceinline__ void ds_row(const float (&pr)[64], const float *sd, u
             st_shared_16(prow + ((chunk ^ (r & 7)) << 4), ds[4 * i], ds[4 * i + 1], ds[4 * i + 2], ds[4 * i + 3]);
         }
     }
+}
+
+// The exponent of key row r's dS in a key tile (warps 0-7, 256 threads; `scratch`:
+// 256 words of shared memory that nothing else uses until the function returns).
+// The tile's keys fall into groups that the same queries see: frames of the mask,
+// from the first key's on.  A query of group f sees the keys
+// of the groups up to f, so key r takes the largest over the groups from its own on; queries behind
+// the last group's first are taken by whole tiles.
+__device__ __forceinline__ int dkv_exponent(const PackedBwdParams &p, const PackedKItem &it, int hk, int r, int *scratch) {
+    const PackedGeom &g = p.g;
+    const int t = threadIdx.x, lane = t & 31, F = g.block;
+    const float v = r < it.n_key ? p.tops.key[(long)hk * g.Tk + it.krow0 + r] : -INFINITY;
+    const int last = it.key0 + it.n_key - 1, frame0 = F ? it.key0 / F : 0, groups = F ? last / F - frame0 + 1 : 1;
+    const int tile0 = (packed_first_query(last, it.off, F) + g.tpt - 1) / g.tpt;
+    const long at = (long)hk * g.Tq + it.qrow0;
+    scratch[t] = ordered(-INFINITY);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    float2 m = make_float2(-INFINITY, -INFINITY);
+    for (int i = tile0 + t; i < it.qt1; i += 256) {
+        const float2 x = p.tops.tile[at + (long)i * g.tpt];
+        m = make_float2(fmaxf(m.x, x.x), fmaxf(m.y, x.y));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+        m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+    }
+    if (lane == 0) {
+        atomicMax(&scratch[groups - 1], ordered(m.x));
+        atomicMax(&scratch[128 + groups - 1], ordered(m.y));
+    }
+    const int end = min(tile0 * g.tpt, it.Lq);
+    for (int i = packed_first_query(it.key0, it.off, F) + t; i < end; i += 256) {
+        const float2 x = p.tops.tok[at + i];
+        const int f = F ? min(groups - 1, (i + it.off) / F - frame0) : 0;  // i + off >= frame0 F
+        atomicMax(&scratch[f], ordered(x.x));
+        atomicMax(&scratch[128 + f], ordered(x.y));
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (t < 64) {  // the largest from each group on: one warp each for |dO| and |D|, four groups a lane
+        int4 *mine = reinterpret_cast<int4 *>(scratch + (t & 32) * 4) + lane;
+        int4 x = *mine;
+        x.z = max(x.z, x.w), x.y = max(x.y, x.z), x.x = max(x.x, x.y);
+        int all = x.x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_down_sync(0xffffffffu, all, o);
+            if (lane + o < 32) all = max(all, y);
+        }
+        int behind = __shfl_down_sync(0xffffffffu, all, 1);
+        if (lane == 31) behind = ordered(-INFINITY);
+        *mine = make_int4(max(x.x, behind), max(x.y, behind), max(x.z, behind), max(x.w, behind));
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int f = F ? min(groups - 1, (it.key0 + r) / F - frame0) : 0;
+    const float top = fmaxf(unordered(scratch[f]) + v, unordered(scratch[128 + f]));
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    return ds_exponent(top);
 }
 
 // ----------------------------------------------------------------- dkv kernel
@@ -753,7 +887,8 @@ __device__ __forceinline__ void dkv_item(uint8_t *smem, const CUtensorMap &tm_q,
     } else {
         const uint32_t lb = tmem + ((uint32_t)(32 * q4) << 16);
         const float sl2 = p.scale_log2;
-        const int e = ds_exponent(p);
+        // dS^T's tile is free until the first step writes it
+        const int e = p.tops.row ? dkv_exponent(p, it, hk, r, reinterpret_cast<int *>(sDS)) : 0;
         const float sc = pow2(e);
         // the first query row (of the sequence, tokens x heads) that sees this key
         const long first = (long)packed_first_query(it.key0 + r, it.off, p.g.block) * p.g.G;
@@ -854,18 +989,27 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
 
 }  // namespace
 
-// Blocks of the pre-pass, from the longer of its two reads (with norms it takes all of v too, which a few new
-// tokens over long caches have far more of): each leaves two norms, which every block of the main kernel reads.
+// Blocks of the pre-pass: a tile each, of queries and (with norms) of keys, up to two a SM.
 unsigned packed_bwd_rows_blocks(const PackedGeom &g, bool norms) {
-    const long q = (long)g.Tq * g.H, v = norms ? (long)g.Tk * g.Hkv : 0;
-    const long want = ((q > v ? q : v) + 63) / 64;
-    return (unsigned)(want < 4L * g.sms ? want : 4L * g.sms);
+    const long want = (g.Tq ? (long)g.cap_q * g.Hkv : 0) + (norms && g.Tk ? (long)g.cap_k * g.Hkv : 0);
+    return (unsigned)(want < 2L * g.sms ? want : 2L * g.sms);
 }
 
-// Workspace: LD, then the blocks' norms.
-size_t packed_bwd_workspace(const PackedGeom &p) {
-    return round256((size_t)p.Tq * p.H * sizeof(float2)) + round256((size_t)p.sms * 4 * 2 * sizeof(float));
-}
+// Workspace: LD, then the tops.
+struct BwdLayout {
+    size_t row, tok, tile, key, ktile, total;
+    explicit BwdLayout(const PackedGeom &p) {
+        const size_t q = (size_t)p.Tq * p.Hkv, k = (size_t)p.Tk * p.Hkv;
+        row = round256(q * p.G * sizeof(float2));
+        tok = row + round256(q * p.G * sizeof(float));
+        tile = tok + round256(q * sizeof(float2));
+        key = tile + round256(q * sizeof(float2));
+        ktile = key + round256(k * sizeof(float));
+        total = ktile + round256(k * sizeof(float));
+    }
+};
+
+size_t packed_bwd_workspace(const PackedGeom &p) { return BwdLayout(p).total; }
 
 cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const void *out, long out_stride,
                               const void *dout, long dout_stride, const float *lse, void *dq, long dq_stride,
@@ -887,13 +1031,21 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     cudaError_t e = set_max_dynamic_smem((const void *)packed_bwd_kernel, pb::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     float2 *LD = static_cast<float2 *>(ws);
-    float *norms = reinterpret_cast<float *>(static_cast<char *>(ws) + round256((size_t)g.Tq * g.H * sizeof(float2)));
-    const unsigned n_rows = packed_bwd_rows_blocks(g, t.qk_f16);
+    PackedTops tops = {};
+    if (t.qk_f16) {
+        const BwdLayout at(g);
+        char *w = static_cast<char *>(ws);
+        tops.row = reinterpret_cast<float *>(w + at.row);
+        tops.tok = reinterpret_cast<float2 *>(w + at.tok);
+        tops.tile = reinterpret_cast<float2 *>(w + at.tile);
+        tops.key = reinterpret_cast<float *>(w + at.key);
+        tops.ktile = reinterpret_cast<float *>(w + at.ktile);
+    }
     if (g.Tq) {
         auto rows = [&](auto kernel) {
-            kernel<<<n_rows, 256, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
+            kernel<<<packed_bwd_rows_blocks(g, t.qk_f16), ROWS_THREADS, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
                                            static_cast<const char *>(dout), dout_stride * 2,
-                                           static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, norms);
+                                           static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, tops);
         };
         if (t.qk_f16) rows(packed_bwd_rows_kernel<true>);
         else rows(packed_bwd_rows_kernel<false>);
@@ -906,8 +1058,7 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     p.scale = (float)(1.0 / sqrt(128.0));
     p.scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
     p.LD = LD;
-    p.norms = t.qk_f16 && g.Tq ? norms : nullptr;
-    p.n_norms = (int)n_rows;
+    p.tops = tops;
     p.dq = static_cast<__nv_bfloat16 *>(dq), p.dk = static_cast<__nv_bfloat16 *>(dk);
     p.dv = static_cast<__nv_bfloat16 *>(dv);
     p.dq_stride = dq_stride, p.dk_stride = dk_stride, p.dv_stride = dv_stride;
