@@ -134,59 +134,6 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
-// The same load delivered to every CTA of the cluster named in `cta_mask`:
-// the bytes land at the same shared-memory offset in each, and each
-// destination's mbarrier at `bar`'s offset receives its complete_tx.
-__device__ __forceinline__ void tma_load_4d_multicast(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1,
-                                                      int c2, int c3, uint16_t cta_mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)),
-        "h"(cta_mask)
-        : "memory");
-}
-
-// ---------------------------------------------------------------- cluster
-
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// The shared::cluster address of the variable at `p` (this CTA's shared
-// memory) in the shared memory of cluster CTA `rank` (same layout).
-__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-
-// Arrive on an mbarrier of another cluster CTA.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
-}
-
-// Arrive on it and raise its expected transaction bytes.
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t caddr, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(caddr),
-                 "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
-    return v;
-}
-
-// Every thread of every CTA of the cluster: memory operations before it
-// (remote arrivals, stores) are visible to all after it.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
 __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
