@@ -30,13 +30,22 @@ class PackedBatch:
     def __init__(self, handle, lens, tokens, kv_heads, mask_block=0):
         import torch
         self.handle, self.tokens, self.kv_heads = handle, int(tokens), int(kv_heads)
-        if not isinstance(lens, torch.Tensor):
-            lens = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+        lens = self._offsets(lens)
         self.offsets = torch.empty_like(lens, device=handle._dev).copy_(lens)  # its own: set_offsets writes to it
         self.plan = handle.packed_plan(self.offsets, None, self.tokens, self.tokens, self.kv_heads, mask_block)
 
+    @staticmethod
+    def _offsets(lens):
+        import torch
+        return lens if isinstance(lens, torch.Tensor) else torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+
     def set_offsets(self, offsets):
-        """Other lengths of as many sequences, in place (a captured layer sees them at its next replay)."""
+        """Other lengths of as many sequences, in place (a captured layer sees them at its next replay): offsets [n + 1],
+        or a list of lengths.  Offsets on the device are copied in stream order; the host waits for a copy of its own."""
+        offsets = self._offsets(offsets)
+        if offsets.shape != self.offsets.shape or offsets.is_floating_point():
+            raise ValueError(f"offsets: want {self.offsets.numel()} integers for {self.offsets.numel() - 1} sequences, got "
+                             f"{offsets.dtype} {tuple(offsets.shape)}")
         self.offsets.copy_(offsets)
         self.handle.packed_replan(self.plan, self.offsets, None)
 
