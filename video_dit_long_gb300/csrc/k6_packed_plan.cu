@@ -203,6 +203,10 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         if (lane == 31) sh.total = at;
     }
     __syncthreads();
+    if (LIST == FWD && sh.total > p.cap_q + p.extra) {  // the same for all threads
+        if (threadIdx.x == 0) sh.bad = 1;
+        return;
+    }
     for (int s = warp; s < p.n_seq; s += WARPS) {
         const Seq q = sequence<LIST>(p, cu_q, cu_k, s);
         for (int t = lane; t < q.tiles; t += 32) {
@@ -230,7 +234,7 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
                 slot = atomicAdd(&sh.slots, n);
                 const int m = atomicAdd(&sh.merges, p.Hkv);
                 for (int hk = 0; hk < p.Hkv; hk++)
-                    plan.merge[m + hk] = {it.tok0, it.n_tok_hk | hk << 8, slot * p.Hkv + hk, n};
+                    if (m + hk < p.cap_merge) plan.merge[m + hk] = {it.tok0, it.n_tok_hk | hk << 8, slot * p.Hkv + hk, n};
             }
             for (int c = 0; c < n; c++, i++) {  // pieces of equal length, to within a tile
                 it.kt0 = (int)((long)hi * c / n), it.kt1 = (int)((long)hi * (c + 1) / n);
@@ -245,6 +249,7 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         if (LIST == FWD) {
             plan.head->n_fwd = sh.total, plan.head->n_merge = sh.merges;
             plan.head->stream = 0, plan.head->slot_step = p.Hkv;
+            if ((long)sh.slots * p.Hkv > p.cap_slots || sh.merges > p.cap_merge) sh.bad = 1;
         } else if (LIST == QTILES) {
             plan.head->n_q = sh.total;
         } else {
@@ -356,7 +361,8 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
                     int slot = -1;
                     if (n > 1) {
                         slot = atomicAdd(&sh.slots, n);
-                        plan.merge[atomicAdd(&sh.merges, 1)] = {it.tok0, it.n_tok_hk, slot, n};
+                        const int m = atomicAdd(&sh.merges, 1);
+                        if (m < p.cap_merge) plan.merge[m] = {it.tok0, it.n_tok_hk, slot, n};
                     }
                     int from = 0, piece = 0, owner = min(p.sms - 1, a / Q);
                     for (int c = c0; c <= c1; c++) {
@@ -373,6 +379,8 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
                         if (k >= 0 && k < p.cap_rows) {
                             plan.fwd[(long)owner * p.cap_rows + k] = it;
                             atomicMax(&sh.items[owner], k + 1);
+                        } else {
+                            sh.bad = 1;
                         }
                         from = x, piece++, owner = c;
                     }
@@ -385,6 +393,7 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
     if (threadIdx.x == 0) {
         plan.head->n_fwd = 0, plan.head->n_merge = sh.merges;
         plan.head->stream = 1, plan.head->slot_step = 1;
+        if (sh.slots > p.cap_slots || sh.merges > p.cap_merge) sh.bad = 1;
     }
     return true;
 }
@@ -415,6 +424,13 @@ __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p
     if (bad) return;
     if (blockIdx.x == 0) {
         if (!build_stretches(p, cu_q, cu_k, plan, sh)) build<FWD>(p, cu_q, cu_k, plan, sh);
+        // work that found no room in the lists (their sizes are upper bounds, so there is none) makes the plan a bad
+        // one: calls report it instead of leaving rows out
+        __syncthreads();
+        if (threadIdx.x == 0 && sh.bad) {
+            plan.head->bad = 1;
+            atomicCAS(err, DEV_OK, DEV_PLAN);
+        }
     } else if (blockIdx.x == 1) build<QTILES>(p, cu_q, cu_k, plan, sh);
     else build<KTILES>(p, cu_q, cu_k, plan, sh);
 }
