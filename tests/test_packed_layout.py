@@ -2,7 +2,8 @@
 
 Where a plan's parts lie in its buffer: what a kernel reads of a plan before its
 header has shown whose it is must lie in every plan, also in one of a smaller
-batch.  And the blocks of the backward pass's pre-pass."""
+batch.  And the blocks of the backward pass's pre-pass, and the sizes
+that the queries answer."""
 import itertools
 import os
 import subprocess
@@ -24,10 +25,15 @@ int main() {
         const k6attn_packed b = {n, kv, 1, q, k};
         const k6::PackedGeom p = k6::packed_geom(g, b, sms);
         const k6::PackedPlan at = k6::packed_plan_at(nullptr, p);
-        printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d %u %u\n", k6::packed_plan_bytes(p), k6::packed_plan_common_bytes(sms),
+        k6attn_handle h;
+        h.g = g, h.g.dtype = K6ATTN_BF16, h.sms = sms, h.device = 5;  // never the current one
+        printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d %u %u %zu %zu %zu %zu %zu %zu\n", k6::packed_plan_bytes(p), k6::packed_plan_common_bytes(sms),
                (size_t)at.count, (size_t)at.merge, (size_t)at.fwd, (size_t)at.sched, (size_t)at.q, (size_t)at.k,
                sizeof(k6::PackedMerge), p.cap_merge, k6::packed_bwd_rows_blocks(p, true),
-               k6::packed_bwd_rows_blocks(p, false));
+               k6::packed_bwd_rows_blocks(p, false), k6attn_packed_plan_bytes(&h, &b),
+               k6attn_packed_workspace_bytes(&h, &b), k6::packed_fwd_workspace(p),
+               k6attn_packed_backward_workspace_bytes(&h, &b), k6::packed_bwd_workspace(p),
+               k6attn_packed_norm_rope_backward_workspace_bytes(&h, q, kv));
     }
 }
 """
@@ -78,3 +84,12 @@ def test_the_pre_pass_of_few_queries_over_long_caches_fills_the_gpu(program):
         (got,) = sizes(program, [(H, kv, 3, 12, k, 152)])
         assert got[10] >= 2 * 152, (H, kv, k, got[10])
         assert 1 <= got[11] <= got[10]
+
+
+def test_sizes_are_host_arithmetic_whichever_device_is_current(program):
+    """The queries need no device: they answer for a handle whose device is not the current one, or without any."""
+    cases = [c for c in CASES if c[3] > 0]
+    for c, got in zip(cases, sizes(program, cases)):
+        plan, fwd, fwd_want, bwd, bwd_want, norm = got[12:]
+        assert (plan, fwd, bwd) == (got[0], fwd_want, bwd_want), c
+        assert plan > 0 and bwd > 0 and norm > 0, c

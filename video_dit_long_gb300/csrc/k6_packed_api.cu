@@ -80,9 +80,9 @@ k6attn_status check_norm(const char *fn, k6attn_t h, long tokens, int kv_heads, 
     return K6ATTN_OK;
 }
 
-k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
-    k6attn_status s = check_handle(fn, h);
-    if (s != K6ATTN_OK) return s;
+// Whether the library takes the batch: host arithmetic alone, whichever device is current.
+k6attn_status check_sizes(const char *fn, k6attn_t h, const k6attn_packed *b) {
+    if (!h) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null handle", fn);
     if (!b) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null batch", fn);
     if (h->g.dtype != K6ATTN_BF16) return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: needs a bf16 handle (d = 128)", fn);
     if (b->n_seq < 1 || b->q_tokens < 0 || b->k_tokens < 0)
@@ -100,6 +100,11 @@ k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
         (b->k_tokens + b->n_seq) * b->kv_heads >= (1L << 31))
         return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: batch too large", fn);
     return K6ATTN_OK;
+}
+
+k6attn_status check_batch(const char *fn, k6attn_t h, const k6attn_packed *b) {
+    const k6attn_status s = check_handle(fn, h);
+    return s != K6ATTN_OK ? s : check_sizes(fn, h, b);
 }
 
 k6attn_status check_plan(const char *fn, const void *plan) {
@@ -222,7 +227,7 @@ k6attn_status k6attn_packed_norm_rope_backward(k6attn_t h, long tokens, int kv_h
 }
 
 size_t k6attn_packed_plan_bytes(k6attn_t h, const k6attn_packed *batch) {
-    if (check_batch("packed_plan_bytes", h, batch) != K6ATTN_OK) return 0;
+    if (check_sizes("packed_plan_bytes", h, batch) != K6ATTN_OK) return 0;
     return packed_plan_bytes(packed_geom(h->g, *batch, h->sms));
 }
 
@@ -250,7 +255,7 @@ k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const i
 }
 
 size_t k6attn_packed_workspace_bytes(k6attn_t h, const k6attn_packed *batch) {
-    if (check_batch("packed_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
+    if (check_sizes("packed_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
     return packed_fwd_workspace(packed_geom(h->g, *batch, h->sms));
 }
 
@@ -291,7 +296,7 @@ k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, cons
 }
 
 size_t k6attn_packed_backward_workspace_bytes(k6attn_t h, const k6attn_packed *batch) {
-    if (check_batch("packed_backward_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
+    if (check_sizes("packed_backward_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
     return packed_bwd_workspace(packed_geom(h->g, *batch, h->sms));
 }
 
