@@ -206,6 +206,16 @@ def _vec(t, shape, dtype, device, what):
     return t.data_ptr()
 
 
+def _cu(offsets, device):
+    """(pointer, sequences) of a batch's offsets, or of none."""
+    if offsets is None:
+        return None, 0
+    n = offsets.numel()
+    if n == 0:  # its pointer is null, which stands for no offsets
+        raise ValueError("offsets: want n_seq + 1 of them, got none")
+    return _vec(offsets, (n,), _DTYPES["int32"], device, "offsets"), n - 1
+
+
 def _room(workspace, device):
     if workspace is None:
         return None, 0
@@ -398,7 +408,7 @@ class Handle:
         dev, st = self._packed(stream)
         d, T, kv = self._d, q.size(0), k.size(1)
         sq, sk, e, f32, i32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32], _DTYPES["int32"]
-        n = 1 if offsets is None else offsets.numel()
+        cu, n_seq = _cu(offsets, dev)
         od = _code(q_out)
         o = q_out.dtype
         pq, lq = _rows(q, sq, e, dev, "q")
@@ -406,7 +416,7 @@ class Handle:
         poq, loq = _rows(q_out, sq, o, dev, "q_out")
         pok, lok = _rows(k_out, sk, o, dev, "k_out")
         s = self._lib.k6attn_packed_norm_rope(
-            self.h, T, kv, _vec(offsets, (n,), i32, dev, "offsets"), n - 1,
+            self.h, T, kv, cu, n_seq,
             _vec(positions, (T, 3), i32, dev, "positions"), pq, lq, pk, lk,
             _vec(q_weight, (d,), f32, dev, "q_weight"), _vec(k_weight, (d,), f32, dev, "k_weight"), eps, poq, loq, pok,
             lok, od, st)
@@ -422,7 +432,7 @@ class Handle:
         dev, st = self._packed(stream)
         d, T, kv = self._d, dq_out.size(0), dk_out.size(1)
         sq, sk, e, f32, i32 = (T, self._H, d), (T, kv, d), self._elem, _DTYPES[F32], _DTYPES["int32"]
-        n = 1 if offsets is None else offsets.numel()
+        cu, n_seq = _cu(offsets, dev)
         pgq, lgq = _rows(dq_out, sq, e, dev, "dq_out")
         pgk, lgk = _rows(dk_out, sk, e, dev, "dk_out")
         pq, lq = (None, 0) if q is None else _rows(q, sq, e, dev, "q")
@@ -431,7 +441,7 @@ class Handle:
         pdk, ldk = _rows(dk, sk, e, dev, "dk")
         ws, nws = _room(workspace, dev)
         s = self._lib.k6attn_packed_norm_rope_backward(
-            self.h, T, kv, _vec(offsets, (n,), i32, dev, "offsets"), n - 1,
+            self.h, T, kv, cu, n_seq,
             _vec(positions, (T, 3), i32, dev, "positions"), pgq, lgq, pgk, lgk, pq, lq, pk, lk,
             _vec(q_weight, (d,), f32, dev, "q_weight"), _vec(k_weight, (d,), f32, dev, "k_weight"), eps, pdq, ldq, pdk,
             ldk, _vec(dq_weight, (d,), f32, dev, "dq_weight"), _vec(dk_weight, (d,), f32, dev, "dk_weight"), ws, nws,
