@@ -424,3 +424,16 @@ def test_a_plan_of_a_smaller_batch_is_reported_and_nothing_is_written(Hkv):
     assert e.value.status == big.K.ERR_INVALID_ARG
     assert all(bool((x == 7.0).all()) for x in grads)
     big.forward().check()  # its own plan still serves
+
+
+def test_a_batch_that_is_refused_keeps_its_status():
+    """Planning: a type the library does not take is 'unsupported', a bad count an invalid argument."""
+    from video_dit_long_gb300 import k6attn as K
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    for h, kw, status in ((K.Handle.for_packed(4, 64, "f32", (16, 24, 24)), {}, K.ERR_UNSUPPORTED),
+                          (K.Handle.for_packed(300), {"kv_heads": 1}, K.ERR_UNSUPPORTED),
+                          (K.Handle.for_packed(4), {"kv_heads": 3}, K.ERR_INVALID_ARG),
+                          (K.Handle.for_packed(4), {"mask_block": 1 << 30}, K.ERR_INVALID_ARG)):
+        with pytest.raises(K.K6Error) as e:
+            h.packed_plan(cu, None, 4, 4, **{"kv_heads": 2, **kw})
+        assert e.value.status == status and "packed_plan" in str(e.value)

@@ -456,8 +456,8 @@ class Handle:
         b = PackedBatch(int(cu_q.numel()) - 1, int(kv_heads), int(mask_block), int(q_tokens), int(k_tokens))
         L = load()
         n = L.k6attn_packed_plan_bytes(self.h, ctypes.byref(b))
-        if not n:
-            raise K6Error(ERR_INVALID_ARG, (L.k6attn_last_error() or b"").decode())
+        if not n:  # the call that makes a plan refuses the batch with its own status
+            _check(L.k6attn_packed_plan(self.h, ctypes.byref(b), None, None, None, 0, None))
         with torch.cuda.stream(_torch_stream(stream, self._dev)):  # memory of the stream that writes it first
             plan = PackedPlan(b, torch.empty(n, dtype=torch.uint8, device=cu_q.device))
         self.packed_replan(plan, cu_q, cu_k, stream=stream)
