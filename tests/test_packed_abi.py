@@ -54,3 +54,23 @@ def test_rotary_turns_in_fixed_point():
             off = Fraction(top, 2 ** 32) - exact
             off -= round(off)
             assert abs(off) <= Fraction(1, 2 ** 32) + abs(pos) * Fraction(1, 2 ** 55), (a, i, pos)
+
+
+def test_rotary_angles_as_floats():
+    """The angle as the kernel takes sin and cos of it, rounded to a 24-bit float: within 2^-26 of a turn (half a step
+    near half a turn) more, and not within 2^-32."""
+    from fractions import Fraction
+    import math
+    np = pytest.importorskip("numpy")
+    worst = Fraction(0)
+    for a, i in ((32, 0), (32, 15), (48, 7), (48, 23)):
+        turns = 10000.0 ** (-2.0 * i / a) / 6.283185307179586476925
+        w = int(math.floor(math.ldexp(turns - math.floor(turns), 64) + 0.5))
+        for pos in (0, 1, -1, 54, 12345, 999983, 2 ** 31 - 1, -2 ** 31):
+            top = ((pos * w) % 2 ** 64) >> 32
+            top -= 2 ** 32 if top >= 2 ** 31 else 0
+            off = Fraction(float(np.float32(top))) / 2 ** 32 - Fraction(turns) * pos
+            off = abs(off - round(off))
+            assert off <= Fraction(1, 2 ** 26) + Fraction(1, 2 ** 32) + abs(pos) * Fraction(1, 2 ** 55), (a, i, pos)
+            worst = max(worst, off)
+    assert worst > Fraction(1, 2 ** 32)

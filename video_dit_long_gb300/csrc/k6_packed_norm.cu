@@ -15,8 +15,9 @@
 // Angles: the frequency of a pair is kept as a 64-bit fixed-point fraction of a
 // turn, so position * frequency modulo 2^64 is the reduced angle with an error
 // below |position| 2^-55 turns, at any 32-bit position, in integer arithmetic;
-// its top 32 bits go to sincospi.  No per-token table is read: 12 bytes of
-// positions serve all heads of a token.
+// its top 32 bits go to sincospi as a float, which costs up to 2^-26 of a turn
+// (2^-23.4 in the angle, the size of sin and cos's own rounding) near half a turn.
+// No per-token table is read: 12 bytes of positions serve all heads of a token.
 //
 // Bound by HBM: each element is read once and written once (backward: x and gz
 // read, dx written).  A head row is 16 lanes (32 for 512-byte rows) of one
