@@ -552,6 +552,8 @@ k6attn_status k6attn_packed_plan(k6attn_t h, const k6attn_packed *batch, const i
  *     that can overlap on the GPU need a workspace each.
  * Results do not depend on the other sequences of the batch beyond the last bits
  * that the splitting of long key ranges moves, and are the same in every run.
+ * The softmax weights are rounded to bf16, v's type, before their product with
+ * v; maxima, row sums, lse, partials and accumulators are fp32.
  */
 size_t k6attn_packed_workspace_bytes(k6attn_t h, const k6attn_packed *batch);
 k6attn_status k6attn_packed_forward(k6attn_t h, const k6attn_packed *batch, const void *plan, const void *q,

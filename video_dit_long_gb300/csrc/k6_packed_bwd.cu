@@ -29,9 +29,11 @@
 //
 // Seven products are executed for the five of the formulas (S and dP in both
 // kinds of item), so that nothing is summed across CTAs.  25,920 tokens causal by
-// frames of 1,620, 24/8 heads, on one GB300: 11.0 ms, 1.39 PFLOP/s executed, 80 %
-// of a long product's; 3,152 + 1,081 + 257 + 77 + 1 tokens, 24/24 heads: 440 us,
-// 5.5 us an item beyond its steps.
+// frames of 1,620, 24/8 heads, on one GB300: 11.1 ms, 1.38 PFLOP/s executed, 80 %
+// of a long product's; 3,152 + 1,081 + 257 + 77 + 1 tokens, 24/24 heads: 448 us,
+// 5.5 us an item beyond its steps.  Items are never cut: few key heads (1,500
+// tokens, 24/1 heads, 530 us) or few queries over many keys (8 over 52,360, 24/4
+// heads, 595 us) leave most SMs idle.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
