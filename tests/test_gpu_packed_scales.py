@@ -131,3 +131,14 @@ def test_the_gradients_of_a_sequence_are_those_of_it_alone(block):
     assert torch.equal(one.out[t], b.out[s])
     for x in ("dq", "dk", "dv"):
         assert torch.equal(getattr(one, x)[t], getattr(b, x)[s]), x
+
+
+@pytest.mark.parametrize("H,Hkv", [(3, 3), (6, 2), (24, 1)])
+@pytest.mark.parametrize("n,most", [(80, 5), (50, 20), (20, 60)])
+def test_many_short_sequences_of_all_sizes(H, Hkv, n, most):
+    """Tiles of a few rows, taken by one to sixteen warps each; sequences 2^-60 to 1 of the largest in turn."""
+    g = torch.Generator().manual_seed(78)
+    lens = torch.randint(0, most + 1, (n,), generator=g).tolist()
+    b = Batch(lens, lens, H, Hkv, 1, seed=79).forward()
+    scale_rows(b.dout, b.pad, [2.0 ** -(20 * (s % 4)) for s, L in enumerate(lens) for _ in range(L)])
+    check(backward(b))

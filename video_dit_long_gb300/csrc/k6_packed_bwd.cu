@@ -30,7 +30,7 @@
 // Seven products are executed for the five of the formulas (S and dP in both
 // kinds of item), so that nothing is summed across CTAs.  25,920 tokens causal by
 // frames of 1,620, 24/8 heads, on one GB300: 11.1 ms, 1.38 PFLOP/s executed, 80 %
-// of a long product's; 3,152 + 1,081 + 257 + 77 + 1 tokens, 24/24 heads: 448 us,
+// of a long product's; 3,152 + 1,081 + 257 + 77 + 1 tokens, 24/24 heads: 445 us,
 // 5.5 us an item beyond its steps.  Items are never cut: few key heads (1,500
 // tokens, 24/1 heads, 530 us) or few queries over many keys (8 over 52,360, 24/4
 // heads, 595 us) leave most SMs idle.
@@ -174,36 +174,40 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 
 // -------------------------------------------------------------- pre-pass
 
-// LD of every query row of the sequences, and for fp16 q/k the tops.  A block takes
-// one query tile of a key head after another (128 rows at most), then key tiles:
-// half a warp (16 lanes x 8 elements) has four rows in flight, whose sums and
-// logarithms it takes side by side, so that all rows of a tile are under way at
-// once.  A token's and a tile's largest are found in shared memory, two tiles'
-// entries in turn, so that a tile costs one barrier.  Bound by HBM: 25,920 tokens,
-// 24/8 heads, 64 us with bf16 q/k, 82 with fp16 (a block of 256 threads, two
-// passes a tile and logarithms row by row: 127).
-constexpr int ROWS_THREADS = 512;
+// LD of every query row of the sequences, and for fp16 q/k the tops.  A team of
+// warps takes one query tile of a key head after another (128 rows at most), then
+// key tiles: half a warp (16 lanes x 8 elements) has four rows in flight, whose
+// sums and logarithms it takes side by side, and the team has as many warps as
+// the batch's tiles have rows for on average (rows_team), so that all rows of a
+// tile are under way at once.  A token's and a tile's largest are found in shared
+// memory, two tiles' entries in turn, so that a tile costs one barrier of its
+// team.  Bound by HBM: 25,920 tokens, 24/8 heads, 64 us with bf16 q/k, 82 with
+// fp16 (256 threads a tile, two passes and logarithms row by row: 127).
+constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
 
 template <bool NORMS>
 __global__ void __launch_bounds__(ROWS_THREADS, 2)
     packed_bwd_rows_kernel(const PackedGeom g, const void *plan_base, const char *out, long out_stride,
                            const char *dout, long dout_stride, const char *v, long v_stride,
-                           const float *__restrict__ lse, float2 *__restrict__ LD, const PackedTops tops) {
-    constexpr int HALVES = ROWS_THREADS / 16;
-    __shared__ int best[2][2][128];  // [tile's turn][|dO|, |D|][token], or [turn][0][key]: ordered
-    const int lane = threadIdx.x & 31, sub = lane & 15, half = threadIdx.x >> 4;
-    const int mine = (sub >> 2) * HALVES + half;  // the row, of those in flight, whose sums this lane gets
+                           const float *__restrict__ lse, float2 *__restrict__ LD, const PackedTops tops,
+                           const int team_warps) {
+    extern __shared__ int best_of[];  // [team][tile's turn][|dO|, |D|][token], or [turn][0][key]: ordered
+    const int lane = threadIdx.x & 31, sub = lane & 15, team = (int)threadIdx.x / 32 / team_warps;
+    const int halves = 2 * team_warps, half = ((int)threadIdx.x >> 4) - team * halves;
+    const int mine = (sub >> 2) * halves + half;  // the row, of those in flight, whose sums this lane gets
+    int(*best)[2][128] = reinterpret_cast<int(*)[2][128]>(best_of + team * 512);
     const PackedPlan plan = packed_plan_at(const_cast<void *>(plan_base), g);
     if (!packed_plan_ok(*plan.head, g)) return;  // the next kernel reports it
     const uint32_t n_q = (uint32_t)plan.head->n_q, n_k = (uint32_t)plan.head->n_k;
     // the host keeps tokens * heads below 2^31
     const uint32_t q_units = n_q * (uint32_t)g.Hkv, units = q_units + (NORMS ? n_k * (uint32_t)g.Hkv : 0);
+    const uint32_t teams = ROWS_WARPS / team_warps;
     if constexpr (NORMS) {
-        for (int i = threadIdx.x; i < 512; i += ROWS_THREADS) (&best[0][0][0])[i] = ordered(-INFINITY);
+        for (int i = threadIdx.x; i < (int)teams * 512; i += ROWS_THREADS) best_of[i] = ordered(-INFINITY);
         __syncthreads();
     }
     int turn = 0;
-    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x * teams + team; u < units; u += gridDim.x * teams) {
         int n;    // tokens or keys of the tile
         long at;  // [Hkv][Tq] or [Hkv][Tk] index of its first
         const bool keys = u >= q_units;
@@ -212,11 +216,11 @@ __global__ void __launch_bounds__(ROWS_THREADS, 2)
             const PackedItem it = plan.q[u - (uint32_t)hk * n_q];
             n = it.n_tok_hk, at = (long)hk * g.Tq + it.tok0;
             const int rows = n * g.G;
-            for (int base = 0; base < rows; base += HALVES * 4) {
+            for (int base = 0; base < rows; base += halves * 4) {
                 uint4 a[4], b[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int r = min(base + i * HALVES + half, rows - 1);
+                    const int r = min(base + i * halves + half, rows - 1);
                     const int t = r / g.G, h = hk * g.G + r - t * g.G;
                     a[i] = reinterpret_cast<const uint4 *>(out + (long)(it.tok0 + t) * out_stride + (long)h * 256)[sub];
                     b[i] = reinterpret_cast<const uint4 *>(dout + (long)(it.tok0 + t) * dout_stride + (long)h * 256)[sub];
@@ -263,11 +267,11 @@ __global__ void __launch_bounds__(ROWS_THREADS, 2)
             const int hk = (int)((u - q_units) / n_k);
             const PackedKItem it = plan.k[u - q_units - (uint32_t)hk * n_k];
             n = it.n_key, at = (long)hk * g.Tk + it.krow0;
-            for (int base = 0; base < n; base += HALVES * 4) {
+            for (int base = 0; base < n; base += halves * 4) {
                 uint4 a[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int r = min(base + i * HALVES + half, n - 1);
+                    const int r = min(base + i * halves + half, n - 1);
                     a[i] = reinterpret_cast<const uint4 *>(v + (long)(it.krow0 + r) * v_stride + (long)hk * 256)[sub];
                 }
                 float q[4];
@@ -293,8 +297,9 @@ __global__ void __launch_bounds__(ROWS_THREADS, 2)
             }
         }
         if constexpr (NORMS) {
-            __syncthreads();
-            if (threadIdx.x < 32) {
+            if (team_warps == 1) __syncwarp();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(team_warps * 32) : "memory");
+            if (half < 2) {  // the team's first warp
                 float2 m = make_float2(-INFINITY, -INFINITY);
                 for (int t = lane; t < n; t += 32) {
                     const float2 x = make_float2(unordered(best[turn][0][t]), unordered(best[turn][1][t]));
@@ -665,8 +670,8 @@ __device__ __forceinline__ void ds_row(const float (&pr)[64], const float *sd, u
 // The exponent of key row r's dS in a key tile (warps 0-7, 256 threads; `scratch`:
 // 256 words of shared memory that nothing else uses until the function returns).
 // The tile's keys fall into groups that the same queries see: frames of the mask,
-// from the first key's on.  A query of group f sees the keys
-// of the groups up to f, so key r takes the largest over the groups from its own on; queries behind
+// from the first key's on.  A query of group f sees the keys of the groups up to
+// f, so key r takes the largest over the groups from its own on; queries behind
 // the last group's first are taken by whole tiles.
 __device__ __forceinline__ int dkv_exponent(const PackedBwdParams &p, const PackedKItem &it, int hk, int r, int *scratch) {
     const PackedGeom &g = p.g;
@@ -674,13 +679,17 @@ __device__ __forceinline__ int dkv_exponent(const PackedBwdParams &p, const Pack
     const float v = r < it.n_key ? p.tops.key[(long)hk * g.Tk + it.krow0 + r] : -INFINITY;
     const int last = it.key0 + it.n_key - 1, frame0 = F ? it.key0 / F : 0, groups = F ? last / F - frame0 + 1 : 1;
     const int tile0 = (packed_first_query(last, it.off, F) + g.tpt - 1) / g.tpt;
+    const int first = packed_first_query(it.key0, it.off, F) + t, end = min(tile0 * g.tpt, it.Lq);
     const long at = (long)hk * g.Tq + it.qrow0;
+    const float2 none = make_float2(-INFINITY, -INFINITY);
+    // the first of each is asked for before any is waited for: a short item has no more
+    float2 m = tile0 + t < it.qt1 ? p.tops.tile[at + (long)(tile0 + t) * g.tpt] : none;
+    float2 x = first < end ? p.tops.tok[at + first] : none;
     scratch[t] = ordered(-INFINITY);
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    float2 m = make_float2(-INFINITY, -INFINITY);
-    for (int i = tile0 + t; i < it.qt1; i += 256) {
-        const float2 x = p.tops.tile[at + (long)i * g.tpt];
-        m = make_float2(fmaxf(m.x, x.x), fmaxf(m.y, x.y));
+    for (int i = tile0 + t + 256; i < it.qt1; i += 256) {
+        const float2 y = p.tops.tile[at + (long)i * g.tpt];
+        m = make_float2(fmaxf(m.x, y.x), fmaxf(m.y, y.y));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -691,15 +700,14 @@ __device__ __forceinline__ int dkv_exponent(const PackedBwdParams &p, const Pack
         atomicMax(&scratch[groups - 1], ordered(m.x));
         atomicMax(&scratch[128 + groups - 1], ordered(m.y));
     }
-    const int end = min(tile0 * g.tpt, it.Lq);
-    for (int i = packed_first_query(it.key0, it.off, F) + t; i < end; i += 256) {
-        const float2 x = p.tops.tok[at + i];
+    for (int i = first; i < end; i += 256) {
+        if (i > first) x = p.tops.tok[at + i];
         const int f = F ? min(groups - 1, (i + it.off) / F - frame0) : 0;  // i + off >= frame0 F
         atomicMax(&scratch[f], ordered(x.x));
         atomicMax(&scratch[128 + f], ordered(x.y));
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (t < 64) {  // the largest from each group on: one warp each for |dO| and |D|, four groups a lane
+    if (groups > 1 && t < 64) {  // the largest from each group on: one warp each for |dO| and |D|, four groups a lane
         int4 *mine = reinterpret_cast<int4 *>(scratch + (t & 32) * 4) + lane;
         int4 x = *mine;
         x.z = max(x.z, x.w), x.y = max(x.y, x.z), x.x = max(x.x, x.y);
@@ -713,7 +721,7 @@ __device__ __forceinline__ int dkv_exponent(const PackedBwdParams &p, const Pack
         if (lane == 31) behind = ordered(-INFINITY);
         *mine = make_int4(max(x.x, behind), max(x.y, behind), max(x.z, behind), max(x.w, behind));
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (groups > 1) asm volatile("bar.sync 1, 256;" ::: "memory");
     const int f = F ? min(groups - 1, (it.key0 + r) / F - frame0) : 0;
     const float top = fmaxf(unordered(scratch[f]) + v, unordered(scratch[128 + f]));
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -991,9 +999,23 @@ __global__ void __launch_bounds__(pb::THREADS, 1)
 
 }  // namespace
 
-// Blocks of the pre-pass: a tile each, of queries and (with norms) of keys, up to two a SM.
+// Tiles of the pre-pass, counted from above, of queries and (with norms) of keys.
+static long rows_units(const PackedGeom &g, bool norms) {
+    return (g.Tq ? (long)g.cap_q * g.Hkv : 0) + (norms && g.Tk ? (long)g.cap_k * g.Hkv : 0);
+}
+
+// Warps of a team: eight rows each, for the rows that a tile has on average.  us, fp16, a call: 1,300 sequences of 20
+// tokens, 24/24 heads, 2,760 with this rule, 3,150 with 16 warps for every tile; long sequences get 16 either way.
+static int rows_team(const PackedGeom &g, bool norms) {
+    const long rows = (long)g.Tq * g.H + (norms ? (long)g.Tk * g.Hkv : 0), units = rows_units(g, norms);
+    int warps = 1;
+    while (warps < ROWS_WARPS && units * warps * 8 < rows) warps *= 2;
+    return warps;
+}
+
+// Blocks of the pre-pass: a tile for each of their teams, up to two blocks a SM.
 unsigned packed_bwd_rows_blocks(const PackedGeom &g, bool norms) {
-    const long want = (g.Tq ? (long)g.cap_q * g.Hkv : 0) + (norms && g.Tk ? (long)g.cap_k * g.Hkv : 0);
+    const long teams = ROWS_WARPS / rows_team(g, norms), want = (rows_units(g, norms) + teams - 1) / teams;
     return (unsigned)(want < 2L * g.sms ? want : 2L * g.sms);
 }
 
@@ -1045,9 +1067,11 @@ cudaError_t launch_packed_bwd(const PackedGeom &g, const PackedPtrs &t, const vo
     }
     if (g.Tq) {
         auto rows = [&](auto kernel) {
-            kernel<<<packed_bwd_rows_blocks(g, t.qk_f16), ROWS_THREADS, 0, st>>>(g, t.plan, static_cast<const char *>(out), out_stride * 2,
-                                           static_cast<const char *>(dout), dout_stride * 2,
-                                           static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, tops);
+            const int team = rows_team(g, t.qk_f16);
+            const size_t smem = t.qk_f16 ? (size_t)(ROWS_WARPS / team) * 512 * sizeof(int) : 0;
+            kernel<<<packed_bwd_rows_blocks(g, t.qk_f16), ROWS_THREADS, smem, st>>>(
+                g, t.plan, static_cast<const char *>(out), out_stride * 2, static_cast<const char *>(dout),
+                dout_stride * 2, static_cast<const char *>(t.v), t.v_stride * 2, lse, LD, tops, team);
         };
         if (t.qk_f16) rows(packed_bwd_rows_kernel<true>);
         else rows(packed_bwd_rows_kernel<false>);
