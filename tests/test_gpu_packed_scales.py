@@ -63,6 +63,8 @@ def one_sequence(q, k, v, out, lse, dout, block):
 def check(b):
     b.h.sync()
     for n, (rq, rk) in enumerate(R.sequences(b.q_lens, b.k_lens, b.pad, b.pad)):
+        if rq.start == rq.stop or rk.start == rk.stop:
+            continue
         refs, bounds = one_sequence(b.q[rq], b.k[rk], b.v[rk], b.out[rq], b.lse[:, rq], b.dout[rq], b.block)
         for got, ref, bound, what in zip((b.dq[rq], b.dk[rk], b.dv[rk]), refs, bounds, ("dq", "dk", "dv")):
             R.assert_within(got, ref, bound, f"{what} of sequence {n}")
