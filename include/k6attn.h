@@ -584,11 +584,110 @@ k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, con
                                      long dk_stride, void *dv, long dv_stride, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/*
+ * Keys and values in pages.  Streams that grow (a frame or a token at a time, or
+ * prompts read in parts) keep the rotated keys and the values of their tokens in
+ * a cache, a pool of pages of page_tokens tokens each; a table names the pages
+ * of each stream in order, so that a stream grows without moving, and streams
+ * with a beginning in common may name the same pages for it ([USP] "KV-cache").
+ * BF16 handles.
+ *  n_seq        streams; stream s has the new (query) tokens [cu_q[s], cu_q[s+1])
+ *               of the packed q, k, v and, with them, k_lens[s] keys: query i of
+ *               Lq is the token at key position Lk - Lq + i.
+ *  kv_heads     key/value heads (divides H, H / kv_heads <= 128).
+ *  mask_block   as in k6attn_packed.
+ *  page_tokens  tokens of a page, a multiple of 16.
+ *  max_pages    columns of the table, int32 [n_seq][max_pages]: key position p of
+ *               stream s lies at token p % page_tokens of page
+ *               table[s][p / page_tokens].  Entries behind a stream's last page
+ *               are not read.
+ *  n_groups     0, or groups of streams with a prefix in common: group g is the
+ *               streams [cu_groups[g], cu_groups[g+1]) (int32 [n_groups + 1],
+ *               ascending; other streams are on their own), whose first shared[g]
+ *               tokens (int32) have the same keys and values, in the same pages
+ *               or in copies.  A stream may be shorter than that.
+ *  n_pages      pages of the pool, n_pages * page_tokens below 2^31.
+ *  q_tokens     token rows of q, k, v (at least the last offset).
+ */
+typedef struct {
+    int n_seq;
+    int kv_heads;
+    int mask_block;
+    int page_tokens;
+    int max_pages;
+    int n_groups;
+    long n_pages;
+    long q_tokens;
+} k6attn_paged;
+
+/*
+ * A pool of pages of keys or of values, [n_pages][page_tokens][kv_heads][128] with
+ * dense head rows and any order of the other three (strides in elements, multiples
+ * of 8; no two rows may overlap).  The pools of k and v may interleave, as parts of
+ * one tensor do.
+ */
+typedef struct {
+    void *data;
+    long page_stride, token_stride, head_stride;
+} k6attn_pages;
+
+/*
+ * The work of a step over pages, made on the device from cu_q, k_lens, the table
+ * and, with groups, cu_groups and shared (int32 device arrays): where each new
+ * token's key lies, and the lists of the attention call.  One plan serves the
+ * calls of every layer of the step, and is not changed by them.  Offsets that are
+ * not ascending or leave [0, q_tokens] (groups: [0, n_seq]), k_lens outside
+ * [0, max_pages * page_tokens] and negative `shared` make K6ATTN_ERR_INVALID_ARG
+ * at k6attn_sync, and so does a call with a batch other than the plan's; the call
+ * then writes nothing.  A table entry in use that is no page of the pool makes the
+ * same error: a new token there is left out of the cache, and the attention of its
+ * stream (with a group, of the whole group) has undefined finite or NaN results;
+ * nothing outside the pool is read or written.
+ */
+size_t k6attn_paged_plan_bytes(k6attn_t h, const k6attn_paged *batch);
+k6attn_status k6attn_paged_plan(k6attn_t h, const k6attn_paged *batch, const int *cu_q, const int *k_lens,
+                                const int *table, const int *cu_groups, const int *shared, void *plan,
+                                size_t plan_bytes, void *stream);
+
+/*
+ * Appends a step's new tokens: q, k, v [q_tokens][H | kv_heads | kv_heads][128]
+ * bf16 (parts of a fused projection, say) with positions [q_tokens][3], as
+ * k6attn_packed_norm_rope takes them.  The normed and rotated queries go to q_out
+ * (out_dtype: BF16 or F16), the normed and rotated keys (out_dtype) and the values
+ * (bf16, as they are) to the tokens' places in the pages.  q and q_out may both be
+ * NULL (keys and values alone).  Rows outside [cu_q[0], cu_q[n_seq]) are neither
+ * read nor written, nor is any other place of the pages; a token before key position 0
+ * (more queries than keys) is not stored.  Pages that two streams share
+ * must not receive new tokens of more than one of them: which of two values at one
+ * place stays is undefined.  q_out may be q for BF16.
+ */
+k6attn_status k6attn_paged_append(k6attn_t h, const k6attn_paged *batch, const void *plan, const void *q,
+                                  long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                  const int *positions, const float *q_weight, const float *k_weight, float eps,
+                                  void *q_out, long q_out_stride, const k6attn_pages *k_cache,
+                                  const k6attn_pages *v_cache, k6attn_dtype out_dtype, void *stream);
+
+/*
+ * Attention of a step's queries over the pages: as k6attn_packed_forward, with the
+ * keys of stream s in its pages (`table` as the plan was made from).  The keys that
+ * a group shares are taken once for all of its streams where that saves work, out of
+ * the pages of one of them; results are those of the call without groups to within
+ * rounding.  Tokens of a page behind the stream's last key may hold anything; those before
+ * it must be finite, also where the mask hides them.  workspace: at least
+ * k6attn_paged_workspace_bytes.
+ */
+size_t k6attn_paged_workspace_bytes(k6attn_t h, const k6attn_paged *batch);
+k6attn_status k6attn_paged_forward(k6attn_t h, const k6attn_paged *batch, const void *plan, const int *table,
+                                   const void *q, long q_stride, const k6attn_pages *k_cache,
+                                   const k6attn_pages *v_cache, k6attn_dtype qk_dtype, void *out, long out_stride,
+                                   float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronise `stream`, then read and clear the handle's device error word:
  * K6ATTN_ERR_TIMEOUT if any kernel of this handle gave up on a wait,
  * K6ATTN_ERR_RANGE if a rotation into fp16 overflowed or a constant-max row
  * underflowed,
- * K6ATTN_ERR_INVALID_ARG if a packed plan's offsets or its use were wrong,
+ * K6ATTN_ERR_INVALID_ARG if a packed or paged plan's offsets or its use were
+ * wrong, or a table named a page that the pool does not have,
  * K6ATTN_ERR_CUDA on an asynchronous CUDA error, or if the device placed
  * the attention kernel's dynamic shared memory off a 1024-byte boundary (the
  * kernel then computes nothing; its tiles need that alignment and its 227 KB

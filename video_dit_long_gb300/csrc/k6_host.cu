@@ -107,6 +107,25 @@ bool make_rows_map(CUtensorMap *m, const void *base, long tokens, int heads, lon
     return true;
 }
 
+bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, const char **why) {
+    const DriverFns &f = driver();
+    if (!f.encode) {
+        if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
+        return false;
+    }
+    cuuint64_t dims[4] = {128, (cuuint64_t)g.g.Hkv, (cuuint64_t)g.page, (cuuint64_t)g.n_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)c.head * 2, (cuuint64_t)c.token * 2, (cuuint64_t)c.page * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)g.box, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (f.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+        if (why) *why = "cuTensorMapEncodeTiled rejected a cache";
+        return false;
+    }
+    return true;
+}
+
 cudaError_t set_max_dynamic_smem(const void *func, int bytes) {
     static std::mutex mu;
     static std::vector<std::pair<const void *, unsigned long long>> done;  // (kernel, context id) set up

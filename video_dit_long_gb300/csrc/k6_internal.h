@@ -239,6 +239,59 @@ size_t packed_fwd_workspace(const PackedGeom &p);
 cudaError_t launch_packed_fwd(const PackedGeom &p, const PackedPtrs &t, void *out, long out_stride, float *lse,
                               void *ws, cudaStream_t st, const char **why);
 
+// A batch over a cache of pages.  Lists, tiles and masks are those of `g`, whose
+// Tk is the most keys that one stream can have.
+struct PagedGeom {
+    PackedGeom g;
+    int page, box;                    // tokens of a page; and of one copy out of it (divides the page and 128)
+    int n_pages, max_pages;           // pages of the pool; columns of the table
+    int n_groups;
+    int cap_prefix;                   // query tiles over shared prefixes, per key head
+    long cap_part;                    // rows of partial outputs
+};
+PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms);
+
+// Pages of keys or values: strides in elements.
+struct PagedCache {
+    void *p;
+    long page, token, head;
+};
+
+size_t paged_plan_bytes(const PagedGeom &p);
+cudaError_t launch_paged_plan(const PagedGeom &p, const int *cu_q, const int *k_lens, const int *table,
+                              const int *cu_groups, const int *shared, void *plan, int *err, cudaStream_t st);
+
+// Norm and rotation of new tokens' queries and keys; keys and values to their pages.
+struct PagedAppend {
+    const void *plan;
+    const void *x[3];                 // queries (or null), keys, values
+    long x_stride[3];
+    void *q_out;
+    long q_out_stride;
+    PagedCache cache[2];              // keys, values
+    const int *positions;
+    const unsigned long long *turns;
+    const float *w[2];
+    float eps;
+    int *err;
+};
+cudaError_t launch_paged_append(const Geom &g, const PagedGeom &p, const PagedAppend &a, k6attn_dtype out,
+                                cudaStream_t st);
+
+struct PagedPtrs {
+    const void *q;
+    long q_stride;
+    PagedCache cache[2];
+    bool qk_f16;
+    const void *plan;
+    const int *table;
+    unsigned long long wait_limit_ns;
+    int *err;
+};
+size_t paged_fwd_workspace(const PagedGeom &p);
+cudaError_t launch_paged_fwd(const PagedGeom &p, const PagedPtrs &t, void *out, long out_stride, float *lse, void *ws,
+                             cudaStream_t st, const char **why);
+
 size_t packed_bwd_workspace(const PackedGeom &p);
 unsigned packed_bwd_rows_blocks(const PackedGeom &p, bool norms);  // of the backward pass's pre-pass
 cudaError_t launch_packed_bwd(const PackedGeom &p, const PackedPtrs &t, const void *out, long out_stride,

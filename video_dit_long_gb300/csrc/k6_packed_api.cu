@@ -1,5 +1,6 @@
-// k6_packed_api.cu -- entry points of the packed-sequence calls: argument checks
-// on the host, then the launches.  Nothing here allocates or aborts.
+// k6_packed_api.cu -- entry points of the packed-sequence calls, over rows and over
+// pages: argument checks on the host, then the launches.  Nothing here allocates or
+// aborts.
 #include <stdint.h>
 
 #include "k6_packed_tma.h"
@@ -111,6 +112,91 @@ k6attn_status check_plan(const char *fn, const void *plan) {
     if (!plan || !aligned16(plan))
         return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null plan, or one that is not 16-byte aligned", fn);
     return K6ATTN_OK;
+}
+
+k6attn_status check_paged_sizes(const char *fn, k6attn_t h, const k6attn_paged *b) {
+    if (!h) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null handle", fn);
+    if (!b) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null batch", fn);
+    const k6attn_packed rows = {b->n_seq, b->kv_heads, b->mask_block, b->q_tokens, 0};
+    const k6attn_status s = check_sizes(fn, h, &rows);
+    if (s != K6ATTN_OK) return s;
+    if (b->page_tokens < 16 || b->page_tokens % 16)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: pages of %d tokens; a multiple of 16 wanted", fn, b->page_tokens);
+    if (b->max_pages < 1 || b->n_pages < 0 || b->n_groups < 0)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: max_pages must be >= 1, n_pages and n_groups >= 0", fn);
+    if (b->page_tokens >= (1 << 24) || (long)b->max_pages * b->page_tokens >= (1L << 29) || b->n_pages >= (1L << 31) ||
+        b->n_pages * b->page_tokens >= (1L << 31) || b->n_groups >= (1 << 24) ||
+        (b->q_tokens + b->n_seq) * h->g.H >= (1L << 29))
+        return set_error(K6ATTN_ERR_UNSUPPORTED, "%s: batch or cache too large", fn);
+    return K6ATTN_OK;
+}
+
+k6attn_status check_paged(const char *fn, k6attn_t h, const k6attn_paged *b) {
+    const k6attn_status s = check_handle(fn, h);
+    return s != K6ATTN_OK ? s : check_paged_sizes(fn, h, b);
+}
+
+// A pool of pages as three strided axes of dense head rows; axes of one entry are given no stride of their own.
+struct Pool {
+    const char *name;
+    PagedCache c;
+    long n[3], stride[3];  // ascending strides
+    long extent;           // elements from the first to behind the last
+};
+
+k6attn_status check_pool(const char *fn, const char *name, const k6attn_pages *pages, const PagedGeom &g, Pool *r) {
+    r->name = name;
+    r->extent = 0;
+    if (!pages || (!pages->data && g.n_pages > 0)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null %s", fn, name);
+    r->c = {pages->data, pages->page_stride, pages->token_stride, pages->head_stride};
+    if (g.n_pages == 0) return K6ATTN_OK;
+    if (!aligned16(pages->data)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+    const long count[3] = {g.g.Hkv, g.page, g.n_pages};
+    long *stride[3] = {&r->c.head, &r->c.token, &r->c.page};
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; i++)
+        if (count[i] == 1) *stride[i] = 128;  // never taken
+    for (int i = 0; i < 3; i++)
+        for (int j = 0; j < 2; j++)
+            if (*stride[order[j]] > *stride[order[j + 1]] ||
+                (*stride[order[j]] == *stride[order[j + 1]] && count[order[j]] > count[order[j + 1]])) {
+                const int x = order[j];
+                order[j] = order[j + 1], order[j + 1] = x;
+            }
+    r->extent = 128;
+    for (int i = 0; i < 3; i++) {
+        const long n = count[order[i]], s = *stride[order[i]];
+        r->n[i] = n, r->stride[i] = s;
+        if (n == 1) continue;
+        if (s < r->extent || s % 8 || s >= (1L << 39))
+            return set_error(K6ATTN_ERR_INVALID_ARG,
+                             "%s: a stride of %s is %ld elements; a multiple of 8 wanted, and rows that do not overlap",
+                             fn, name, s);
+        r->extent += (n - 1) * s;
+    }
+    return K6ATTN_OK;
+}
+
+Rows flat(const Pool &p) { return flat(p.name, p.c.p, (size_t)p.extent * 2); }
+
+// Whether two pools share a byte.  Parts of one tensor interleave: with the same strides, and the distance between
+// them modulo one stride clear of what the smaller strides span, where the larger strides are multiples of that one.
+bool share(const Pool &a, const Pool &b) {
+    if (!overlap(a.c.p, (size_t)a.extent * 2, b.c.p, (size_t)b.extent * 2)) return false;
+    long delta = (long)(reinterpret_cast<uintptr_t>(b.c.p) - reinterpret_cast<uintptr_t>(a.c.p));
+    for (int i = 0; i < 3; i++)
+        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.stride[i] != b.stride[i])) return true;
+    long width = 128 * 2;
+    for (int i = 0; i < 3; i++) {
+        if (a.n[i] == 1) continue;
+        const long s = a.stride[i] * 2;
+        bool multiples = true;
+        for (int j = i + 1; j < 3; j++) multiples = multiples && (a.n[j] == 1 || a.stride[j] * 2 % s == 0);
+        const long at = ((delta % s) + s) % s;
+        if (multiples && at >= width && at + width <= s) return false;
+        width += (a.n[i] - 1) * s;
+    }
+    return true;
 }
 
 }  // namespace
@@ -344,6 +430,143 @@ k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, con
                                             dv, dv_stride, workspace, static_cast<cudaStream_t>(stream), &why);
     if (e != cudaSuccess && why) return set_error(K6ATTN_ERR_CUDA, "%s: %s", fn, why);
     return cuda_check(e, "packed_backward launch");
+}
+
+size_t k6attn_paged_plan_bytes(k6attn_t h, const k6attn_paged *batch) {
+    if (check_paged_sizes("paged_plan_bytes", h, batch) != K6ATTN_OK) return 0;
+    return paged_plan_bytes(paged_geom(h->g, *batch, h->sms));
+}
+
+k6attn_status k6attn_paged_plan(k6attn_t h, const k6attn_paged *batch, const int *cu_q, const int *k_lens,
+                                const int *table, const int *cu_groups, const int *shared, void *plan,
+                                size_t plan_bytes, void *stream) {
+    const char *fn = "paged_plan";
+    clear_error();
+    k6attn_status s = check_paged(fn, h, batch);
+    if (s != K6ATTN_OK) return s;
+    if (!cu_q || !k_lens || !table) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null cu_q, k_lens or table", fn);
+    if (batch->n_groups > 0 && (!cu_groups || !shared))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null cu_groups or shared, with groups", fn);
+    if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(k_lens) | reinterpret_cast<uintptr_t>(table) |
+         reinterpret_cast<uintptr_t>(cu_groups) | reinterpret_cast<uintptr_t>(shared)) & 3)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: offsets, lengths and the table must be 4-byte aligned", fn);
+    const PagedGeom g = paged_geom(h->g, *batch, h->sms);
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
+    const size_t need = paged_plan_bytes(g);
+    if (plan_bytes < need)
+        return set_error(K6ATTN_ERR_WORKSPACE, "%s: plan of %zu bytes needed, %zu given", fn, need, plan_bytes);
+    const size_t n = (size_t)batch->n_seq * 4, groups = (size_t)batch->n_groups * 4;
+    if (overlap(plan, need, cu_q, n + 4) || overlap(plan, need, k_lens, n) ||
+        overlap(plan, need, table, n * batch->max_pages) ||
+        (groups && (overlap(plan, need, cu_groups, groups + 4) || overlap(plan, need, shared, groups))))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: the plan overlaps the offsets, the lengths or the table", fn);
+    return cuda_check(launch_paged_plan(g, cu_q, k_lens, table, cu_groups, shared, plan, h->err,
+                                        static_cast<cudaStream_t>(stream)),
+                      "paged_plan launch");
+}
+
+k6attn_status k6attn_paged_append(k6attn_t h, const k6attn_paged *batch, const void *plan, const void *q,
+                                  long q_stride, const void *k, long k_stride, const void *v, long v_stride,
+                                  const int *positions, const float *q_weight, const float *k_weight, float eps,
+                                  void *q_out, long q_out_stride, const k6attn_pages *k_cache,
+                                  const k6attn_pages *v_cache, k6attn_dtype out_dtype, void *stream) {
+    const char *fn = "paged_append";
+    clear_error();
+    k6attn_status s = check_paged(fn, h, batch);
+    if (s != K6ATTN_OK) return s;
+    if (out_dtype != K6ATTN_BF16 && out_dtype != K6ATTN_F16)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: output type must be BF16 or F16", fn);
+    const PagedGeom g = paged_geom(h->g, *batch, h->sms);
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
+    const long T = g.g.Tq, wq = (long)g.g.H * 128, wk = (long)g.g.Hkv * 128;
+    if ((q == nullptr) != (q_out == nullptr))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: give both q and q_out, or neither", fn);
+    if (T > 0 && !positions) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null positions", fn);
+    if (q && (q_weight == nullptr) != (k_weight == nullptr))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: give both norm weights, or neither", fn);
+    if (!(eps >= 0.f)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+    if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(q_weight) |
+         reinterpret_cast<uintptr_t>(k_weight)) & 3)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: positions and weights must be 4-byte aligned", fn);
+    if (!q) q_weight = nullptr;
+    const Rows in[] = {{"q", q, q ? T : 0, q_stride, wq, 2},
+                       {"k", k, T, k_stride, wk, 2},
+                       {"v", v, T, v_stride, wk, 2},
+                       flat("the positions", positions, (size_t)T * 12),
+                       flat("a weight", q_weight, q_weight ? 512 : 0),
+                       flat("a weight", k_weight, k_weight ? 512 : 0),
+                       flat("the plan", plan, paged_plan_bytes(g))};
+    const Rows q_rows = {"q_out", q_out, q ? T : 0, q_out_stride, wq, 2};
+    Pool pool[2];
+    for (int i = 0; i < 3; i++)
+        if ((s = check_rows(fn, in[i])) != K6ATTN_OK) return s;
+    if ((s = check_rows(fn, q_rows)) != K6ATTN_OK || (s = check_pool(fn, "k_cache", k_cache, g, &pool[0])) != K6ATTN_OK ||
+        (s = check_pool(fn, "v_cache", v_cache, g, &pool[1])) != K6ATTN_OK)
+        return s;
+    const bool in_place = q && q_out == q && q_out_stride == q_stride && out_dtype == K6ATTN_BF16;
+    const Rows caches[] = {flat(pool[0]), flat(pool[1])};
+    if ((s = check_apart(fn, &q_rows, 1, in + (in_place ? 1 : 0), in_place ? 6 : 7)) != K6ATTN_OK ||
+        (s = check_apart(fn, &q_rows, 1, caches, 2)) != K6ATTN_OK)
+        return s;
+    for (int i = 0; i < 2; i++)
+        if ((s = check_apart(fn, caches + i, 1, in, 7)) != K6ATTN_OK) return s;
+    if (share(pool[0], pool[1])) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: k_cache overlaps v_cache", fn);
+    PagedAppend a = {};
+    a.plan = plan;
+    a.x[0] = q, a.x_stride[0] = q_stride, a.x[1] = k, a.x_stride[1] = k_stride, a.x[2] = v, a.x_stride[2] = v_stride;
+    a.q_out = q_out, a.q_out_stride = q_out_stride;
+    a.cache[0] = pool[0].c, a.cache[1] = pool[1].c;
+    a.positions = positions, a.turns = h->turns, a.w[0] = q_weight, a.w[1] = k_weight, a.eps = eps, a.err = h->err;
+    return cuda_check(launch_paged_append(h->g, g, a, out_dtype, static_cast<cudaStream_t>(stream)),
+                      "paged_append launch");
+}
+
+size_t k6attn_paged_workspace_bytes(k6attn_t h, const k6attn_paged *batch) {
+    if (check_paged_sizes("paged_workspace_bytes", h, batch) != K6ATTN_OK) return 0;
+    return paged_fwd_workspace(paged_geom(h->g, *batch, h->sms));
+}
+
+k6attn_status k6attn_paged_forward(k6attn_t h, const k6attn_paged *batch, const void *plan, const int *table,
+                                   const void *q, long q_stride, const k6attn_pages *k_cache,
+                                   const k6attn_pages *v_cache, k6attn_dtype qk_dtype, void *out, long out_stride,
+                                   float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    const char *fn = "paged_forward";
+    clear_error();
+    k6attn_status s = check_paged(fn, h, batch);
+    if (s != K6ATTN_OK) return s;
+    if (qk_dtype != K6ATTN_BF16 && qk_dtype != K6ATTN_F16)
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: q/k type must be BF16 or F16", fn);
+    const PagedGeom g = paged_geom(h->g, *batch, h->sms);
+    if ((s = check_plan(fn, plan)) != K6ATTN_OK) return s;
+    if (!table || (reinterpret_cast<uintptr_t>(table) & 3))
+        return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null or misaligned table", fn);
+    const long wq = (long)g.g.H * 128;
+    const size_t need = paged_fwd_workspace(g);
+    if (need && (!workspace || workspace_bytes < need))
+        return set_error(K6ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                         workspace ? workspace_bytes : (size_t)0);
+    if (need && !aligned16(workspace)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: workspace misaligned", fn);
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: lse misaligned", fn);
+    Pool pool[2];
+    if ((s = check_pool(fn, "k_cache", k_cache, g, &pool[0])) != K6ATTN_OK ||
+        (s = check_pool(fn, "v_cache", v_cache, g, &pool[1])) != K6ATTN_OK)
+        return s;
+    const Rows in[] = {{"q", q, g.g.Tq, q_stride, wq, 2},
+                       flat(pool[0]),
+                       flat(pool[1]),
+                       flat("the table", table, (size_t)g.g.n_seq * g.max_pages * 4),
+                       flat("the plan", plan, paged_plan_bytes(g))};
+    const Rows out_[] = {{"out", out, g.g.Tq, out_stride, wq, 2},
+                         flat("lse", lse, (size_t)g.g.Tq * g.g.H * 4),
+                         flat("the workspace", workspace, need)};
+    if ((s = check_rows(fn, in[0])) != K6ATTN_OK || (s = check_rows(fn, out_[0])) != K6ATTN_OK ||
+        (s = check_apart(fn, out_, 3, in, 5)) != K6ATTN_OK)
+        return s;
+    const PagedPtrs t{q, q_stride, {pool[0].c, pool[1].c}, qk_dtype == K6ATTN_F16, plan, table, h->wait_limit_ns, h->err};
+    const char *why = nullptr;
+    const cudaError_t e = launch_paged_fwd(g, t, out, out_stride, lse, workspace, static_cast<cudaStream_t>(stream), &why);
+    if (e != cudaSuccess && why) return set_error(K6ATTN_ERR_CUDA, "%s: %s", fn, why);
+    return cuda_check(e, "paged_forward launch");
 }
 
 }  // extern "C"

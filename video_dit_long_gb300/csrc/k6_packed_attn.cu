@@ -30,6 +30,12 @@
 // 3.4 us beyond its tiles: 1 warp a scheduler runs its serial code slowly.)
 // All waits are bounded (DEV_TIMEOUT), as in the other kernels.
 //
+// Keys in pages (k6_paged.cuh): the same kernel, whose producers fetch a tile as
+// copies of `box` tokens out of the pages that the table names, one lane a copy; a
+// page that the table does not name right is left to the copy's zero fill and
+// reported.  Partials lie row behind row, and paged_merge_kernel joins a row's own
+// with those over the keys that its group shares.
+//
 // Bounds and figures on one GB300.  Long clips: the tensor pipe under the power
 // cap; 25,920 tokens causal by frames of 1,620, 24/8 heads, 2.98 ms = 1.47
 // PFLOP/s, 77 % of a library product's burst (the pipe active 79 % of the time; a
@@ -40,8 +46,10 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "k6_device.cuh"
-#include "k6_packed.cuh"
+#include "k6_paged.cuh"
 #include "k6_packed_tma.h"
 
 namespace k6 {
@@ -95,6 +103,12 @@ struct PackedFwdParams {
     int *err;
 };
 
+// Keys in pages: besides the above, whose g is pg.g.
+struct PagedFwdParams : PackedFwdParams {
+    PagedGeom pg;
+    const int *table;                         // [n_seq][max_pages]
+};
+
 namespace {
 
 // exp2 of a difference from a maximum that may be -inf (nothing seen yet): 0 then.
@@ -107,7 +121,8 @@ struct Walk {
     const int *sched;   // null: list is this CTA's own
     uint32_t rounds, n_items;
     int slots;          // partials that one slot number stands for (1, or one for every key head)
-    __device__ Walk(const PackedPlan &plan, const PackedGeom &g, bool ok) {
+    template <class Plan>
+    __device__ Walk(const Plan &plan, const PackedGeom &g, bool ok) {
         list = plan.fwd;
         const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
         slots = plan.head->slot_step;
@@ -143,10 +158,60 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
                  : "memory");
 }
 
+// The plan of a call, and whether it is the batch's.
+__device__ __forceinline__ PackedPlan plan_of(const PackedFwdParams &p) {
+    return packed_plan_at(const_cast<void *>(p.plan), p.g);
+}
+__device__ __forceinline__ PagedPlan plan_of(const PagedFwdParams &p) {
+    return paged_plan_at(const_cast<void *>(p.plan), p.pg);
+}
+__device__ __forceinline__ bool plan_ok_for(const PackedPlan &plan, const PackedFwdParams &p) {
+    return packed_plan_ok(*plan.head, p.g);
+}
+__device__ __forceinline__ bool plan_ok_for(const PagedPlan &plan, const PagedFwdParams &p) {
+    return paged_plan_ok(*plan.head, p.pg);
+}
+
+// The copies that bring tile `kt` of 128 keys of an item and head hk to dst.  The whole warp; returns with the barrier
+// told of all of their bytes.
+__device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedItem &it, int kt, int hk, const void *tm,
+                                          uint8_t *dst, uint64_t *bar, bool leader) {
+    using namespace pf;
+    if (leader) {
+        const int row = it.krow0 + kt * BN;
+        mbar_arrive_expect_tx(bar, TILE);
+        tma_load_4d(dst, tm, bar, 0, hk, row, 0);
+        tma_load_4d(dst + PANEL, tm, bar, 64, hk, row, 0);
+    }
+}
+
+// Keys in pages.  Lane l brings box l of the tile, both panels; boxes wholly behind the stream's last key are left out
+// (their rows of S are masked, those of V zeroed, and no page is theirs).
+__device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedItem &it, int kt, int hk, const void *tm,
+                                          uint8_t *dst, uint64_t *bar, bool leader) {
+    using namespace pf;
+    const int box = p.pg.box, lane = threadIdx.x & 31, n = paged_boxes(p.pg, it.Lk, kt);
+    int column, page = 0;
+    const int tok = paged_box(p.pg, kt, lane, column);
+    if (lane < n) {
+        const int named = p.table[(long)it.krow0 * p.pg.max_pages + column];
+        page = paged_page(p.pg, named);
+        if (page != named) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+    }
+    if (leader) mbar_arrive_expect_tx(bar, (uint32_t)(n * box) * 256u);
+    __syncwarp();
+    if (lane < n) {
+        tma_load_4d(dst + lane * box * 128, tm, bar, 0, hk, tok, page);
+        tma_load_4d(dst + PANEL + lane * box * 128, tm, bar, 64, hk, tok, page);
+    }
+}
+
+template <class Params>
 __global__ void __launch_bounds__(pf::THREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const PackedFwdParams p) {
+                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
     using namespace pf;
+    constexpr bool PAGED = std::is_same<Params, PagedFwdParams>::value;
     extern __shared__ __align__(1024) uint8_t smem[];
     launch_next_kernel();
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
@@ -208,8 +273,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     wait_previous_kernel();
-    const PackedPlan plan = packed_plan_at(const_cast<void *>(p.plan), p.g);
-    const bool plan_ok = packed_plan_ok(*plan.head, p.g);
+    const auto plan = plan_of(p);
+    const bool plan_ok = plan_ok_for(plan, p);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
     const Walk walk(plan, p.g, plan_ok);  // nothing to walk under a plan that is not this batch's
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
@@ -241,13 +306,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 for (int j = 0; j < T && ok; j++, n++) {
                     const uint32_t slot = n % NSLOT;
                     if (!(ok = mbar_wait_w(&empty[slot], ((n / NSLOT) & 1) ^ 1, w))) break;
-                    if (leader) {
-                        uint8_t *dst = ring + slot * TILE;
-                        const int row = it.krow0 + (it.kt0 + j) * BN;
-                        mbar_arrive_expect_tx(&full[slot], TILE);
-                        tma_load_4d(dst, tm, &full[slot], 0, hk, row, 0);
-                        tma_load_4d(dst + PANEL, tm, &full[slot], 64, hk, row, 0);
-                    }
+                    load_tile(p, it, it.kt0 + j, hk, tm, ring + slot * TILE, &full[slot], leader);
                     if (j == 0 && warp == 8) {  // Q once the last S of the item before has read its tile
                         if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) {
                             n++;  // this tile's load was issued
@@ -376,7 +435,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             tc_fence_after();
             // each thread stores its row, a 32-byte sector at a time
             const bool part = it.slot >= 0;
-            const long prow = ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM + r;
+            const long prow = PAGED ? (long)it.slot + (walk.slots > 1 ? hk * n_tok * p.g.G : 0) + r
+                                    : ((long)it.slot * walk.slots + (walk.slots > 1 ? hk : 0)) * BM + r;
             if (part) {
                 float *dst = p.part_o + prow * D;
 #pragma unroll 1
@@ -589,6 +649,40 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     }
 }
 
+// Takes up N more partials of a row, 8 values a lane: lse l (base 2; -inf: nothing), outputs o.
+template <int N>
+__device__ __forceinline__ void join(const float (&l)[N], const float4 (&o)[N][2], float &top, float &sum,
+                                     float (&acc)[8]) {
+    float m_new = top;
+#pragma unroll
+    for (int i = 0; i < N; i++) m_new = fmaxf(m_new, l[i]);
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const float old = ex2(top - ref);  // 0 from -inf
+    top = m_new;
+    sum *= old;
+#pragma unroll
+    for (int e = 0; e < 8; e++) acc[e] *= old;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const float f = ex2(l[i] - ref);
+        sum += f;
+        const float v[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; e++) acc[e] = fmaf(f, v[e], acc[e]);
+    }
+}
+
+// The joined row of token tok and query head `head_q`.
+__device__ __forceinline__ void store_joined(const PackedFwdParams &p, float top, float sum, const float (&acc)[8], long tok,
+                                             int head_q, int lane) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint4 *>(p.out + tok * p.out_stride + (long)head_q * 128 + lane * 8) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (lane == 0 && p.lse)
+        p.lse[(long)head_q * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
 // Joins the partials of the split tiles: half a warp per row of a split tile,
 // 32 bytes a lane,
 //   lse = log2 sum_c 2^lse_c,   o = sum_c 2^(lse_c - lse) o_c.
@@ -630,60 +724,71 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
                 o[i][1] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane + 1];
             }
         }
-        float m_new = top;
+        join<kU>(l, o, top, sum, acc);
+    }
+    store_joined(p, top, sum, acc, (long)m.tok0 + r / p.g.G, (m.n_tok_hk >> 8) * p.g.G + r % p.g.G, lane);
+}
+
+// Joins the partials of every row that has some over pages: half a warp per row,
+// as packed_merge_kernel, first those over the keys that its group shares, then its
+// own, each in key order.
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedFwdParams p) {
+    launch_next_kernel();
+    wait_previous_kernel();
+    const PagedPlan plan = plan_of(p);
+    const int lane = threadIdx.x & 15;
+    const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 4;
+    const uint32_t mi = x / (uint32_t)p.g.rows;
+    const int r = (int)(x - mi * (uint32_t)p.g.rows);
+    if (mi >= (uint32_t)p.g.cap_merge) return;
+    const bool early = mi < (uint32_t)p.g.sms;  // as in packed_merge_kernel
+    PagedMerge m;
+    if (early) m = plan.merge[mi];
+    const PagedHeader head = *plan.head;
+    if (!paged_plan_ok(head, p.pg) || mi >= (uint32_t)head.n_merge) return;
+    if (!early) m = plan.merge[mi];
+    const int rtok = r / p.g.G, rhead = r - rtok * p.g.G, hk = m.n_tok_hk >> 8;
+    if (rtok >= (m.n_tok_hk & 255)) return;
+    PagedParts pre = {0, 0, 0, 0};
+    if (m.prefix >= 0) {
+        const int i = m.tok0 + rtok - m.group_q0, tile = i / p.g.tpt;
+        pre = plan.prefix[(long)hk * p.pg.cap_prefix + m.prefix + tile];
+        pre.row += (i - tile * p.g.tpt) * p.g.G + rhead;
+    }
+    const int n = pre.n + m.own.n;
+    const long own = (long)m.own.row + r;
+    constexpr int kU = 4;  // partials in flight
+    float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
-        for (int i = 0; i < kU; i++) m_new = fmaxf(m_new, l[i]);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float old = ex2(top - ref);  // 0 from -inf
-        top = m_new;
-        sum *= old;
-#pragma unroll
-        for (int e = 0; e < 8; e++) acc[e] *= old;
+    for (int e = 0; e < 8; e++) acc[e] = 0.f;
+    for (int c = 0; c < n; c += kU) {
+        float4 o[kU][2];
+        float l[kU];
 #pragma unroll
         for (int i = 0; i < kU; i++) {
-            const float f = ex2(l[i] - ref);
-            sum += f;
-            const float v[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
-#pragma unroll
-            for (int e = 0; e < 8; e++) acc[e] = fmaf(f, v[e], acc[e]);
+            l[i] = -INFINITY, o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + i < n) {
+                const long row = c + i < pre.n ? pre.row + (long)(c + i) * pre.step
+                                               : own + (long)(c + i - pre.n) * m.own.step;
+                l[i] = p.part_lse[row];
+                o[i][0] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane];
+                o[i][1] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane + 1];
+            }
         }
+        join<kU>(l, o, top, sum, acc);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long tok = (long)m.tok0 + r / p.g.G;
-    const int head_q = (m.n_tok_hk >> 8) * p.g.G + r % p.g.G;
-    *reinterpret_cast<uint4 *>(p.out + tok * p.out_stride + (long)head_q * 128 + lane * 8) =
-        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-    if (lane == 0 && p.lse)
-        p.lse[(long)head_q * p.g.Tq + tok] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    store_joined(p, top, sum, acc, (long)m.tok0 + rtok, hk * p.g.G + rhead, lane);
 }
 
-}  // namespace
-
-size_t packed_fwd_workspace(const PackedGeom &p) {
-    const size_t rows = (size_t)p.cap_slots * 128;
-    return rows ? round256(rows * 128 * 4) + round256(rows * 4) + 256 : 0;  // 256: see launch_packed_fwd
-}
-
-cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *out, long out_stride, float *lse,
-                              void *ws, cudaStream_t st, const char **why) {
-    if (g.Tq == 0) return cudaSuccess;
-    CUtensorMap mq, mk, mv;
-    // without key rows no tile has keys and the maps of k and v are never used
-    if (!packed_q_map(&mq, t.q, g, t.q_stride, why) ||
-        !packed_kv_map(&mk, g.Tk ? t.k : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.k_stride : t.q_stride, why) ||
-        !packed_kv_map(&mv, g.Tk ? t.v : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.v_stride : t.q_stride, why))
-        return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel, pf::SMEM_TOTAL);
-    if (e != cudaSuccess) return e;
-    PackedFwdParams p;
+// What both launches tell their kernels; `rows` rows of partials in the workspace.
+template <class Params, class Ptrs>
+void fill(Params &p, const PackedGeom &g, const Ptrs &t, size_t rows, void *out, long out_stride, float *lse, void *ws) {
     p.g = g;
     p.plan = t.plan;
     p.scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.out_stride = out_stride;
     p.lse = lse;
-    const size_t rows = (size_t)g.cap_slots * 128;
     // partial rows are stored 32 bytes at a time; the caller's workspace may be 16-byte aligned only
     char *at = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31);
     p.part_o = reinterpret_cast<float *>(at);
@@ -694,9 +799,55 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
     p.wide = (reinterpret_cast<uintptr_t>(out) % 32 == 0 && out_stride * 2 % 32 == 0) ? 1 : 0;
     p.wait_limit_ns = t.wait_limit_ns;
     p.err = t.err;
-    e = launch_after(packed_fwd_kernel, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
+}
+
+size_t partials_bytes(size_t rows) {
+    return rows ? round256(rows * 128 * 4) + round256(rows * 4) + 256 : 0;  // 256: see fill()
+}
+
+}  // namespace
+
+size_t packed_fwd_workspace(const PackedGeom &p) { return partials_bytes((size_t)p.cap_slots * 128); }
+
+size_t paged_fwd_workspace(const PagedGeom &p) { return partials_bytes((size_t)p.cap_part); }
+
+cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *out, long out_stride, float *lse,
+                              void *ws, cudaStream_t st, const char **why) {
+    if (g.Tq == 0) return cudaSuccess;
+    CUtensorMap mq, mk, mv;
+    // without key rows no tile has keys and the maps of k and v are never used
+    if (!packed_q_map(&mq, t.q, g, t.q_stride, why) ||
+        !packed_kv_map(&mk, g.Tk ? t.k : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.k_stride : t.q_stride, why) ||
+        !packed_kv_map(&mv, g.Tk ? t.v : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.v_stride : t.q_stride, why))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel<PackedFwdParams>, pf::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    PackedFwdParams p;
+    fill(p, g, t, (size_t)g.cap_slots * 128, out, out_stride, lse, ws);
+    e = launch_after(packed_fwd_kernel<PackedFwdParams>, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
     if (e != cudaSuccess || g.extra == 0) return e;
     return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 15) / 16), 256, 0, st, p);
+}
+
+cudaError_t launch_paged_fwd(const PagedGeom &pg, const PagedPtrs &t, void *out, long out_stride, float *lse, void *ws,
+                             cudaStream_t st, const char **why) {
+    const PackedGeom &g = pg.g;
+    if (g.Tq == 0) return cudaSuccess;
+    CUtensorMap mq, mk, mv;
+    if (!packed_q_map(&mq, t.q, g, t.q_stride, why)) return cudaErrorInvalidValue;
+    // without pages no tile has keys and the maps of the caches are never used
+    mk = mv = mq;
+    if (pg.n_pages > 0 && (!make_pages_map(&mk, t.cache[0], pg, why) || !make_pages_map(&mv, t.cache[1], pg, why)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel<PagedFwdParams>, pf::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    PagedFwdParams p;
+    fill(p, g, t, (size_t)pg.cap_part, out, out_stride, lse, ws);
+    p.pg = pg;
+    p.table = t.table;
+    e = launch_after(packed_fwd_kernel<PagedFwdParams>, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
+    if (e != cudaSuccess || g.cap_merge == 0) return e;
+    return launch_after(paged_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 15) / 16), 256, 0, st, p);
 }
 
 }  // namespace k6

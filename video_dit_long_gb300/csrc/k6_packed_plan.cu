@@ -29,7 +29,11 @@
 // The order inside a class of equal work, and so which SM runs an item and
 // which slot holds a partial, may differ between runs; every item writes rows
 // of its own and partials are joined in key order, so results do not.
-#include "k6_packed.cuh"
+//
+// Streams over a cache of pages (k6_paged.cuh) are planned by the same code, from
+// units of tiles that the kernel first makes of the streams and of the groups that
+// share a prefix.
+#include "k6_paged.cuh"
 
 namespace k6 {
 
@@ -37,6 +41,7 @@ constexpr int MIN_PIECE = 4;       // key tiles of a piece at least
 constexpr int ITEM_COST = 2;       // start and end of an item in key tiles: 1.6 us against 0.7 us a tile
 constexpr int STREAM_MOST = 256;   // cost per SM up to which the batch is cut into one stretch per SM
 constexpr int STREAM_SEQS = 1024;  // and sequences
+constexpr int SHARE_LEAST = 8;     // key tiles that a shared prefix saves at least
 
 PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
     PackedGeom p;
@@ -64,6 +69,40 @@ PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
     return p;
 }
 
+PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms) {
+    PagedGeom r;
+    r.page = b.page_tokens, r.n_pages = (int)b.n_pages, r.max_pages = b.max_pages, r.n_groups = b.n_groups;
+    for (r.box = 128; r.page % r.box; r.box /= 2) {}
+    PackedGeom &p = r.g;
+    p.n_seq = b.n_seq;
+    p.H = g.H, p.Hkv = b.kv_heads, p.G = g.H / b.kv_heads, p.block = b.mask_block;
+    p.Tq = (int)b.q_tokens, p.Tk = b.max_pages * b.page_tokens;
+    p.tpt = 128 / p.G;
+    p.rows = p.tpt * p.G;
+    p.sms = sms;
+    // a group is taken together only where that halves its query tiles: at most two of each stream's, half of that
+    // over the shared keys
+    r.cap_prefix = b.n_groups > 0 ? b.n_seq : 0;
+    const long own = (long)p.Tq / p.tpt + b.n_seq, joined = b.n_groups > 0 ? (own < 2L * b.n_seq ? own : 2L * b.n_seq) : 0;
+    p.cap_q = (int)own + r.cap_prefix;
+    p.cap_k = 0;
+    p.extra = p.Tk > (2 * MIN_PIECE - 1) * 128 ? (sms + p.Hkv - 1) / p.Hkv : 0;
+    p.cap_slots = p.extra ? 2 * (p.extra * p.Hkv > sms ? p.extra * p.Hkv : sms) : 0;
+    p.cap_merge = (int)(p.cap_slots / 2 + joined * p.Hkv);
+    const long rows = (long)p.Tq * p.H, own_rows = joined * p.Hkv * p.rows, prefix_rows = (long)r.cap_prefix * p.Hkv * p.rows;
+    r.cap_part = (long)p.cap_slots * p.rows + (own_rows < rows ? own_rows : rows) + (prefix_rows < rows ? prefix_rows : rows);
+    const long most = ((long)p.cap_q * p.Hkv * ((p.Tk + 127L) / 128 + 1 + ITEM_COST) + sms - 1) / sms;
+    p.cap_rows = (int)(most < STREAM_MOST ? most : STREAM_MOST) / (ITEM_COST + 1) + 8;
+    const long list = (long)p.cap_q + p.extra, all = (long)sms * p.cap_rows;
+    p.cap_fwd = (int)(list > all ? list : all);
+    p.cap_sched = most <= STREAM_MOST && p.n_seq + b.n_groups <= STREAM_SEQS ? 0 : (list * p.Hkv + sms - 1) / sms * sms;
+    return r;
+}
+
+size_t paged_plan_bytes(const PagedGeom &p) {
+    return reinterpret_cast<size_t>(paged_plan_at(nullptr, p).slot) + (size_t)p.g.Tq * sizeof(int);
+}
+
 size_t packed_plan_bytes(const PackedGeom &p) {
     const PackedPlan at = packed_plan_at(nullptr, p);
     return reinterpret_cast<size_t>(at.k) + (size_t)p.cap_k * sizeof(PackedKItem);
@@ -77,15 +116,74 @@ enum List { FWD, QTILES, KTILES };
 
 struct Seq {
     int q0, Lq, k0, Lk, tiles;
+    int lo;            // first key tile
+    bool parts;        // its rows are joined with others': partials, whether cut or not
+    bool seen;         // every key is seen by every row, whatever the mask
+    int prefix, group_q0;
 };
 
-template <List LIST>
-__device__ __forceinline__ Seq sequence(const PackedGeom &p, const int *cu_q, const int *cu_k, int s) {
-    Seq r;
-    r.q0 = cu_q[s], r.Lq = cu_q[s + 1] - r.q0;
-    r.k0 = cu_k[s], r.Lk = cu_k[s + 1] - r.k0;
-    r.tiles = LIST == KTILES ? (r.Lk + 127) / 128 : (r.Lq + p.tpt - 1) / p.tpt;
-    return r;
+// What the lists are made of.  Batch: packed sequences.
+struct Batch {
+    const int *cu_q, *cu_k;
+    PackedPlan plan;
+    int n;
+    template <List LIST>
+    __device__ __forceinline__ Seq sequence(const PackedGeom &p, int s) const {
+        Seq r;
+        r.q0 = cu_q[s], r.Lq = cu_q[s + 1] - r.q0;
+        r.k0 = cu_k[s], r.Lk = cu_k[s + 1] - r.k0;
+        r.tiles = LIST == KTILES ? (r.Lk + 127) / 128 : (r.Lq + p.tpt - 1) / p.tpt;
+        r.lo = 0, r.parts = r.seen = false, r.prefix = r.group_q0 = -1;
+        return r;
+    }
+    // Room for the n partials of a tile, of every key head from hk0 on up to hk1, and its joins: the first one's slot,
+    // and how far the next piece's lies behind it.
+    __device__ __forceinline__ int partials(const PackedGeom &p, int &slots, int &merges, const Seq &, int, int tok0,
+                                            int n_tok, int hk0, int hk1, int n, int &step) const {
+        const int heads = hk1 - hk0, slot = atomicAdd(&slots, n), m = atomicAdd(&merges, heads);
+        for (int h = 0; h < heads; h++)
+            if (m + h < p.cap_merge) plan.merge[m + h] = {tok0, n_tok | (hk0 + h) << 8, slot * heads + h, n};
+        step = 1;
+        return slot;
+    }
+    __device__ __forceinline__ bool full(const PackedGeom &p, int slots, int heads) const {
+        return (long)slots * heads > p.cap_slots;
+    }
+};
+
+// Pages: units of tiles; those behind the streams' own are over shared keys.  A slot is a row of the partials.
+struct PagedBatch {
+    PagedPlan plan;
+    int n, n_seq, cap_prefix;
+    long cap_part;
+    template <List LIST>
+    __device__ __forceinline__ Seq sequence(const PackedGeom &, int s) const {
+        const PagedUnits u = plan.units[s];
+        Seq r;
+        r.q0 = u.q0, r.Lq = u.Lq, r.k0 = u.row, r.Lk = u.Lk, r.tiles = u.tiles, r.lo = u.lo;
+        r.parts = u.prefix >= 0, r.seen = s >= n_seq;
+        r.prefix = u.prefix, r.group_q0 = u.group_q0;
+        return r;
+    }
+    __device__ __forceinline__ int partials(const PackedGeom &p, int &slots, int &merges, const Seq &s, int t, int tok0,
+                                            int n_tok, int hk0, int hk1, int n, int &step) const {
+        const int rows = n_tok * p.G, heads = hk1 - hk0;
+        step = rows * heads;
+        const int slot = n > 0 ? atomicAdd(&slots, n * step) : 0;
+        const int m = s.seen ? 0 : atomicAdd(&merges, heads);
+        for (int h = 0; h < heads; h++) {
+            const PagedParts own = {slot + h * rows, n, step, 0};
+            if (s.seen) plan.prefix[(long)(hk0 + h) * cap_prefix + s.prefix + t] = own;
+            else if (m + h < p.cap_merge) plan.merge[m + h] = {tok0, n_tok | (hk0 + h) << 8, s.prefix, s.group_q0, own};
+        }
+        return slot;
+    }
+    __device__ __forceinline__ bool full(const PackedGeom &, int slots, int) const { return slots > cap_part; }
+};
+
+// Key position of a tile's first token; beyond every key where all of them are seen.
+__device__ __forceinline__ int first_pos(const PackedGeom &p, const Seq &s, int t) {
+    return s.seen ? 1 << 29 : t * p.tpt + s.Lk - s.Lq;
 }
 
 // Tiles of the other side that tile t of the sequence meets: [lo, hi).
@@ -97,8 +195,9 @@ __device__ __forceinline__ void range(const PackedGeom &p, const Seq &s, int t, 
         if (lo > hi) lo = hi;
     } else {
         const int last = min((t + 1) * p.tpt, s.Lq) - 1;
-        lo = 0;
-        hi = (packed_limit(last + s.Lk - s.Lq, s.Lk, p.block) + 127) / 128;
+        lo = s.lo;
+        hi = s.seen ? s.Lk / 128 : (packed_limit(last + s.Lk - s.Lq, s.Lk, p.block) + 127) / 128;
+        if (hi < lo) hi = lo;
     }
 }
 
@@ -121,7 +220,8 @@ struct Shared {
 };
 
 // The schedule of n items for every key head (see the head of this file).
-__device__ void deal(const PackedGeom &p, const PackedPlan &plan, Shared &sh, int n) {
+template <class Plan>
+__device__ void deal(const PackedGeom &p, const Plan &plan, Shared &sh, int n) {
     const long units = (long)n * p.Hkv;
     const int t = threadIdx.x, side = t / (THREADS / 2), i = t % (THREADS / 2);  // half the threads rank each side
     if (side == 0 && i < p.sms) sh.load[i] = 0;
@@ -157,16 +257,17 @@ __device__ void deal(const PackedGeom &p, const PackedPlan &plan, Shared &sh, in
     }
 }
 
-template <List LIST>
-__device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, const PackedPlan &plan, Shared &sh) {
+template <List LIST, class B>
+__device__ void build(const PackedGeom &p, const B &b, Shared &sh) {
+    const auto &plan = b.plan;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int most = LIST == KTILES ? (p.Tq + p.tpt - 1) / p.tpt : (p.Tk + 127) / 128;
     int chunk = 1 << 30;
     if (LIST == FWD && p.extra > 0) {
         // key tiles per item: the batch's work over the items aimed at
         unsigned long long w = 0;
-        for (int s = warp; s < p.n_seq; s += WARPS) {
-            const Seq q = sequence<LIST>(p, cu_q, cu_k, s);
+        for (int s = warp; s < b.n; s += WARPS) {
+            const Seq q = b.template sequence<LIST>(p, s);
             for (int t = lane; t < q.tiles; t += 32) {
                 int lo, hi;
                 range<LIST>(p, q, t, lo, hi);
@@ -179,8 +280,8 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         const unsigned long long c = (sh.work + p.extra - 1) / p.extra;
         chunk = c < (1u << 30) ? max(2 * MIN_PIECE, (int)c) : 1 << 30;
     }
-    for (int s = warp; s < p.n_seq; s += WARPS) {
-        const Seq q = sequence<LIST>(p, cu_q, cu_k, s);
+    for (int s = warp; s < b.n; s += WARPS) {
+        const Seq q = b.template sequence<LIST>(p, s);
         for (int t = lane; t < q.tiles; t += 32) {
             int lo, hi;
             range<LIST>(p, q, t, lo, hi);
@@ -210,12 +311,12 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         if (threadIdx.x == 0) sh.bad = 1;
         return;
     }
-    for (int s = warp; s < p.n_seq; s += WARPS) {
-        const Seq q = sequence<LIST>(p, cu_q, cu_k, s);
+    for (int s = warp; s < b.n; s += WARPS) {
+        const Seq q = b.template sequence<LIST>(p, s);
         for (int t = lane; t < q.tiles; t += 32) {
             int lo, hi;
             range<LIST>(p, q, t, lo, hi);
-            if (LIST == KTILES) {
+            if constexpr (LIST == KTILES) {
                 PackedKItem it;
                 it.krow0 = q.k0 + t * 128;
                 it.key0 = t * 128;
@@ -231,18 +332,16 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
             it.tok0 = q.q0 + t * p.tpt;
             it.n_tok_hk = min(p.tpt, q.Lq - t * p.tpt);
             it.krow0 = q.k0, it.Lk = q.Lk;
-            it.pos0 = t * p.tpt + q.Lk - q.Lq;
-            int slot = -1;
-            if (n > 1) {
-                slot = atomicAdd(&sh.slots, n);
-                const int m = atomicAdd(&sh.merges, p.Hkv);
-                for (int hk = 0; hk < p.Hkv; hk++)
-                    if (m + hk < p.cap_merge) plan.merge[m + hk] = {it.tok0, it.n_tok_hk | hk << 8, slot * p.Hkv + hk, n};
-            }
+            it.pos0 = first_pos(p, q, t);
+            int slot = -1, step = 0;
+            const bool parts = n > 1 || (q.parts && hi > lo);
+            if (parts || q.parts)
+                slot = b.partials(p, sh.slots, sh.merges, q, t, it.tok0, it.n_tok_hk, 0, p.Hkv, parts ? n : 0, step);
             for (int c = 0; c < n; c++, i++) {  // pieces of equal length, to within a tile
-                it.kt0 = (int)((long)hi * c / n), it.kt1 = (int)((long)hi * (c + 1) / n);
-                it.slot = n > 1 ? slot + c : -1;
-                (LIST == FWD ? plan.fwd : plan.q)[i] = it;
+                it.kt0 = lo + (int)((long)(hi - lo) * c / n), it.kt1 = lo + (int)((long)(hi - lo) * (c + 1) / n);
+                it.slot = parts ? slot + c * step : -1;
+                if constexpr (LIST == FWD) plan.fwd[i] = it;
+                else plan.q[i] = it;
             }
         }
     }
@@ -252,7 +351,7 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
         if (LIST == FWD) {
             plan.head->n_fwd = sh.total, plan.head->n_merge = sh.merges;
             plan.head->stream = 0, plan.head->slot_step = p.Hkv;
-            if ((long)sh.slots * p.Hkv > p.cap_slots || sh.merges > p.cap_merge) sh.bad = 1;
+            if (b.full(p, sh.slots, p.Hkv) || sh.merges > p.cap_merge) sh.bad = 1;
         } else if (LIST == QTILES) {
             plan.head->n_q = sh.total;
         } else {
@@ -263,19 +362,20 @@ __device__ void build(const PackedGeom &p, const int *cu_q, const int *cu_k, con
 
 // The batch cut into one stretch per SM.  False (the same for all threads): too
 // large, nothing was written.
-__device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int *cu_k, const PackedPlan &plan,
-                                Shared &sh) {
+template <class B>
+__device__ bool build_stretches(const PackedGeom &p, const B &b, Shared &sh) {
+    const auto &plan = b.plan;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (p.n_seq > STREAM_SEQS) return false;
+    if (b.n > STREAM_SEQS) return false;
     // cost and tiles of each sequence, then of those before it
     unsigned long long all = 0;
-    for (int s = warp; s < p.n_seq; s += WARPS) {
-        const Seq q = sequence<FWD>(p, cu_q, cu_k, s);
+    for (int s = warp; s < b.n; s += WARPS) {
+        const Seq q = b.template sequence<FWD>(p, s);
         unsigned long long c = 0;
         for (int t = lane; t < q.tiles; t += 32) {
             int lo, hi;
             range<FWD>(p, q, t, lo, hi);
-            c += max(hi, 1) + ITEM_COST;
+            c += max(hi - lo, 1) + ITEM_COST;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
@@ -296,7 +396,7 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
     }
     {  // exclusive sums over the sequences: one thread each (STREAM_SEQS threads)
         const int s = threadIdx.x;
-        const int c = s < p.n_seq ? sh.cost[s] : 0, n = s < p.n_seq ? sh.tiles[s] : 0;
+        const int c = s < b.n ? sh.cost[s] : 0, n = s < b.n ? sh.tiles[s] : 0;
         for (int pass = 0; pass < 2; pass++) {
             const int mine = pass ? n : c;
             int upto = mine;
@@ -319,14 +419,15 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
     __syncthreads();
     // pass 0: the unit that each stretch begins with; pass 1: the items
     for (int pass = 0; pass < 2; pass++) {
-        for (int s = warp; s < p.n_seq; s += WARPS) {
-            const Seq q = sequence<FWD>(p, cu_q, cu_k, s);
+        for (int s = warp; s < b.n; s += WARPS) {
+            const Seq q = b.template sequence<FWD>(p, s);
             int run = sh.cost[s];
             for (int t0 = 0; t0 < q.tiles; t0 += 32) {
                 const int t = t0 + lane;
                 int lo = 0, work = 0, cost = 0;
                 if (t < q.tiles) {
                     range<FWD>(p, q, t, lo, work);
+                    work -= lo;
                     cost = max(work, 1) + ITEM_COST;
                 }
                 int upto = cost;
@@ -338,8 +439,8 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
                 run += __shfl_sync(0xffffffffu, upto, 31);
                 if (t >= q.tiles) continue;
                 for (int hk = 0; hk < p.Hkv; hk++) {
-                    const int a = hk * head_cost + at, b = a + cost, unit = hk * head_tiles + sh.tiles[s] + t;
-                    const int c0 = (a + Q - 1) / Q, c1 = min(p.sms, (b + Q - 1) / Q);  // borders in [a, b): [c0, c1)
+                    const int a = hk * head_cost + at, z = a + cost, unit = hk * head_tiles + sh.tiles[s] + t;
+                    const int c0 = (a + Q - 1) / Q, c1 = min(p.sms, (z + Q - 1) / Q);  // borders in [a, z): [c0, c1)
                     // tile at which border c cuts the unit, moved to its ends where a piece would be too short (and
                     // to multiples of MIN_PIECE where the borders are closer than that)
                     auto cut = [&](int c) {
@@ -360,13 +461,12 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
                     it.tok0 = q.q0 + t * p.tpt;
                     it.n_tok_hk = min(p.tpt, q.Lq - t * p.tpt) | hk << 8;
                     it.krow0 = q.k0, it.Lk = q.Lk;
-                    it.pos0 = t * p.tpt + q.Lk - q.Lq;
-                    int slot = -1;
-                    if (n > 1) {
-                        slot = atomicAdd(&sh.slots, n);
-                        const int m = atomicAdd(&sh.merges, 1);
-                        if (m < p.cap_merge) plan.merge[m] = {it.tok0, it.n_tok_hk, slot, n};
-                    }
+                    it.pos0 = first_pos(p, q, t);
+                    int slot = -1, step = 0;
+                    const bool parts = n > 1 || (q.parts && work > 0);
+                    if (parts || q.parts)
+                        slot = b.partials(p, sh.slots, sh.merges, q, t, it.tok0, it.n_tok_hk & 255, hk, hk + 1,
+                                          parts ? n : 0, step);
                     int from = 0, piece = 0, owner = min(p.sms - 1, a / Q);
                     for (int c = c0; c <= c1; c++) {
                         const int x = c < c1 ? cut(c) : work;
@@ -377,8 +477,8 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
                         }
                         // the piece [from, x) belongs to `owner`; the border c begins the next one
                         const int k = unit - sh.first[owner];
-                        it.kt0 = from, it.kt1 = x;
-                        it.slot = n > 1 ? slot + piece : -1;
+                        it.kt0 = lo + from, it.kt1 = lo + x;
+                        it.slot = parts ? slot + piece * step : -1;
                         if (k >= 0 && k < p.cap_rows) {
                             plan.fwd[(long)owner * p.cap_rows + k] = it;
                             atomicMax(&sh.items[owner], k + 1);
@@ -396,7 +496,7 @@ __device__ bool build_stretches(const PackedGeom &p, const int *cu_q, const int 
     if (threadIdx.x == 0) {
         plan.head->n_fwd = 0, plan.head->n_merge = sh.merges;
         plan.head->stream = 1, plan.head->slot_step = 1;
-        if (sh.slots > p.cap_slots || sh.merges > p.cap_merge) sh.bad = 1;
+        if (b.full(p, sh.slots, 1) || sh.merges > p.cap_merge) sh.bad = 1;
     }
     return true;
 }
@@ -425,8 +525,9 @@ __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p
         if (bad) atomicCAS(err, DEV_OK, DEV_PLAN);
     }
     if (bad) return;
+    const Batch b{cu_q, cu_k, plan, p.n_seq};
     if (blockIdx.x == 0) {
-        if (!build_stretches(p, cu_q, cu_k, plan, sh)) build<FWD>(p, cu_q, cu_k, plan, sh);
+        if (!build_stretches(p, b, sh)) build<FWD>(p, b, sh);
         // work that found no room in the lists (their sizes are upper bounds, so there is none) makes the plan a bad
         // one: calls report it instead of leaving rows out
         __syncthreads();
@@ -434,11 +535,127 @@ __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p
             plan.head->bad = 1;
             atomicCAS(err, DEV_OK, DEV_PLAN);
         }
-    } else if (blockIdx.x == 1) build<QTILES>(p, cu_q, cu_k, plan, sh);
-    else build<KTILES>(p, cu_q, cu_k, plan, sh);
+    } else if (blockIdx.x == 1) build<QTILES>(p, b, sh);
+    else build<KTILES>(p, b, sh);
+}
+
+// The units of a batch over pages: the streams' own keys, and a group's shared
+// ones where taking its streams together at least halves its query tiles and saves
+// SHARE_LEAST key tiles.
+__device__ void paged_units(const PagedGeom &pg, const PagedPlan &plan, const int *cu_q, const int *k_lens,
+                            const int *cu_groups, const int *shared, int *prefix_tiles) {
+    const PackedGeom &p = pg.g;
+    for (int s = threadIdx.x; s < p.n_seq; s += THREADS) {
+        const int q0 = cu_q[s], Lq = cu_q[s + 1] - q0;
+        plan.units[s] = {q0, Lq, k_lens[s], 0, s, (Lq + p.tpt - 1) / p.tpt, -1, 0};
+    }
+    __syncthreads();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int g = warp; g < pg.n_groups; g += WARPS) {
+        const int s0 = cu_groups[g], s1 = cu_groups[g + 1];
+        int keys = shared[g], first = s1, tiles = 0;
+        for (int s = s0 + lane; s < s1; s += 32) {
+            const PagedUnits u = plan.units[s];
+            if (u.Lq == 0) continue;
+            keys = min(keys, packed_limit(u.Lk - u.Lq, u.Lk, p.block));  // what the stream's first query sees
+            first = min(first, s);
+            tiles += u.tiles;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            keys = min(keys, __shfl_xor_sync(0xffffffffu, keys, o));
+            first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        }
+        const int q0 = cu_q[s0], Lq = cu_q[s1] - q0, together = (Lq + p.tpt - 1) / p.tpt, lo = keys / 128;
+        bool use = lo > 0 && 2 * together <= tiles && (long)(tiles - together) * lo >= SHARE_LEAST;
+        int at = 0;
+        if (use && lane == 0) at = atomicAdd(prefix_tiles, together);
+        at = __shfl_sync(0xffffffffu, at, 0);
+        use = use && at + together <= pg.cap_prefix;
+        if (lane == 0) plan.units[p.n_seq + g] = {q0, Lq, lo * 128, 0, first, use ? together : 0, at, q0};
+        if (!use) continue;
+        for (int s = s0 + lane; s < s1; s += 32) plan.units[s].lo = lo, plan.units[s].prefix = at, plan.units[s].group_q0 = q0;
+    }
+    __syncthreads();
+}
+
+// Block 0: the lists.  The others: where each new token's key lies.
+__global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg, const int *__restrict__ cu_q,
+                                                             const int *__restrict__ k_lens,
+                                                             const int *__restrict__ table,
+                                                             const int *__restrict__ cu_groups,
+                                                             const int *__restrict__ shared, void *base, int *err) {
+    const PackedGeom &p = pg.g;
+    const PagedPlan plan = paged_plan_at(base, pg);
+    if (blockIdx.x > 0) {
+        for (int t = (blockIdx.x - 1) * THREADS + threadIdx.x; t < p.Tq; t += (gridDim.x - 1) * THREADS) {
+            int s = 0, z = p.n_seq;  // the last stream that begins at t or before
+            while (z - s > 1) {
+                const int m = s + (z - s) / 2;
+                if (cu_q[m] <= t) s = m;
+                else z = m;
+            }
+            int slot = -1;
+            const int end = cu_q[s + 1], Lk = k_lens[s];
+            if (cu_q[s] <= t && t < end && Lk <= p.Tk) {
+                const int pos = Lk - (end - t);
+                if (pos >= 0) {
+                    const int page = table[(long)s * pg.max_pages + pos / pg.page];
+                    if ((unsigned)page < (unsigned)pg.n_pages) slot = page * pg.page + pos % pg.page;
+                    else atomicCAS(err, DEV_OK, DEV_PLAN);
+                }
+            }
+            plan.slot[t] = slot;
+        }
+        return;
+    }
+    __shared__ Shared sh;
+    __shared__ int prefix_tiles;
+    if (threadIdx.x < CLASSES) sh.count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        sh.work = 0;
+        sh.slots = sh.merges = prefix_tiles = 0;
+        sh.bad = cu_q[0] < 0 || cu_q[p.n_seq] > p.Tq;
+        if (pg.n_groups > 0 && (cu_groups[0] < 0 || cu_groups[pg.n_groups] > p.n_seq)) sh.bad = 1;
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.n_seq; s += THREADS)
+        if (cu_q[s + 1] < cu_q[s] || k_lens[s] < 0 || k_lens[s] > p.Tk) sh.bad = 1;
+    for (int g = threadIdx.x; g < pg.n_groups; g += THREADS)
+        if (cu_groups[g + 1] < cu_groups[g] || shared[g] < 0) sh.bad = 1;
+    __syncthreads();
+    const bool bad = sh.bad;
+    if (threadIdx.x == 0) {
+        PagedHeader *h = plan.head;
+        h->magic = PAGED_MAGIC;
+        h->n_seq = p.n_seq, h->H = p.H, h->Hkv = p.Hkv, h->block = p.block, h->Tq = p.Tq, h->Tk = p.Tk;
+        h->q_lo = cu_q[0], h->q_hi = cu_q[p.n_seq], h->k_lo = h->k_hi = 0;
+        h->n_q = h->n_k = 0;
+        h->page = pg.page, h->n_pages = pg.n_pages, h->max_pages = pg.max_pages, h->n_groups = pg.n_groups;
+        h->bad = bad;
+        if (bad) atomicCAS(err, DEV_OK, DEV_PLAN);
+    }
+    if (bad) return;
+    paged_units(pg, plan, cu_q, k_lens, cu_groups, shared, &prefix_tiles);
+    const PagedBatch b{plan, p.n_seq + pg.n_groups, p.n_seq, pg.cap_prefix, pg.cap_part};
+    if (!build_stretches(p, b, sh)) build<FWD>(p, b, sh);
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.bad) {
+        plan.head->bad = 1;
+        atomicCAS(err, DEV_OK, DEV_PLAN);
+    }
 }
 
 }  // namespace
+
+cudaError_t launch_paged_plan(const PagedGeom &p, const int *cu_q, const int *k_lens, const int *table,
+                              const int *cu_groups, const int *shared, void *plan, int *err, cudaStream_t st) {
+    const long blocks = ((long)p.g.Tq + THREADS - 1) / THREADS;
+    paged_plan_kernel<<<(unsigned)(1 + (blocks < p.g.sms ? blocks : p.g.sms)), THREADS, 0, st>>>(
+        p, cu_q, k_lens, table, cu_groups, shared, plan, err);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_packed_plan(const PackedGeom &p, const int *cu_q, const int *cu_k, void *plan, int *err,
                                cudaStream_t st) {

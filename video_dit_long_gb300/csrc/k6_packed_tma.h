@@ -1,6 +1,6 @@
 // k6_packed_tma.h -- tensor maps over packed token rows [tokens][heads][128] of
-// 16-bit elements with a stride between tokens: 64-dim panels in 128-byte
-// swizzled rows, zero fill past the last token.
+// 16-bit elements with a stride between tokens, and over pages of such rows:
+// 64-dim panels in 128-byte swizzled rows, zero fill past the last token or page.
 #pragma once
 
 #include <cuda.h>
@@ -12,6 +12,9 @@ namespace k6 {
 // box = 64 dims x box_heads x box_tokens; smem row = token * box_heads + head.
 bool make_rows_map(CUtensorMap *m, const void *base, long tokens, int heads, long stride, int box_heads,
                    int box_tokens, const char **why);
+
+// Pages of one head's keys: box = 64 dims x 1 head x g.box tokens x 1 page.
+bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, const char **why);
 
 // A query tile: the G heads of one key head of g.tpt tokens.
 static inline bool packed_q_map(CUtensorMap *m, const void *q, const PackedGeom &g, long stride, const char **why) {

@@ -1,0 +1,109 @@
+// k6_paged.cuh -- the plan of a batch of streams whose keys lie in pages: what
+// the plan kernel writes and the append and attention kernels read.
+//
+// Stream s has the query tokens [cu_q[s], cu_q[s+1]) and k_lens[s] keys, the new
+// tokens' own among them: query i of Lq sits at key position Lk - Lq + i, and key
+// position p lies at token p % page of page table[s][p / page].  The mask is that
+// of packed sequences (k6_packed.cuh).
+//
+// Streams of a group have their first `shared` tokens in common.  Where it saves
+// work the tokens of the whole group form the rows of tiles over those keys,
+// fetched out of the first stream's pages, up to a multiple of 128 that every
+// query of the group sees; the streams' own tiles then begin there.  Each row has
+// partials of both, joined like those of a split key range:
+//   out = sum_c 2^(lse_c - lse) out_c,   lse = log2 sum_c 2^lse_c.
+#pragma once
+
+#include "k6_packed.cuh"
+
+namespace k6 {
+
+constexpr unsigned PAGED_MAGIC = 0x6b365047u;
+
+struct PagedHeader : PackedHeader {
+    int page, n_pages, max_pages, n_groups;
+};
+static_assert(sizeof(PagedHeader) <= PACKED_HEADER_BYTES, "plan header");
+
+// The rows of one unit of tiles: a stream's own keys, or a group's shared ones.
+struct __align__(16) PagedUnits {
+    int q0, Lq;        // query tokens
+    int Lk;            // keys, from the stream's first one (also where lo > 0)
+    int lo;            // first key tile
+    int row;           // row of the table
+    int tiles;         // query tiles; 0: no work of its own
+    int prefix;        // the group's first tile over shared keys, or -1: none
+    int group_q0;      // first query token of the group
+};
+
+// The partials of a tile: n of them from row `row` on, `step` rows apart.
+struct __align__(16) PagedParts {
+    int row, n, step, unused;
+};
+
+// A tile of one key head whose rows have partials: its own, and (prefix >= 0)
+// those of the group's tiles over shared keys, from tile `prefix` on.
+struct __align__(16) PagedMerge {
+    int tok0, n_tok_hk;
+    int prefix, group_q0;
+    PagedParts own;
+};
+
+struct PagedPlan {
+    PagedHeader *head;
+    int *count;           // [sms], fwd and sched: as in a PackedPlan
+    PagedMerge *merge;    // [cap_merge, or one per SM where that is more]
+    PagedParts *prefix;   // [Hkv][cap_prefix] partials of the tiles over shared keys
+    PagedUnits *units;    // [n_seq + n_groups]
+    PackedItem *fwd;      // krow0 is the row of the table
+    int *sched;
+    int *slot;            // [Tq] where a new token's key lies: page * page tokens + place, or -1: nowhere
+};
+
+// The start of every plan on a GPU of `sms` SMs: see packed_plan_common_bytes.
+static inline __host__ __device__ PagedPlan paged_plan_at(void *base, const PagedGeom &p) {
+    PagedPlan r;
+    char *b = static_cast<char *>(base);
+    r.head = reinterpret_cast<PagedHeader *>(b);
+    b += PACKED_HEADER_BYTES;
+    r.count = reinterpret_cast<int *>(b);
+    b += ((size_t)p.g.sms * sizeof(int) + 15) / 16 * 16;
+    r.merge = reinterpret_cast<PagedMerge *>(b);
+    b += (size_t)packed_merge_rows(p.g) * sizeof(PagedMerge);
+    r.prefix = reinterpret_cast<PagedParts *>(b);
+    b += (size_t)p.cap_prefix * p.g.Hkv * sizeof(PagedParts);
+    r.units = reinterpret_cast<PagedUnits *>(b);
+    b += ((size_t)p.g.n_seq + p.n_groups) * sizeof(PagedUnits);
+    r.fwd = reinterpret_cast<PackedItem *>(b);
+    b += (size_t)p.g.cap_fwd * sizeof(PackedItem);
+    r.sched = reinterpret_cast<int *>(b);
+    b += ((size_t)p.g.cap_sched * sizeof(int) + 15) / 16 * 16;
+    r.slot = reinterpret_cast<int *>(b);
+    return r;
+}
+
+// A tile of 128 keys comes in boxes of g.box tokens of one page each (the box
+// divides both): box i of tile kt of a stream of Lk keys is `tok` tokens into the
+// page of the table's column `column`.  paged_boxes: how many of them hold keys.
+static inline __host__ __device__ int paged_boxes(const PagedGeom &g, int Lk, int kt) {
+    const int left = Lk - kt * 128;
+    return ((left < 128 ? left : 128) + g.box - 1) / g.box;
+}
+static inline __host__ __device__ int paged_box(const PagedGeom &g, int kt, int i, int &column) {
+    const int pos = kt * 128 + i * g.box;
+    column = pos / g.page;
+    return pos - column * g.page;
+}
+// The page to copy from: one that the pool does not have becomes the first behind it, where a copy fills with zeros.
+static inline __host__ __device__ int paged_page(const PagedGeom &g, int page) {
+    return (unsigned)page < (unsigned)g.n_pages ? page : g.n_pages;
+}
+
+// True if the plan was made for this batch and holds valid lists.
+static inline __device__ bool paged_plan_ok(const PagedHeader &h, const PagedGeom &p) {
+    return h.magic == PAGED_MAGIC && !h.bad && h.n_seq == p.g.n_seq && h.H == p.g.H && h.Hkv == p.g.Hkv &&
+           h.block == p.g.block && h.Tq == p.g.Tq && h.page == p.page && h.n_pages == p.n_pages &&
+           h.max_pages == p.max_pages && h.n_groups == p.n_groups;
+}
+
+}  // namespace k6

@@ -29,7 +29,8 @@ SYMBOLS = ["k6attn_create", "k6attn_destroy", "k6attn_rope_tables", "k6attn_rope
            "k6attn_packed_norm_rope", "k6attn_packed_norm_rope_backward",
            "k6attn_packed_norm_rope_backward_workspace_bytes", "k6attn_packed_plan_bytes", "k6attn_packed_plan",
            "k6attn_packed_workspace_bytes", "k6attn_packed_forward", "k6attn_packed_backward_workspace_bytes",
-           "k6attn_packed_backward"]
+           "k6attn_packed_backward", "k6attn_paged_plan_bytes", "k6attn_paged_plan", "k6attn_paged_append",
+           "k6attn_paged_workspace_bytes", "k6attn_paged_forward"]
 
 
 class K6Error(RuntimeError):
@@ -57,6 +58,27 @@ class PackedPlan:
         self.batch, self.buffer = batch, buffer
         self.ref, self.ptr = ctypes.byref(batch), buffer.data_ptr()
         self.q_tokens, self.k_tokens, self.kv_heads = batch.q_tokens, batch.k_tokens, batch.kv_heads
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("kv_heads", ctypes.c_int), ("mask_block", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_groups", ctypes.c_int),
+                ("n_pages", ctypes.c_long), ("q_tokens", ctypes.c_long)]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_long), ("token_stride", ctypes.c_long),
+                ("head_stride", ctypes.c_long)]
+
+
+class PagedPlan:
+    """A step over pages and its work list on the device, with the table of pages it was made from (Handle.paged_plan)."""
+
+    def __init__(self, batch, buffer, table):
+        self.batch, self.buffer, self.table = batch, buffer, table
+        self.ref, self.ptr = ctypes.byref(batch), buffer.data_ptr()
+        self.q_tokens, self.kv_heads = batch.q_tokens, batch.kv_heads
+        self.pages = (batch.n_pages, batch.page_tokens, batch.kv_heads, 128)
 
 
 _lib = None
@@ -122,6 +144,13 @@ def load(build_if_missing: bool = True):
         getattr(L, "k6attn_packed_" + name).argtypes = [P, B]
     for name in ("plan_bytes", "workspace_bytes", "backward_workspace_bytes", "norm_rope_backward_workspace_bytes"):
         getattr(L, "k6attn_packed_" + name).restype = Z
+    B, C = ctypes.POINTER(PagedBatch), ctypes.POINTER(Pages)
+    L.k6attn_paged_plan.argtypes = [P, B, P, P, P, P, P, P, Z, P]
+    L.k6attn_paged_append.argtypes = [P, B, P, P, W, P, W, P, W, P, P, P, F, P, W, C, C, I, P]
+    L.k6attn_paged_forward.argtypes = [P, B, P, P, P, W, C, C, I, P, W, P, P, Z, P]
+    for name in ("plan_bytes", "workspace_bytes"):
+        getattr(L, "k6attn_paged_" + name).argtypes = [P, B]
+        getattr(L, "k6attn_paged_" + name).restype = Z
     L.k6attn_sync.argtypes = [P, P]
     L.k6attn_set_option.argtypes = [P, I, ctypes.c_longlong]
     L.k6attn_status_string.argtypes = [I]
@@ -134,7 +163,7 @@ def load(build_if_missing: bool = True):
                  "k6attn_rope_split_heads", "k6attn_lse_merge_heads", "k6attn_attention_chunk_groups_bounded",
                  "k6attn_seq2head_relayout", "k6attn_sync", "k6attn_set_option", "k6attn_packed_norm_rope",
                  "k6attn_packed_norm_rope_backward", "k6attn_packed_plan", "k6attn_packed_forward",
-                 "k6attn_packed_backward"):
+                 "k6attn_packed_backward", "k6attn_paged_plan", "k6attn_paged_append", "k6attn_paged_forward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -204,6 +233,17 @@ def _vec(t, shape, dtype, device, what):
         raise ValueError(f"{what}: want a dense {dtype} tensor of shape {shape} on cuda:{device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _pages(t, shape, dtype, device, what):
+    """A pool of pages [n_pages][page_tokens][kv_heads][d] on `device` whose head rows are dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what}: want a {dtype} tensor of shape {shape} on cuda:{device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    a, b, c, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{what}: the head dim must be dense (strides {(a, b, c, d)})")
+    return Pages(t.data_ptr(), a, b, c)
 
 
 def _cu(offsets, device):
@@ -510,6 +550,84 @@ class Handle:
         s = self._lib.k6attn_packed_backward(
             self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _code(q), po, lo, pg, lg,
             _vec(lse, (H, plan.q_tokens), _DTYPES[F32], dev, "lse"), pdq, ldq, pdk, ldk, pdv, ldv, ws, nws, st)
+        if s:
+            _check(s)
+
+    def paged_plan(self, cu_q, k_lens, table, q_tokens, kv_heads, page_tokens, n_pages, mask_block=0, *, cu_groups=None,
+                   shared=None, stream=None) -> PagedPlan:
+        """Plan a step of streams whose keys lie in pages: offsets cu_q [n + 1] into q_tokens rows, k_lens [n] keys of
+        each stream with the new ones, table [n][max_pages] of its pages (int32, on the device; the table is kept
+        and has to stay as it is while the plan is in use).  The pools have n_pages pages of page_tokens tokens.
+        Streams [cu_groups[g], cu_groups[g + 1]) have their first shared[g] tokens in common.  mask_block as in
+        packed_plan."""
+        torch = _torch_types()
+        if table.dim() != 2:
+            raise ValueError(f"table: want [streams][pages], got {tuple(table.shape)}")
+        if (cu_groups is None) != (shared is None):
+            raise ValueError("cu_groups, shared: give both, or neither")
+        n_groups = 0 if shared is None else shared.numel()
+        b = PagedBatch(int(cu_q.numel()) - 1, int(kv_heads), int(mask_block), int(page_tokens), int(table.size(1)),
+                       int(n_groups), int(n_pages), int(q_tokens))
+        L = load()
+        n = L.k6attn_paged_plan_bytes(self.h, ctypes.byref(b))
+        if not n:  # the call that makes a plan refuses the batch with its own status
+            _check(L.k6attn_paged_plan(self.h, ctypes.byref(b), None, None, None, None, None, None, 0, None))
+        with torch.cuda.stream(_torch_stream(stream, self._dev)):  # memory of the stream that writes it first
+            plan = PagedPlan(b, torch.empty(n, dtype=torch.uint8, device=cu_q.device), table)
+        self.paged_replan(plan, cu_q, k_lens, table, cu_groups=cu_groups, shared=shared, stream=stream)
+        return plan
+
+    def paged_replan(self, plan, cu_q, k_lens, table, *, cu_groups=None, shared=None, stream=None):
+        """Make the plan anew for the next step of a batch of the same size (in place: captured calls that were given
+        the same table see it)."""
+        dev, st = self._packed(stream)
+        b, i32 = plan.batch, _DTYPES["int32"]
+        if b.n_groups > 0 and (cu_groups is None or shared is None):
+            raise ValueError("cu_groups, shared: the plan is of a batch with groups")
+        s = load().k6attn_paged_plan(
+            self.h, plan.ref, _vec(cu_q, (b.n_seq + 1,), i32, dev, "cu_q"), _vec(k_lens, (b.n_seq,), i32, dev, "k_lens"),
+            _vec(table, (b.n_seq, b.max_pages), i32, dev, "table"),
+            _vec(cu_groups, (b.n_groups + 1,), i32, dev, "cu_groups"), _vec(shared, (b.n_groups,), i32, dev, "shared"),
+            plan.ptr, plan.buffer.numel(), st)
+        _check(s)
+        plan.table = table
+
+    def paged_append(self, plan, q, k, v, positions, q_weight=None, k_weight=None, eps=1e-6, *, q_out, k_cache, v_cache,
+                     stream=None):
+        """QK-norm (with weights) and rotation of a step's new tokens q [T][H][d], k [T][kv_heads][d] (bf16), the
+        queries into q_out, the keys and the values v into their places in k_cache (both fp16 or both bf16) and
+        v_cache (bf16), [n_pages][page_tokens][kv_heads][d].  q and q_out may be None."""
+        dev, st = self._packed(stream)
+        d, T, kv, f32, bf = self._d, plan.q_tokens, plan.kv_heads, _DTYPES[F32], _DTYPES[BF16]
+        sq, sk, o = (T, self._H, d), (T, kv, d), k_cache.dtype
+        pq, lq = (None, 0) if q is None else _rows(q, sq, bf, dev, "q")
+        pk, lk = _rows(k, sk, bf, dev, "k")
+        pv, lv = _rows(v, sk, bf, dev, "v")
+        po, lo = (None, 0) if q_out is None else _rows(q_out, sq, o, dev, "q_out")
+        s = self._lib.k6attn_paged_append(
+            self.h, plan.ref, plan.ptr, pq, lq, pk, lk, pv, lv, _vec(positions, (T, 3), _DTYPES["int32"], dev, "positions"),
+            _vec(q_weight, (d,), f32, dev, "q_weight"), _vec(k_weight, (d,), f32, dev, "k_weight"), eps, po, lo,
+            _pages(k_cache, plan.pages, o, dev, "k_cache"), _pages(v_cache, plan.pages, bf, dev, "v_cache"),
+            _code(k_cache), st)
+        if s:
+            _check(s)
+
+    def paged_workspace_bytes(self, plan) -> int:
+        return load().k6attn_paged_workspace_bytes(self.h, plan.ref)
+
+    def paged_forward(self, plan, q, k_cache, v_cache, out, lse=None, *, workspace=None, stream=None):
+        """Attention of a planned step: q [Tq][H][d] (bf16 or fp16, as k_cache) over the streams' pages, into out
+        (bf16, as q) and lse (fp32 [H][Tq])."""
+        dev, st = self._packed(stream)
+        H, d, bf = self._H, self._d, _DTYPES[BF16]
+        sq, x = (plan.q_tokens, H, d), q.dtype
+        pq, lq = _rows(q, sq, x, dev, "q")
+        po, lo = _rows(out, sq, bf, dev, "out")
+        ws, nws = _room(workspace, dev)
+        s = self._lib.k6attn_paged_forward(
+            self.h, plan.ref, plan.ptr, plan.table.data_ptr(), pq, lq, _pages(k_cache, plan.pages, x, dev, "k_cache"),
+            _pages(v_cache, plan.pages, bf, dev, "v_cache"), _code(q), po, lo,
+            _vec(lse, (H, plan.q_tokens), _DTYPES[F32], dev, "lse"), ws, nws, st)
         if s:
             _check(s)
 
