@@ -15,7 +15,7 @@ SOURCE = r"""
 #include "k6_paged.cuh"
 #include "k6_packed_api.cu"
 // "geom": H kv n_seq q_tokens page max_pages n_groups sms;  "tile": page n_pages Lk kt page_named;
-// "pools": Hkv page n_pages, three strides, three strides, distance (elements)
+// "div": page x;  "pools": Hkv page n_pages, three strides, three strides, distance (elements)
 int main() {
     char what[16];
     while (scanf("%15s", what) == 1) {
@@ -33,15 +33,22 @@ int main() {
             printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu %d %d %d %ld %d %d %zu %zu %zu %zu %zu\n", k6::paged_plan_bytes(p),
                    k6::packed_plan_common_bytes(sms), (size_t)at.count, (size_t)at.merge, (size_t)at.prefix, (size_t)at.units,
                    (size_t)at.fwd, (size_t)at.sched, (size_t)at.slot, p.g.cap_q, p.g.cap_merge, p.cap_prefix, p.cap_part,
-                   p.g.cap_slots, p.box, k6attn_paged_plan_bytes(&h, &b), k6attn_paged_workspace_bytes(&h, &b),
+                   p.g.cap_slots, 1 << p.box_log2, k6attn_paged_plan_bytes(&h, &b), k6attn_paged_workspace_bytes(&h, &b),
                    k6::paged_fwd_workspace(p), sizeof(k6::PagedMerge), sizeof(k6::PagedUnits));
+        } else if (what[0] == 'd') {
+            k6::PagedGeom p = {};
+            unsigned x;
+            if (scanf("%d %u", &p.page, &x) != 2) return 1;
+            k6::paged_set_page(p, p.page);
+            printf("%llu %u\n", (unsigned long long)x * p.page_mul >> p.page_shift, p.page_shift);
         } else if (what[0] == 't') {
             k6::PagedGeom p = {};
             int Lk, kt, named;
             if (scanf("%d %d %d %d %d", &p.page, &p.n_pages, &Lk, &kt, &named) != 5) return 1;
-            for (p.box = 128; p.page % p.box; p.box /= 2) {}
-            const int n = k6::paged_boxes(p, Lk, kt);
-            printf("%d %d %d", p.box, n, k6::paged_page(p, named));
+            k6::paged_set_page(p, p.page);
+            const int n = k6::paged_boxes(p, Lk, kt), span = p.page / 8 + 3;
+            printf("%d %d %d %d %d %d", 1 << p.box_log2, n, k6::paged_page(p, named), k6::paged_group(p, span, named, 16 % p.page), span,
+                   k6::paged_groups(p, span));
             for (int i = 0; i < n; i++) {
                 int column;
                 const int tok = k6::paged_box(p, kt, i, column);
@@ -96,18 +103,22 @@ def test_plan_layout_and_room(run):
         (total, common, count, merge, prefix, units, fwd, sched, slot, cap_q, cap_merge, cap_prefix, cap_part, cap_slots, box,
          asked, ws_asked, ws, merge_size, units_size) = r
         G, rows = H // kv, 128 // (H // kv) * (H // kv)
-        assert [count, merge] == [256, 256 + (sms * 4 + 15) // 16 * 16]
+        assert count == 256
         assert 0 < merge < prefix <= units <= fwd <= sched <= slot and total == slot + 4 * q
         assert all(x % 16 == 0 for x in (merge, prefix, units, fwd, sched, slot))
         # what the join reads of a plan before the header has shown whose it is: its first `sms` entries
+        assert merge == count + (sms * 4 + 15) // 16 * 16 + sms * 32
         assert prefix - merge >= sms * merge_size and units - prefix == cap_prefix * kv * 16
         assert fwd - units == (n + groups) * units_size
         assert asked == total and ws_asked == ws and (ws >= cap_part * 516 if cap_part else ws == 0)
         assert page % box == 0 and 128 % box == 0 and box >= 16
         # units of a batch whose groups all are taken together: at most two tiles of each stream, one over its prefix
         assert cap_q >= q // (128 // G) + n + cap_prefix and cap_prefix == (n if groups else 0)
+        # joins of 16 rows: of tiles that are cut, and of the rows of every stream that a group may share
+        assert cap_merge >= cap_slots // 2 * -(-rows // 16)
         if groups:
-            assert cap_merge >= cap_slots // 2 + min(2 * n, q // (128 // G) + n) * kv
+            tiles = min(2 * n, q // (128 // G) + n)
+            assert cap_merge >= cap_slots // 2 * -(-rows // 16) + kv * (min(tiles * rows, q * G) // 16 + tiles)
             assert cap_part >= cap_slots * rows + min(2 * n * kv * rows, q * H) + min(n * kv * rows, q * H)
 
 
@@ -134,8 +145,13 @@ def test_boxes_of_a_tile(run):
         Lk = rng.randint(1, 3000)
         cases.append((page, rng.randint(0, 50), Lk, rng.randint(0, (Lk + 127) // 128 - 1),
                       rng.choice([0, 3, 49, 50, 51, -1, -2 ** 31, 2 ** 31 - 1])))
-    for (page, n_pages, Lk, kt, named), (box, n, got, *at) in zip(cases, run(["tile " + " ".join(map(str, c)) for c in cases])):
+        if cases[-1][1] == 0:
+            cases[-1] = (page, 1, *cases[-1][2:])
+    for (page, n_pages, Lk, kt, named), (box, n, got, group, span, groups, *at) in zip(cases, run(["tile " + " ".join(map(str, c)) for c in cases])):
         assert got == (named if 0 <= named < n_pages else n_pages)
+        # the group that a copy begins at: inside the page's own; of a page that is none, behind the last group
+        assert groups == (n_pages - 1) * span + page // 8
+        assert group == (named * span + 16 % page // 8 if 0 <= named < n_pages else groups)
         rows = []
         for column, tok in zip(at[::2], at[1::2]):
             assert 0 <= tok and tok + box <= page and column <= (Lk - 1) // page
@@ -143,6 +159,17 @@ def test_boxes_of_a_tile(run):
         assert len(at) == 2 * n and len(rows) <= 128
         assert rows == list(range(kt * 128, kt * 128 + len(rows)))  # in order, from the tile's first key
         assert len(rows) == 128 or len(rows) >= Lk - kt * 128       # all keys; none skipped but those behind the last
+
+
+def test_division_by_the_page(run):
+    rng = random.Random(3)
+    cases = []
+    for _ in range(3000):
+        page = 16 * rng.choice([1, 2, 3, 7, rng.randint(1, 1 << 20), (1 << 20) - 1])
+        q = rng.randint(0, (2 ** 29 - 1) // page)
+        cases.append((page, max(0, min(2 ** 29 - 1, rng.choice([q * page, q * page - 1, q * page + page - 1, 2 ** 29 - 1])))))
+    for (page, x), (q, shift) in zip(cases, run([f"div {page} {x}" for page, x in cases])):
+        assert q == x // page and shift < 64
 
 
 def test_pools_that_interleave_and_pools_that_overlap(run):
@@ -164,7 +191,9 @@ def test_pools_that_interleave_and_pools_that_overlap(run):
         cases.append("pools " + " ".join(map(str, (*n, *(128 * s for s in stride[::-1]), *(128 * s for s in other[::-1]),
                                                    128 * d))))
     seen = {True: 0, False: 0}
-    for c, (a, b, size), (sx, sy, shared) in zip(cases, want, run(cases)):
+    made = run(cases)
+    assert sum(r[0] == 0 for r in made) > 1000
+    for c, (a, b, size), (sx, sy, shared) in zip(cases, want, made):
         assert (sx == 0) <= (len(a) == size) and (sy == 0) <= (len(b) == size), c
         assert sx == 0, c  # strides made without overlap
         if sy == 0:

@@ -17,6 +17,7 @@
 
 #include "k6_internal.h"
 #include "k6_packed_tma.h"
+#include "k6_paged.cuh"
 
 namespace k6 {
 
@@ -107,17 +108,22 @@ bool make_rows_map(CUtensorMap *m, const void *base, long tokens, int heads, lon
     return true;
 }
 
-bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, const char **why) {
+bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, bool grouped, const char **why) {
     const DriverFns &f = driver();
     if (!f.encode) {
         if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
         return false;
     }
-    cuuint64_t dims[4] = {128, (cuuint64_t)g.g.Hkv, (cuuint64_t)g.page, (cuuint64_t)g.n_pages};
-    cuuint64_t strides[3] = {(cuuint64_t)c.head * 2, (cuuint64_t)c.token * 2, (cuuint64_t)c.page * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)g.box, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    if (f.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t heads = (cuuint64_t)g.g.Hkv, head = (cuuint64_t)c.head * 2, token = (cuuint64_t)c.token * 2;
+    const cuuint64_t dims4[4] = {128, heads, (cuuint64_t)g.page, (cuuint64_t)g.n_pages};
+    const cuuint64_t strides4[3] = {head, token, (cuuint64_t)c.page * 2};
+    const cuuint32_t box4[4] = {64, 1, 1u << g.box_log2, 1};
+    const cuuint64_t dims5[5] = {64, 8, 2, (cuuint64_t)paged_groups(g, c.span), heads};
+    const cuuint64_t strides5[4] = {token, 128, token * 8, head};
+    const cuuint32_t box5[5] = {64, 8, 2, (1u << g.box_log2) / 8, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (f.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, grouped ? 5 : 4, c.p, grouped ? dims5 : dims4,
+                 grouped ? strides5 : strides4, grouped ? box5 : box4, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
         if (why) *why = "cuTensorMapEncodeTiled rejected a cache";

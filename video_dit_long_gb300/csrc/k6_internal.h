@@ -243,7 +243,9 @@ cudaError_t launch_packed_fwd(const PackedGeom &p, const PackedPtrs &t, void *ou
 // Tk is the most keys that one stream can have.
 struct PagedGeom {
     PackedGeom g;
-    int page, box;                    // tokens of a page; and of one copy out of it (divides the page and 128)
+    int page;                         // tokens of a page
+    int box_log2;                     // of the tokens of one copy out of it, which divide the page and 128
+    unsigned page_mul, page_shift;    // x / page = x page_mul >> page_shift for x < 2^29
     int n_pages, max_pages;           // pages of the pool; columns of the table
     int n_groups;
     int cap_prefix;                   // query tiles over shared prefixes, per key head
@@ -251,10 +253,12 @@ struct PagedGeom {
 };
 PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms);
 
-// Pages of keys or values: strides in elements.
+// Pages of keys or values: strides in elements; span: groups of 8 tokens from one page to the next, or 0 where the
+// strides make that no whole number.
 struct PagedCache {
     void *p;
     long page, token, head;
+    int span;
 };
 
 size_t paged_plan_bytes(const PagedGeom &p);

@@ -148,7 +148,7 @@ k6attn_status check_pool(const char *fn, const char *name, const k6attn_pages *p
     r->name = name;
     r->extent = 0;
     if (!pages || (!pages->data && g.n_pages > 0)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: null %s", fn, name);
-    r->c = {pages->data, pages->page_stride, pages->token_stride, pages->head_stride};
+    r->c = {pages->data, pages->page_stride, pages->token_stride, pages->head_stride, 0};
     if (g.n_pages == 0) return K6ATTN_OK;
     if (!aligned16(pages->data)) return set_error(K6ATTN_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
     const long count[3] = {g.g.Hkv, g.page, g.n_pages};
@@ -174,6 +174,9 @@ k6attn_status check_pool(const char *fn, const char *name, const k6attn_pages *p
                              fn, name, s);
         r->extent += (n - 1) * s;
     }
+    const bool whole = g.n_pages == 1 || r->c.page % (8 * r->c.token) == 0;
+    const long span = g.n_pages == 1 ? g.page / 8 : whole ? r->c.page / (8 * r->c.token) : 0;
+    r->c.span = span * g.n_pages < (1L << 31) ? (int)span : 0;
     return K6ATTN_OK;
 }
 

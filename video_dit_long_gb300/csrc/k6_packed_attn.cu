@@ -89,6 +89,14 @@ constexpr float RESCALE_THRESHOLD = 8.0f;     // log2 units: O is rescaled when 
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 }  // namespace pf
 
+// How tiles of keys lie in shared memory: bytes from one 64-dim panel to the other, from 8 keys to the next 8.  ROWS: a
+// copy brings one panel of rows.  GROUPS: a copy brings both panels of a box, 8 keys at a time.
+enum Copies { ROWS, GROUPS };
+template <Copies HOW>
+struct KeyTile {
+    static constexpr int PANEL = HOW == GROUPS ? 1024 : pf::PANEL, KEYS8 = HOW == GROUPS ? 2048 : 1024;
+};
+
 struct PackedFwdParams {
     PackedGeom g;
     const void *plan;
@@ -107,6 +115,7 @@ struct PackedFwdParams {
 struct PagedFwdParams : PackedFwdParams {
     PagedGeom pg;
     const int *table;                         // [n_seq][max_pages]
+    int span[2];                              // of the pools of keys and of values (PagedCache)
 };
 
 namespace {
@@ -158,13 +167,13 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
                  : "memory");
 }
 
-// The plan of a call, and whether it is the batch's.
 __device__ __forceinline__ PackedPlan plan_of(const PackedFwdParams &p) {
     return packed_plan_at(const_cast<void *>(p.plan), p.g);
 }
 __device__ __forceinline__ PagedPlan plan_of(const PagedFwdParams &p) {
     return paged_plan_at(const_cast<void *>(p.plan), p.pg);
 }
+// Whether the plan is the batch's.
 __device__ __forceinline__ bool plan_ok_for(const PackedPlan &plan, const PackedFwdParams &p) {
     return packed_plan_ok(*plan.head, p.g);
 }
@@ -172,9 +181,29 @@ __device__ __forceinline__ bool plan_ok_for(const PagedPlan &plan, const PagedFw
     return paged_plan_ok(*plan.head, p.pg);
 }
 
-// The copies that bring tile `kt` of 128 keys of an item and head hk to dst.  The whole warp; returns with the barrier
-// told of all of their bytes.
-__device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedItem &it, int kt, int hk, const void *tm,
+// The first item, for the producers, which everything else waits for.  Over pages the plan keeps it beside the header.
+__device__ __forceinline__ bool first_item(const PackedPlan &, const Walk &walk, PackedItem &it, int &hk) {
+    return walk.rounds > 0 && walk.at(0, it, hk);
+}
+__device__ __forceinline__ bool first_item(const PagedPlan &plan, const Walk &walk, PackedItem &it, int &hk) {
+    it = plan.first[blockIdx.x];
+    hk = it.n_tok_hk >> 8;
+    return walk.rounds > 0;
+}
+
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2, int c3,
+                                            int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The copies that bring tile `kt` of 128 keys of an item and head hk to dst, keys (which = 0) or values.  The whole warp;
+// returns with the barrier told of all of their bytes.
+template <Copies HOW>
+__device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedItem &it, int kt, int hk, int, const void *tm,
                                           uint8_t *dst, uint64_t *bar, bool leader) {
     using namespace pf;
     if (leader) {
@@ -184,34 +213,38 @@ __device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedI
         tma_load_4d(dst + PANEL, tm, bar, 64, hk, row, 0);
     }
 }
-
-// Keys in pages.  Lane l brings box l of the tile, both panels; boxes wholly behind the stream's last key are left out
-// (their rows of S are masked, those of V zeroed, and no page is theirs).
-__device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedItem &it, int kt, int hk, const void *tm,
-                                          uint8_t *dst, uint64_t *bar, bool leader) {
-    using namespace pf;
-    const int box = p.pg.box, lane = threadIdx.x & 31, n = paged_boxes(p.pg, it.Lk, kt);
+// Keys in pages.  Lane l brings box l of the tile; boxes wholly behind the stream's last key are left out (their rows of S
+// are masked, those of V zeroed, and no page is theirs).  The tile's arithmetic divides by shifts and a product: with the
+// compiler's divisions in this loop the whole kernel ran 3 to 25 % slower, the more the smaller the boxes.
+template <Copies HOW>
+__device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedItem &it, int kt, int hk, int which,
+                                          const void *tm, uint8_t *dst, uint64_t *bar, bool leader) {
+    const int lane = threadIdx.x & 31, n = paged_boxes(p.pg, it.Lk, kt);
     int column, page = 0;
     const int tok = paged_box(p.pg, kt, lane, column);
     if (lane < n) {
-        const int named = p.table[(long)it.krow0 * p.pg.max_pages + column];
-        page = paged_page(p.pg, named);
-        if (page != named) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+        page = p.table[(long)it.krow0 * p.pg.max_pages + column];
+        if (paged_page(p.pg, page) != page) atomicCAS(p.err, DEV_OK, DEV_PLAN);
     }
-    if (leader) mbar_arrive_expect_tx(bar, (uint32_t)(n * box) * 256u);
+    if (leader) mbar_arrive_expect_tx(bar, (uint32_t)n << (p.pg.box_log2 + 8));
     __syncwarp();
     if (lane < n) {
-        tma_load_4d(dst + lane * box * 128, tm, bar, 0, hk, tok, page);
-        tma_load_4d(dst + PANEL + lane * box * 128, tm, bar, 64, hk, tok, page);
+        if constexpr (HOW == GROUPS) {
+            tma_load_5d(dst + (lane << (p.pg.box_log2 + 8)), tm, bar, 0, 0, 0, paged_group(p.pg, p.span[which], page, tok), hk);
+        } else {
+            tma_load_4d(dst + (lane << (p.pg.box_log2 + 7)), tm, bar, 0, hk, tok, paged_page(p.pg, page));
+            tma_load_4d(dst + pf::PANEL + (lane << (p.pg.box_log2 + 7)), tm, bar, 64, hk, tok, paged_page(p.pg, page));
+        }
     }
 }
 
-template <class Params>
+template <class Params, Copies HOW>
 __global__ void __launch_bounds__(pf::THREADS, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
     using namespace pf;
     constexpr bool PAGED = std::is_same<Params, PagedFwdParams>::value;
+    using Tile = KeyTile<HOW>;
     extern __shared__ __align__(1024) uint8_t smem[];
     launch_next_kernel();
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
@@ -297,16 +330,16 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             uint32_t n = 0;       // tiles loaded
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
-            for (uint32_t k = 0; k < walk.rounds && ok; k++) {
-                PackedItem it;
-                int hk;
-                if (!walk.at(k, it, hk)) continue;
-                const int T = it.kt1 - it.kt0;
-                if (T <= 0) continue;
+            PackedItem it;
+            int hk;
+            bool have = first_item(plan, walk, it, hk);
+            for (uint32_t k = 0; k < walk.rounds && ok; k++, have = k < walk.rounds && walk.at(k, it, hk)) {
+                const int T = have ? it.kt1 - it.kt0 : 0;
                 for (int j = 0; j < T && ok; j++, n++) {
                     const uint32_t slot = n % NSLOT;
                     if (!(ok = mbar_wait_w(&empty[slot], ((n / NSLOT) & 1) ^ 1, w))) break;
-                    load_tile(p, it, it.kt0 + j, hk, tm, ring + slot * TILE, &full[slot], leader);
+                    load_tile<HOW>(p, it, it.kt0 + j, hk, warp == 8 ? 0 : 1, tm, ring + slot * TILE, &full[slot],
+                                   leader);
                     if (j == 0 && warp == 8) {  // Q once the last S of the item before has read its tile
                         if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) {
                             n++;  // this tile's load was issued
@@ -329,8 +362,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             // ------------------------------------------------- MMA issuers
             const uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
             const uint64_t dq0 = smem_desc_sw128(smem_u32(smem + SMEM_Q), 16, 1024);     // Q / K: K-major
-            const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + SMEM_KV), 16, 1024);
-            const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + SMEM_V), PANEL, 1024);  // V: MN-major
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + SMEM_KV), 16, Tile::KEYS8);
+            const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + SMEM_V), Tile::PANEL, Tile::KEYS8);  // V: MN-major
             uint32_t tile = 0;    // key tiles of earlier items
             uint32_t uc = 0;
             bool ok = true;
@@ -352,7 +385,8 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; kk++) {
                             const uint64_t off = (uint64_t)((kk >> 2) * PANEL + (kk & 3) * 32) >> 4;
-                            mma_ss_w(tmem + (n % NBUF) * BN, dq0 + off, kb + off, p.idesc_qk, kk > 0);
+                            const uint64_t koff = (uint64_t)((kk >> 2) * Tile::PANEL + (kk & 3) * 32) >> 4;
+                            mma_ss_w(tmem + (n % NBUF) * BN, dq0 + off, kb + koff, p.idesc_qk, kk > 0);
                         }
                         tc_commit_w(&s_full[n % NBUF]);  // K(n)'s slot is freed by the softmax, which sees S(n)
                     }
@@ -365,8 +399,9 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                         if (valid < BN) {  // rows behind the sequence's last key: zero (P is)
                             uint8_t *v = smem + SMEM_V + slot * TILE;
                             for (int c = valid * 8 + lane; c < BN * 8; c += 32) {
-                                *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4 *>(v + PANEL + c * 16) = make_uint4(0, 0, 0, 0);
+                                uint8_t *at = v + (c >> 6) * Tile::KEYS8 + (c & 63) * 16;
+                                *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(at + Tile::PANEL) = make_uint4(0, 0, 0, 0);
                             }
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
@@ -380,7 +415,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                             tc_fence_after();
 #pragma unroll
                             for (int kk = q * (KP / 16); kk < (q + 1) * (KP / 16); kk++)
-                                mma_ts_w(tmem + O_COL, pb + kk * 8, vb + ((uint64_t)(kk * 16 * 128) >> 4), idesc_pv,
+                                mma_ts_w(tmem + O_COL, pb + kk * 8, vb + ((uint64_t)(kk * 2 * Tile::KEYS8) >> 4), idesc_pv,
                                          (j > 0 || kk > 0) ? 1u : 0u);
                         }
                         if (!ok) break;
@@ -729,55 +764,78 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
     store_joined(p, top, sum, acc, (long)m.tok0 + r / p.g.G, (m.n_tok_hk >> 8) * p.g.G + r % p.g.G, lane);
 }
 
-// Joins the partials of every row that has some over pages: half a warp per row,
-// as packed_merge_kernel, first those over the keys that its group shares, then its
-// own, each in key order.
-__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedFwdParams p) {
+constexpr int MERGE_BLOCKS_PER_SM = 4;
+
+// Joins the partials of every row that has some over pages: a block an entry of the
+// plan's list, first the partials over the keys that a row's group shares, then its
+// own, each in key order.  Half a warp takes a row, 8 values a lane; with fewer rows
+// than half warps (a new token has its key head's G) several share one, each taking
+// every so many-th partial, and are joined in order through shared memory.
+__global__ void __launch_bounds__(16 * MERGE_ROWS) paged_merge_kernel(const PagedFwdParams p) {
+    __shared__ float part[MERGE_ROWS][10][16];
     launch_next_kernel();
     wait_previous_kernel();
     const PagedPlan plan = plan_of(p);
-    const int lane = threadIdx.x & 15;
-    const uint32_t x = (blockIdx.x * blockDim.x + threadIdx.x) >> 4;
-    const uint32_t mi = x / (uint32_t)p.g.rows;
-    const int r = (int)(x - mi * (uint32_t)p.g.rows);
-    if (mi >= (uint32_t)p.g.cap_merge) return;
-    const bool early = mi < (uint32_t)p.g.sms;  // as in packed_merge_kernel
+    const int lane = threadIdx.x & 15, half = threadIdx.x >> 4;
+    const bool early = blockIdx.x < (unsigned)p.g.sms;  // as in packed_merge_kernel
     PagedMerge m;
-    if (early) m = plan.merge[mi];
+    if (early) m = plan.merge[blockIdx.x];
     const PagedHeader head = *plan.head;
-    if (!paged_plan_ok(head, p.pg) || mi >= (uint32_t)head.n_merge) return;
-    if (!early) m = plan.merge[mi];
-    const int rtok = r / p.g.G, rhead = r - rtok * p.g.G, hk = m.n_tok_hk >> 8;
-    if (rtok >= (m.n_tok_hk & 255)) return;
-    PagedParts pre = {0, 0, 0, 0};
-    if (m.prefix >= 0) {
-        const int i = m.tok0 + rtok - m.group_q0, tile = i / p.g.tpt;
-        pre = plan.prefix[(long)hk * p.pg.cap_prefix + m.prefix + tile];
-        pre.row += (i - tile * p.g.tpt) * p.g.G + rhead;
-    }
-    const int n = pre.n + m.own.n;
-    const long own = (long)m.own.row + r;
-    constexpr int kU = 4;  // partials in flight
-    float top = -INFINITY, sum = 0.f, acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; e++) acc[e] = 0.f;
-    for (int c = 0; c < n; c += kU) {
-        float4 o[kU][2];
-        float l[kU];
-#pragma unroll
-        for (int i = 0; i < kU; i++) {
-            l[i] = -INFINITY, o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + i < n) {
-                const long row = c + i < pre.n ? pre.row + (long)(c + i) * pre.step
-                                               : own + (long)(c + i - pre.n) * m.own.step;
-                l[i] = p.part_lse[row];
-                o[i][0] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane];
-                o[i][1] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane + 1];
-            }
+    if (!paged_plan_ok(head, p.pg)) return;
+    for (int mi = blockIdx.x; mi < head.n_merge; mi += gridDim.x) {
+        if (!early || mi >= (int)gridDim.x) m = plan.merge[mi];
+        const int rows = min(MERGE_ROWS, (m.n_tok_hk & 255) * p.g.G - m.r0);
+        const int row_log2 = 32 - __clz(rows - 1);  // 16 half warps = 2^row_log2 rows of as many shares
+        const int share = half >> row_log2, shares = MERGE_ROWS >> row_log2;
+        const int r = m.r0 + (half & ((1 << row_log2) - 1));
+        const bool live = r - m.r0 < rows;
+        const int rtok = r / p.g.G, rhead = r - rtok * p.g.G, hk = m.n_tok_hk >> 8;
+        PagedParts pre = {0, 0, 0, 0};
+        if (m.prefix >= 0 && live) {
+            const int i = m.tok0 + rtok - m.group_q0, tile = i / p.g.tpt;
+            pre = plan.prefix[(long)hk * p.pg.cap_prefix + m.prefix + tile];
+            pre.row += (i - tile * p.g.tpt) * p.g.G + rhead;
         }
-        join<kU>(l, o, top, sum, acc);
+        const int n = live ? pre.n + m.n : 0;
+        const long own = (long)m.row + r;
+        constexpr int kU = 8;  // partials in flight
+        float top = -INFINITY, sum = 0.f, acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) acc[e] = 0.f;
+        for (int c0 = share; c0 < n; c0 += kU * shares) {
+            float4 o[kU][2];
+            float l[kU];
+#pragma unroll
+            for (int i = 0; i < kU; i++) {
+                const int c = c0 + i * shares;
+                l[i] = -INFINITY, o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c < n) {
+                    const long row = c < pre.n ? pre.row + (long)c * pre.step : own + (long)(c - pre.n) * m.step;
+                    l[i] = p.part_lse[row];
+                    o[i][0] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane];
+                    o[i][1] = reinterpret_cast<const float4 *>(p.part_o + row * 128)[2 * lane + 1];
+                }
+            }
+            join<kU>(l, o, top, sum, acc);
+        }
+        if (shares > 1) {  // the same for the whole block
+#pragma unroll
+            for (int e = 0; e < 8; e++) part[half][e][lane] = acc[e];
+            part[half][8][lane] = top, part[half][9][lane] = sum;
+            __syncthreads();
+            for (int s = 1; s < shares && share == 0; s++) {
+                const int from = half + (s << row_log2);
+                const float t1 = part[from][8][lane], t = fmaxf(top, t1), ref = t == -INFINITY ? 0.f : t;
+                const float f0 = ex2(top - ref), f1 = ex2(t1 - ref);
+                top = t;
+                sum = sum * f0 + part[from][9][lane] * f1;
+#pragma unroll
+                for (int e = 0; e < 8; e++) acc[e] = acc[e] * f0 + part[from][e][lane] * f1;
+            }
+            __syncthreads();
+        }
+        if (share == 0 && live) store_joined(p, top, sum, acc, (long)m.tok0 + rtok, hk * p.g.G + rhead, lane);
     }
-    store_joined(p, top, sum, acc, (long)m.tok0 + rtok, hk * p.g.G + rhead, lane);
 }
 
 // What both launches tell their kernels; `rows` rows of partials in the workspace.
@@ -820,11 +878,11 @@ cudaError_t launch_packed_fwd(const PackedGeom &g, const PackedPtrs &t, void *ou
         !packed_kv_map(&mk, g.Tk ? t.k : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.k_stride : t.q_stride, why) ||
         !packed_kv_map(&mv, g.Tk ? t.v : t.q, g.Tk ? g.Tk : g.Tq, g.Tk ? g.Hkv : 1, g.Tk ? t.v_stride : t.q_stride, why))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel<PackedFwdParams>, pf::SMEM_TOTAL);
+    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel<PackedFwdParams, ROWS>, pf::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     PackedFwdParams p;
     fill(p, g, t, (size_t)g.cap_slots * 128, out, out_stride, lse, ws);
-    e = launch_after(packed_fwd_kernel<PackedFwdParams>, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
+    e = launch_after(packed_fwd_kernel<PackedFwdParams, ROWS>, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
     if (e != cudaSuccess || g.extra == 0) return e;
     return launch_after(packed_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 15) / 16), 256, 0, st, p);
 }
@@ -837,17 +895,25 @@ cudaError_t launch_paged_fwd(const PagedGeom &pg, const PagedPtrs &t, void *out,
     if (!packed_q_map(&mq, t.q, g, t.q_stride, why)) return cudaErrorInvalidValue;
     // without pages no tile has keys and the maps of the caches are never used
     mk = mv = mq;
-    if (pg.n_pages > 0 && (!make_pages_map(&mk, t.cache[0], pg, why) || !make_pages_map(&mv, t.cache[1], pg, why)))
+    // Boxes of 16 and 32 tokens come as groups, larger ones as rows.  Measured in a captured graph, us, boxes of 16 / 32 /
+    // 64 / 128 tokens: two streams' next frame as rows 86.1 / 66.6 / 65.1 / 65.3, as groups 71.2 / 65.3 / 65.4 / 65.4; six
+    // samples' frames as rows 129.3 / 102.7 / 101.5 / 99.6, as groups 108.4 / 99.7 / 99.9 / 100.9.
+    const bool grouped = pg.box_log2 <= 5 && t.cache[0].span > 0 && t.cache[1].span > 0;
+    if (pg.n_pages > 0 &&
+        (!make_pages_map(&mk, t.cache[0], pg, grouped, why) || !make_pages_map(&mv, t.cache[1], pg, grouped, why)))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem((const void *)packed_fwd_kernel<PagedFwdParams>, pf::SMEM_TOTAL);
+    auto *kernel = grouped ? packed_fwd_kernel<PagedFwdParams, GROUPS> : packed_fwd_kernel<PagedFwdParams, ROWS>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, pf::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     PagedFwdParams p;
     fill(p, g, t, (size_t)pg.cap_part, out, out_stride, lse, ws);
     p.pg = pg;
     p.table = t.table;
-    e = launch_after(packed_fwd_kernel<PagedFwdParams>, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
+    p.span[0] = t.cache[0].span, p.span[1] = t.cache[1].span;
+    e = launch_after(kernel, (unsigned)g.sms, pf::THREADS, pf::SMEM_TOTAL, st, mq, mk, mv, p);
     if (e != cudaSuccess || g.cap_merge == 0) return e;
-    return launch_after(paged_merge_kernel, (unsigned)(((long)g.cap_merge * g.rows + 15) / 16), 256, 0, st, p);
+    const int most = g.sms * MERGE_BLOCKS_PER_SM;
+    return launch_after(paged_merge_kernel, (unsigned)(g.cap_merge < most ? g.cap_merge : most), 16 * MERGE_ROWS, 0, st, p);
 }
 
 }  // namespace k6

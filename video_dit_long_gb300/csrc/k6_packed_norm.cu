@@ -559,7 +559,7 @@ cudaError_t launch_paged_append(const Geom &g, const PagedGeom &p, const PagedAp
     a.n.x[0] = rows(t.x[0], t.x_stride[0]), a.n.x[1] = rows(t.x[1], t.x_stride[1]), a.v = rows(t.x[2], t.x_stride[2]);
     a.n.z[0] = rows(t.q_out, t.q_out_stride);
     for (int c = 0; c < 2; c++)
-        a.cache[c] = {t.cache[c].p, t.cache[c].page * 2, t.cache[c].token * 2, t.cache[c].head * 2}, a.n.w[c] = t.w[c];
+        a.cache[c] = {t.cache[c].p, t.cache[c].page * 2, t.cache[c].token * 2, t.cache[c].head * 2, 0}, a.n.w[c] = t.w[c];
     a.n.positions = t.positions, a.n.turns = t.turns;
     a.n.seg1 = g.axis_dim[0] / 2, a.n.seg2 = (g.axis_dim[0] + g.axis_dim[1]) / 2;
     a.n.eps = t.eps, a.n.err = t.err;

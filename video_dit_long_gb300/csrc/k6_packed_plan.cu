@@ -71,8 +71,8 @@ PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
 
 PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms) {
     PagedGeom r;
-    r.page = b.page_tokens, r.n_pages = (int)b.n_pages, r.max_pages = b.max_pages, r.n_groups = b.n_groups;
-    for (r.box = 128; r.page % r.box; r.box /= 2) {}
+    paged_set_page(r, b.page_tokens);
+    r.n_pages = (int)b.n_pages, r.max_pages = b.max_pages, r.n_groups = b.n_groups;
     PackedGeom &p = r.g;
     p.n_seq = b.n_seq;
     p.H = g.H, p.Hkv = b.kv_heads, p.G = g.H / b.kv_heads, p.block = b.mask_block;
@@ -88,7 +88,10 @@ PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms) {
     p.cap_k = 0;
     p.extra = p.Tk > (2 * MIN_PIECE - 1) * 128 ? (sms + p.Hkv - 1) / p.Hkv : 0;
     p.cap_slots = p.extra ? 2 * (p.extra * p.Hkv > sms ? p.extra * p.Hkv : sms) : 0;
-    p.cap_merge = (int)(p.cap_slots / 2 + joined * p.Hkv);
+    // joins of MERGE_ROWS rows: of whole tiles that are cut, and of every row that a group may share
+    const long joined_rows = joined * p.rows < (long)p.Tq * p.G ? joined * p.rows : (long)p.Tq * p.G;
+    p.cap_merge = (int)((long)p.cap_slots / 2 * ((p.rows + MERGE_ROWS - 1) / MERGE_ROWS) +
+                        (joined_rows / MERGE_ROWS + joined) * p.Hkv);
     const long rows = (long)p.Tq * p.H, own_rows = joined * p.Hkv * p.rows, prefix_rows = (long)r.cap_prefix * p.Hkv * p.rows;
     r.cap_part = (long)p.cap_slots * p.rows + (own_rows < rows ? own_rows : rows) + (prefix_rows < rows ? prefix_rows : rows);
     const long most = ((long)p.cap_q * p.Hkv * ((p.Tk + 127L) / 128 + 1 + ITEM_COST) + sms - 1) / sms;
@@ -170,11 +173,14 @@ struct PagedBatch {
         const int rows = n_tok * p.G, heads = hk1 - hk0;
         step = rows * heads;
         const int slot = n > 0 ? atomicAdd(&slots, n * step) : 0;
-        const int m = s.seen ? 0 : atomicAdd(&merges, heads);
+        const int per_head = (rows + MERGE_ROWS - 1) / MERGE_ROWS;
+        int m = s.seen ? 0 : atomicAdd(&merges, heads * per_head);
         for (int h = 0; h < heads; h++) {
-            const PagedParts own = {slot + h * rows, n, step, 0};
-            if (s.seen) plan.prefix[(long)(hk0 + h) * cap_prefix + s.prefix + t] = own;
-            else if (m + h < p.cap_merge) plan.merge[m + h] = {tok0, n_tok | (hk0 + h) << 8, s.prefix, s.group_q0, own};
+            const int row = slot + h * rows;
+            if (s.seen) plan.prefix[(long)(hk0 + h) * cap_prefix + s.prefix + t] = {row, n, step, 0};
+            else
+                for (int r0 = 0; r0 < rows; r0 += MERGE_ROWS, m++)
+                    if (m < p.cap_merge) plan.merge[m] = {tok0, n_tok | (hk0 + h) << 8, s.prefix, s.group_q0, row, n, step, r0};
         }
         return slot;
     }
@@ -639,11 +645,24 @@ __global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg,
     if (bad) return;
     paged_units(pg, plan, cu_q, k_lens, cu_groups, shared, &prefix_tiles);
     const PagedBatch b{plan, p.n_seq + pg.n_groups, p.n_seq, pg.cap_prefix, pg.cap_part};
-    if (!build_stretches(p, b, sh)) build<FWD>(p, b, sh);
+    const bool stretches = build_stretches(p, b, sh);
+    if (!stretches) build<FWD>(p, b, sh);
     __syncthreads();
     if (threadIdx.x == 0 && sh.bad) {
         plan.head->bad = 1;
         atomicCAS(err, DEV_OK, DEV_PLAN);
+    }
+    const int n = sh.total, per_sm = stretches ? 0 : (int)(((long)n * p.Hkv + p.sms - 1) / p.sms);
+    for (int c = threadIdx.x; c < p.sms && !sh.bad; c += THREADS) {
+        PackedItem it;
+        it.kt0 = it.kt1 = it.n_tok_hk = 0;  // a CTA without one
+        if (stretches) {
+            if (plan.count[c] > 0) it = plan.fwd[(long)c * p.cap_rows];
+        } else {
+            const int u = per_sm > 0 ? plan.sched[c] : -1;
+            if (u >= 0) it = plan.fwd[u % n], it.n_tok_hk |= u / n << 8;
+        }
+        plan.first[c] = it;
     }
 }
 

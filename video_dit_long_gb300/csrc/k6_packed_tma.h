@@ -13,8 +13,10 @@ namespace k6 {
 bool make_rows_map(CUtensorMap *m, const void *base, long tokens, int heads, long stride, int box_heads,
                    int box_tokens, const char **why);
 
-// Pages of one head's keys: box = 64 dims x 1 head x g.box tokens x 1 page.
-bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, const char **why);
+// Pages of one head's keys.  A box is 2^g.box_log2 tokens: 64 dims of them, [pages][tokens]
+// [heads][128], or (grouped; c.span wanted) both 64-dim panels as groups of 8
+// tokens, each group's panels one behind the other.
+bool make_pages_map(CUtensorMap *m, const PagedCache &c, const PagedGeom &g, bool grouped, const char **why);
 
 // A query tile: the G heads of one key head of g.tpt tokens.
 static inline bool packed_q_map(CUtensorMap *m, const void *q, const PackedGeom &g, long stride, const char **why) {

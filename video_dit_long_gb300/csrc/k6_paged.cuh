@@ -41,17 +41,21 @@ struct __align__(16) PagedParts {
     int row, n, step, unused;
 };
 
-// A tile of one key head whose rows have partials: its own, and (prefix >= 0)
-// those of the group's tiles over shared keys, from tile `prefix` on.
+// MERGE_ROWS rows, from r0 on, of a tile of one key head that have partials: the
+// tile's own, and (prefix >= 0) those of the group's tiles over shared keys, from
+// tile `prefix` on.
+constexpr int MERGE_ROWS = 16;
 struct __align__(16) PagedMerge {
     int tok0, n_tok_hk;
     int prefix, group_q0;
-    PagedParts own;
+    int row, n, step;  // as in PagedParts, of the tile's row 0
+    int r0;
 };
 
 struct PagedPlan {
     PagedHeader *head;
-    int *count;           // [sms], fwd and sched: as in a PackedPlan
+    int *count;           // [sms] items of each CTA (fwd and sched as in a PackedPlan)
+    PackedItem *first;    // [sms] the first item of each CTA, beside the header, with the key head above its tokens
     PagedMerge *merge;    // [cap_merge, or one per SM where that is more]
     PagedParts *prefix;   // [Hkv][cap_prefix] partials of the tiles over shared keys
     PagedUnits *units;    // [n_seq + n_groups]
@@ -60,7 +64,8 @@ struct PagedPlan {
     int *slot;            // [Tq] where a new token's key lies: page * page tokens + place, or -1: nowhere
 };
 
-// The start of every plan on a GPU of `sms` SMs: see packed_plan_common_bytes.
+// The plan's parts.  Those up to the first `sms` entries of merge lie in every plan
+// on a GPU of that many SMs: see packed_plan_common_bytes.
 static inline __host__ __device__ PagedPlan paged_plan_at(void *base, const PagedGeom &p) {
     PagedPlan r;
     char *b = static_cast<char *>(base);
@@ -68,6 +73,8 @@ static inline __host__ __device__ PagedPlan paged_plan_at(void *base, const Page
     b += PACKED_HEADER_BYTES;
     r.count = reinterpret_cast<int *>(b);
     b += ((size_t)p.g.sms * sizeof(int) + 15) / 16 * 16;
+    r.first = reinterpret_cast<PackedItem *>(b);
+    b += (size_t)p.g.sms * sizeof(PackedItem);
     r.merge = reinterpret_cast<PagedMerge *>(b);
     b += (size_t)packed_merge_rows(p.g) * sizeof(PagedMerge);
     r.prefix = reinterpret_cast<PagedParts *>(b);
@@ -82,21 +89,37 @@ static inline __host__ __device__ PagedPlan paged_plan_at(void *base, const Page
     return r;
 }
 
-// A tile of 128 keys comes in boxes of g.box tokens of one page each (the box
+// A tile of 128 keys comes in boxes of 2^box_log2 tokens of one page each (a box
 // divides both): box i of tile kt of a stream of Lk keys is `tok` tokens into the
 // page of the table's column `column`.  paged_boxes: how many of them hold keys.
 static inline __host__ __device__ int paged_boxes(const PagedGeom &g, int Lk, int kt) {
     const int left = Lk - kt * 128;
-    return ((left < 128 ? left : 128) + g.box - 1) / g.box;
+    return ((left < 128 ? left : 128) + (1 << g.box_log2) - 1) >> g.box_log2;
 }
 static inline __host__ __device__ int paged_box(const PagedGeom &g, int kt, int i, int &column) {
-    const int pos = kt * 128 + i * g.box;
-    column = pos / g.page;
+    const int pos = kt * 128 + (i << g.box_log2);
+    column = (int)((unsigned long long)(unsigned)pos * g.page_mul >> g.page_shift);
     return pos - column * g.page;
+}
+// The geometry's part of that.  page_mul = ceil(2^s / page) with 2^(s - 29) >= page: its excess over 2^s / page, below 1,
+// times x / 2^s stays below 1 / page, so the quotient's integer part is right; page_mul < 2^30 + 1.
+static inline void paged_set_page(PagedGeom &g, int page) {
+    g.page = page;
+    for (g.box_log2 = 7; page % (1 << g.box_log2); g.box_log2--) {}
+    for (g.page_shift = 29; 1ll << (g.page_shift - 29) < page; g.page_shift++) {}
+    g.page_mul = (unsigned)(((1ull << g.page_shift) + page - 1) / page);
 }
 // The page to copy from: one that the pool does not have becomes the first behind it, where a copy fills with zeros.
 static inline __host__ __device__ int paged_page(const PagedGeom &g, int page) {
     return (unsigned)page < (unsigned)g.n_pages ? page : g.n_pages;
+}
+// The same in groups of 8 tokens, `span` of them from one page to the next: how many the pool has, and the one that a
+// box begins at.
+static inline __host__ __device__ int paged_groups(const PagedGeom &g, int span) {
+    return (g.n_pages - 1) * span + g.page / 8;
+}
+static inline __host__ __device__ int paged_group(const PagedGeom &g, int span, int page, int tok) {
+    return (unsigned)page < (unsigned)g.n_pages ? page * span + tok / 8 : paged_groups(g, span);
 }
 
 // True if the plan was made for this batch and holds valid lists.
