@@ -131,12 +131,11 @@ struct Walk {
     uint32_t rounds, n_items;
     int slots;          // partials that one slot number stands for (1, or one for every key head)
     template <class Plan>
-    __device__ Walk(const Plan &plan, const PackedGeom &g, bool ok) {
+    __device__ Walk(const Plan &plan, const PackedHeader &head, int mine, const PackedGeom &g, bool ok) {
         list = plan.fwd;
-        const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
-        slots = plan.head->slot_step;
-        n_items = (uint32_t)plan.head->n_fwd;
-        if (plan.head->stream) {
+        slots = head.slot_step;
+        n_items = (uint32_t)head.n_fwd;
+        if (head.stream) {
             list += (long)blockIdx.x * g.cap_rows;
             sched = nullptr;
             rounds = (uint32_t)mine;
@@ -174,11 +173,11 @@ __device__ __forceinline__ PagedPlan plan_of(const PagedFwdParams &p) {
     return paged_plan_at(const_cast<void *>(p.plan), p.pg);
 }
 // Whether the plan is the batch's.
-__device__ __forceinline__ bool plan_ok_for(const PackedPlan &plan, const PackedFwdParams &p) {
-    return packed_plan_ok(*plan.head, p.g);
+__device__ __forceinline__ bool plan_ok_for(const PackedHeader &head, const PackedFwdParams &p) {
+    return packed_plan_ok(head, p.g);
 }
-__device__ __forceinline__ bool plan_ok_for(const PagedPlan &plan, const PagedFwdParams &p) {
-    return paged_plan_ok(*plan.head, p.pg);
+__device__ __forceinline__ bool plan_ok_for(const PagedHeader &head, const PagedFwdParams &p) {
+    return paged_plan_ok(head, p.pg);
 }
 
 // The first item, for the producers, which everything else waits for.  Over pages the plan keeps it beside the header.
@@ -307,9 +306,11 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     wait_previous_kernel();
     const auto plan = plan_of(p);
-    const bool plan_ok = plan_ok_for(plan, p);
+    const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
+    const auto head = *plan.head;             // as a whole: its comparisons would else read it one word after the other
+    const bool plan_ok = plan_ok_for(head, p);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
-    const Walk walk(plan, p.g, plan_ok);  // nothing to walk under a plan that is not this batch's
+    const Walk walk(plan, head, mine, p.g, plan_ok);  // nothing to walk under a plan that is not this batch's
     const WaitCtx w{p.wait_limit_ns, p.err, abort_flag};
 
     float *xm = reinterpret_cast<float *>(smem + SMEM_XCH);  // [row]: max after the latest tile
@@ -764,14 +765,16 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
     store_joined(p, top, sum, acc, (long)m.tok0 + r / p.g.G, (m.n_tok_hk >> 8) * p.g.G + r % p.g.G, lane);
 }
 
-constexpr int MERGE_BLOCKS_PER_SM = 4;
+// Blocks an SM, and partials that a half warp has in flight.  Measured in a captured graph, us (new tokens over a shared
+// prompt, 12 tokens over long caches): 8 partials x 2 blocks 17.7, 49.2; 4 x 3 18.1, 49.6; 4 x 4 19.5, 50.9 (spills).
+constexpr int MERGE_BLOCKS_PER_SM = 2, MERGE_UNROLL = 8;
 
 // Joins the partials of every row that has some over pages: a block an entry of the
 // plan's list, first the partials over the keys that a row's group shares, then its
 // own, each in key order.  Half a warp takes a row, 8 values a lane; with fewer rows
 // than half warps (a new token has its key head's G) several share one, each taking
 // every so many-th partial, and are joined in order through shared memory.
-__global__ void __launch_bounds__(16 * MERGE_ROWS) paged_merge_kernel(const PagedFwdParams p) {
+__global__ void __launch_bounds__(16 * MERGE_ROWS, MERGE_BLOCKS_PER_SM) paged_merge_kernel(const PagedFwdParams p) {
     __shared__ float part[MERGE_ROWS][10][16];
     launch_next_kernel();
     wait_previous_kernel();
@@ -790,7 +793,8 @@ __global__ void __launch_bounds__(16 * MERGE_ROWS) paged_merge_kernel(const Page
         const int r = m.r0 + (half & ((1 << row_log2) - 1));
         const bool live = r - m.r0 < rows;
         const int rtok = r / p.g.G, rhead = r - rtok * p.g.G, hk = m.n_tok_hk >> 8;
-        PagedParts pre = {0, 0, 0, 0};
+        PagedParts pre = m.shared;
+        pre.row += r;
         if (m.prefix >= 0 && live) {
             const int i = m.tok0 + rtok - m.group_q0, tile = i / p.g.tpt;
             pre = plan.prefix[(long)hk * p.pg.cap_prefix + m.prefix + tile];
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(16 * MERGE_ROWS) paged_merge_kernel(const Page
         }
         const int n = live ? pre.n + m.n : 0;
         const long own = (long)m.row + r;
-        constexpr int kU = 8;  // partials in flight
+        constexpr int kU = MERGE_UNROLL;  // partials in flight
         float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) acc[e] = 0.f;

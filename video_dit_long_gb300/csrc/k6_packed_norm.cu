@@ -12,12 +12,7 @@
 // Statistics, angles and sums are fp32 or wider; the one rounding is that of
 // each output element to its type.
 //
-// Angles: the frequency of a pair is kept as a 64-bit fixed-point fraction of a
-// turn, so position * frequency modulo 2^64 is the reduced angle with an error
-// below |position| 2^-55 turns, at any 32-bit position, in integer arithmetic;
-// its top 32 bits go to sincospi as a float, which costs up to 2^-26 of a turn
-// (2^-23.4 in the angle, the size of sin and cos's own rounding) near half a turn.
-// No per-token table is read: 12 bytes of positions serve all heads of a token.
+// Angles: k6_norm_rope.cuh.
 //
 // Bound by HBM: each element is read once and written once (backward: x and gz
 // read, dx written).  A head row is 16 lanes (32 for 512-byte rows) of one
@@ -31,63 +26,12 @@
 
 #include <type_traits>
 
-#include "k6_device.cuh"
-#include "k6_paged.cuh"
+#include "k6_internal.h"
+#include "k6_norm_rope.cuh"
 
 namespace k6 {
 
 namespace {
-
-// 16 bytes of a row as pairs (2k, 2k + 1) in fp32, and back.
-template <typename T>
-struct Row;
-template <>
-struct Row<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ static void unpack(const uint4 &u, uint64_t (&x)[4]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; k++) x[k] = f2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-    }
-    __device__ static uint4 pack(const float (&x)[8]) {
-        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                          pack_bf16x2(x[6], x[7]));
-    }
-};
-template <>
-struct Row<__half> {
-    __device__ static uint4 pack(const float (&x)[8]) {
-        uint4 u;
-        __half2 *b = reinterpret_cast<__half2 *>(&u);
-#pragma unroll
-        for (int k = 0; k < 4; k++) b[k] = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-        return u;
-    }
-};
-template <>
-struct Row<float> {
-    static constexpr int N = 4;
-    __device__ static void unpack(const uint4 &u, uint64_t (&x)[2]) {
-        x[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
-        x[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
-    }
-    __device__ static uint4 pack(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    }
-};
-
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// The larger of m, |a| and |b|; NaN if one is.
-__device__ __forceinline__ float max_abs(float m, float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
-    return r;
-}
 
 // Blocks of 256 threads resident on an SM: what the registers are bounded to, and the grid.
 // Vectors that a lane has in flight (of x; in the backward pass of x and of gz each).  Measured at 52,360
@@ -122,20 +66,11 @@ struct NormRopeArgs {
     int *err;
 };
 
-// cos and sin of the NP pairs from pair0 on, at a token's positions.  The
-// frequencies are re-read (L1) rather than kept: 2 NP registers less a lane.
-// No load here takes the non-coherent path: a kernel that begins while the one
-// before it ends may read what that one wrote.
+// cos and sin of the NP pairs from pair0 on, at a token's positions.
 template <int NP>
 __device__ __forceinline__ void cos_sin(const NormRopeArgs &a, long tok, int pair0, float (&c)[NP], float (&s)[NP]) {
-    const int p0 = a.positions[3 * tok], p1 = a.positions[3 * tok + 1], p2 = a.positions[3 * tok + 2];
-#pragma unroll
-    for (int k = 0; k < NP; k++) {
-        const int p = pair0 + k < a.seg1 ? p0 : pair0 + k < a.seg2 ? p1 : p2;
-        const unsigned long long turns = a.turns[pair0 + k];
-        const int top = (int)(((unsigned long long)(long long)p * turns) >> 32);  // in [-1/2, 1/2) turns
-        sincospif((float)top * 0x1p-31f, &s[k], &c[k]);
-    }
+    const int p[3] = {__ldg(a.positions + 3 * tok), __ldg(a.positions + 3 * tok + 1), __ldg(a.positions + 3 * tok + 2)};
+    cos_sin_at<NP>(p, a.turns, a.seg1, a.seg2, pair0, c, s);
 }
 
 // The tokens that belong to a sequence, [r[0], r[1]), where offsets say.  The whole block.
@@ -160,54 +95,6 @@ __device__ __forceinline__ Unit unit_at(const NormRopeArgs &a, long u) {
     return r;
 }
 
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// What turns and weighs the NP pairs of a lane at a unit's token, p: a pair becomes
-// z = r (x0 p0 - x1 p1, x0 p2 + x1 p3), the weights times cos and sin.
-template <int NP, bool NORM>
-__device__ __forceinline__ void turn_and_weigh(const NormRopeArgs &a, const Unit &un, int sub, float (&p)[NP][4]) {
-    float c[NP], s[NP];
-    cos_sin<NP>(a, un.tok, sub * NP, c, s);
-#pragma unroll
-    for (int k = 0; k < NP; k++) {
-        float w0 = 1.f, w1 = 1.f;
-        if constexpr (NORM) {
-            w0 = a.w[un.t][sub * 2 * NP + 2 * k];
-            w1 = a.w[un.t][sub * 2 * NP + 2 * k + 1];
-        }
-        p[k][0] = w0 * c[k], p[k][1] = w1 * s[k], p[k][2] = w0 * s[k], p[k][3] = w1 * c[k];
-    }
-}
-
-// A lane's vector of a head row: normed by the row's lanes, weighed and turned.
-template <typename T, int D, bool NORM, int NP>
-__device__ __forceinline__ void turned(const uint4 &raw, const float (&p)[NP][4], float eps, float (&z)[2 * NP]) {
-    uint64_t x[NP];
-    Row<T>::unpack(raw, x);
-    if constexpr (NORM) {
-        uint64_t ss = fmul2(x[0], x[0]);
-#pragma unroll
-        for (int k = 1; k < NP; k++) ss = ffma2(x[k], x[k], ss);
-        float s0, s1;
-        f2_split(ss, s0, s1);
-        const float r = rsqrtf(lanes_sum<D / (2 * NP)>(s0 + s1) * (1.f / D) + eps);
-#pragma unroll
-        for (int k = 0; k < NP; k++) x[k] = fmul2(x[k], f2(r, r));
-    }
-#pragma unroll
-    for (int k = 0; k < NP; k++) {
-        float x0, x1;
-        f2_split(x[k], x0, x1);
-        z[2 * k] = x0 * p[k][0] - x1 * p[k][1];
-        z[2 * k + 1] = x0 * p[k][2] + x1 * p[k][3];
-    }
-}
-
 // D = head dim, T = element type of the rows, TO = of the output.
 template <typename T, typename TO, int D, bool NORM>
 __global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kernel(const NormRopeArgs a) {
@@ -227,7 +114,7 @@ __global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kerne
         if (a.cu && (un.tok < range[0] || un.tok >= range[1])) continue;  // padding: whatever it holds
         const char *x0 = a.x[un.t].base + un.tok * a.x[un.t].stride + sub * 16;
         char *z0 = a.z[un.t].base + un.tok * a.z[un.t].stride + sub * 16;
-        float p[NP][4];
+        Turn<NP> turn;
         for (int hb = un.h0; hb < un.h1; hb += HPW * kU) {
             uint4 raw[kU];
 #pragma unroll
@@ -236,11 +123,17 @@ __global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kerne
                 raw[i] = make_uint4(0, 0, 0, 0);
                 if (h < un.h1) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + (long)h * ROW));
             }
-            if (hb == un.h0) turn_and_weigh<NP, NORM>(a, un, sub, p);
+            if (hb == un.h0) {
+                float c[NP], s[NP], w[N];
+                cos_sin<NP>(a, un.tok, sub * NP, c, s);
+#pragma unroll
+                for (int k = 0; k < N; k++) w[k] = NORM ? __ldg(a.w[un.t] + sub * N + k) : 1.f;
+                turn.set(c, s, w);
+            }
 #pragma unroll
             for (int i = 0; i < kU; i++) {
                 float z[N];
-                turned<T, D, NORM>(raw[i], p, a.eps, z);
+                turned<T, D, NORM>(raw[i], turn, a.eps, z);
                 const int h = hb + grp + i * HPW;
                 if (h < un.h1) {
                     if constexpr (std::is_same<TO, __half>::value) {
@@ -254,109 +147,6 @@ __global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) packed_norm_rope_kerne
     }
     if constexpr (std::is_same<TO, __half>::value) {
         if (!(top < 65520.f)) atomicCAS(a.err, DEV_OK, DEV_RANGE);  // not a finite half
-    }
-}
-
-// New tokens over a cache of pages: q as above; k as above, but to the place in the
-// pages that the plan gives the token; v as it is, beside it.
-struct AppendArgs {
-    NormRopeArgs n;                // of q, k, v: x; z[0] the rotated queries
-    PagedGeom g;
-    const void *plan;
-    int heads_v, run_v, runs_v;
-    long units_qk;                 // runs of q and k; those of v behind them up to n.units
-    Rows v;
-    PagedCache cache[2];           // strides in bytes
-};
-
-// A token's place: byte offset of head 0 in cache c.
-__device__ __forceinline__ long cache_at(const AppendArgs &a, int c, int slot) {
-    const int page = slot / a.g.page, tok = slot - page * a.g.page;
-    return (long)page * a.cache[c].page + (long)tok * a.cache[c].token;
-}
-
-template <typename TO, bool NORM>
-__global__ void __launch_bounds__(256, FWD_BLOCKS_PER_SM) paged_append_kernel(const AppendArgs a) {
-    using T = __nv_bfloat16;
-    constexpr int D = 128, N = 8, NP = N / 2, LPH = D / N, HPW = 32 / LPH, kU = FWD_VECS, ROW = D * sizeof(T);
-    launch_next_kernel();
-    wait_previous_kernel();
-    const PagedPlan plan = paged_plan_at(const_cast<void *>(a.plan), a.g);
-    const PagedHeader head = *plan.head;
-    if (!paged_plan_ok(head, a.g)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(a.n.err, DEV_OK, DEV_PLAN);
-        return;
-    }
-    const int lane = threadIdx.x & 31, sub = lane % LPH, grp = lane / LPH;
-    const long nwarps = ((long)gridDim.x * blockDim.x) >> 5;
-    float top = 0.f;
-    for (long u = (blockIdx.x * (long)blockDim.x + threadIdx.x) >> 5; u < a.n.units; u += nwarps) {
-        Unit un;
-        if (u < a.units_qk) {
-            un = unit_at(a.n, u);
-        } else {
-            const long w = u - a.units_qk;
-            un.t = 2;
-            un.tok = a.runs_v == 1 ? w : w / a.runs_v;
-            un.h0 = (int)(w - un.tok * a.runs_v) * a.run_v;
-            un.h1 = min(un.h0 + a.run_v, a.heads_v);
-        }
-        if (un.tok < head.q_lo || un.tok >= head.q_hi) continue;  // padding: whatever it holds
-        const Rows x = un.t == 2 ? a.v : a.n.x[un.t];
-        const char *x0 = x.base + un.tok * x.stride + sub * 16;
-        char *z0;
-        long step = ROW;
-        if (un.t == 0) {
-            z0 = a.n.z[0].base + un.tok * a.n.z[0].stride + sub * 16;
-        } else {
-            const int slot = plan.slot[un.tok];
-            if (slot < 0) continue;  // more queries than keys, or a page that is not one (the plan reported it)
-            z0 = static_cast<char *>(a.cache[un.t - 1].p) + cache_at(a, un.t - 1, slot) + sub * 16;
-            step = a.cache[un.t - 1].head;
-        }
-        if (un.t == 2) {
-            for (int hb = un.h0; hb < un.h1; hb += HPW * kU) {
-                uint4 raw[kU];
-#pragma unroll
-                for (int i = 0; i < kU; i++) {
-                    const int h = hb + grp + i * HPW;
-                    if (h < un.h1) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + (long)h * ROW));
-                }
-#pragma unroll
-                for (int i = 0; i < kU; i++) {
-                    const int h = hb + grp + i * HPW;
-                    if (h < un.h1) *reinterpret_cast<uint4 *>(z0 + h * step) = raw[i];
-                }
-            }
-            continue;
-        }
-        float p[NP][4];
-        for (int hb = un.h0; hb < un.h1; hb += HPW * kU) {
-            uint4 raw[kU];
-#pragma unroll
-            for (int i = 0; i < kU; i++) {
-                const int h = hb + grp + i * HPW;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (h < un.h1) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + (long)h * ROW));
-            }
-            if (hb == un.h0) turn_and_weigh<NP, NORM>(a.n, un, sub, p);
-#pragma unroll
-            for (int i = 0; i < kU; i++) {
-                float z[N];
-                turned<T, D, NORM>(raw[i], p, a.n.eps, z);
-                const int h = hb + grp + i * HPW;
-                if (h < un.h1) {
-                    if constexpr (std::is_same<TO, __half>::value) {
-#pragma unroll
-                        for (int k = 0; k < NP; k++) top = max_abs(top, z[2 * k], z[2 * k + 1]);
-                    }
-                    *reinterpret_cast<uint4 *>(z0 + h * step) = Row<TO>::pack(z);
-                }
-            }
-        }
-    }
-    if constexpr (std::is_same<TO, __half>::value) {
-        if (!(top < 65520.f)) atomicCAS(a.n.err, DEV_OK, DEV_RANGE);  // not a finite half
     }
 }
 
@@ -534,7 +324,7 @@ NormRopeArgs norm_args(const Geom &g, const PackedNormRope &p) {
 // 300 8.6 and 7.1, 2,432 16.3 and 17.1, 12,000 55.0 and 57.6.
 void choose_runs(NormRopeArgs &a, int pass, int sms) {
     for (int t = 0; t < 2; t++) {
-        a.run[t] = a.tokens >= 16L * sms && a.heads[t] > 0 ? (a.heads[t] + pass - 1) / pass * pass : pass;
+        a.run[t] = a.tokens >= 16L * sms ? (a.heads[t] + pass - 1) / pass * pass : pass;
         a.runs[t] = (a.heads[t] + a.run[t] - 1) / a.run[t];
     }
     a.units_q = a.tokens * a.runs[0];
@@ -548,34 +338,6 @@ long norm_blocks(const NormRopeArgs &a, int per_sm, int sms) {
 }
 
 }  // namespace
-
-cudaError_t launch_paged_append(const Geom &g, const PagedGeom &p, const PagedAppend &t, k6attn_dtype out,
-                                cudaStream_t st) {
-    if (p.g.Tq == 0) return cudaSuccess;
-    AppendArgs a = {};
-    a.n.tokens = p.g.Tq;
-    a.n.heads[0] = t.x[0] ? g.H : 0, a.n.heads[1] = p.g.Hkv, a.heads_v = p.g.Hkv;
-    auto rows = [&](const void *x, long stride) { return Rows{static_cast<char *>(const_cast<void *>(x)), stride * 2}; };
-    a.n.x[0] = rows(t.x[0], t.x_stride[0]), a.n.x[1] = rows(t.x[1], t.x_stride[1]), a.v = rows(t.x[2], t.x_stride[2]);
-    a.n.z[0] = rows(t.q_out, t.q_out_stride);
-    for (int c = 0; c < 2; c++)
-        a.cache[c] = {t.cache[c].p, t.cache[c].page * 2, t.cache[c].token * 2, t.cache[c].head * 2, 0}, a.n.w[c] = t.w[c];
-    a.n.positions = t.positions, a.n.turns = t.turns;
-    a.n.seg1 = g.axis_dim[0] / 2, a.n.seg2 = (g.axis_dim[0] + g.axis_dim[1]) / 2;
-    a.n.eps = t.eps, a.n.err = t.err;
-    a.g = p, a.plan = t.plan;
-    const int pass = FWD_VECS * 32 * 8 / 128;
-    choose_runs(a.n, pass, p.g.sms);
-    a.run_v = a.n.run[1], a.runs_v = a.n.runs[1];
-    a.units_qk = a.n.units;
-    a.n.units += a.n.tokens * a.runs_v;
-    auto launch = [&](auto kernel) {
-        return launch_after(kernel, (unsigned)norm_blocks(a.n, FWD_BLOCKS_PER_SM, p.g.sms), 256, 0, st, a);
-    };
-    const bool norm = t.w[0] || t.w[1];
-    if (out == K6ATTN_F16) return norm ? launch(paged_append_kernel<__half, true>) : launch(paged_append_kernel<__half, false>);
-    return norm ? launch(paged_append_kernel<__nv_bfloat16, true>) : launch(paged_append_kernel<__nv_bfloat16, false>);
-}
 
 size_t packed_norm_rope_bwd_workspace(const Geom &g, long tokens, int sms) {
     if (tokens <= 0) return 0;

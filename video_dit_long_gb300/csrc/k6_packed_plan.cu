@@ -41,6 +41,9 @@ constexpr int MIN_PIECE = 4;       // key tiles of a piece at least
 constexpr int ITEM_COST = 2;       // start and end of an item in key tiles: 1.6 us against 0.7 us a tile
 constexpr int STREAM_MOST = 256;   // cost per SM up to which the batch is cut into one stretch per SM
 constexpr int STREAM_SEQS = 1024;  // and sequences
+// Over pages, where new tokens are few and joins are by rows: measured in a captured graph, us, pieces of 4 and of 2 at
+// least, new tokens over shared prompts 18.1 and 17.3, two streams' next frame 67.8 and 66.8, a mixed step 35.5 and 34.9.
+constexpr int PAGED_PIECE = 2;
 constexpr int SHARE_LEAST = 8;     // key tiles that a shared prefix saves at least
 
 PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
@@ -86,7 +89,7 @@ PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms) {
     const long own = (long)p.Tq / p.tpt + b.n_seq, joined = b.n_groups > 0 ? (own < 2L * b.n_seq ? own : 2L * b.n_seq) : 0;
     p.cap_q = (int)own + r.cap_prefix;
     p.cap_k = 0;
-    p.extra = p.Tk > (2 * MIN_PIECE - 1) * 128 ? (sms + p.Hkv - 1) / p.Hkv : 0;
+    p.extra = p.Tk > (2 * PAGED_PIECE - 1) * 128 ? (sms + p.Hkv - 1) / p.Hkv : 0;
     p.cap_slots = p.extra ? 2 * (p.extra * p.Hkv > sms ? p.extra * p.Hkv : sms) : 0;
     // joins of MERGE_ROWS rows: of whole tiles that are cut, and of every row that a group may share
     const long joined_rows = joined * p.rows < (long)p.Tq * p.G ? joined * p.rows : (long)p.Tq * p.G;
@@ -127,6 +130,7 @@ struct Seq {
 
 // What the lists are made of.  Batch: packed sequences.
 struct Batch {
+    static constexpr int PIECE = MIN_PIECE;
     const int *cu_q, *cu_k;
     PackedPlan plan;
     int n;
@@ -156,6 +160,7 @@ struct Batch {
 
 // Pages: units of tiles; those behind the streams' own are over shared keys.  A slot is a row of the partials.
 struct PagedBatch {
+    static constexpr int PIECE = PAGED_PIECE;
     PagedPlan plan;
     int n, n_seq, cap_prefix;
     long cap_part;
@@ -180,7 +185,8 @@ struct PagedBatch {
             if (s.seen) plan.prefix[(long)(hk0 + h) * cap_prefix + s.prefix + t] = {row, n, step, 0};
             else
                 for (int r0 = 0; r0 < rows; r0 += MERGE_ROWS, m++)
-                    if (m < p.cap_merge) plan.merge[m] = {tok0, n_tok | (hk0 + h) << 8, s.prefix, s.group_q0, row, n, step, r0};
+                    if (m < p.cap_merge) 
+                        plan.merge[m] = {tok0, n_tok | (hk0 + h) << 8, s.prefix, s.group_q0, row, n, step, r0, {0, 0, 0, 0}};
         }
         return slot;
     }
@@ -221,40 +227,52 @@ struct Shared {
     int first[MAX_SMS], items[MAX_SMS];
     int cost[STREAM_SEQS + 1], tiles[STREAM_SEQS + 1];
     int warp_sum[WARPS];
-    // dealing out: each SM's load, a round's works, and both by rank
-    int load[MAX_SMS], work_of[MAX_SMS], sm_at[MAX_SMS], unit_at[MAX_SMS];
+    // dealing out: each SM's load, a round's works, the ranks of both, and both by rank
+    int load[MAX_SMS], work_of[MAX_SMS], rank[2][MAX_SMS], sm_at[MAX_SMS], unit_at[MAX_SMS];
 };
 
 // The schedule of n items for every key head (see the head of this file).
 template <class Plan>
 __device__ void deal(const PackedGeom &p, const Plan &plan, Shared &sh, int n) {
     const long units = (long)n * p.Hkv;
-    const int t = threadIdx.x, side = t / (THREADS / 2), i = t % (THREADS / 2);  // half the threads rank each side
-    if (side == 0 && i < p.sms) sh.load[i] = 0;
+    // half the threads rank each side; as many as fit share one entry's comparisons
+    const int side = threadIdx.x / (THREADS / 2), x = threadIdx.x % (THREADS / 2);
+    const int shares = THREADS / 2 / p.sms, i = x % p.sms, share = x / p.sms;
+    const bool one = side == 0 && x < p.sms;  // a thread for each SM
+    if (one) sh.load[i] = 0;
+    // the work of unit base + i, read a round ahead; item: its place among those of a key head
+    int item = n > 0 ? i % n : 0;
+    auto work = [&](long u) {
+        if (!one || u >= units) return 0;
+        const PackedItem &it = plan.fwd[item];
+        const int w = it.kt1 - it.kt0 + ITEM_COST;
+        for (item += p.sms; item >= n;) item -= n;
+        return w;
+    };
+    int next = work(i);
     for (long base = 0; base < units; base += p.sms) {
-        if (side == 0 && i < p.sms) {
-            int w = 0;
-            if (base + i < units) {
-                const PackedItem &it = plan.fwd[(base + i) % n];
-                w = it.kt1 - it.kt0 + ITEM_COST;
-            }
-            sh.work_of[i] = w;
+        if (one) {
+            sh.work_of[i] = next;
+            sh.rank[0][i] = sh.rank[1][i] = 0;
         }
+        next = work(base + p.sms + i);
         __syncthreads();
-        if (i < p.sms) {
+        if (share < shares) {
+            const int j0 = (int)((long)p.sms * share / shares), j1 = (int)((long)p.sms * (share + 1) / shares);
             int rank = 0;
             if (side == 0) {  // the least loaded SM first
                 const int mine = sh.load[i];
-                for (int j = 0; j < p.sms; j++) rank += sh.load[j] < mine || (sh.load[j] == mine && j < i);
-                sh.sm_at[rank] = i;
+                for (int j = j0; j < j1; j++) rank += sh.load[j] < mine || (sh.load[j] == mine && j < i);
             } else {  // the heaviest unit first
                 const int mine = sh.work_of[i];
-                for (int j = 0; j < p.sms; j++) rank += sh.work_of[j] > mine || (sh.work_of[j] == mine && j < i);
-                sh.unit_at[rank] = i;
+                for (int j = j0; j < j1; j++) rank += sh.work_of[j] > mine || (sh.work_of[j] == mine && j < i);
             }
+            atomicAdd(&sh.rank[side][i], rank);
         }
         __syncthreads();
-        if (side == 0 && i < p.sms) {
+        if (one) sh.sm_at[sh.rank[0][i]] = i, sh.unit_at[sh.rank[1][i]] = i;
+        __syncthreads();
+        if (one) {
             const int sm = sh.sm_at[i], u = sh.unit_at[i];
             plan.sched[base + sm] = base + u < units ? (int)(base + u) : -1;
             sh.load[sm] += sh.work_of[u];
@@ -267,14 +285,17 @@ template <List LIST, class B>
 __device__ void build(const PackedGeom &p, const B &b, Shared &sh) {
     const auto &plan = b.plan;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // a warp to a sequence; with fewer sequences than warps all threads to each
+    const bool few = b.n < WARPS;
+    const int s0 = few ? 0 : warp, ds = few ? 1 : WARPS, t0 = few ? (int)threadIdx.x : lane, dt = few ? THREADS : 32;
     const int most = LIST == KTILES ? (p.Tq + p.tpt - 1) / p.tpt : (p.Tk + 127) / 128;
     int chunk = 1 << 30;
     if (LIST == FWD && p.extra > 0) {
         // key tiles per item: the batch's work over the items aimed at
         unsigned long long w = 0;
-        for (int s = warp; s < b.n; s += WARPS) {
+        for (int s = s0; s < b.n; s += ds) {
             const Seq q = b.template sequence<LIST>(p, s);
-            for (int t = lane; t < q.tiles; t += 32) {
+            for (int t = t0; t < q.tiles; t += dt) {
                 int lo, hi;
                 range<LIST>(p, q, t, lo, hi);
                 w += hi - lo;
@@ -284,11 +305,11 @@ __device__ void build(const PackedGeom &p, const B &b, Shared &sh) {
         __syncthreads();
         // extra * chunk >= work, so that the pieces beyond one per tile number at most extra
         const unsigned long long c = (sh.work + p.extra - 1) / p.extra;
-        chunk = c < (1u << 30) ? max(2 * MIN_PIECE, (int)c) : 1 << 30;
+        chunk = c < (1u << 30) ? max(2 * B::PIECE, (int)c) : 1 << 30;
     }
-    for (int s = warp; s < b.n; s += WARPS) {
+    for (int s = s0; s < b.n; s += ds) {
         const Seq q = b.template sequence<LIST>(p, s);
-        for (int t = lane; t < q.tiles; t += 32) {
+        for (int t = t0; t < q.tiles; t += dt) {
             int lo, hi;
             range<LIST>(p, q, t, lo, hi);
             const int n = max(1, (hi - lo + chunk - 1) / chunk);
@@ -317,9 +338,9 @@ __device__ void build(const PackedGeom &p, const B &b, Shared &sh) {
         if (threadIdx.x == 0) sh.bad = 1;
         return;
     }
-    for (int s = warp; s < b.n; s += WARPS) {
+    for (int s = s0; s < b.n; s += ds) {
         const Seq q = b.template sequence<LIST>(p, s);
-        for (int t = lane; t < q.tiles; t += 32) {
+        for (int t = t0; t < q.tiles; t += dt) {
             int lo, hi;
             range<LIST>(p, q, t, lo, hi);
             if constexpr (LIST == KTILES) {
@@ -429,30 +450,34 @@ __device__ bool build_stretches(const PackedGeom &p, const B &b, Shared &sh) {
             const Seq q = b.template sequence<FWD>(p, s);
             int run = sh.cost[s];
             for (int t0 = 0; t0 < q.tiles; t0 += 32) {
-                const int t = t0 + lane;
-                int lo = 0, work = 0, cost = 0;
-                if (t < q.tiles) {
-                    range<FWD>(p, q, t, lo, work);
-                    work -= lo;
-                    cost = max(work, 1) + ITEM_COST;
+                int tile_lo = 0, tile_work = 0, tile_cost = 0;
+                if (t0 + lane < q.tiles) {
+                    range<FWD>(p, q, t0 + lane, tile_lo, tile_work);
+                    tile_work -= tile_lo;
+                    tile_cost = max(tile_work, 1) + ITEM_COST;
                 }
-                int upto = cost;
+                int upto = tile_cost;
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, upto, o);
                     if (lane >= o) upto += v;
                 }
-                const int at = run + upto - cost;
+                const int tile_at = run + upto - tile_cost;
                 run += __shfl_sync(0xffffffffu, upto, 31);
-                if (t >= q.tiles) continue;
-                for (int hk = 0; hk < p.Hkv; hk++) {
+                // the units of these tiles and every key head, one a lane
+                const int units = min(32, q.tiles - t0) * p.Hkv;
+                for (int u0 = 0; u0 < units; u0 += 32) {
+                    const int u = min(u0 + lane, units - 1), src = u / p.Hkv, hk = u - src * p.Hkv, t = t0 + src;
+                    const int at = __shfl_sync(0xffffffffu, tile_at, src), cost = __shfl_sync(0xffffffffu, tile_cost, src);
+                    const int lo = __shfl_sync(0xffffffffu, tile_lo, src), work = __shfl_sync(0xffffffffu, tile_work, src);
+                    if (u0 + lane >= units) continue;
                     const int a = hk * head_cost + at, z = a + cost, unit = hk * head_tiles + sh.tiles[s] + t;
                     const int c0 = (a + Q - 1) / Q, c1 = min(p.sms, (z + Q - 1) / Q);  // borders in [a, z): [c0, c1)
                     // tile at which border c cuts the unit, moved to its ends where a piece would be too short (and
-                    // to multiples of MIN_PIECE where the borders are closer than that)
+                    // to multiples of that least piece where the borders are closer)
                     auto cut = [&](int c) {
                         int x = max(0, c * Q - a - ITEM_COST);
-                        if (Q < MIN_PIECE) x -= x % MIN_PIECE;
-                        return x < MIN_PIECE ? 0 : work - x < MIN_PIECE ? work : x;
+                        if (Q < B::PIECE) x -= x % B::PIECE;
+                        return x < B::PIECE ? 0 : work - x < B::PIECE ? work : x;
                     };
                     if (pass == 0) {
                         for (int c = c0; c < c1; c++) sh.first[c] = unit + (cut(c) >= max(work, 1) ? 1 : 0);
@@ -651,6 +676,17 @@ __global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg,
     if (threadIdx.x == 0 && sh.bad) {
         plan.head->bad = 1;
         atomicCAS(err, DEV_OK, DEV_PLAN);
+    }
+    for (int i = threadIdx.x; i < sh.merges && !sh.bad; i += THREADS) {
+        PagedMerge &m = plan.merge[i];
+        if (m.prefix < 0) continue;
+        // the first and the last token of the rows, in the group's tiles
+        const int n_tok = m.n_tok_hk & 255, at = m.tok0 - m.group_q0;
+        const int a = (at + m.r0 / p.G) / p.tpt, z = (at + min(n_tok - 1, (m.r0 + MERGE_ROWS - 1) / p.G)) / p.tpt;
+        if (a != z) continue;
+        m.shared = plan.prefix[(long)(m.n_tok_hk >> 8) * pg.cap_prefix + m.prefix + a];
+        m.shared.row += (at - a * p.tpt) * p.G;
+        m.prefix = -1;
     }
     const int n = sh.total, per_sm = stretches ? 0 : (int)(((long)n * p.Hkv + p.sms - 1) / p.sms);
     for (int c = threadIdx.x; c < p.sms && !sh.bad; c += THREADS) {

@@ -43,13 +43,15 @@ struct __align__(16) PagedParts {
 
 // MERGE_ROWS rows, from r0 on, of a tile of one key head that have partials: the
 // tile's own, and (prefix >= 0) those of the group's tiles over shared keys, from
-// tile `prefix` on.
+// tile `prefix` on.  Where all of the rows belong to one of those tiles its
+// partials stand here (prefix = -1): the join is a read less deep.
 constexpr int MERGE_ROWS = 16;
 struct __align__(16) PagedMerge {
     int tok0, n_tok_hk;
     int prefix, group_q0;
     int row, n, step;  // as in PagedParts, of the tile's row 0
     int r0;
+    PagedParts shared; // of the tile's row 0; n = 0: none, or not here
 };
 
 struct PagedPlan {
