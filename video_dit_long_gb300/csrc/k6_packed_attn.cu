@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     constexpr bool PAGED = std::is_same<Params, PagedFwdParams>::value;
     using Tile = KeyTile<HOW>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    launch_next_kernel();
+    if constexpr (!PAGED) launch_next_kernel();
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the CTA leaves before any barrier
         wait_previous_kernel();
         if (threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_LAYOUT);
@@ -304,7 +304,14 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
     wait_previous_kernel();
+    // over pages only now, so that the join, which begins when every CTA has come here, may read the plan before it waits
+    if constexpr (PAGED) launch_next_kernel();
     const auto plan = plan_of(p);
     const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
     const auto head = *plan.head;             // as a whole: its comparisons would else read it one word after the other
@@ -324,10 +331,6 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             const CUtensorMap *tm = warp == 8 ? &tm_k : &tm_v;
             uint64_t *full = warp == 8 ? k_full : v_full, *empty = warp == 8 ? k_empty : v_empty;
             uint8_t *ring = smem + (warp == 8 ? SMEM_KV : SMEM_V);
-            if (leader) {
-                prefetch_tmap(tm);
-                if (warp == 8) prefetch_tmap(&tm_q);
-            }
             uint32_t n = 0;       // tiles loaded
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
@@ -777,16 +780,20 @@ constexpr int MERGE_BLOCKS_PER_SM = 2, MERGE_UNROLL = 8;
 __global__ void __launch_bounds__(16 * MERGE_ROWS, MERGE_BLOCKS_PER_SM) paged_merge_kernel(const PagedFwdParams p) {
     __shared__ float part[MERGE_ROWS][10][16];
     launch_next_kernel();
-    wait_previous_kernel();
+    // The plan is read ahead of the wait: the attention kernel only reads it too, and lets this one begin when it has
+    // itself waited for whatever made the plan.
     const PagedPlan plan = plan_of(p);
     const int lane = threadIdx.x & 15, half = threadIdx.x >> 4;
     const bool early = blockIdx.x < (unsigned)p.g.sms;  // as in packed_merge_kernel
     PagedMerge m;
     if (early) m = plan.merge[blockIdx.x];
     const PagedHeader head = *plan.head;
-    if (!paged_plan_ok(head, p.pg)) return;
+    const bool ok = paged_plan_ok(head, p.pg);
+    if (ok && !early && (int)blockIdx.x < head.n_merge) m = plan.merge[blockIdx.x];
+    wait_previous_kernel();
+    if (!ok) return;
     for (int mi = blockIdx.x; mi < head.n_merge; mi += gridDim.x) {
-        if (!early || mi >= (int)gridDim.x) m = plan.merge[mi];
+        if (mi >= (int)gridDim.x) m = plan.merge[mi];
         const int rows = min(MERGE_ROWS, (m.n_tok_hk & 255) * p.g.G - m.r0);
         const int row_log2 = 32 - __clz(rows - 1);  // 16 half warps = 2^row_log2 rows of as many shares
         const int share = half >> row_log2, shares = MERGE_ROWS >> row_log2;
