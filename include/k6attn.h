@@ -637,7 +637,7 @@ typedef struct {
  * token's key lies, and the lists of the attention call.  One plan serves the
  * calls of every layer of the step, and is not changed by them.  Offsets that are
  * not ascending or leave [0, q_tokens] (groups: [0, n_seq]), k_lens outside
- * [0, max_pages * page_tokens] and negative `shared` make K6ATTN_ERR_INVALID_ARG
+ * [0, max_pages * page_tokens] (without pages: other than 0) and negative `shared` make K6ATTN_ERR_INVALID_ARG
  * at k6attn_sync, and so does a call with a batch other than the plan's; the call
  * then writes nothing.  A table entry in use that is no page of the pool makes the
  * same error: a new token there is left out of the cache, and the attention of its

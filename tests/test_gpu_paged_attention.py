@@ -392,6 +392,23 @@ def test_no_queries_no_pages_and_no_lse():
     assert torch.equal(b.out, want)
 
 
+def test_keys_without_pages_make_a_bad_plan():
+    """A pool of no pages has no tensor map: a plan with keys must not reach the copies."""
+    from video_dit_long_gb300 import k6attn as K
+    h = K.Handle.for_packed(4)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = lambda *s: torch.full((*s, 128), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    p = h.paged_plan(i32(0, 5), i32(20), torch.zeros((1, 2), dtype=torch.int32, device="cuda"), 5, 2, 16, 0, 0)
+    with pytest.raises(K.K6Error) as err:
+        h.sync()
+    assert err.value.status == K.ERR_INVALID_ARG
+    out = e(5, 4)
+    h.paged_forward(p, e(5, 4), e(0, 16, 2), e(0, 16, 2), out)
+    with pytest.raises(K.K6Error) as err:
+        h.sync()
+    assert err.value.status == K.ERR_INVALID_ARG and bool((out == 7.0).all())
+
+
 def test_refusals():
     b = Step([90], [90], 4, 2, 1, qk="bf16", seed=16)
     K, h = b.K, b.h

@@ -651,8 +651,9 @@ __global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg,
         if (pg.n_groups > 0 && (cu_groups[0] < 0 || cu_groups[pg.n_groups] > p.n_seq)) sh.bad = 1;
     }
     __syncthreads();
+    const int most = pg.n_pages > 0 ? p.Tk : 0;  // without pages there are no keys, and the calls have no map of them
     for (int s = threadIdx.x; s < p.n_seq; s += THREADS)
-        if (cu_q[s + 1] < cu_q[s] || k_lens[s] < 0 || k_lens[s] > p.Tk) sh.bad = 1;
+        if (cu_q[s + 1] < cu_q[s] || k_lens[s] < 0 || k_lens[s] > most) sh.bad = 1;
     for (int g = threadIdx.x; g < pg.n_groups; g += THREADS)
         if (cu_groups[g + 1] < cu_groups[g] || shared[g] < 0) sh.bad = 1;
     __syncthreads();

@@ -1,4 +1,5 @@
-"""The attention of one layer over a packed batch of clips, forward and backward.
+"""The attention of one layer over a packed batch of clips, forward and backward,
+and of the new tokens of growing streams over a cache of pages.
 
 A batch of clips (or images, prompts, new tokens of running streams) of different
 lengths lies one behind another in [tokens] rows.  The layer's fused projection
@@ -11,6 +12,12 @@ attention):
             k6attn_packed_forward     attention of the rotated q, k and of v in qkv
   backward: k6attn_packed_backward    gradients of the rotated q, k, and of v into dqkv
             k6attn_packed_norm_rope_backward   those of q, k into dqkv, and of the norm's weights
+
+Streams that grow keep their keys and values in pages (PagedBatch, PagedAttention);
+a step of new tokens is
+
+            k6attn_paged_append       rotated q out of qkv, rotated k and v into the pages
+            k6attn_paged_forward      attention of q over the streams' pages
 
 All arithmetic runs in the library's kernels.  A layer stack makes one
 PackedBatch per batch of lengths and one PackedAttention per layer whose
@@ -95,3 +102,73 @@ class PackedAttention:
                                          dq=dq, dk=dk, dq_weight=self.dq_weight, dk_weight=self.dk_weight,
                                          workspace=self.workspace, offsets=self.batch.offsets)
         return self.dq_weight, self.dk_weight
+
+
+class PagedBatch:
+    """A step of streams whose keys lie in pages: its offsets, lengths, table of pages and work list, shared by the layers
+    of the step and made anew for the next one.
+
+    lens: new tokens of each stream (a list, or int32 offsets [n + 1]); k_lens: keys of each with the new ones; table
+    [n][max_pages]: its pages in order.  tokens: rows of qkv.  groups: [(streams, shared tokens)] of the streams in
+    order that have a prefix in common, or None; mask_block as for PackedBatch."""
+
+    def __init__(self, handle, lens, k_lens, table, tokens, kv_heads, page_tokens, n_pages, mask_block=1, groups=None):
+        import torch
+        self.handle, self.tokens, self.kv_heads = handle, int(tokens), int(kv_heads)
+        own = lambda x: torch.as_tensor(x).to(device=handle._dev, dtype=torch.int32, copy=True)  # noqa: E731
+        self.offsets, self.k_lens, self.table = own(PackedBatch._offsets(lens)), own(k_lens), own(table)
+        self.groups = {}
+        if groups:
+            self.groups = dict(cu_groups=own(PackedBatch._offsets([n for n, _ in groups])), shared=own([n for _, n in groups]))
+        self.plan = handle.paged_plan(self.offsets, self.k_lens, self.table, self.tokens, self.kv_heads, page_tokens, n_pages,
+                                      mask_block, **self.groups)
+
+    def next(self, lens=None, k_lens=None, table=None, shared=None):
+        """The next step of as many streams, in place (captured layers see it at their next replay); what is not given
+        stays as it is.  Tensors on the device are copied in stream order; the host waits for copies of its own."""
+        import torch
+        given = [(self.offsets, None if lens is None else PackedBatch._offsets(lens)), (self.k_lens, k_lens),
+                 (self.table, table), (self.groups.get("shared"), shared)]
+        given = [(to, torch.as_tensor(x)) for to, x in given if x is not None]
+        for to, x in given:
+            if to is None:
+                raise ValueError("shared: the batch has no groups")
+            if x.shape != to.shape or x.is_floating_point():
+                raise ValueError(f"want integers of shape {tuple(to.shape)}, got {x.dtype} {tuple(x.shape)}")
+        for to, x in given:
+            to.copy_(x)
+        self.handle.paged_replan(self.plan, self.offsets, self.k_lens, self.table, **self.groups)
+
+
+class PagedAttention:
+    """One layer's attention over a PagedBatch, with the layer's pools of keys and values.
+
+    by_head: a page holds one head's tokens after another's (else one token's heads).  qk: the type of rotated queries
+    and keys."""
+
+    def __init__(self, batch, q_weight, k_weight, eps=1e-6, qk="f16", by_head=False):
+        import torch
+        if qk not in ("f16", "bf16"):
+            raise ValueError(qk)
+        self.batch, self.h = batch, batch.handle
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        T, self.H, self.kv, self.d = batch.tokens, self.h._H, batch.kv_heads, self.h._d
+        n, page, kv, d = batch.plan.pages
+        t = torch.float16 if qk == "f16" else torch.bfloat16
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.h._dev)  # noqa: E731
+        pool = lambda t: new(n, kv, page, d, dtype=t).transpose(1, 2) if by_head else new(n, page, kv, d, dtype=t)  # noqa: E731
+        self.k_cache, self.v_cache = pool(t), pool(torch.bfloat16)
+        self.q, self.out, self.lse = new(T, self.H, d, dtype=t), new(T, self.H, d).zero_(), new(self.H, T, dtype=torch.float32)
+        self.workspace = new(self.h.paged_workspace_bytes(batch.plan), dtype=torch.uint8)
+
+    parts = PackedAttention.parts
+
+    def forward(self, qkv, positions):
+        """qkv bf16 [tokens][(H + 2 kv_heads) * d], positions int32 [tokens][3] of the step's new tokens: their keys and
+        values join the pages; returns out [tokens][H][d] (bf16; rows outside the streams stay)."""
+        q, k, v = self.parts(qkv)
+        plan = self.batch.plan
+        self.h.paged_append(plan, q, k, v, positions, self.q_weight, self.k_weight, self.eps, q_out=self.q,
+                            k_cache=self.k_cache, v_cache=self.v_cache)
+        self.h.paged_forward(plan, self.q, self.k_cache, self.v_cache, self.out, self.lse, workspace=self.workspace)
+        return self.out
