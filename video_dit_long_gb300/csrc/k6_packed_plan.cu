@@ -44,6 +44,9 @@ constexpr int STREAM_SEQS = 1024;  // and sequences
 // Over pages, where new tokens are few and joins are by rows: measured in a captured graph, us, pieces of 4 and of 2 at
 // least, new tokens over shared prompts 18.1 and 17.3, two streams' next frame 67.8 and 66.8, a mixed step 35.5 and 34.9.
 constexpr int PAGED_PIECE = 2;
+// An item of few rows has tiles that wait for HBM, beside which its start costs less: 1 against 2 took 32 tokens over a
+// shared prefix from 37.7 to 36.7 us, a mixed step from 34.0 to 33.5, 12 tokens over long caches from 48.3 to 48.6.
+constexpr int FEW_ROWS = 64, FEW_ROWS_ITEM = 1;
 constexpr int SHARE_LEAST = 8;     // key tiles that a shared prefix saves at least
 
 PackedGeom packed_geom(const Geom &g, const k6attn_packed &b, int sms) {
@@ -98,7 +101,7 @@ PagedGeom paged_geom(const Geom &g, const k6attn_paged &b, int sms) {
     const long rows = (long)p.Tq * p.H, own_rows = joined * p.Hkv * p.rows, prefix_rows = (long)r.cap_prefix * p.Hkv * p.rows;
     r.cap_part = (long)p.cap_slots * p.rows + (own_rows < rows ? own_rows : rows) + (prefix_rows < rows ? prefix_rows : rows);
     const long most = ((long)p.cap_q * p.Hkv * ((p.Tk + 127L) / 128 + 1 + ITEM_COST) + sms - 1) / sms;
-    p.cap_rows = (int)(most < STREAM_MOST ? most : STREAM_MOST) / (ITEM_COST + 1) + 8;
+    p.cap_rows = (int)(most < STREAM_MOST ? most : STREAM_MOST) / (FEW_ROWS_ITEM + 1) + 8;
     const long list = (long)p.cap_q + p.extra, all = (long)sms * p.cap_rows;
     p.cap_fwd = (int)(list > all ? list : all);
     p.cap_sched = most <= STREAM_MOST && p.n_seq + b.n_groups <= STREAM_SEQS ? 0 : (list * p.Hkv + sms - 1) / sms * sms;
@@ -131,6 +134,7 @@ struct Seq {
 // What the lists are made of.  Batch: packed sequences.
 struct Batch {
     static constexpr int PIECE = MIN_PIECE;
+    __device__ __forceinline__ static int item_cost(const PackedGeom &, const Seq &, int) { return ITEM_COST; }
     const int *cu_q, *cu_k;
     PackedPlan plan;
     int n;
@@ -161,6 +165,9 @@ struct Batch {
 // Pages: units of tiles; those behind the streams' own are over shared keys.  A slot is a row of the partials.
 struct PagedBatch {
     static constexpr int PIECE = PAGED_PIECE;
+    __device__ __forceinline__ static int item_cost(const PackedGeom &p, const Seq &s, int t) {
+        return min(p.tpt, s.Lq - t * p.tpt) * p.G <= FEW_ROWS ? FEW_ROWS_ITEM : ITEM_COST;
+    }
     PagedPlan plan;
     int n, n_seq, cap_prefix;
     long cap_part;
@@ -402,7 +409,7 @@ __device__ bool build_stretches(const PackedGeom &p, const B &b, Shared &sh) {
         for (int t = lane; t < q.tiles; t += 32) {
             int lo, hi;
             range<FWD>(p, q, t, lo, hi);
-            c += max(hi - lo, 1) + ITEM_COST;
+            c += max(hi - lo, 1) + b.item_cost(p, q, t);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
@@ -454,7 +461,7 @@ __device__ bool build_stretches(const PackedGeom &p, const B &b, Shared &sh) {
                 if (t0 + lane < q.tiles) {
                     range<FWD>(p, q, t0 + lane, tile_lo, tile_work);
                     tile_work -= tile_lo;
-                    tile_cost = max(tile_work, 1) + ITEM_COST;
+                    tile_cost = max(tile_work, 1) + b.item_cost(p, q, t0 + lane);
                 }
                 int upto = tile_cost;
                 for (int o = 1; o < 32; o <<= 1) {
@@ -470,12 +477,13 @@ __device__ bool build_stretches(const PackedGeom &p, const B &b, Shared &sh) {
                     const int at = __shfl_sync(0xffffffffu, tile_at, src), cost = __shfl_sync(0xffffffffu, tile_cost, src);
                     const int lo = __shfl_sync(0xffffffffu, tile_lo, src), work = __shfl_sync(0xffffffffu, tile_work, src);
                     if (u0 + lane >= units) continue;
+                    const int start = b.item_cost(p, q, t);
                     const int a = hk * head_cost + at, z = a + cost, unit = hk * head_tiles + sh.tiles[s] + t;
                     const int c0 = (a + Q - 1) / Q, c1 = min(p.sms, (z + Q - 1) / Q);  // borders in [a, z): [c0, c1)
                     // tile at which border c cuts the unit, moved to its ends where a piece would be too short (and
                     // to multiples of that least piece where the borders are closer)
                     auto cut = [&](int c) {
-                        int x = max(0, c * Q - a - ITEM_COST);
+                        int x = max(0, c * Q - a - start);
                         if (Q < B::PIECE) x -= x % B::PIECE;
                         return x < B::PIECE ? 0 : work - x < B::PIECE ? work : x;
                     };
