@@ -42,7 +42,17 @@
 // tile takes 1,370 cycles, its products 1,024).  New tokens over long caches: HBM;
 // 12 streams of 1 to 52,360 keys, 24/4 heads, 51.7 us, 77 % of a copy's rate, of
 // which the start and the join take 8 us.  Short prompts: the start and end of one
-// item, 7.2 us a call in a captured graph (the binding's call takes 8 on the host).
+// item, 6.5 us a call in a captured graph (the binding's call takes 8 on the host).
+// Over pages, in a captured graph: the 12 streams out of pages of 64 tokens 48.5 us;
+// 32 tokens over a shared prefix of 25,920 keys, 24/8 heads, 37 us (182 MB: 27 at a
+// copy's rate), where on their own they would read 5.7 GB; the second half of a clip of
+// 25,920 tokens over its pages 1.96-2.1 ms (1.54-1.64 PFLOP/s, the power cap).
+//
+// What a tile's pace comes from, by leaving parts out of copies of the kernel (two
+// streams' next frame, 64.7 us): the products 57.9; the exps 64.2; both 53.7; the
+// maximum, sums and most of the reads of S too 50.3.  What is then left, 950 cycles
+// a tile, is about what 64 KB of K and V take from L2 at 64 bytes a clock: copies, products
+// and exps each come to some 1,000 cycles, and the tile to 1,370.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
