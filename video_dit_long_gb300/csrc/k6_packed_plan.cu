@@ -134,6 +134,7 @@ struct Seq {
 // What the lists are made of.  Batch: packed sequences.
 struct Batch {
     static constexpr int PIECE = MIN_PIECE;
+    static constexpr bool CAPACITY = false;  // Tk is the batch's keys
     __device__ __forceinline__ static int item_cost(const PackedGeom &, const Seq &, int) { return ITEM_COST; }
     const int *cu_q, *cu_k;
     PackedPlan plan;
@@ -165,6 +166,7 @@ struct Batch {
 // Pages: units of tiles; those behind the streams' own are over shared keys.  A slot is a row of the partials.
 struct PagedBatch {
     static constexpr int PIECE = PAGED_PIECE;
+    static constexpr bool CAPACITY = true;  // Tk is the most that a stream's table has room for
     __device__ __forceinline__ static int item_cost(const PackedGeom &p, const Seq &s, int t) {
         return min(p.tpt, s.Lq - t * p.tpt) * p.G <= FEW_ROWS ? FEW_ROWS_ITEM : ITEM_COST;
     }
@@ -229,6 +231,7 @@ struct Shared {
     int at[CLASSES];
     int bad, total;
     unsigned long long work;
+    int top;           // the largest unit's
     int slots, merges;
     // stretches: first unit and item count of each CTA; cost and tiles of the sequences before each one
     int first[MAX_SMS], items[MAX_SMS];
@@ -295,21 +298,25 @@ __device__ void build(const PackedGeom &p, const B &b, Shared &sh) {
     // a warp to a sequence; with fewer sequences than warps all threads to each
     const bool few = b.n < WARPS;
     const int s0 = few ? 0 : warp, ds = few ? 1 : WARPS, t0 = few ? (int)threadIdx.x : lane, dt = few ? THREADS : 32;
-    const int most = LIST == KTILES ? (p.Tq + p.tpt - 1) / p.tpt : (p.Tk + 127) / 128;
+    int most = LIST == KTILES ? (p.Tq + p.tpt - 1) / p.tpt : (p.Tk + 127) / 128;
     int chunk = 1 << 30;
     if (LIST == FWD && p.extra > 0) {
         // key tiles per item: the batch's work over the items aimed at
         unsigned long long w = 0;
+        int top = 1;
         for (int s = s0; s < b.n; s += ds) {
             const Seq q = b.template sequence<LIST>(p, s);
             for (int t = t0; t < q.tiles; t += dt) {
                 int lo, hi;
                 range<LIST>(p, q, t, lo, hi);
                 w += hi - lo;
+                top = max(top, hi - lo);
             }
         }
         atomicAdd(&sh.work, w);
+        atomicMax(&sh.top, top);
         __syncthreads();
+        if (B::CAPACITY) most = sh.top;  // the classes then span what there is, not what there may be
         // extra * chunk >= work, so that the pieces beyond one per tile number at most extra
         const unsigned long long c = (sh.work + p.extra - 1) / p.extra;
         chunk = c < (1u << 30) ? max(2 * B::PIECE, (int)c) : 1 << 30;
@@ -547,6 +554,7 @@ __global__ void __launch_bounds__(THREADS) packed_plan_kernel(const PackedGeom p
     if (threadIdx.x < CLASSES) sh.count[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         sh.work = 0;
+        sh.top = 0;
         sh.slots = sh.merges = 0;
         sh.bad = cu_q[0] < 0 || cu_k[0] < 0 || cu_q[p.n_seq] > p.Tq || cu_k[p.n_seq] > p.Tk;
     }
@@ -654,6 +662,7 @@ __global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg,
     if (threadIdx.x < CLASSES) sh.count[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         sh.work = 0;
+        sh.top = 0;
         sh.slots = sh.merges = prefix_tiles = 0;
         sh.bad = cu_q[0] < 0 || cu_q[p.n_seq] > p.Tq;
         if (pg.n_groups > 0 && (cu_groups[0] < 0 || cu_groups[pg.n_groups] > p.n_seq)) sh.bad = 1;
