@@ -190,16 +190,6 @@ __device__ __forceinline__ bool plan_ok_for(const PagedHeader &head, const Paged
     return paged_plan_ok(head, p.pg);
 }
 
-// The first item, for the producers, which everything else waits for.  Over pages the plan keeps it beside the header.
-__device__ __forceinline__ bool first_item(const PackedPlan &, const Walk &walk, PackedItem &it, int &hk) {
-    return walk.rounds > 0 && walk.at(0, it, hk);
-}
-__device__ __forceinline__ bool first_item(const PagedPlan &plan, const Walk &walk, PackedItem &it, int &hk) {
-    it = plan.first[blockIdx.x];
-    hk = it.n_tok_hk >> 8;
-    return walk.rounds > 0;
-}
-
 __device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2, int c3,
                                             int c4) {
     asm volatile(
@@ -344,11 +334,15 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             uint32_t n = 0;       // tiles loaded
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
-            PackedItem it;
-            int hk;
-            bool have = first_item(plan, walk, it, hk);
-            for (uint32_t k = 0; k < walk.rounds && ok; k++, have = k < walk.rounds && walk.at(k, it, hk)) {
-                const int T = have ? it.kt1 - it.kt0 : 0;
+            PackedItem first;  // everything waits for its copies; over pages the plan keeps it beside the header
+            if constexpr (PAGED) first = plan.first[blockIdx.x];
+            for (uint32_t k = 0; k < walk.rounds && ok; k++) {
+                PackedItem it;
+                int hk;
+                if (PAGED && k == 0) it = first, hk = first.n_tok_hk >> 8;
+                else if (!walk.at(k, it, hk)) continue;
+                const int T = it.kt1 - it.kt0;
+                if (T <= 0) continue;
                 for (int j = 0; j < T && ok; j++, n++) {
                     const uint32_t slot = n % NSLOT;
                     if (!(ok = mbar_wait_w(&empty[slot], ((n / NSLOT) & 1) ^ 1, w))) break;
