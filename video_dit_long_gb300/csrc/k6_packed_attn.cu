@@ -43,8 +43,8 @@
 // 12 streams of 1 to 52,360 keys, 24/4 heads, 51.7 us, 77 % of a copy's rate, of
 // which the start and the join take 8 us.  Short prompts: the start and end of one
 // item, 6.5 us a call in a captured graph (the binding's call takes 8 on the host).
-// Over pages, in a captured graph: the 12 streams out of pages of 64 tokens 48.5 us;
-// 32 tokens over a shared prefix of 25,920 keys, 24/8 heads, 37 us (182 MB: 27 at a
+// Over pages, in a captured graph: the 12 streams out of pages of 64 tokens 47-48 us;
+// 32 tokens over a shared prefix of 25,920 keys, 24/8 heads, 36-37 us (182 MB: 27 at a
 // copy's rate), where on their own they would read 5.7 GB; the second half of a clip of
 // 25,920 tokens over its pages 1.96-2.1 ms (1.54-1.64 PFLOP/s, the power cap).
 //
@@ -202,8 +202,8 @@ __device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, ui
 // The copies that bring tile `kt` of 128 keys of an item and head hk to dst, keys (which = 0) or values.  The whole warp;
 // returns with the barrier told of all of their bytes.
 template <Copies HOW>
-__device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedItem &it, int kt, int hk, int, const void *tm,
-                                          uint8_t *dst, uint64_t *bar, bool leader) {
+__device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedItem &it, int kt, int hk, int, int,
+                                          const void *tm, uint8_t *dst, uint64_t *bar, bool leader) {
     using namespace pf;
     if (leader) {
         const int row = it.krow0 + kt * BN;
@@ -212,19 +212,24 @@ __device__ __forceinline__ void load_tile(const PackedFwdParams &, const PackedI
         tma_load_4d(dst + PANEL, tm, bar, 64, hk, row, 0);
     }
 }
-// Keys in pages.  Lane l brings box l of the tile; boxes wholly behind the stream's last key are left out (their rows of S
+// Keys in pages: the page of box l of the tile, for lane l.
+__device__ __forceinline__ int page_of(const PackedFwdParams &, const PackedItem &, int) { return 0; }
+__device__ __forceinline__ int page_of(const PagedFwdParams &p, const PackedItem &it, int kt) {
+    const int lane = threadIdx.x & 31;
+    int column;
+    paged_box(p.pg, kt, lane, column);
+    return lane < paged_boxes(p.pg, it.Lk, kt) ? p.table[(long)it.krow0 * p.pg.max_pages + column] : 0;
+}
+// Lane l brings box l of the tile; boxes wholly behind the stream's last key are left out (their rows of S
 // are masked, those of V zeroed, and no page is theirs).  The tile's arithmetic divides by shifts and a product: with the
 // compiler's divisions in this loop the whole kernel ran 3 to 25 % slower, the more the smaller the boxes.
 template <Copies HOW>
 __device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedItem &it, int kt, int hk, int which,
-                                          const void *tm, uint8_t *dst, uint64_t *bar, bool leader) {
+                                          int page, const void *tm, uint8_t *dst, uint64_t *bar, bool leader) {
     const int lane = threadIdx.x & 31, n = paged_boxes(p.pg, it.Lk, kt);
-    int column, page = 0;
+    int column;
     const int tok = paged_box(p.pg, kt, lane, column);
-    if (lane < n) {
-        page = p.table[(long)it.krow0 * p.pg.max_pages + column];
-        if (paged_page(p.pg, page) != page) atomicCAS(p.err, DEV_OK, DEV_PLAN);
-    }
+    if (lane < n && paged_page(p.pg, page) != page) atomicCAS(p.err, DEV_OK, DEV_PLAN);
     if (leader) mbar_arrive_expect_tx(bar, (uint32_t)n << (p.pg.box_log2 + 8));
     __syncwarp();
     if (lane < n) {
@@ -309,11 +314,29 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    if constexpr (PAGED) {
+        // The plan's and the table's lines to L2 while the kernel before drains (it may still write them: nothing is read
+        // yet).  2 us lie between the wait and the first copy, of these reads one behind another; 0.1-0.4 us of a call less.
+        if (warp == 1) {
+            const PagedPlan at = plan_of(p);
+            const void *line = nullptr;
+            if (lane == 0) line = at.head;
+            else if (lane == 1) line = &at.count[blockIdx.x];
+            else if (lane == 2) line = &at.first[blockIdx.x];
+            else {
+                const long i = ((long)(lane - 3) * gridDim.x + blockIdx.x) * 32;
+                if (i < (long)p.g.n_seq * p.pg.max_pages) line = p.table + i;
+            }
+            if (line) prefetch_l2(line);
+        }
+    }
     wait_previous_kernel();
     // over pages only now, so that the join, which begins when every CTA has come here, may read the plan before it waits
     if constexpr (PAGED) launch_next_kernel();
     const auto plan = plan_of(p);
     const int mine = plan.count[blockIdx.x];  // beside the header, in every plan: no wait between the two (the grid is g.sms)
+    PackedItem first;                         // over pages so is the CTA's first item
+    if constexpr (PAGED) first = plan.first[blockIdx.x];
     const auto head = *plan.head;             // as a whole: its comparisons would else read it one word after the other
     const bool plan_ok = plan_ok_for(head, p);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(p.err, DEV_OK, DEV_PLAN);
@@ -334,8 +357,6 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
             uint32_t n = 0;       // tiles loaded
             uint32_t uc = 0;      // items with keys so far
             bool ok = true;
-            PackedItem first;  // everything waits for its copies; over pages the plan keeps it beside the header
-            if constexpr (PAGED) first = plan.first[blockIdx.x];
             for (uint32_t k = 0; k < walk.rounds && ok; k++) {
                 PackedItem it;
                 int hk;
@@ -345,8 +366,14 @@ __global__ void __launch_bounds__(pf::THREADS, 1)
                 if (T <= 0) continue;
                 for (int j = 0; j < T && ok; j++, n++) {
                     const uint32_t slot = n % NSLOT;
+                    int page = 0;
+                    // Small boxes read the table ahead of the wait, large ones behind it.  Measured in a captured graph, us,
+                    // behind / ahead: next frame over pages of 16 67.4 / 66.4, of 64 62.5 / 64.6, six samples' frames (48)
+                    // 100.1 / 98.2, new tokens over shared prompts (16) 15.4 / 15.2; a tile ahead of that 65.6, 65.7, 100.5, 15.6.
+                    if (HOW == GROUPS) page = page_of(p, it, it.kt0 + j);
                     if (!(ok = mbar_wait_w(&empty[slot], ((n / NSLOT) & 1) ^ 1, w))) break;
-                    load_tile<HOW>(p, it, it.kt0 + j, hk, warp == 8 ? 0 : 1, tm, ring + slot * TILE, &full[slot],
+                    if (HOW == ROWS) page = page_of(p, it, it.kt0 + j);
+                    load_tile<HOW>(p, it, it.kt0 + j, hk, warp == 8 ? 0 : 1, page, tm, ring + slot * TILE, &full[slot],
                                    leader);
                     if (j == 0 && warp == 8) {  // Q once the last S of the item before has read its tile
                         if (!(ok = uc == 0 || mbar_wait_w(q_empty, (uc - 1) & 1, w))) {
@@ -773,7 +800,8 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(const PackedFwdParams
 }
 
 // Blocks an SM, and partials that a half warp has in flight.  Measured in a captured graph, us (new tokens over a shared
-// prompt, 12 tokens over long caches): 8 partials x 2 blocks 17.7, 49.2; 4 x 3 18.1, 49.6; 4 x 4 19.5, 50.9 (spills).
+// prompt, 12 tokens over long caches; no entry halved): 8 partials x 2 blocks 17.7, 49.2; 4 x 3 18.1, 49.6; 4 x 4 19.5,
+// 50.9 (spills).
 constexpr int MERGE_BLOCKS_PER_SM = 2, MERGE_UNROLL = 8;
 
 // Joins the partials of every row that has some over pages: a block an entry of the
@@ -789,16 +817,24 @@ __global__ void __launch_bounds__(16 * MERGE_ROWS, MERGE_BLOCKS_PER_SM) paged_me
     const PagedPlan plan = plan_of(p);
     const int lane = threadIdx.x & 15, half = threadIdx.x >> 4;
     const bool early = blockIdx.x < (unsigned)p.g.sms;  // as in packed_merge_kernel
-    PagedMerge m;
+    PagedMerge m, halved = plan.merge[blockIdx.x >> 1];  // (of at most 2 g.sms blocks)
     if (early) m = plan.merge[blockIdx.x];
     const PagedHeader head = *plan.head;
     const bool ok = paged_plan_ok(head, p.pg);
-    if (ok && !early && (int)blockIdx.x < head.n_merge) m = plan.merge[blockIdx.x];
+    // Two blocks to an entry where there are as many: half warps then share a row's partials (new tokens over shared prompts
+    // 16.0 -> 15.4 us, 12 tokens over long caches 47.7 -> 46.9).  Entries of 8 rows for every step made two streams' next
+    // frame 62 -> 70 us, whose joins then come in more rounds.
+    const int split = 2 * head.n_merge <= (int)gridDim.x ? 1 : 0, at_most = MERGE_ROWS >> split;
+    if (split) {
+        m = halved;
+        m.r0 += (blockIdx.x & 1) * at_most;
+    } else if (ok && !early && (int)blockIdx.x < head.n_merge) m = plan.merge[blockIdx.x];
     wait_previous_kernel();
     if (!ok) return;
-    for (int mi = blockIdx.x; mi < head.n_merge; mi += gridDim.x) {
+    for (int mi = blockIdx.x >> split; mi < head.n_merge; mi += gridDim.x) {
         if (mi >= (int)gridDim.x) m = plan.merge[mi];
-        const int rows = min(MERGE_ROWS, (m.n_tok_hk & 255) * p.g.G - m.r0);
+        const int rows = min(at_most, (m.n_tok_hk & 255) * p.g.G - m.r0);
+        if (rows <= 0) return;  // the second half of a short entry
         const int row_log2 = 32 - __clz(rows - 1);  // 16 half warps = 2^row_log2 rows of as many shares
         const int share = half >> row_log2, shares = MERGE_ROWS >> row_log2;
         const int r = m.r0 + (half & ((1 << row_log2) - 1));
