@@ -222,3 +222,24 @@ def test_refusals():
         assert e.value.status == K.ERR_INVALID_ARG, bad.keys()
     b.h.sync()
     assert bool((b.q_out == 7.0).all()) and bool((b.k_cache == 7.0).all())
+
+
+@pytest.mark.parametrize("Hkv,queries", [(8, True), (12, True), (24, False), (8, False)])
+def test_enough_tokens_for_strides(Hkv, queries):
+    """Past 40 tokens a SM, with key heads for whole passes, warps stride over the tokens; the last stream's rows too."""
+    b = Step([6100, 0, 77], [6103, 5, 100], 24, Hkv, page=64, seed=6)
+    b.append(**({} if queries else dict(q=None, q_out=None))).h.sync()
+    a, n = b.pad, b.q_out.shape[0] - b.pad
+    if queries:
+        b.near(b.q_out[a:n], b.q[a:n], b.qw, "q")
+        assert bool((b.q_out[:a] == 7.0).all()) and bool((b.q_out[n:] == 7.0).all())
+    else:
+        assert bool((b.q_out == 7.0).all())
+    at = torch.cat((torch.arange(3, 6103, device="cuda"), torch.arange(23, 100, device="cuda")))
+    row = torch.cat((b.table[0].expand(6100, -1), b.table[2].expand(77, -1)))
+    pages = row.gather(1, (at // 64)[:, None])[:, 0].long()
+    b.near(b.k_cache[pages, at % 64], b.k[a:n], b.kw, "k")
+    assert torch.equal(b.v_cache[pages, at % 64], b.v[a:n])
+    for cache in (b.k_cache, b.v_cache):  # nothing else
+        cache[pages, at % 64] = 7.0
+        assert bool((cache == 7.0).all())
