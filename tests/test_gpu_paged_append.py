@@ -243,3 +243,29 @@ def test_enough_tokens_for_strides(Hkv, queries):
     for cache in (b.k_cache, b.v_cache):  # nothing else
         cache[pages, at % 64] = 7.0
         assert bool((cache == 7.0).all())
+
+
+@pytest.mark.parametrize("order", [(1, 0, 2), (2, 0, 1), (1, 2, 0), (2, 1, 0)])
+def test_any_order_of_the_pool(order):
+    b, c = (Step([1, 3, 70, 5], [1, 129, 500, 65], 6, 2, page=48, seed=7) for _ in range(2))
+    b.append().check()
+    back = [order.index(i) for i in range(3)]
+    c.k_cache, c.v_cache = (x.permute(*order, 3).contiguous().permute(*back, 3) for x in (c.k_cache, c.v_cache))
+    c.append().h.sync()
+    assert torch.equal(b.k_cache, c.k_cache) and torch.equal(b.v_cache, c.v_cache) and torch.equal(b.q_out, c.q_out)
+
+
+def test_two_appends_at_once_on_two_streams():
+    """Two layers' calls from one plan, into pools of their own, on streams of their own, over and over."""
+    b = Step([700, 1, 77], [900, 40, 77], 24, 8, page=16, seed=8)
+    b.append().h.sync()
+    pools = [(torch.full_like(b.k_cache, 7.0), torch.full_like(b.v_cache, 7.0), torch.full_like(b.q_out, 7.0)) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (k, v, q) in zip(streams, pools):
+            b.append(k_cache=k, v_cache=v, q_out=q, stream=s)
+    torch.cuda.synchronize()
+    b.h.sync()
+    for k, v, q in pools:
+        assert torch.equal(k, b.k_cache) and torch.equal(v, b.v_cache) and torch.equal(q, b.q_out)

@@ -464,3 +464,38 @@ def test_everything_sixteen_byte_aligned_only():
     b.plan.ptr = b.plan.buffer.data_ptr()
     b.forward().check()
     assert torch.equal(b.out[3:-3], want.out[3:-3]) and torch.equal(b.lse[:, 3:-3], want.lse[:, 3:-3])
+
+
+def laid(cache, order):
+    """The pool's axes (pages, tokens, heads) from the outermost to the innermost in memory."""
+    return cache.permute(*order, 3).contiguous().permute(*[order.index(i) for i in range(3)], 3)
+
+
+@pytest.mark.parametrize("order", [(1, 0, 2), (2, 0, 1), (1, 2, 0), (2, 1, 0)])
+@pytest.mark.parametrize("page", [16, 32, 64, 80])
+def test_any_order_of_the_pool(order, page):
+    """Tokens or heads outermost, pages innermost: a call takes what strides can say."""
+    b = Step([1, 3, 70, 5], [1, 129, 500, 65], 6, 2, 1, page=page, seed=21)
+    b.k_cache = laid(b.k_cache, order)
+    b.forward().check()  # keys in one order, values in another
+    b.out.fill_(7.0)
+    b.v_cache = laid(b.v_cache, order)
+    b.forward().check()
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (0, 2, 1), (2, 1, 0)])
+@pytest.mark.parametrize("page,k", [(16, 16), (16, 9), (32, 31), (64, 60), (1024, 1000)])
+def test_a_pool_of_one_page(order, page, k):
+    b = Step([2], [k], 6, 2, 1, page=page, seed=22)
+    b.k_cache, b.v_cache = (laid(c[b.table[0, :1].long()], order) for c in (b.k_cache, b.v_cache))
+    b.table.fill_(-1)
+    b.table[0, 0] = 0
+    b.plan = b.h.paged_plan(b.cu_q, b.k_now, b.table, b.q.shape[0], 2, page, 1, 1)
+    b.ws = torch.full((b.h.paged_workspace_bytes(b.plan),), 255, dtype=torch.uint8, device="cuda")
+    b.forward().check()
+
+
+def test_joins_of_few_and_of_many_rows():
+    """A stream alone in a step, whose joins take two blocks an entry, and among streams enough for whole entries."""
+    Step([5], [9000], 24, 8, 1, page=64, seed=23).forward().check().again_the_same()
+    Step([5] + [60] * 12, [9000] + [2000 + 37 * n for n in range(12)], 24, 8, 1, page=64, seed=23).forward().check().again_the_same()
