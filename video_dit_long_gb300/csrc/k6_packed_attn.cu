@@ -199,6 +199,8 @@ __device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
+
 // The copies that bring tile `kt` of 128 keys of an item and head hk to dst, keys (which = 0) or values.  The whole warp;
 // returns with the barrier told of all of their bytes.
 template <Copies HOW>
