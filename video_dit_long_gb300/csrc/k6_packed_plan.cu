@@ -644,14 +644,12 @@ __global__ void __launch_bounds__(THREADS) paged_plan_kernel(const PagedGeom pg,
                 else z = m;
             }
             int slot = -1;
-            const int end = cu_q[s + 1], Lk = k_lens[s];
-            if (cu_q[s] <= t && t < end && Lk <= p.Tk) {
-                const int pos = Lk - (end - t);
-                if (pos >= 0) {
-                    const int page = table[(long)s * pg.max_pages + pos / pg.page];
-                    if ((unsigned)page < (unsigned)pg.n_pages) slot = page * pg.page + pos % pg.page;
-                    else atomicCAS(err, DEV_OK, DEV_PLAN);
-                }
+            const int end = cu_q[s + 1];
+            const int pos = cu_q[s] <= t && t < end ? paged_position(pg, t, end, k_lens[s]) : -1;
+            if (pos >= 0) {
+                const int page = table[(long)s * pg.max_pages + pos / pg.page];
+                if ((unsigned)page < (unsigned)pg.n_pages) slot = page * pg.page + pos % pg.page;
+                else atomicCAS(err, DEV_OK, DEV_PLAN);
             }
             plan.slot[t] = slot;
         }

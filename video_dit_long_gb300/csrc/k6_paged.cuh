@@ -124,6 +124,13 @@ static inline __host__ __device__ int paged_group(const PagedGeom &g, int span, 
     return (unsigned)page < (unsigned)g.n_pages ? page * span + tok / 8 : paged_groups(g, span);
 }
 
+// Key position of the query token in row t of a stream of Lk keys whose rows end at `end` (t < end), or -1: the token lies
+// before position 0, or Lk is no length that the table has room for.  Lk comes from the device: it may be any int, and
+// neither the comparisons nor the difference leave an int's range.
+static inline __host__ __device__ int paged_position(const PagedGeom &g, int t, int end, int Lk) {
+    return 0 <= Lk && Lk <= g.g.Tk && end - t <= Lk ? Lk - (end - t) : -1;
+}
+
 // True if the plan was made for this batch and holds valid lists.
 static inline __device__ bool paged_plan_ok(const PagedHeader &h, const PagedGeom &p) {
     return h.magic == PAGED_MAGIC && !h.bad && h.n_seq == p.g.n_seq && h.H == p.g.H && h.Hkv == p.g.Hkv &&
