@@ -143,10 +143,12 @@ class PagedBatch:
 class PagedAttention:
     """One layer's attention over a PagedBatch, with the layer's pools of keys and values.
 
-    by_head: a page holds one head's tokens after another's (else one token's heads).  qk: the type of rotated queries
-    and keys."""
+    qk: the type of rotated queries and keys.  k_cache, v_cache [n_pages][page_tokens][kv_heads][d] (qk's type, and bf16):
+    pools that the layer already has, as when it goes on from the batch that read the prompts to the one that takes the
+    steps; without them it makes its own, with one head's tokens after another's in a page where by_head says so (else
+    one token's heads)."""
 
-    def __init__(self, batch, q_weight, k_weight, eps=1e-6, qk="f16", by_head=False):
+    def __init__(self, batch, q_weight, k_weight, eps=1e-6, qk="f16", by_head=False, *, k_cache=None, v_cache=None):
         import torch
         if qk not in ("f16", "bf16"):
             raise ValueError(qk)
@@ -157,7 +159,13 @@ class PagedAttention:
         t = torch.float16 if qk == "f16" else torch.bfloat16
         new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=self.h._dev)  # noqa: E731
         pool = lambda t: new(n, kv, page, d, dtype=t).transpose(1, 2) if by_head else new(n, page, kv, d, dtype=t)  # noqa: E731
-        self.k_cache, self.v_cache = pool(t), pool(torch.bfloat16)
+        if (k_cache is None) != (v_cache is None):
+            raise ValueError("k_cache, v_cache: give both, or neither")
+        if k_cache is None:
+            k_cache, v_cache = pool(t), pool(torch.bfloat16)
+        K._pages(k_cache, batch.plan.pages, t, self.h._dev, "k_cache")
+        K._pages(v_cache, batch.plan.pages, torch.bfloat16, self.h._dev, "v_cache")
+        self.k_cache, self.v_cache = k_cache, v_cache
         self.q, self.out, self.lse = new(T, self.H, d, dtype=t), new(T, self.H, d).zero_(), new(self.H, T, dtype=torch.float32)
         self.workspace = new(self.h.paged_workspace_bytes(batch.plan), dtype=torch.uint8)
 
