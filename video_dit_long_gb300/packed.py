@@ -28,6 +28,17 @@ from __future__ import annotations
 from . import k6attn as K
 
 
+def _int32(x):
+    """x as a tensor of integers that int32 holds: anything else would be cut off without a word.  (Numbers on the device
+    are taken as they are; the plan checks what it makes of them.)"""
+    import torch
+    x = torch.as_tensor(x)
+    if x.is_floating_point() or (not x.is_cuda and x.numel() and not -2 ** 31 <= int(x.min()) <= int(x.max()) < 2 ** 31):
+        raise ValueError(f"want integers of 32 bits, got {x.dtype} {tuple(x.shape)}"
+                         + ("" if x.is_floating_point() else f" from {int(x.min())} to {int(x.max())}"))
+    return x
+
+
 class PackedBatch:
     """The offsets, mask and work list of a batch, shared by the layers that attend over it.
 
@@ -44,7 +55,7 @@ class PackedBatch:
     @staticmethod
     def _offsets(lens):
         import torch
-        return lens if isinstance(lens, torch.Tensor) else torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+        return lens if isinstance(lens, torch.Tensor) else _int32(torch.tensor([0] + list(lens)).cumsum(0)).to(torch.int32)
 
     def set_offsets(self, offsets):
         """Other lengths of as many sequences, in place (a captured layer sees them at its next replay): offsets [n + 1],
@@ -115,7 +126,7 @@ class PagedBatch:
     def __init__(self, handle, lens, k_lens, table, tokens, kv_heads, page_tokens, n_pages, mask_block=1, groups=None):
         import torch
         self.handle, self.tokens, self.kv_heads = handle, int(tokens), int(kv_heads)
-        own = lambda x: torch.as_tensor(x).to(device=handle._dev, dtype=torch.int32, copy=True)  # noqa: E731
+        own = lambda x: _int32(x).to(device=handle._dev, dtype=torch.int32, copy=True)  # noqa: E731
         self.offsets, self.k_lens, self.table = own(PackedBatch._offsets(lens)), own(k_lens), own(table)
         self.groups = {}
         if groups:
@@ -126,15 +137,14 @@ class PagedBatch:
     def next(self, lens=None, k_lens=None, table=None, shared=None):
         """The next step of as many streams, in place (captured layers see it at their next replay); what is not given
         stays as it is.  Tensors on the device are copied in stream order; the host waits for copies of its own."""
-        import torch
         given = [(self.offsets, None if lens is None else PackedBatch._offsets(lens)), (self.k_lens, k_lens),
                  (self.table, table), (self.groups.get("shared"), shared)]
-        given = [(to, torch.as_tensor(x)) for to, x in given if x is not None]
+        given = [(to, _int32(x)) for to, x in given if x is not None]
         for to, x in given:
             if to is None:
                 raise ValueError("shared: the batch has no groups")
-            if x.shape != to.shape or x.is_floating_point():
-                raise ValueError(f"want integers of shape {tuple(to.shape)}, got {x.dtype} {tuple(x.shape)}")
+            if x.shape != to.shape:
+                raise ValueError(f"want integers of shape {tuple(to.shape)}, got {tuple(x.shape)}")
         for to, x in given:
             to.copy_(x)
         self.handle.paged_replan(self.plan, self.offsets, self.k_lens, self.table, **self.groups)
