@@ -2,7 +2,8 @@
 every kind of copy, calls of different data at once."""
 import pytest
 
-from .test_gpu_paged_attention import Step
+from .test_gpu_paged_append import Step as Append
+from .test_gpu_paged_attention import GROUPS, Step, laid
 from .test_gpu_paged_layer import EPS, Streams, pages_for
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,150 @@ def test_a_layer_goes_on_with_its_pools(by_head, qk):
         PagedAttention(batch, *st.w, EPS, qk=qk, k_cache=layer.k_cache[1:], v_cache=layer.v_cache)
     with pytest.raises(ValueError):
         PagedAttention(batch, *st.w, EPS, qk="bf16" if qk == "f16" else "f16", k_cache=layer.k_cache, v_cache=layer.v_cache)
+
+
+@pytest.mark.parametrize("case", GROUPS)
+@pytest.mark.parametrize("page,order", [(16, "heads"), (16, (1, 0, 2)), (32, (2, 1, 0)), (48, "tokens"), (64, "tokens"),
+                                        (64, "heads"), (112, "tokens"), (128, "tokens"), (128, (2, 0, 1)), (384, "heads")])
+def test_shared_prefixes_over_every_kind_of_copy(case, page, order):
+    """Boxes of 16 and 32 tokens by groups of 8 and, in orders of the pool that groups cannot say, by rows; larger ones."""
+    q, k, groups = case
+    b = Step(q, k, 6, 2, 1, page=page, seed=30, groups=groups, order=order if order == "heads" else "tokens")
+    if isinstance(order, tuple):
+        b.k_cache, b.v_cache = laid(b.k_cache, order), laid(b.v_cache, order)
+    b.forward().check().again_the_same()
+
+
+@pytest.mark.parametrize("page", [48, 64, 128])
+@pytest.mark.parametrize("copies", [False, True])
+def test_groups_dealt_out_over_every_kind_of_copy(page, copies):
+    """More streams than are cut into stretches, two groups among them, one whose streams have copies of the prefix."""
+    q = [1, 2, 0, 1] * 280
+    k = [30 + s % 7 for s in range(40)] + [1500 + s for s in range(60)] + [40] * 1020
+    Step(q, k, 4, 2, 1, page=page, seed=31, groups=[(40, 0), (60, 1490)], copies=copies).forward().check().again_the_same()
+
+
+def test_two_steps_of_different_data_at_once():
+    """One plan and table, two streams, queries and pools of their own: each call's results are its own."""
+    lens = [1] * 8, [2100 + n for n in range(8)]
+    a, b = (Step(*lens, 8, 4, 1, seed=19, groups=[(8, 2000)]) for _ in "ab")
+    g = torch.Generator(device="cuda").manual_seed(32)
+    b.q[b.pad:-b.pad] = torch.randn(b.q[b.pad:-b.pad].shape, generator=g, device="cuda").to(b.q.dtype)
+    b.k_cache.neg_()
+    b.v_cache.mul_(0.5)
+    b.k, b.v = [-x for x in b.k], [x * 0.5 for x in b.v]
+    want = []
+    for x in (a, b):
+        x.forward().check()
+        want.append((x.out.clone(), x.lse.clone()))
+    assert not torch.equal(want[0][0], want[1][0])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        for s, x in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                x.out.fill_(7.0)
+                x.lse.fill_(7.0)
+                x.ws.fill_(255)
+                x.h.paged_forward(a.plan, x.q, x.k_cache, x.v_cache, x.out, x.lse, workspace=x.ws)
+        torch.cuda.synchronize()
+        for x, (out, lse) in zip((a, b), want):
+            x.h.sync()
+            assert torch.equal(x.out, out) and torch.equal(x.lse, lse)
+
+
+def test_two_appends_of_different_data_at_once():
+    """One plan, two streams, tokens and pools of their own, cleared in every round."""
+    b = Append([700, 1, 77], [900, 40, 77], 24, 8, page=16, seed=8)
+    n = slice(b.pad, b.q.shape[0] - b.pad)
+    g = torch.Generator(device="cuda").manual_seed(33)
+    other = b.qkv.clone()
+    other[n] = torch.randn(other[n].shape, generator=g, device="cuda").to(torch.bfloat16)
+    made = []
+    for x in (b.qkv, other):
+        pools = [torch.full_like(t, 7.0) for t in (b.k_cache, b.v_cache, b.q_out)]
+        args = dict(q=x[:, :24], k=x[:, 24:32], v=x[:, 32:], k_cache=pools[0], v_cache=pools[1], q_out=pools[2])
+        b.append(**args).h.sync()
+        made.append((args, pools, [t.clone() for t in pools]))
+    assert not any(torch.equal(x, y) for x, y in zip(made[0][2], made[1][2]))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        for s, (args, pools, _) in zip(streams, made):
+            with torch.cuda.stream(s):
+                for t in pools:
+                    t.fill_(7.0)
+                b.append(**args)
+        torch.cuda.synchronize()
+        b.h.sync()
+        for _, pools, want in made:
+            assert all(torch.equal(x, y) for x, y in zip(pools, want))
+
+
+@pytest.mark.parametrize("lens", [([1], [1]), ([90, 200], [90, 200]), ([1] * 40, [900] * 40)])
+def test_plans_of_rows_and_of_pages_are_no_plans_of_each_other(lens):
+    """Reported, and nothing is written.  (Each has room for what the other's calls read before its header:
+    test_paged_apart.py.)"""
+    b = Step(*lens, 4, 2, 1, seed=34)
+    K, h, T = b.K, b.h, b.q.shape[0]
+    cu_k = torch.tensor([0] + lens[1], dtype=torch.int32, device="cuda").cumsum(0).to(torch.int32)
+    rows = h.packed_plan(b.cu_q, cu_k, T, sum(lens[1]), 2, 1)
+    h.sync()
+
+    def refused(call):
+        with pytest.raises(K.K6Error) as e:
+            call()  # at once where the room that the plan should have, and has not, holds another argument
+            h.sync()
+        assert e.value.status == K.ERR_INVALID_ARG
+        assert bool((b.out == 7.0).all()) and bool((b.lse == 7.0).all())
+
+    p = K.PagedPlan(b.plan.batch, rows.buffer, b.table)
+    refused(lambda: h.paged_forward(p, b.q, b.k_cache, b.v_cache, b.out, b.lse, workspace=b.ws))
+    pools = [torch.full_like(x, 7.0) for x in (b.k_cache, b.v_cache)]
+    x = torch.zeros((T, 8, 128), dtype=torch.bfloat16, device="cuda")
+    rotated = torch.full_like(b.q, 7.0)
+    pos = torch.zeros((T, 3), dtype=torch.int32, device="cuda")
+    refused(lambda: h.paged_append(p, x[:, :4], x[:, 4:6], x[:, 6:], pos, q_out=rotated, k_cache=pools[0], v_cache=pools[1]))
+    assert all(bool((x == 7.0).all()) for x in (rotated, *pools))
+    p = K.PackedPlan(rows.batch, b.plan.buffer)
+    k, v = (torch.zeros((sum(lens[1]), 2, 128), dtype=t, device="cuda") for t in (b.q.dtype, torch.bfloat16))
+    ws = torch.empty(h.packed_workspace_bytes(rows), dtype=torch.uint8, device="cuda")
+    refused(lambda: h.packed_forward(p, b.q, k, v, b.out, b.lse, workspace=ws))
+    b.forward().check()
+
+
+@pytest.mark.parametrize("Hkv", [1, 3, 8])
+@pytest.mark.parametrize("tokens", [2540, 6079, 6080])
+def test_tokens_on_both_sides_of_the_strides(Hkv, tokens):
+    """Stretches of passes below 40 tokens a SM, and with few key heads beyond; whole runs in strides from there on."""
+    b = Append([tokens - 40, 40 - 4], [tokens - 40, 300], 24, Hkv, page=64, seed=35, pad=2).append()
+    b.h.sync()
+    a, n = b.pad, b.q_out.shape[0] - b.pad
+    assert b.q_out.shape[0] == tokens
+    b.near(b.q_out[a:n], b.q[a:n], b.qw, "q")
+    at = torch.cat((torch.arange(tokens - 40, device="cuda"), torch.arange(264, 300, device="cuda")))
+    row = torch.cat((b.table[0].expand(tokens - 40, -1), b.table[1].expand(36, -1)))
+    pages = row.gather(1, (at // 64)[:, None])[:, 0].long()
+    b.near(b.k_cache[pages, at % 64], b.k[a:n], b.kw, "k")
+    assert torch.equal(b.v_cache[pages, at % 64], b.v[a:n])
+    for cache in (b.k_cache, b.v_cache):  # nothing else
+        cache[pages, at % 64] = 7.0
+        assert bool((cache == 7.0).all())
+
+
+def test_appends_past_four_gigabytes():
+    """A pool of 5.4 GB of keys and as much of values, whose last pages are a stream's."""
+    n_pages, page, Hkv = 82_000, 64, 4
+    b = Append([70], [250], 8, Hkv, page=page, seed=36)
+    k, v = (torch.zeros((n_pages, page, Hkv, 128), dtype=t, device="cuda") for t in (b.t, torch.bfloat16))
+    assert k.numel() * 2 > 1 << 32
+    table = torch.tensor([[n_pages - 1, 5, n_pages - 2, n_pages - 9]], dtype=torch.int32, device="cuda")
+    plan = b.h.paged_plan(b.cu_q, b.k_now, table, b.q.shape[0], Hkv, page, n_pages, 1)
+    b.append(plan=plan, k_cache=k, v_cache=v).h.sync()
+    at = torch.arange(180, 250, device="cuda")
+    pages, n = table[0].long()[at // page], slice(b.pad, b.pad + 70)
+    b.near(k[pages, at % page], b.k[n], b.kw, "k")
+    assert torch.equal(v[pages, at % page], b.v[n])
+    for cache in (k, v):
+        cache[pages, at % page] = 0.0
+        assert not cache.any()
