@@ -213,3 +213,27 @@ def test_appends_past_four_gigabytes():
     for cache in (k, v):
         cache[pages, at % page] = 0.0
         assert not cache.any()
+
+
+def part_of(t, width, at):
+    """The rows of t as a part of wider ones: heads `at` and on of `width`, sevens beside them."""
+    x = torch.full((t.shape[0], width, 128), 7.0, dtype=t.dtype, device="cuda")
+    x[:, at:at + t.shape[1]] = t
+    return x, x[:, at:at + t.shape[1]]
+
+
+@pytest.mark.parametrize("qk", ["f16", "bf16"])
+@pytest.mark.parametrize("lse", [True, False])
+def test_rows_that_are_parts_of_wider_ones(qk, lse):
+    """Queries out of a fused projection, results into part of a wider tensor, joins and shared prefixes among them; with
+    and without lse."""
+    lens = [1, 1, 1, 1, 90], [1300, 1301, 1302, 700, 5000]
+    want = Step(*lens, 6, 2, 1, qk=qk, seed=37, groups=[(4, 690)]).forward().check()
+    b = Step(*lens, 6, 2, 1, qk=qk, seed=37, groups=[(4, 690)])
+    _, b.q = part_of(b.q, 11, 0)
+    whole, b.out = part_of(b.out, 9, 2)
+    b.h.paged_forward(b.plan, b.q, b.k_cache, b.v_cache, b.out, b.lse if lse else None, workspace=b.ws)
+    b.h.sync()
+    assert torch.equal(b.out, want.out) and (not lse or torch.equal(b.lse, want.lse))
+    assert lse or bool((b.lse == 7.0).all())
+    assert bool((whole[:, :2] == 7.0).all()) and bool((whole[:, 8:] == 7.0).all())
