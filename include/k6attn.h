@@ -605,7 +605,12 @@ k6attn_status k6attn_packed_backward(k6attn_t h, const k6attn_packed *batch, con
  *               streams [cu_groups[g], cu_groups[g+1]) (int32 [n_groups + 1],
  *               ascending; other streams are on their own), whose first shared[g]
  *               tokens (int32) have the same keys and values, in the same pages
- *               or in copies.  A stream may be shorter than that.
+ *               or in copies.  A stream may be shorter than that, or its new
+ *               tokens may begin inside the prefix: only what all of the group's
+ *               streams with new tokens see of it is then taken together, so a
+ *               stream that sees much less of it than the others is better left
+ *               out of the group (as a group of one, or behind the last group):
+ *               results are the same, but the others then keep what they share.
  *  n_pages      pages of the pool, n_pages * page_tokens below 2^31.
  *  q_tokens     token rows of q, k, v (at least the last offset).
  */

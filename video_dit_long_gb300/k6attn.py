@@ -558,8 +558,9 @@ class Handle:
         """Plan a step of streams whose keys lie in pages: offsets cu_q [n + 1] into q_tokens rows, k_lens [n] keys of
         each stream with the new ones, table [n][max_pages] of its pages (int32, on the device; the table is kept
         and has to stay as it is while the plan is in use).  The pools have n_pages pages of page_tokens tokens.
-        Streams [cu_groups[g], cu_groups[g + 1]) have their first shared[g] tokens in common.  mask_block as in
-        packed_plan."""
+        Streams [cu_groups[g], cu_groups[g + 1]) have their first shared[g] tokens in common; what all of them with new
+        tokens see of those is read once, so a stream that sees much less is better left out of the group.  mask_block
+        as in packed_plan."""
         torch = _torch_types()
         if table.dim() != 2:
             raise ValueError(f"table: want [streams][pages], got {tuple(table.shape)}")

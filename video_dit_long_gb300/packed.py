@@ -121,7 +121,8 @@ class PagedBatch:
 
     lens: new tokens of each stream (a list, or int32 offsets [n + 1]); k_lens: keys of each with the new ones; table
     [n][max_pages]: its pages in order.  tokens: rows of qkv.  groups: [(streams, shared tokens)] of the streams in
-    order that have a prefix in common, or None; mask_block as for PackedBatch."""
+    order that have a prefix in common, or None (a stream that sees much less of it than the others cuts what is read once
+    for all of them: better a group of its own); mask_block as for PackedBatch."""
 
     def __init__(self, handle, lens, k_lens, table, tokens, kv_heads, page_tokens, n_pages, mask_block=1, groups=None):
         import torch
