@@ -40,16 +40,18 @@
 // cap; 25,920 tokens causal by frames of 1,620, 24/8 heads, 2.98 ms = 1.47
 // PFLOP/s, 77 % of a library product's burst (the pipe active 79 % of the time; a
 // tile takes 1,370 cycles, its products 1,024).  New tokens over long caches: HBM;
-// 12 streams of 1 to 52,360 keys, 24/4 heads, 51.7 us, 77 % of a copy's rate, of
+// 12 streams of 1 to 52,360 keys, 24/4 heads, 50-51 us, 79 % of a copy's rate, of
 // which the start and the join take 8 us.  Short prompts: the start and end of one
-// item, 6.5 us a call in a captured graph (the binding's call takes 8 on the host).
-// Over pages, in a captured graph: the 12 streams out of pages of 64 tokens 47-48 us;
-// 32 tokens over a shared prefix of 25,920 keys, 24/8 heads, 36-37 us (182 MB: 27 at a
+// item, 6.5 us a call in a captured graph (7.5 with inputs out of HBM; the binding's
+// call takes 8 on the host).
+// Over pages, in a captured graph: the 12 streams out of pages of 64 tokens 48 us;
+// 32 tokens over a shared prefix of 25,920 keys, 24/8 heads, 36.6 us (182 MB: 27 at a
 // copy's rate), where on their own they would read 5.7 GB; the second half of a clip of
-// 25,920 tokens over its pages 1.96-2.1 ms (1.54-1.64 PFLOP/s, the power cap).
+// 25,920 tokens over its pages 2.16-2.19 ms (1.47-1.49 PFLOP/s at the power cap, SM clock
+// 1,560-1,580 MHz; 1.91-2.04 ms in bursts that end before the cap).
 //
 // What a tile's pace comes from, by leaving parts out of copies of the kernel (two
-// streams' next frame, 64.7 us): the products 57.9; the exps 64.2; both 53.7; the
+// streams' next frame, in bursts: 64.7 us): the products 57.9; the exps 64.2; both 53.7; the
 // maximum, sums and most of the reads of S too 50.3.  What is then left, 950 cycles
 // a tile, is about what 64 KB of K and V take from L2 at 64 bytes a clock: copies, products
 // and exps each come to some 1,000 cycles, and the tile to 1,370.
@@ -224,7 +226,8 @@ __device__ __forceinline__ int page_of(const PagedFwdParams &p, const PackedItem
 }
 // Lane l brings box l of the tile; boxes wholly behind the stream's last key are left out (their rows of S
 // are masked, those of V zeroed, and no page is theirs).  The tile's arithmetic divides by shifts and a product: with the
-// compiler's divisions in this loop the whole kernel ran 3 to 25 % slower, the more the smaller the boxes.
+// compiler's divisions in this loop two streams' next frame takes 78 us for 67 over pages of 16 tokens and 71 for 67 over
+// pages of 128, a mixed step 35-36 for 33, new tokens over long caches 0-4 % more.
 template <Copies HOW>
 __device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedItem &it, int kt, int hk, int which,
                                           int page, const void *tm, uint8_t *dst, uint64_t *bar, bool leader) {
