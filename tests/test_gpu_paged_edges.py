@@ -2,6 +2,7 @@
 every kind of copy, calls of different data at once."""
 import pytest
 
+from . import packed_ref as R
 from .test_gpu_paged_append import Step as Append
 from .test_gpu_paged_attention import GROUPS, Step, laid
 from .test_gpu_paged_layer import EPS, Streams, pages_for
@@ -237,3 +238,87 @@ def test_rows_that_are_parts_of_wider_ones(qk, lse):
     assert torch.equal(b.out, want.out) and (not lse or torch.equal(b.lse, want.lse))
     assert lse or bool((b.lse == 7.0).all())
     assert bool((whole[:, :2] == 7.0).all()) and bool((whole[:, 8:] == 7.0).all())
+
+
+@pytest.mark.parametrize("page,columns,cut", [(65536, 8191, 0), (64, 8388607, 5), (1 << 20, 511, 1)])
+def test_positions_up_to_the_limit(page, columns, cut):
+    """Streams of nearly 2^29 keys, every column of whose table names the pool's one page: attention is that over the
+    page, every key as often as it comes, and new tokens lie at the end of it."""
+    from video_dit_long_gb300 import k6attn as K
+    g = torch.Generator(device="cuda").manual_seed(38)
+    Lk, H, T = page * columns - cut, 2, 3
+    k, v = (torch.randn((1, page, 1, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in "kv")
+    v[..., :64] = 1.0
+    q = torch.randn((T, H, 128), generator=g, device="cuda").to(torch.bfloat16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros((1, columns), dtype=torch.int32, device="cuda")
+    h = K.Handle.for_packed(H)
+    plan = h.paged_plan(i32(0, T), i32(Lk), table, T, 1, page, 1, 0)
+    out, lse = torch.empty_like(q), torch.empty((H, T), device="cuda")
+    ws = torch.empty(h.paged_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+    h.paged_forward(plan, q, k, v, out, lse, workspace=ws)
+    h.sync()
+    s = torch.einsum("thd,kd->htk", q.double(), k[0, :, 0].double()) / 128 ** 0.5
+    a = torch.einsum("thd,kd->htk", q.double().abs(), k[0, :, 0].double().abs()).amax(-1) / 128 ** 0.5
+    times = torch.full((page,), columns, dtype=torch.float64, device="cuda")
+    times[page - cut:] -= 1
+    want = torch.logsumexp(s + times.log(), -1)
+    # as packed_ref.attention; the fp32 row sums add a term of 128 keys at a time, each off by 2^-24 of the sum
+    tiles = Lk / 128 / torch.cuda.get_device_properties(0).multi_processor_count
+    R.assert_within(lse, want, 2.0 ** -19 * (a + 1) + 2.0 ** -20 * want.abs() + tiles * 2.0 ** -24, "lse")
+    p = torch.exp(s + times.log() - want[..., None])
+    ref, mag = (torch.einsum("htk,kd->thd", p, x) for x in (v[0, :, 0].double(), v[0, :, 0].double().abs()))
+    # a tile adds 8 products of 16 keys to O, each sum cut off below 2^-23 of it
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -13 + tiles * 8 * 2.0 ** -23) * mag
+    R.assert_within(out, ref, bound, "out")
+    kc, vc = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    x = torch.randn((T, H + 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    zero = torch.zeros((T, 3), dtype=torch.int32, device="cuda")
+    h.paged_append(plan, None, x[:, H:H + 1], x[:, H + 1:], zero, q_out=None, k_cache=kc, v_cache=vc)
+    h.sync()
+    at = (torch.arange(Lk - T, Lk, device="cuda") % page)
+    for cache, rows in ((kc, x[:, H:H + 1]), (vc, x[:, H + 1:])):  # at position (0, 0, 0) nothing turns
+        assert torch.equal(cache[0, at], rows)
+        cache[0, at] = 7.0
+        assert bool((cache == 7.0).all())
+
+
+@pytest.mark.parametrize("page,order", [(16, (1, 0, 2)), (48, "tokens"), (64, "tokens"), (64, "heads"), (128, "tokens")])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 2 ** 31 - 1, "behind"])
+def test_a_page_that_is_none_over_every_kind_of_copy(page, order, bad):
+    """A group's first stream names it: the group has results of some kind, the streams beside it theirs; reported."""
+    q, k = [1, 1, 1, 1, 2, 70], [700, 701, 702, 703, 300, 500]
+    b = Step(q, k, 6, 2, 1, page=page, seed=39, groups=[(4, 690)], order="heads" if order == "heads" else "tokens")
+    if isinstance(order, tuple):
+        b.k_cache, b.v_cache = laid(b.k_cache, order), laid(b.v_cache, order)
+    want = b.forward().check().out.clone()
+    good = b.table.clone()
+    b.table[0, 200 // page] = b.k_cache.shape[0] if bad == "behind" else bad
+    b.out.fill_(7.0)
+    b.forward()
+    with pytest.raises(b.K.K6Error) as e:
+        b.h.sync()
+    assert e.value.status == b.K.ERR_INVALID_ARG
+    own = slice(b.pad + 4, None)
+    assert torch.equal(b.out[own], want[own]) and bool((b.out[:b.pad] == 7.0).all())
+    b.table.copy_(good)
+    b.forward().check()
+    assert torch.equal(b.out, want)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("bad", [-1, 1, 2 ** 31 - 1])
+def test_a_page_that_a_pool_of_one_does_not_have(page, bad):
+    b = Step([2, 1], [page, page - 3], 6, 2, 1, page=page, seed=40)
+    b.k_cache, b.v_cache = (c[b.table[0, :1].long()] for c in (b.k_cache, b.v_cache))
+    b.table.fill_(-1)
+    b.table[0, 0], b.table[1, 0] = 0, bad
+    b.plan = b.h.paged_plan(b.cu_q, b.k_now, b.table, b.q.shape[0], 2, page, 1, 1)
+    with pytest.raises(b.K.K6Error):  # the new token has no place
+        b.h.sync()
+    b.forward()
+    with pytest.raises(b.K.K6Error) as e:
+        b.h.sync()
+    assert e.value.status == b.K.ERR_INVALID_ARG
+    ref, _, bo, _ = R.attention(b.q[b.pad:b.pad + 2], b.k[0], b.v[0], [2], [page], 1)
+    R.assert_within(b.out[b.pad:b.pad + 2], ref, bo, "out")

@@ -234,7 +234,7 @@ __device__ __forceinline__ void load_tile(const PagedFwdParams &p, const PackedI
     const int lane = threadIdx.x & 31, n = paged_boxes(p.pg, it.Lk, kt);
     int column;
     const int tok = paged_box(p.pg, kt, lane, column);
-    if (lane < n && paged_page(p.pg, page) != page) atomicCAS(p.err, DEV_OK, DEV_PLAN);
+    if (lane < n && paged_page(p.pg, page) == p.pg.n_pages) atomicCAS(p.err, DEV_OK, DEV_PLAN);
     if (leader) mbar_arrive_expect_tx(bar, (uint32_t)n << (p.pg.box_log2 + 8));
     __syncwarp();
     if (lane < n) {
