@@ -30,6 +30,10 @@
 // 3.4 us beyond its tiles: 1 warp a scheduler runs its serial code slowly.)
 // All waits are bounded (DEV_TIMEOUT), as in the other kernels.
 //
+// Logits, maxima, row sums, O and partials are fp32; P is rounded to V's type.  Tensor
+// memory cuts sums off where the row sums round them: O loses some 1.5 2^-24 of itself
+// for every 16 keys of an item (0.03 % after 52,360 keys, 2 % after 3.5 million).
+//
 // Keys in pages (k6_paged.cuh): the same kernel, whose producers fetch a tile as
 // copies of `box` tokens out of the pages that the table names, one lane a copy; a
 // page that the table does not name right is left to the copy's zero fill and
