@@ -322,3 +322,21 @@ def test_a_page_that_a_pool_of_one_does_not_have(page, bad):
     assert e.value.status == b.K.ERR_INVALID_ARG
     ref, _, bo, _ = R.attention(b.q[b.pad:b.pad + 2], b.k[0], b.v[0], [2], [page], 1)
     R.assert_within(b.out[b.pad:b.pad + 2], ref, bo, "out")
+
+
+@pytest.mark.parametrize("cu,shared", [([2, 8], [690]), ([0, 0, 2, 2, 2, 8, 8, 8, 8, 8, 8, 8], [5, 0, 2 ** 31 - 1, 9, 698, 1, 1, 1, 1, 1, 1]),
+                                       ([8, 8], [3]), ([3, 5, 8], [690, 650])])
+def test_groups_anywhere_among_the_streams(cu, shared):
+    """Streams before the first group, groups of no streams, more groups than streams."""
+    q, k = [4, 1, 1, 1, 0, 1, 1, 2], [100, 40, 700, 701, 702, 703, 704, 705]
+    b = Step(q, k, 6, 2, 1, page=32, seed=41, groups=[(1, 0), (1, 0), (6, 698)])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    b.more = dict(cu_groups=i32(cu), shared=i32(shared))
+    b.plan = b.h.paged_plan(b.cu_q, b.k_now, b.table, b.q.shape[0], 2, 32, b.k_cache.shape[0], 1, **b.more)
+    b.ws = torch.full((b.h.paged_workspace_bytes(b.plan),), 255, dtype=torch.uint8, device="cuda")
+    b.forward().check().again_the_same()
+
+
+def test_a_group_whose_streams_have_nothing_new():
+    b = Step([0, 0, 3, 0], [700, 701, 90, 700], 6, 2, 1, page=64, seed=42, groups=[(2, 690), (1, 0), (1, 700)])
+    b.forward().check().again_the_same()
